@@ -193,6 +193,90 @@ int pa_kv_append(pa_handle h, const void* k_new, const void* v_new, int n_new, i
                  const int32_t* block_table_row, int8_t* k_pool, int8_t* v_pool, float* k_scale, float* v_scale,
                  void* stream);
 
+/* Norm and rotation: the step from a layer's projected rows to the queries and
+ * keys the calls above take.  For every row x of 256 values (one token, one head)
+ *   r = 1 / sqrt(mean(x^2) + eps),  y_d = x_d * r * (weight_offset + weight_d)
+ * and then the rotary positions on the first rot_dim dims: pair i (dims i and
+ * i + rot_dim/2 with PA_ROPE_HALF, 2i and 2i + 1 with PA_ROPE_ADJACENT) turned
+ * by the angle a = position[axis[i]] * inv_freq[i],
+ *   (y1, y2) -> (y1 cos a - y2 sin a, y2 cos a + y1 sin a).
+ * All in fp32, rounded to bf16 once at the end; the angle is reduced to a
+ * fraction of a turn in 64-bit integers, so it is as exact at position 2^31 as
+ * at 0.  Several axes: positions of time, height and width for images and
+ * video, each pair following the axis its table names. */
+#define PA_ROPE_HALF 0
+#define PA_ROPE_ADJACENT 1
+#define PA_ROPE_MAX_AXES 4
+
+/* A rotation, filled by pa_rope_init; plain data, copied by every call that takes it. */
+typedef struct {
+  int rot_dim;        /* leading dims of a head that are turned; 0: none */
+  int pairing;        /* PA_ROPE_HALF | PA_ROPE_ADJACENT */
+  int n_axes;         /* position axes, 1 .. PA_ROPE_MAX_AXES */
+  int reserved;
+  uint64_t turn[128]; /* pair i: turns per position, a binary fraction of 64 bits */
+  uint8_t axis[128];  /* pair i: the axis whose position turns it */
+} pa_rope;
+
+/* bf16 rows [token][head][256] in device memory: strides in elements, each a
+ * multiple of 8 and >= 0; the 256 values of a row are contiguous; data 16-byte
+ * aligned.  So the rows may be slices of one fused projection buffer. */
+typedef struct {
+  const void* data;
+  long long tok_stride;
+  long long head_stride;
+} pa_rows;
+
+/* Host-only.  rot_dim: a multiple of 16 in [0, 256].  inv_freq (host, rot_dim/2
+ * entries): radians per position.  pair_axis (host, rot_dim/2 entries; NULL:
+ * all 0): the axis of each pair, in [0, n_axes).  PA_EINVAL for anything else,
+ * or a frequency that is not finite. */
+int pa_rope_init(pa_rope* rope, int rot_dim, int pairing, int n_axes, const double* inv_freq,
+                 const int32_t* pair_axis);
+
+/* Norm and rotation of n_tok tokens' query rows (n_q_heads of the handle) into
+ * q_out and key rows (n_kv_heads) into k_out, bf16 [n_tok][heads][256]
+ * contiguous, what pa_prefill* / pa_decode* and pa_kv_append take.
+ *   q, k            host structs of device rows; q NULL (with q_out NULL) or k
+ *                   NULL (with k_out NULL) leaves that kind out
+ *   q_weight,
+ *   k_weight        device bf16 [256], 16-byte aligned, or NULL: gain 1
+ *                   (weight_offset is then not used)
+ *   eps             >= 0; a row of zeros with eps 0 gives zeros
+ *   rope            host struct, or NULL: norm only
+ *   positions       device int32 [n_axes][pos_stride], entry t of each axis for
+ *                   token t; any int32; NULL only without a rotation
+ * q_out may be q.data, and k_out k.data, where those rows are contiguous (in
+ * place); any other overlap of an output with an input or the other output
+ * is PA_EINVAL, as are bad strides, alignment or ranges.  Inputs must be
+ * finite with |x| < 2^56.  n_tok 0 does nothing.  Asynchronous on `stream`. */
+int pa_qk_norm_rope(pa_handle h, int n_tok, const pa_rows* q, const pa_rows* k, const void* q_weight,
+                    const void* k_weight, float weight_offset, float eps, const pa_rope* rope,
+                    const int32_t* positions, long long pos_stride, void* q_out, void* k_out, void* stream);
+
+/* pa_qk_norm_rope for a batch of sequences whose keys and values go straight
+ * into the pool: one launch per 512 sequences in place of pa_qk_norm_rope and
+ * a pa_kv_append for each.  seqs (host) as pa_prefill_batch takes it: sequence
+ * s has seqs[s].n_q new tokens at positions [q_start, q_start + n_q), their
+ * rows in q, k, v and q_out from row q_off on; block_table row s (device, row
+ * stride max_pages_per_seq) lists its pages.  K rows are quantised from the
+ * fp32 normed and turned values (no bf16 in between), V rows as they are,
+ * both by pa_kv_append's rule (scale absmax/127, codes half to even, decided
+ * on correctly rounded quotients).
+ *   positions       as above, by row (so pos_stride is at least the largest q_off + n_q);
+ *                   NULL: every axis takes the token's own position
+ *   q               NULL (with q_out NULL): keys and values only
+ * Rows of no sequence, and slots of no new token, are left as they were.
+ * Sequences must not share rows (PA_EINVAL) nor the pages they write (the
+ * slot's contents are then undefined).  A page entry outside the pool is never
+ * dereferenced: the token's K and V are skipped and pa_last_error reports
+ * PA_EBADPAGE.  Other errors and requirements as pa_qk_norm_rope and
+ * pa_kv_append; n_seq 0 does nothing.  Asynchronous on `stream`. */
+int pa_qkv_append(pa_handle h, int n_seq, const pa_seq* seqs, const pa_rows* q, const pa_rows* k, const pa_rows* v,
+                  const void* q_weight, const void* k_weight, float weight_offset, float eps, const pa_rope* rope,
+                  const int32_t* positions, long long pos_stride, const int32_t* block_table, int8_t* k_pool,
+                  int8_t* v_pool, float* k_scale, float* v_scale, void* q_out, void* stream);
+
 /* Decode: one new query token per sequence against the same pool and mask
  * (the decode path that shares the prefill's window selection, "int8
  * tensor-core prefill attention", sections "Why the attention, and why tensor
@@ -301,6 +385,19 @@ int pa_debug_maskset(pa_handle h, int n_seq, const pa_seq* seqs, int n_sink_blk,
  * Synchronous on `stream`.  PA_EINVAL for a negative count, NULL or misaligned
  * pointers; PA_ECUDA if the launch fails. */
 int pa_debug_qcodes(const void* q_rows, int n_rows, int8_t* codes, float* scales, void* stream);
+
+/* Debug (tests), host-only, no GPU needed: what pa_qk_norm_rope and
+ * pa_qkv_append say of their arguments (PA_OK or PA_EINVAL) on a handle of
+ * these shapes; no pointer but those to host structs is read. */
+int pa_debug_qk_norm_rope_check(int n_q_heads, int n_kv_heads, int n_tok, const pa_rows* q, const pa_rows* k,
+                                const void* q_weight, const void* k_weight, float weight_offset, float eps,
+                                const pa_rope* rope, const int32_t* positions, long long pos_stride, void* q_out,
+                                void* k_out);
+int pa_debug_qkv_append_check(int n_q_heads, int n_kv_heads, int max_pages_per_seq, int n_seq, const pa_seq* seqs,
+                              const pa_rows* q, const pa_rows* k, const pa_rows* v, const void* q_weight,
+                              const void* k_weight, float weight_offset, float eps, const pa_rope* rope,
+                              const int32_t* positions, long long pos_stride, const int32_t* block_table,
+                              int8_t* k_pool, int8_t* v_pool, float* k_scale, float* v_scale, void* q_out);
 
 /* Allocation-free variant of pa_prefill (one sequence, default
  * containers).  The pages have no counterpart of this entry point: it exists

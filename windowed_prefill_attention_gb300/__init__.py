@@ -28,13 +28,15 @@ PA_NOALLOC_SCRATCH_BYTES = 32 << 20
 UNIT_ROWS = 256
 PA_Q_BF16, PA_Q_INT8 = 0, 1
 PA_P_F16, PA_P_U8 = 0, 1
+PA_ROPE_HALF, PA_ROPE_ADJACENT, PA_ROPE_MAX_AXES = 0, 1, 4
 
 EXPORTED = ("pa_default_options", "pa_create", "pa_destroy", "pa_prefill", "pa_prefill_batch",
-            "pa_prefill_batch_gated", "pa_prefill_host", "pa_kv_append", "pa_decode",
+            "pa_prefill_batch_gated", "pa_prefill_host", "pa_kv_append", "pa_rope_init", "pa_qk_norm_rope",
+            "pa_qkv_append", "pa_decode",
             "pa_last_error", "pa_timing", "pa_strerror", "pa_plan", "pa_plan_pairs", "pa_host_chunks", "pa_decode_plan",
             "pa_debug_gather",
             "pa_debug_maskset", "pa_debug_qcodes", "pa_debug_copy_streams_idle", "pa_prefill_noalloc",
-            "pa_debug_noalloc_units")
+            "pa_debug_noalloc_units", "pa_debug_qk_norm_rope_check", "pa_debug_qkv_append_check")
 
 
 class pa_options(C.Structure):
@@ -44,6 +46,15 @@ class pa_options(C.Structure):
 
 class pa_seq(C.Structure):
     _fields_ = [("q_off", C.c_int), ("q_start", C.c_int), ("n_q", C.c_int), ("n_ctx", C.c_int)]
+
+
+class pa_rope(C.Structure):
+    _fields_ = [("rot_dim", C.c_int), ("pairing", C.c_int), ("n_axes", C.c_int), ("reserved", C.c_int),
+                ("turn", C.c_uint64 * 128), ("axis", C.c_uint8 * 128)]
+
+
+class pa_rows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("tok_stride", C.c_longlong), ("head_stride", C.c_longlong)]
 
 
 _vp, _i, _f = C.c_void_p, C.c_int, C.c_float
@@ -57,6 +68,14 @@ _lib.pa_prefill_batch.argtypes = [_vp, _i, C.POINTER(pa_seq)] + [_vp] * 6 + [_i,
 _lib.pa_prefill_host.argtypes = _lib.pa_prefill_batch.argtypes
 _lib.pa_prefill_batch_gated.argtypes = [_vp, _i, C.POINTER(pa_seq)] + [_vp] * 7 + [_i, _i, _f, _vp, _vp]
 _lib.pa_kv_append.argtypes = [_vp, _vp, _vp, _i, _i] + [_vp] * 6
+_ll = C.c_longlong
+_lib.pa_rope_init.argtypes = [C.POINTER(pa_rope), _i, _i, _i, _vp, _vp]
+_lib.pa_qk_norm_rope.argtypes = [_vp, _i, C.POINTER(pa_rows), C.POINTER(pa_rows), _vp, _vp, _f, _f, C.POINTER(pa_rope),
+                                 _vp, _ll, _vp, _vp, _vp]
+_lib.pa_qkv_append.argtypes = ([_vp, _i, C.POINTER(pa_seq)] + [C.POINTER(pa_rows)] * 3
+                               + [_vp, _vp, _f, _f, C.POINTER(pa_rope), _vp, _ll] + [_vp] * 7)
+_lib.pa_debug_qk_norm_rope_check.argtypes = [_i, _i] + _lib.pa_qk_norm_rope.argtypes[1:-1]
+_lib.pa_debug_qkv_append_check.argtypes = [_i, _i, _i] + _lib.pa_qkv_append.argtypes[1:-1]
 _lib.pa_decode.argtypes = _lib.pa_prefill_batch.argtypes
 _lib.pa_last_error.argtypes = [_vp, _vp]
 _lib.pa_timing.argtypes = [_vp, _i, C.POINTER(C.c_double), C.POINTER(C.c_double), C.POINTER(_i)]
@@ -131,10 +150,33 @@ def _stream(stream):
     return C.c_void_p(stream.cuda_stream)
 
 
+def _torch():
+    import torch
+    return torch
+
+
+def _stream_of(t, stream):
+    """The given stream, or the current one of the tensor's device."""
+    if stream is None:
+        stream = _torch().cuda.current_stream(t.device)
+    return C.c_void_p(stream.cuda_stream)
+
+
 def pa_default_options() -> pa_options:
     o = pa_options()
     _lib.pa_default_options(C.byref(o))
     return o
+
+
+# (q heads, kv heads, pool pages, pages per sequence) of the live handles, for the calls that check their tensors
+_geometry = {}
+
+
+def _geometry_of(h):
+    g = _geometry.get(h.value) if isinstance(h, C.c_void_p) else None
+    if g is None:
+        raise ValueError("not a live handle")
+    return g
 
 
 def pa_create(n_q_heads, n_kv_heads, n_pool_pages, max_pages_per_seq, head_dim=256, page_size=16,
@@ -145,10 +187,12 @@ def pa_create(n_q_heads, n_kv_heads, n_pool_pages, max_pages_per_seq, head_dim=2
     h = C.c_void_p()
     _check(_lib.pa_create(C.byref(h), n_q_heads, n_kv_heads, head_dim, page_size, n_pool_pages, max_pages_per_seq,
                           C.byref(o)), "pa_create")
+    _geometry[h.value] = (n_q_heads, n_kv_heads, n_pool_pages, max_pages_per_seq)
     return h
 
 
 def pa_destroy(h) -> None:
+    _geometry.pop(h.value, None)
     _lib.pa_destroy(h)
 
 
@@ -202,6 +246,115 @@ def pa_kv_append(h, k_new, v_new, tok_start, block_table_row, k_pool, v_pool, k_
                              _dev(k_pool, torch.int8, "k_pool"), _dev(v_pool, torch.int8, "v_pool"),
                              _dev(k_scale, torch.float32, "k_scale"), _dev(v_scale, torch.float32, "v_scale"),
                              _stream(stream)), "pa_kv_append")
+
+
+def pa_rope_init(inv_freq, pairing=PA_ROPE_HALF, pair_axis=None) -> pa_rope:
+    """A rotation of the first 2 * len(inv_freq) dims of a head: radians per position of each pair, and
+    the position axis each pair follows (None: one axis)."""
+    freq = np.ascontiguousarray(inv_freq, dtype=np.float64).reshape(-1)
+    axis = None if pair_axis is None else np.ascontiguousarray(pair_axis, dtype=np.int32).reshape(-1)
+    if axis is not None and axis.size != freq.size:
+        raise ValueError("pair_axis and inv_freq must have one entry for each pair")
+    n_axes = 1 if axis is None or axis.size == 0 else int(axis.max()) + 1
+    r = pa_rope()
+    _check(_lib.pa_rope_init(C.byref(r), 2 * freq.size, pairing, n_axes, freq.ctypes.data_as(C.c_void_p),
+                             None if axis is None else axis.ctypes.data_as(C.c_void_p)), "pa_rope_init")
+    return r
+
+
+def _rows(t, name, heads, tokens):
+    """bf16 rows [token, head, 256] at any strides (the 256 values of a row contiguous)."""
+    if not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype != _torch().bfloat16:
+        raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    if t.shape != (tokens, heads, 256) or t.stride(2) != 1:
+        raise ValueError("%s must be [%d, %d, 256] with contiguous rows, got %s" % (name, tokens, heads, tuple(t.shape)))
+    return C.byref(pa_rows(t.data_ptr(), t.stride(0), t.stride(1)))
+
+
+def _gain(w, name):
+    if w is None:
+        return None
+    if w.numel() != 256:
+        raise ValueError("%s must have 256 entries" % name)
+    return _dev(w, _torch().bfloat16, name)
+
+
+def _positions(positions, rope, tokens):
+    """int32 [tokens] or [axes, tokens] -> pointer and row stride."""
+    if positions is None:
+        return None, 0
+    if not positions.is_cuda or positions.dtype != _torch().int32:
+        raise TypeError("positions must be a CUDA int32 tensor")
+    if positions.stride(-1) != 1 and positions.size(-1) > 1:
+        raise ValueError("positions must be contiguous along the tokens")
+    n_axes = positions.size(0) if positions.dim() == 2 else 1
+    if positions.dim() not in (1, 2) or positions.size(-1) < tokens:
+        raise ValueError("positions must be [tokens] or [axes, tokens]")
+    if rope is not None and rope.rot_dim > 0 and n_axes < rope.n_axes:
+        raise ValueError("positions must have %d axes, got %d" % (rope.n_axes, n_axes))
+    return C.c_void_p(positions.data_ptr()), positions.stride(0) if n_axes > 1 else positions.size(-1)
+
+
+def _shaped(t, shape, dtype, name):
+    p = _dev(t, dtype, name)
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, shape, tuple(t.shape)))
+    return p
+
+
+def _pool_args(geometry, n_seq, block_table, k_pool, v_pool, k_scale, v_scale):
+    """Block table, pools and scales of the handle's shapes."""
+    torch = _torch()
+    _, hkv, n_pool, max_pages = geometry
+    if block_table.dim() != 2 or block_table.size(0) < n_seq or block_table.size(1) != max_pages:
+        raise ValueError("block_table must have a row of %d pages for each sequence" % max_pages)
+    rows = (n_pool, 16, hkv)
+    return (_dev(block_table, torch.int32, "block_table"), _shaped(k_pool, rows + (256,), torch.int8, "k_pool"),
+            _shaped(v_pool, rows + (256,), torch.int8, "v_pool"), _shaped(k_scale, rows, torch.float32, "k_scale"),
+            _shaped(v_scale, rows, torch.float32, "v_scale"))
+
+
+def pa_qk_norm_rope(h, q, k, q_weight, k_weight, eps, rope, positions, q_out, k_out, weight_offset=0.0,
+                    stream=None) -> None:
+    """Norm and rotate query rows q [tokens, HQ, 256] into q_out and key rows k [tokens, HKV, 256] into k_out
+    (contiguous; q or k None leaves that kind out).  rope: a pa_rope, or None for the norm alone; positions
+    int32 [tokens] or [axes, tokens]."""
+    some = k if q is None else q
+    if some is None:
+        raise ValueError("q or k is needed")
+    hq, hkv = _geometry_of(h)[:2]
+    bf16, n = _torch().bfloat16, some.size(0)
+    pos, pos_stride = _positions(positions, rope, n)
+    _check(_lib.pa_qk_norm_rope(
+        h, n, None if q is None else _rows(q, "q", hq, n), None if k is None else _rows(k, "k", hkv, n),
+        _gain(q_weight, "q_weight"), _gain(k_weight, "k_weight"), weight_offset, eps,
+        None if rope is None else C.byref(rope), pos, pos_stride,
+        None if q is None else _shaped(q_out, (n, hq, 256), bf16, "q_out"),
+        None if k is None else _shaped(k_out, (n, hkv, 256), bf16, "k_out"), _stream_of(some, stream)),
+        "pa_qk_norm_rope")
+
+
+def pa_qkv_append(h, seqs, q, k, v, q_weight, k_weight, eps, rope, positions, block_table, k_pool, v_pool, k_scale,
+                  v_scale, q_out, weight_offset=0.0, stream=None) -> None:
+    """The new tokens of a batch of sequences (rows q_off .. q_off + n_q of q, k, v): queries normed and rotated
+    into q_out, keys normed, rotated and quantised, values quantised into the pool.  positions None: the tokens'
+    own; q None (with q_out None): keys and values only."""
+    geometry = _geometry_of(h)
+    hq, hkv = geometry[:2]
+    s = _seqs(seqs)
+    n = k.size(0)
+    if len(s) and max(e.q_off + e.n_q for e in s) > n:
+        raise ValueError("a sequence's rows are outside k")
+    pos, pos_stride = _positions(positions, rope, n)
+    _check(_lib.pa_qkv_append(
+        h, len(s), s, None if q is None else _rows(q, "q", hq, n), _rows(k, "k", hkv, n), _rows(v, "v", hkv, n),
+        _gain(q_weight, "q_weight"), _gain(k_weight, "k_weight"), weight_offset, eps,
+        None if rope is None else C.byref(rope), pos, pos_stride,
+        *_pool_args(geometry, len(s), block_table, k_pool, v_pool, k_scale, v_scale),
+        None if q is None else _shaped(q_out, (n, hq, 256), _torch().bfloat16, "q_out"), _stream_of(k, stream)),
+        "pa_qkv_append")
 
 
 def pa_prefill_host(h, seqs, q, k_pool, v_pool, k_scale, v_scale, block_table, n_sink_blk, n_win_blk, sm_scale,

@@ -1,6 +1,7 @@
 // C-ABI host side: handle, argument checks, the window-aware work planner
 // (longest-first unit order), workspace, tensor maps and launches.
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -14,6 +15,7 @@
 #include "../../include/pa.h"
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
+#include "pa_qkv.h"
 
 using namespace pa;
 
@@ -1071,6 +1073,283 @@ int pa_kv_append(pa_handle h, const void* k_new, const void* v_new, int n_new, i
   p.err = h->d_err;
   PA_CUDA(launch_kv_append(p, static_cast<cudaStream_t>(stream)));
   return PA_OK;
+}
+
+namespace {
+// The handle's device is the current one inside the guard's scope.
+struct OnDevice {
+  int prev = -1;
+  bool ok = true;
+  explicit OnDevice(int device) {
+    int cur = -1;
+    if (cudaGetDevice(&cur) != cudaSuccess) ok = false;
+    else if (cur != device) {
+      ok = cudaSetDevice(device) == cudaSuccess;
+      prev = cur;
+    }
+  }
+  ~OnDevice() {
+    if (prev >= 0) (void)cudaSetDevice(prev);
+  }
+};
+
+// Bytes [lo, hi) of an array.
+struct Span {
+  uintptr_t lo = 0, hi = 0;
+  bool meets(const Span& o) const { return lo < o.hi && o.lo < hi; }
+};
+Span span_of(const void* p, size_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return Span{a, a + bytes};
+}
+
+// Checks a host description of `tokens` rows of `heads` heads (row indexes
+// below `tokens`) and fills the kernel's form and the bytes they lie in.
+bool rows_ok(const pa_rows* r, long long tokens, int heads, RowsIn& in, Span& span) {
+  if (!r || !r->data || !aligned(r->data, 16)) return false;
+  const long long ts = r->tok_stride, hs = r->head_stride;
+  if (ts < 0 || hs < 0 || ts % 8 || hs % 8) return false;
+  const long long most = 1ll << 46;  // elements: far above any device's memory, and no product below overflows
+  if ((tokens > 1 && ts > most / tokens) || (heads > 1 && hs > most / heads)) return false;
+  in = RowsIn{static_cast<const __nv_bfloat16*>(r->data), ts, hs};
+  span = span_of(r->data, (size_t)((tokens - 1) * ts + (heads - 1) * hs + kHeadDim) * 2);
+  return true;
+}
+
+// An output [tokens][heads][256] against the rows it is made from: apart, or the same rows in place.
+bool out_ok(const Span& out, const Span& in, const RowsIn& rows, int heads, long long tokens) {
+  if (!out.meets(in)) return true;
+  return out.lo == in.lo && (heads == 1 || rows.hs == kHeadDim) &&
+         (tokens == 1 || rows.ts == (long long)heads * kHeadDim);
+}
+
+bool rope_ok(const pa_rope* r) {
+  if (r->rot_dim < 0 || r->rot_dim > kHeadDim || r->rot_dim % 16) return false;
+  if (r->pairing != PA_ROPE_HALF && r->pairing != PA_ROPE_ADJACENT) return false;
+  if (r->n_axes < 1 || r->n_axes > PA_ROPE_MAX_AXES) return false;
+  for (int i = 0; i < r->rot_dim / 2; ++i)
+    if (r->axis[i] >= r->n_axes) return false;
+  return true;
+}
+
+// The arguments the two calls share: query and key rows of `tokens` row
+// indexes, gains, eps, rotation, positions, the query's output.
+struct QkvSpans {
+  Span q, k, q_out;
+};
+struct Heads {
+  int HQ, HKV;
+};
+int qkv_common(const Heads& h, long long tokens, const pa_rows* q, const pa_rows* k, const void* qw, const void* kw,
+               float w_off, float eps, const pa_rope* rope, const int32_t* pos, long long pos_stride, void* q_out,
+               QkvParams& p, QkvSpans& sp) {
+  if ((q == nullptr) != (q_out == nullptr)) return PA_EINVAL;
+  if (!std::isfinite(eps) || eps < 0.f || !std::isfinite(w_off)) return PA_EINVAL;
+  if (qw && !aligned(qw, 16)) return PA_EINVAL;
+  if (kw && !aligned(kw, 16)) return PA_EINVAL;
+  if (q) {
+    if (!rows_ok(q, tokens, h.HQ, p.q, sp.q) || !aligned(q_out, 16)) return PA_EINVAL;
+    sp.q_out = span_of(q_out, (size_t)tokens * h.HQ * kHeadDim * 2);
+    if (!out_ok(sp.q_out, sp.q, p.q, h.HQ, tokens)) return PA_EINVAL;
+    p.n_q = h.HQ;
+  }
+  if (k) {
+    if (!rows_ok(k, tokens, h.HKV, p.k, sp.k)) return PA_EINVAL;
+    if (q && sp.q_out.meets(sp.k)) return PA_EINVAL;
+    p.n_k = h.HKV;
+  }
+  p.qw = static_cast<const __nv_bfloat16*>(qw);
+  p.kw = static_cast<const __nv_bfloat16*>(kw);
+  p.w_off = w_off;
+  p.eps = eps;
+  p.rope.n_axes = 1;
+  if (rope) {
+    if (!rope_ok(rope)) return PA_EINVAL;
+    p.rope = *rope;
+  }
+  if (p.rope.rot_dim > 0 && pos) {
+    if (!aligned(pos, 4) || pos_stride < 0 || (p.rope.n_axes > 1 && pos_stride < tokens)) return PA_EINVAL;
+    p.pos = pos;
+    p.pos_stride = pos_stride;
+  }
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  return PA_OK;
+}
+
+// Whether two sequences of a batch have a row in common.
+bool rows_shared(int n_seq, const pa_seq* seqs) {
+  bool sorted = true;
+  for (int s = 1; s < n_seq && sorted; ++s) sorted = seqs[s].q_off >= seqs[s - 1].q_off + seqs[s - 1].n_q;
+  if (sorted) return false;
+  std::vector<std::pair<int, int>> r((size_t)n_seq);
+  for (int s = 0; s < n_seq; ++s) r[(size_t)s] = {seqs[s].q_off, seqs[s].q_off + seqs[s].n_q};
+  std::sort(r.begin(), r.end());
+  for (size_t s = 1; s < r.size(); ++s)
+    if (r[s].first < r[s - 1].second) return true;
+  return false;
+}
+
+// Arguments of pa_qk_norm_rope (n_tok >= 1) -> the kernel's parameters.
+int qk_norm_rope_args(const Heads& h, int n_tok, const pa_rows* q, const pa_rows* k, const void* qw, const void* kw,
+                      float w_off, float eps, const pa_rope* rope, const int32_t* pos, long long pos_stride,
+                      void* q_out, void* k_out, QkvParams& p) {
+  if ((!q && !k) || (k == nullptr) != (k_out == nullptr)) return PA_EINVAL;
+  QkvSpans sp;
+  const int rc = qkv_common(h, n_tok, q, k, qw, kw, w_off, eps, rope, pos, pos_stride, q_out, p, sp);
+  if (rc) return rc;
+  if (p.rope.rot_dim > 0 && !p.pos) return PA_EINVAL;
+  if (k) {
+    if (!aligned(k_out, 16)) return PA_EINVAL;
+    const Span ko = span_of(k_out, (size_t)n_tok * h.HKV * kHeadDim * 2);
+    if (!out_ok(ko, sp.k, p.k, h.HKV, n_tok)) return PA_EINVAL;
+    if (q && (ko.meets(sp.q) || ko.meets(sp.q_out))) return PA_EINVAL;
+    p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  }
+  p.n_tok = n_tok;
+  return PA_OK;
+}
+
+// Arguments of pa_qkv_append (n_seq >= 1) -> the kernel's parameters, but for each launch's sequences.
+int qkv_append_args(const Heads& h, int max_pages, int n_seq, const pa_seq* seqs, const pa_rows* q, const pa_rows* k,
+                    const pa_rows* v, const void* qw, const void* kw, float w_off, float eps, const pa_rope* rope,
+                    const int32_t* pos, long long pos_stride, const int32_t* bt, int8_t* kp, int8_t* vp, float* ksc,
+                    float* vsc, void* q_out, QkvParams& p) {
+  if (!seqs || !k || !v || !bt || !kp || !vp || !ksc || !vsc) return PA_EINVAL;
+  if (!aligned(kp, 16) || !aligned(vp, 16) || !aligned(ksc, 4) || !aligned(vsc, 4) || !aligned(bt, 4))
+    return PA_EINVAL;
+  long long tokens = 0;  // rows of the arrays
+  for (int s = 0; s < n_seq; ++s) {
+    const pa_seq& a = seqs[s];
+    if (a.n_q < 1 || a.q_start < 0 || a.q_off < 0 || (long long)a.q_start + a.n_q > a.n_ctx ||
+        (long long)a.q_start + a.n_q > (long long)max_pages * kPage || (long long)a.q_off + a.n_q > (1ll << 30))
+      return PA_EINVAL;
+    tokens = std::max(tokens, (long long)a.q_off + a.n_q);
+  }
+  if (rows_shared(n_seq, seqs)) return PA_EINVAL;
+  QkvSpans sp;
+  const int rc = qkv_common(h, tokens, q, k, qw, kw, w_off, eps, rope, pos, pos_stride, q_out, p, sp);
+  if (rc) return rc;
+  Span vs;
+  if (!rows_ok(v, tokens, h.HKV, p.v, vs) || (q && sp.q_out.meets(vs))) return PA_EINVAL;
+  p.n_v = h.HKV;
+  p.block_table = bt;
+  p.bt_stride = max_pages;
+  p.HKV = h.HKV;
+  p.k_pool = kp;
+  p.v_pool = vp;
+  p.k_scale = ksc;
+  p.v_scale = vsc;
+  return PA_OK;
+}
+
+// A launch over n_tok tokens: how many rows a warp takes.
+void qkv_split(QkvParams& p, int n_tok, int n_sm) {
+  const int rows = p.n_q + p.n_k + p.n_v;
+  p.n_tok = n_tok;
+  p.rows_per_part = qkv_rows_per_part(n_tok, rows, n_sm);
+  p.parts = (rows + p.rows_per_part - 1) / p.rows_per_part;
+}
+
+bool heads_ok(int HQ, int HKV) {  // pa_create's requirements
+  return HQ > 0 && HKV > 0 && HKV <= 8 && HQ % HKV == 0 && HQ / HKV <= kRows && kRows % (HQ / HKV) == 0;
+}
+}  // namespace
+
+int pa_rope_init(pa_rope* rope, int rot_dim, int pairing, int n_axes, const double* inv_freq,
+                 const int32_t* pair_axis) {
+  if (!rope || rot_dim < 0 || rot_dim > kHeadDim || rot_dim % 16 || n_axes < 1 || n_axes > PA_ROPE_MAX_AXES ||
+      (pairing != PA_ROPE_HALF && pairing != PA_ROPE_ADJACENT) || (rot_dim > 0 && !inv_freq))
+    return PA_EINVAL;
+  pa_rope r;
+  std::memset(&r, 0, sizeof r);
+  r.rot_dim = rot_dim;
+  r.pairing = pairing;
+  r.n_axes = n_axes;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const int a = pair_axis ? pair_axis[i] : 0;
+    if (a < 0 || a >= n_axes || !std::isfinite(inv_freq[i])) return PA_EINVAL;
+    r.axis[i] = (uint8_t)a;
+    // whole turns drop out; the fraction of one, times 2^64 (exact: a power of two)
+    const double turns = inv_freq[i] / 6.283185307179586476925286766559;
+    const double frac = turns - std::floor(turns);
+    r.turn[i] = frac < 1.0 ? (uint64_t)std::ldexp(frac, 64) : 0u;
+  }
+  *rope = r;
+  return PA_OK;
+}
+
+int pa_qk_norm_rope(pa_handle h, int n_tok, const pa_rows* q, const pa_rows* k, const void* q_weight,
+                    const void* k_weight, float weight_offset, float eps, const pa_rope* rope,
+                    const int32_t* positions, long long pos_stride, void* q_out, void* k_out, void* stream) {
+  if (!h || n_tok < 0 || n_tok > (1 << 30)) return PA_EINVAL;
+  if (n_tok == 0) return PA_OK;
+  QkvParams p{};
+  const int rc = qk_norm_rope_args(Heads{h->HQ, h->HKV}, n_tok, q, k, q_weight, k_weight, weight_offset, eps, rope,
+                                   positions, pos_stride, q_out, k_out, p);
+  if (rc) return rc;
+  qkv_split(p, n_tok, h->n_sm);
+  OnDevice dev(h->device);
+  if (!dev.ok) return PA_ECUDA;
+  PA_CUDA(launch_qk_norm_rope(p, h->n_sm, static_cast<cudaStream_t>(stream)));
+  return PA_OK;
+}
+
+int pa_qkv_append(pa_handle h, int n_seq, const pa_seq* seqs, const pa_rows* q, const pa_rows* k, const pa_rows* v,
+                  const void* q_weight, const void* k_weight, float weight_offset, float eps, const pa_rope* rope,
+                  const int32_t* positions, long long pos_stride, const int32_t* block_table, int8_t* k_pool,
+                  int8_t* v_pool, float* k_scale, float* v_scale, void* q_out, void* stream) {
+  if (!h || n_seq < 0) return PA_EINVAL;
+  if (n_seq == 0) return PA_OK;
+  QkvParams p{};
+  const int rc = qkv_append_args(Heads{h->HQ, h->HKV}, h->max_pages, n_seq, seqs, q, k, v, q_weight, k_weight,
+                                 weight_offset, eps, rope, positions, pos_stride, block_table, k_pool, v_pool,
+                                 k_scale, v_scale, q_out, p);
+  if (rc) return rc;
+  p.n_pool = h->n_pool;
+  p.err = h->d_err;
+  OnDevice dev(h->device);
+  if (!dev.ok) return PA_ECUDA;
+  QkvSeqs<kQkvSeqs> tab;
+  for (int s0 = 0; s0 < n_seq; s0 += kQkvSeqs) {
+    const int n = std::min(kQkvSeqs, n_seq - s0);
+    int first = 0;
+    p.same_len = seqs[s0].n_q;
+    for (int i = 0; i < n; ++i) {
+      const pa_seq& a = seqs[s0 + i];
+      tab.s[i] = make_int4(a.q_off, a.q_start, first, 0);
+      first += a.n_q;  // at most 2^30: the sequences' rows are disjoint
+      if (a.n_q != p.same_len) p.same_len = 0;
+    }
+    p.n_seq = n;
+    p.bt_row0 = s0;
+    qkv_split(p, first, h->n_sm);
+    PA_CUDA(launch_qkv_append(p, tab, h->n_sm, static_cast<cudaStream_t>(stream)));
+  }
+  return PA_OK;
+}
+
+int pa_debug_qk_norm_rope_check(int n_q_heads, int n_kv_heads, int n_tok, const pa_rows* q, const pa_rows* k,
+                                const void* q_weight, const void* k_weight, float weight_offset, float eps,
+                                const pa_rope* rope, const int32_t* positions, long long pos_stride, void* q_out,
+                                void* k_out) {
+  if (!heads_ok(n_q_heads, n_kv_heads) || n_tok < 0 || n_tok > (1 << 30)) return PA_EINVAL;
+  if (n_tok == 0) return PA_OK;
+  QkvParams p{};
+  return qk_norm_rope_args(Heads{n_q_heads, n_kv_heads}, n_tok, q, k, q_weight, k_weight, weight_offset, eps, rope,
+                           positions, pos_stride, q_out, k_out, p);
+}
+
+int pa_debug_qkv_append_check(int n_q_heads, int n_kv_heads, int max_pages_per_seq, int n_seq, const pa_seq* seqs,
+                              const pa_rows* q, const pa_rows* k, const pa_rows* v, const void* q_weight,
+                              const void* k_weight, float weight_offset, float eps, const pa_rope* rope,
+                              const int32_t* positions, long long pos_stride, const int32_t* block_table,
+                              int8_t* k_pool, int8_t* v_pool, float* k_scale, float* v_scale, void* q_out) {
+  if (!heads_ok(n_q_heads, n_kv_heads) || n_seq < 0) return PA_EINVAL;
+  if (n_seq == 0) return PA_OK;
+  QkvParams p{};
+  return qkv_append_args(Heads{n_q_heads, n_kv_heads}, max_pages_per_seq, n_seq, seqs, q, k, v, q_weight, k_weight,
+                         weight_offset, eps, rope, positions, pos_stride, block_table, k_pool, v_pool, k_scale,
+                         v_scale, q_out, p);
 }
 
 namespace {
