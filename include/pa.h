@@ -314,6 +314,44 @@ int pa_decode_plan(int n_kv_heads, int slots, int n_seq, const pa_seq* seqs, int
                    int32_t* runs_out, int cap, int* n_cta, int* per_cta, int* max_slots, int* listed,
                    long long* total_blocks);
 
+/* Decode of a batch that shares a prefix: pa_decode for sequences whose first
+ * n_prefix tokens (a multiple of 16, so whole pages; below every n_ctx) are the
+ * same, in the same pool pages, such as a system prompt or a document asked
+ * many questions.  The prefix's keys are read once for all sequences (up to
+ * 512 a launch) and multiplied with all their queries on the tensor cores;
+ * each sequence's own keys are computed as pa_decode does, and the parts are
+ * merged.  The result is pa_decode's on the same keys, but for the order of
+ * sums and the roundings of P' to fp16.
+ *   block_table   row s holds sequence s's pages; the prefix's pages are those
+ *                 of row 0, and the other rows' entries for it are not read
+ *   others        as pa_decode; sequences must not share a row of q / out (PA_EINVAL)
+ * A prefix page outside the pool is skipped for all sequences, one of a
+ * sequence's own pages for that sequence (PA_EBADPAGE through pa_last_error).
+ * Three kernel launches per 512 sequences, asynchronous on `stream`.  Calls on
+ * one handle share its work buffers: issue them, and replay graphs captured
+ * from them, one after another.  The buffers grow by allocation; a call on a
+ * capturing stream that would have to grow them returns PA_ENOMEM (make a call
+ * of that size before the capture).  They are freed with the handle only, so a
+ * graph stays valid while its handle lives. */
+int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, const void* q, const int8_t* k_pool,
+                     const int8_t* v_pool, const float* k_scale, const float* v_scale, const int32_t* block_table,
+                     int n_sink_blk, int n_win_blk, float sm_scale, void* out, void* stream);
+
+/* Host-only, no GPU needed: how pa_decode_shared splits the work of one launch
+ * (the first min(n_seq, 512) sequences) on a GPU of n_sm SMs.  prefix_out (may
+ * be NULL) receives *n_prefix_runs entries of int32[8] = {CTA, kv head, first
+ * sequence, sequences, sink, lo, first, last}: entries first .. last - 1 of the
+ * list of blocks 0 .. sink - 1, then lo, lo + 1, ... (the prefix's blocks that
+ * some of the sequences see) against those sequences' queries of the head.
+ * own_out (may be NULL): *n_own_runs entries, one CTA each, of int32[7] =
+ * {sequence, kv head, base, sink, lo, first, last}: entries first .. last - 1 of
+ * the list of blocks base .. base + sink - 1, then lo, lo + 1, ...  PA_EINVAL
+ * for what pa_decode_shared refuses of these arguments, or a list that does
+ * not fit its cap. */
+int pa_decode_shared_plan(int n_q_heads, int n_kv_heads, int max_pages_per_seq, int n_sm, int n_seq,
+                          const pa_seq* seqs, int n_prefix, int n_sink_blk, int n_win_blk, int32_t* prefix_out,
+                          int prefix_cap, int* n_prefix_runs, int32_t* own_out, int own_cap, int* n_own_runs);
+
 /* Query rows per work unit: the G = n_q_heads / n_kv_heads q heads of one kv
  * head times PA_UNIT_ROWS / G consecutive tokens starting on a multiple of
  * PA_UNIT_ROWS / G.  One unit is one 256-row tensor-core tile computed by a

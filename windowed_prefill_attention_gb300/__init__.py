@@ -32,7 +32,7 @@ PA_ROPE_HALF, PA_ROPE_ADJACENT, PA_ROPE_MAX_AXES = 0, 1, 4
 
 EXPORTED = ("pa_default_options", "pa_create", "pa_destroy", "pa_prefill", "pa_prefill_batch",
             "pa_prefill_batch_gated", "pa_prefill_host", "pa_kv_append", "pa_rope_init", "pa_qk_norm_rope",
-            "pa_qkv_append", "pa_decode",
+            "pa_qkv_append", "pa_decode", "pa_decode_shared", "pa_decode_shared_plan",
             "pa_last_error", "pa_timing", "pa_strerror", "pa_plan", "pa_plan_pairs", "pa_host_chunks", "pa_decode_plan",
             "pa_debug_gather",
             "pa_debug_maskset", "pa_debug_qcodes", "pa_debug_copy_streams_idle", "pa_prefill_noalloc",
@@ -77,6 +77,9 @@ _lib.pa_qkv_append.argtypes = ([_vp, _i, C.POINTER(pa_seq)] + [C.POINTER(pa_rows
 _lib.pa_debug_qk_norm_rope_check.argtypes = [_i, _i] + _lib.pa_qk_norm_rope.argtypes[1:-1]
 _lib.pa_debug_qkv_append_check.argtypes = [_i, _i, _i] + _lib.pa_qkv_append.argtypes[1:-1]
 _lib.pa_decode.argtypes = _lib.pa_prefill_batch.argtypes
+_lib.pa_decode_shared.argtypes = [_vp, _i, C.POINTER(pa_seq), _i] + [_vp] * 6 + [_i, _i, _f, _vp, _vp]
+_lib.pa_decode_shared_plan.argtypes = ([_i] * 5 + [C.POINTER(pa_seq)] + [_i] * 3
+                                       + [_vp, _i, C.POINTER(_i), _vp, _i, C.POINTER(_i)])
 _lib.pa_last_error.argtypes = [_vp, _vp]
 _lib.pa_timing.argtypes = [_vp, _i, C.POINTER(C.c_double), C.POINTER(C.c_double), C.POINTER(_i)]
 _lib.pa_strerror.argtypes = [_i]
@@ -234,6 +237,22 @@ def pa_decode(h, seqs, q, k_pool, v_pool, k_scale, v_scale, block_table, n_sink_
     args = _dev_inputs(q, k_pool, v_pool, k_scale, v_scale, block_table)
     _check(_lib.pa_decode(h, len(s), s, *args, n_sink_blk, n_win_blk, float(sm_scale),
                           _dev(out, torch.bfloat16, "out"), _stream(stream)), "pa_decode")
+
+
+def pa_decode_shared(h, seqs, n_prefix, q, k_pool, v_pool, k_scale, v_scale, block_table, n_sink_blk, n_win_blk,
+                     sm_scale, out, stream=None) -> None:
+    """pa_decode for sequences that share their first n_prefix tokens (the pages of block_table row 0)."""
+    geometry = _geometry_of(h)
+    bf16, s = _torch().bfloat16, _seqs(seqs)
+    if q.dim() != 3 or q.size(1) != geometry[0] or q.size(2) != 256:
+        raise ValueError("q must be [rows, %d, 256]" % geometry[0])
+    if len(s) and max(e.q_off for e in s) >= q.size(0):
+        raise ValueError("a sequence's row is outside q")
+    _check(_lib.pa_decode_shared(
+        h, len(s), s, n_prefix, _dev(q, bf16, "q"),
+        *_pool_args(geometry, len(s), block_table, k_pool, v_pool, k_scale, v_scale)[1:],
+        C.c_void_p(block_table.data_ptr()), n_sink_blk, n_win_blk, sm_scale, _shaped(out, q.shape, bf16, "out"),
+        _stream_of(q, stream)), "pa_decode_shared")
 
 
 def pa_kv_append(h, k_new, v_new, tok_start, block_table_row, k_pool, v_pool, k_scale, v_scale,
@@ -453,6 +472,19 @@ def pa_decode_plan(n_kv_heads, slots, seqs, n_sink_blk, n_win_blk):
     runs = np.zeros((n_cta.value, 3), dtype=np.int32)
     _check(_lib.pa_decode_plan(*args(runs.ctypes.data_as(C.c_void_p), n_cta.value)), "pa_decode_plan")
     return runs, per_cta.value, max_slots.value, bool(listed.value), total.value
+
+
+def pa_decode_shared_plan(n_q_heads, n_kv_heads, max_pages_per_seq, n_sm, seqs, n_prefix, n_sink_blk, n_win_blk):
+    """Host-only: pa_decode_shared's work split of one launch (see include/pa.h): (prefix runs int32 [n, 8],
+    own runs int32 [m, 7])."""
+    s = _seqs(seqs)
+    n, m = C.c_int(), C.c_int()
+    args = (n_q_heads, n_kv_heads, max_pages_per_seq, n_sm, len(s), s, n_prefix, n_sink_blk, n_win_blk)
+    _check(_lib.pa_decode_shared_plan(*args, None, 0, C.byref(n), None, 0, C.byref(m)), "pa_decode_shared_plan")
+    pre, own = np.zeros((n.value, 8), dtype=np.int32), np.zeros((m.value, 7), dtype=np.int32)
+    _check(_lib.pa_decode_shared_plan(*args, pre.ctypes.data_as(C.c_void_p), n.value, C.byref(n),
+                                      own.ctypes.data_as(C.c_void_p), m.value, C.byref(m)), "pa_decode_shared_plan")
+    return pre, own
 
 
 def pa_debug_gather(h, seqs, k_pool, v_pool, k_scale, v_scale, block_table, n_sink_blk, n_win_blk, seq, cap,

@@ -6,8 +6,9 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("pa_api.cu", "pa_kernels.cu", "pa_attention.cu", "pa_noalloc.cu", "pa_decode.cu",
-                                              "pa_qkv.cu")]
-HEADERS = [os.path.join(CSRC, f) for f in ("pa_internal.h", "pa_ptx.cuh", "pa_tiles.cuh", "pa_qkv.h")] + [
+                                              "pa_qkv.cu", "pa_shared.cu")]
+HEADERS = [os.path.join(CSRC, f) for f in ("pa_internal.h", "pa_ptx.cuh", "pa_tiles.cuh", "pa_qkv.h",
+                                              "pa_shared.h")] + [
     os.path.join(HERE, "..", "include", "pa.h")]
 LIB = os.path.join(HERE, "libpa.so")
 # the tensor-core throughput probe the benchmark's roofline uses (its own library)

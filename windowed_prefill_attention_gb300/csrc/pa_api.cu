@@ -16,6 +16,7 @@
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
 #include "pa_qkv.h"
+#include "pa_shared.h"
 
 using namespace pa;
 
@@ -193,6 +194,13 @@ int host_chunk_ends(int HQ, int HKV, int n_seq, const pa_seq* seqs, int n_pairs,
 
 }  // namespace
 
+// A device buffer that grows; the ones it outgrew are freed with the handle.
+struct Workspace {
+  void* p = nullptr;
+  size_t bytes = 0;
+  std::vector<void*> outgrown;
+};
+
 struct pa_ctx {
   int HQ = 0, HKV = 0, G = 0, TQ = 0, n_pool = 0, max_pages = 0;
   pa_options opt{};
@@ -238,6 +246,10 @@ struct pa_ctx {
   int part_cap = 0;
   unsigned long long* d_tickets = nullptr;
   int tickets_cap = 0;
+
+  // shared-prefix decode: partials of the prefix and of the sequences' own keys.  A buffer that became too
+  // small is kept until the handle goes, since a captured graph may still write it.
+  Workspace sh_pre, sh_own;
 
   // host-buffer path staging
   void* hb[7] = {nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
@@ -658,6 +670,10 @@ void pa_destroy(pa_handle h) {
                   h->d_tickets};
   for (void* p : ptrs)
     if (p) cudaFree(p);
+  for (Workspace* w : {&h->sh_pre, &h->sh_own}) {
+    if (w->p) cudaFree(w->p);
+    for (void* p : w->outgrown) cudaFree(p);
+  }
   for (int i = 0; i < 7; ++i)
     if (h->hb[i]) cudaFree(h->hb[i]);
   if (h->h_stage) cudaFreeHost(h->h_stage);
@@ -1593,6 +1609,194 @@ int pa_decode(pa_handle h, int n_seq, const pa_seq* seqs, const void* q, const i
       }
     PA_CUDA(launch_decode(p, tab, h->dec_maps, L.n_cta, st));
   }
+  return PA_OK;
+}
+
+namespace {
+int decode_shared_check(int HQ, int HKV, int max_pages, int n_seq, const pa_seq* seqs, int n_prefix, int S,
+                        float sm_scale) {
+  if (!heads_ok(HQ, HKV) || HQ / HKV > 8 || n_seq < 1 || !seqs || S < 0) return PA_EINVAL;
+  if (!std::isfinite(sm_scale) || sm_scale < 0.f) return PA_EINVAL;
+  if (n_prefix < 0 || n_prefix % kPage || (n_prefix > 0 && n_prefix / kPage > max_pages)) return PA_EINVAL;
+  for (int s = 0; s < n_seq; ++s)
+    if (!decode_seq_ok(seqs[s], max_pages) || seqs[s].n_ctx <= n_prefix || seqs[s].n_ctx > (1 << 30) ||
+        seqs[s].q_off >= (1 << 30))
+      return PA_EINVAL;
+  return rows_shared(n_seq, seqs) ? PA_EINVAL : PA_OK;
+}
+
+// One launch (sequences [s0, s0 + n)) of the shared-prefix decode: its table and split.
+// The prefix pass: the rows of a kv head in groups of 128, per group the
+// blocks some row sees, in 128-key tiles; all tiles cut evenly over at most
+// n_sm CTAs.  The per-sequence pass: chunks of equal block counts, about two
+// CTAs per SM, four to 128 blocks each.
+void decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, int n, int n_prefix, int S, int W,
+                        SharedParams& p, SharedSeqs& t) {
+  const int G = HQ / HKV, Pb = n_prefix / kPage;
+  p.n_seq = n;
+  p.bt_row0 = s0;
+  p.HQ = HQ;
+  p.HKV = HKV;
+  p.G = G;
+  p.S = S;
+  p.W = W;
+  p.prefix_blk = Pb;
+  p.n_grp = n < 2 || Pb == 0 ? 0 : (n * G + kRows - 1) / kRows;
+  p.first_blk = p.n_grp > 0 ? Pb : 0;
+  p.tiles_head = 0;
+  const int per = kRows / G;  // sequences per group
+  for (int j = 0; j < p.n_grp; ++j) {
+    int lo = Pb;
+    for (int s = j * per; s < std::min(n, (j + 1) * per); ++s) lo = std::min(lo, shared_win_lo(seqs[s0 + s].n_ctx, W));
+    ShGroup& g = t.grp[j];
+    g.x0 = p.tiles_head;
+    g.lo = lo;
+    g.sink = W > 0 ? std::min(S, lo) : 0;
+    g.n_blk = g.sink + Pb - lo;
+    p.tiles_head += (g.n_blk + kTileBlocks - 1) / kTileBlocks;
+  }
+  p.n_cta = (int)std::min<long long>(n_sm, (long long)HKV * p.tiles_head);
+  long long own = 0;
+  for (int s = 0; s < n; ++s) {
+    const pa_seq& q = seqs[s0 + s];
+    own += shared_own(q.n_ctx, shared_win_lo(q.n_ctx, W), p.first_blk, S, W).n;
+  }
+  const long long even = (own * HKV + 2 * n_sm - 1) / (2 * n_sm);
+  p.chunk = (int)std::min<long long>(128, (std::max(4ll, even) + 3) / 4 * 4);
+  int chunks = 0;
+  for (int s = 0; s < n; ++s) {
+    const pa_seq& q = seqs[s0 + s];
+    const int lo = shared_win_lo(q.n_ctx, W);
+    t.s[s] = make_int4(q.q_off, q.n_ctx, chunks, lo);
+    chunks += (shared_own(q.n_ctx, lo, p.first_blk, S, W).n + p.chunk - 1) / p.chunk;
+  }
+  p.chunks_head = chunks;
+}
+
+constexpr size_t kPrePartial = (size_t)kHeadDim * kRows * sizeof(float), kPreStats = (size_t)kRows * sizeof(float2);
+constexpr size_t kOwnPartial = (size_t)kHeadDim * 8 * sizeof(float), kOwnStats = 8 * sizeof(float2);
+size_t pre_partials(const SharedParams& p) { return p.tiles_head > 0 ? (size_t)p.n_cta + (size_t)p.n_grp * p.HKV : 0; }
+size_t own_partials(const SharedParams& p) { return (size_t)p.HKV * p.chunks_head; }
+
+int reserve(Workspace& w, size_t need, bool capturing) {
+  if (w.bytes >= need) return PA_OK;
+  if (capturing) return PA_ENOMEM;  // an allocation would end the capture
+  const size_t n = std::max(need, w.bytes + w.bytes / 2);
+  void* p = nullptr;
+  PA_CUDA(cudaMalloc(&p, n));
+  if (w.p) w.outgrown.push_back(w.p);
+  w.p = p;
+  w.bytes = n;
+  return PA_OK;
+}
+}  // namespace
+
+int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, const void* q, const int8_t* k_pool,
+                     const int8_t* v_pool, const float* k_scale, const float* v_scale, const int32_t* block_table,
+                     int n_sink_blk, int n_win_blk, float sm_scale, void* out, void* stream) {
+  int rc = check_inputs(h, q, k_pool, v_pool, k_scale, v_scale, block_table, out);
+  if (rc) return rc;
+  if ((rc = decode_shared_check(h->HQ, h->HKV, h->max_pages, n_seq, seqs, n_prefix, n_sink_blk, sm_scale))) return rc;
+  OnDevice dev(h->device);
+  if (!dev.ok) return PA_ECUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  PA_CUDA(cudaStreamIsCapturing(st, &capture));
+  SharedParams p{};
+  SharedSeqs t;
+  size_t pre = 0, own = 0;
+  for (int s0 = 0; s0 < n_seq; s0 += kShSeqs) {
+    decode_shared_plan(h->HQ, h->HKV, h->n_sm, seqs, s0, std::min(kShSeqs, n_seq - s0), n_prefix, n_sink_blk,
+                       n_win_blk, p, t);
+    pre = std::max(pre, pre_partials(p));
+    own = std::max(own, own_partials(p));
+  }
+  const bool capturing = capture != cudaStreamCaptureStatusNone;
+  if ((rc = reserve(h->sh_pre, pre * (kPrePartial + kPreStats), capturing))) return rc;
+  if ((rc = reserve(h->sh_own, own * (kOwnPartial + kOwnStats), capturing))) return rc;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.block_table = block_table;
+  p.bt_stride = h->max_pages;
+  p.n_pool = h->n_pool;
+  p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+  p.pre_o = static_cast<float4*>(h->sh_pre.p);
+  p.pre_ml = reinterpret_cast<float2*>(static_cast<char*>(h->sh_pre.p) + pre * kPrePartial);
+  p.own_o = static_cast<float4*>(h->sh_own.p);
+  p.own_ml = reinterpret_cast<float2*>(static_cast<char*>(h->sh_own.p) + own * kOwnPartial);
+  p.err = h->d_err;
+  p.wait_ns = (unsigned long long)h->opt.wait_timeout_ms * 1000000ull;
+  for (int s0 = 0; s0 < n_seq; s0 += kShSeqs) {
+    if (n_seq > kShSeqs)
+      decode_shared_plan(h->HQ, h->HKV, h->n_sm, seqs, s0, std::min(kShSeqs, n_seq - s0), n_prefix, n_sink_blk,
+                         n_win_blk, p, t);
+    PA_CUDA(launch_decode_shared(p, t, st));
+  }
+  return PA_OK;
+}
+
+int pa_decode_shared_plan(int n_q_heads, int n_kv_heads, int max_pages_per_seq, int n_sm, int n_seq,
+                          const pa_seq* seqs, int n_prefix, int n_sink_blk, int n_win_blk, int32_t* prefix_out,
+                          int prefix_cap, int* n_prefix_runs, int32_t* own_out, int own_cap, int* n_own_runs) {
+  if (n_sm < 1 || max_pages_per_seq < 1 || !n_prefix_runs || !n_own_runs) return PA_EINVAL;
+  const int rc = decode_shared_check(n_q_heads, n_kv_heads, max_pages_per_seq, n_seq, seqs, n_prefix, n_sink_blk, 1.f);
+  if (rc) return rc;
+  SharedParams p{};
+  SharedSeqs t;
+  decode_shared_plan(n_q_heads, n_kv_heads, n_sm, seqs, 0, std::min(n_seq, kShSeqs), n_prefix, n_sink_blk, n_win_blk,
+                     p, t);
+  const long long T = (long long)p.HKV * p.tiles_head;
+  int np = 0;
+  for (int g = 0; g < p.HKV; ++g)
+    for (int j = 0; j < p.n_grp; ++j) {
+      const ShGroup& gr = t.grp[j];
+      const int nt = (gr.n_blk + kTileBlocks - 1) / kTileBlocks;
+      const long long a = (long long)g * p.tiles_head + gr.x0;
+      for (int t0 = 0; t0 < nt;) {
+        const int c = shared_cta_of(a + t0, T, p.n_cta);
+        const int t1 = (int)std::min<long long>(nt, shared_cut(c + 1, T, p.n_cta) - a);
+        if (prefix_out) {
+          if (np >= prefix_cap) return PA_EINVAL;
+          int32_t* o = prefix_out + 8 * np;
+          o[0] = c;
+          o[1] = g;
+          o[2] = j * (kRows / p.G);
+          o[3] = std::min(p.n_seq, (j + 1) * (kRows / p.G)) - o[2];
+          o[4] = gr.sink;
+          o[5] = gr.lo;
+          o[6] = t0 * kTileBlocks;
+          o[7] = std::min(gr.n_blk, t1 * kTileBlocks);
+        }
+        ++np;
+        t0 = t1;
+      }
+    }
+  int no = 0;
+  for (int s = 0; s < p.n_seq; ++s) {
+    const ShOwn o = shared_own(t.s[s].y, t.s[s].w, p.first_blk, p.S, p.W);
+    const int n_ch = (o.n + p.chunk - 1) / p.chunk;
+    for (int g = 0; g < p.HKV; ++g)
+      for (int c = 0; c < n_ch; ++c) {
+        if (own_out) {
+          if (no >= own_cap) return PA_EINVAL;
+          int32_t* r = own_out + 7 * no;
+          r[0] = s;
+          r[1] = g;
+          r[2] = p.first_blk;
+          r[3] = o.sink;
+          r[4] = o.lo;
+          r[5] = c * p.chunk;
+          r[6] = std::min(o.n, (c + 1) * p.chunk);
+        }
+        ++no;
+      }
+  }
+  *n_prefix_runs = np;
+  *n_own_runs = no;
   return PA_OK;
 }
 

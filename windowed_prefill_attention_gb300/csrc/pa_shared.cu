@@ -1,0 +1,928 @@
+// Decode of a batch that shares a long prefix (sm_103a): one new query token
+// per sequence, the first keys of every sequence the same pages of the pool.
+//
+// Softmax over the visible keys splits over any partition of them: with
+// (m, l, O) the reference, sum and unnormalised output of a part,
+//   m = max m_i,  l = sum 2^(m_i - m) l_i,  O = sum 2^(m_i - m) O_i.
+// Three kernels:
+//   prefix_kernel  the prefix's keys against the queries of ALL sequences: per
+//                  kv head a matrix of n_seq x G rows, so its K and V codes are
+//                  read once and the products run on the tensor cores
+//                  (tcgen05) instead of once per sequence
+//   own_kernel     each sequence's own keys, as pa_decode splits them
+//   merge_kernel   the partials of both, and the division
+//
+// prefix_kernel.  Groups of 128 query rows x tiles of 128 keys.  The int8
+// codes are widened to fp16 (exact) on their way into shared memory, K and V
+// alike as [key][64 dims] rows of 128 bytes: a K-major B operand for S = Q K^T
+// and an MN-major one for O = P V, so V needs no transpose.  Scores, softmax
+// and P' are those of the decode kernel: the bf16 query enters as fp16
+// through a power of two per row, P' = p * v_scale * 2^-e in fp16, fp32 sums.
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "pa_internal.h"
+#include "pa_ptx.cuh"
+#include "pa_shared.h"
+
+namespace pa {
+namespace {
+
+constexpr unsigned kAllLanes = 0xffffffffu;
+constexpr float kMaxLift = 8.f;  // the softmax reference moves when a row's maximum passes it by more than 2^8
+constexpr uint64_t kShDrainNs = 200000000ull;
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Four codes (bytes) -> two words of fp16 pairs: (b ^ 0x80) in the low byte of
+// 0x64__ is 1152 + b, and the subtraction is exact.
+__device__ __forceinline__ uint32_t minus_1152(uint32_t u) {
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480u)));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t lo_pair(uint32_t flipped) { return minus_1152(__byte_perm(flipped, 0x64646464u, 0x5140)); }
+__device__ __forceinline__ uint32_t hi_pair(uint32_t flipped) { return minus_1152(__byte_perm(flipped, 0x64646464u, 0x7362)); }
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// 2^e for e in [-126, 127].
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// e with 2^(e-1) <= x < 2^e, in [-100, 100]; -100 for x <= 0.
+__device__ __forceinline__ int exp_above(float x) {
+  return x > 0.f ? max(-100, min(100, (int)((__float_as_uint(x) >> 23) & 0xff) - 126)) : -100;
+}
+// The exponent k of the power of two that puts a row's absolute maximum in [64, 128).
+__device__ __forceinline__ int row_shift(float am) {
+  return am > 0.f ? min(127, 133 - (int)((__float_as_uint(am) >> 23) & 0xff)) : 0;
+}
+__device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = __uint_as_float(u[j] << 16);
+    x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+  }
+}
+
+// ====================================================================
+// The prefix
+// ====================================================================
+constexpr int kSoftWarps = 4;                       // warps 0-3: softmax, one row per thread
+constexpr int kConvWarps = 8;                       // warps 4-11: codes -> fp16 operands, and the queries
+constexpr int kIssueWarp = kSoftWarps + kConvWarps; // warp 12: TMEM, the MMAs
+constexpr int kScaleWarp = kIssueWarp + 1;          // warp 13: the tiles' scales
+constexpr int kPreThreads = 32 * (kScaleWarp + 1);
+
+constexpr int kChunkBytes = 32768;                  // half a tile of K (128 keys x 128 dims) or V (64 keys x 256 dims)
+// Shared memory from a 1024-byte aligned base.
+constexpr int kSmQ = 0;                             // 4 regions [128 rows][64 dims]
+constexpr int kSmK = 65536;                         // 2 chunks, each 2 regions [128 keys][64 dims]
+constexpr int kSmV = kSmK + 2 * kChunkBytes;        // 2 chunks, each 4 regions [64 keys][64 dims]
+constexpr int kSmScale = kSmV + 2 * kChunkBytes;    // [2] x {K scales 128, V scales 128, valid blocks, exponent}
+constexpr int kScaleSlot = 2 * 512 + 16;
+constexpr int kSmRow = kSmScale + 2 * kScaleSlot;   // [2][128] row factors, by segment parity
+constexpr int kSmBar = kSmRow + 2 * 512;
+enum : int {
+  B_KF = 0,    // [2] K chunk written
+  B_KE = 2,    // [2] K chunk's products done
+  B_VF = 4,    // [2]
+  B_VE = 6,    // [2]
+  B_SF = 8,    // [2] scores of a tile in TMEM, by tile parity
+  B_PF = 10,   // [2] P' of a tile in TMEM
+  B_OD = 12,   // a tile's P V done
+  B_SCF = 13,  // [2] scales written
+  B_SCE = 15,  // [2] scales read
+  B_QF = 17,   // queries written
+  B_QE = 18,   // a segment's last Q K^T done
+  B_OE = 19,   // a segment's O read
+  B_DRAIN = 20,
+  kPreBars = 21
+};
+constexpr int kSmTmem = kSmBar + kPreBars * 8;
+constexpr int kPreSmem = kSmTmem + 16 + 1024;
+static_assert(kPreSmem <= 227 * 1024, "shared memory");
+
+constexpr uint32_t kTmemO = 0, kTmemS = 256;        // O [0, 256), S of even / odd tiles [256, 384) / [384, 512)
+
+// The B operand of O = P V: V as [key][64 dims] rows of 128 bytes with the
+// 128-byte swizzle, dims (N) contiguous: 8-key atoms of 1024 bytes along K,
+// regions of 64 keys x 128 bytes along N.
+__device__ __forceinline__ uint64_t sdesc_v(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(8192 >> 4) << 16;      // leading byte offset: the next 64 dims
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;      // stride byte offset: the next 8 keys
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+constexpr uint32_t kIdescQK = idesc_f16(128, 128, false, false);
+constexpr uint32_t kIdescPV = idesc_f16(128, 256, false, false) | (1u << 16);  // B is N-major
+
+// A run of tiles of one group: a CTA's work is one or more of these.
+struct Segment {
+  int j, g, rg;     // group number (head-major), kv head, row group
+  ShGroup grp;
+  int t0, t1;       // tiles of the group
+  int rows;         // query rows of the group
+};
+__device__ __forceinline__ Segment segment_at(const SharedParams& p, const SharedSeqs& tab, long long x,
+                                              long long x_end) {
+  Segment s;
+  s.g = (int)(x / p.tiles_head);
+  const int xh = (int)(x - (long long)s.g * p.tiles_head);
+  s.rg = 0;
+  while (s.rg + 1 < p.n_grp && tab.grp[s.rg + 1].x0 <= xh) ++s.rg;
+  s.j = s.g * p.n_grp + s.rg;
+  s.grp = tab.grp[s.rg];
+  s.t0 = xh - s.grp.x0;
+  const int nt = (s.grp.n_blk + kTileBlocks - 1) / kTileBlocks;
+  s.t1 = (int)min((long long)nt, s.t0 + (x_end - x));
+  s.rows = min(kRows, p.n_seq * p.G - s.rg * kRows);
+  return s;
+}
+// Logical block of the b-th visible block of a group.
+__device__ __forceinline__ int group_block(const ShGroup& g, int b) { return b < g.sink ? b : g.lo + (b - g.sink); }
+// Pool page of it, -1 past the list or outside the pool.
+__device__ __forceinline__ int group_page(const SharedParams& p, const ShGroup& g, int b) {
+  if (b >= g.n_blk) return -1;
+  const int phys = __ldg(p.block_table + group_block(g, b));
+  return phys >= 0 && phys < p.n_pool ? phys : -1;
+}
+
+struct PreCtx {
+  uint32_t sb;  // shared base
+  uint32_t tm;  // TMEM base
+  long long x0, x1;
+  WaitCtl wc;
+  __device__ uint32_t bar(int i) const { return sb + kSmBar + 8 * i; }
+  // One outcome for the warp.
+  __device__ bool wait(int i, uint32_t parity) const {
+    return __all_sync(kAllLanes, mbar_wait(bar(i), parity & 1u, wc, 80 + i));
+  }
+};
+
+// ---- converters.  Thread i of 256 holds its share of one whole tile of codes
+// in registers (64 KB a CTA in flight): chunk by chunk it widens what has
+// arrived, then loads the same chunk of the next tile.
+// K chunk c (dims [128 c, +128)): 16 bytes of keys 32 n + i / 8, dims 16 (i % 8).
+// V chunk c (keys [64 c, +64)): 16 bytes of keys 16 n + i / 16, dims 16 (i % 16).
+struct Codes {
+  uint4 k[2][4], v[2][4];
+};
+
+// 16 codes of one row as 32 bytes at 16-byte pieces 2 (u % 4) and + 1 of a
+// 128-byte swizzled row.  Threads u = 4..7 write their pieces in the other
+// order, so that the eight threads of a row hit eight different pieces.
+__device__ __forceinline__ void widen16(const uint4 c, uint32_t row_addr, int row, int u, bool swap) {
+  const uint32_t w[4] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u, c.z ^ 0x80808080u, c.w ^ 0x80808080u};
+  uint32_t h[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[2 * e] = lo_pair(w[e]), h[2 * e + 1] = hi_pair(w[e]);
+  const int c0 = 2 * (u & 3);
+  const uint32_t a0 = row_addr + (uint32_t)(((c0) ^ (row & 7)) << 4), a1 = row_addr + (uint32_t)(((c0 + 1) ^ (row & 7)) << 4);
+  if (swap) {
+    sts128(a1, h[4], h[5], h[6], h[7]);
+    sts128(a0, h[0], h[1], h[2], h[3]);
+  } else {
+    sts128(a0, h[0], h[1], h[2], h[3]);
+    sts128(a1, h[4], h[5], h[6], h[7]);
+  }
+}
+
+__device__ __forceinline__ void role_convert(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
+  const int i = threadIdx.x - 32 * kSoftWarps, lane = threadIdx.x & 31, warp = i >> 5;
+  uint32_t n_tile = 0, n_seg = 0;
+  const size_t tok = (size_t)p.HKV * kHeadDim;  // bytes from a token to the next
+  for (long long x = c.x0; x < c.x1; ++n_seg) {
+    const Segment s = segment_at(p, tab, x, c.x1);
+    const int8_t* kp = p.k_pool + (size_t)s.g * kHeadDim;
+    const int8_t* vp = p.v_pool + (size_t)s.g * kHeadDim;
+    // pages of the segment's blocks, 32 (four tiles) at a time, one per lane
+    const int b0 = s.t0 * kTileBlocks;
+    int pg = group_page(p, s.grp, b0 + lane), pg_next = group_page(p, s.grp, b0 + 32 + lane);
+    Codes r;
+    auto load_k = [&](int ch, int t4) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int page = __shfl_sync(kAllLanes, pg, t4 * kTileBlocks + 2 * n + (i >> 7));
+        r.k[ch][n] = make_uint4(0, 0, 0, 0);
+        if (page >= 0)
+          r.k[ch][n] = ldg_stream(kp + ((size_t)page * kPage + ((i >> 3) & 15)) * tok + 128 * ch + 16 * (i & 7));
+      }
+    };
+    auto load_v = [&](int ch, int t4) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int page = __shfl_sync(kAllLanes, pg, t4 * kTileBlocks + 4 * ch + n);
+        r.v[ch][n] = make_uint4(0, 0, 0, 0);
+        if (page >= 0) r.v[ch][n] = ldg_stream(vp + ((size_t)page * kPage + (i >> 4)) * tok + 16 * (i & 15));
+      }
+    };
+    load_k(0, 0);
+    load_k(1, 0);
+    load_v(0, 0);
+    load_v(1, 0);
+    // the group's queries: a warp takes a row at a time
+    if (n_seg > 0 && !c.wait(B_QE, n_seg - 1)) return;
+    float* rowc = reinterpret_cast<float*>(__cvta_shared_to_generic(c.sb + kSmRow + (n_seg & 1) * 512));
+    for (int row = warp; row < kRows; row += kConvWarps) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+      if (row < s.rows) {
+        const int rr = s.rg * kRows + row;
+        const int4 sq = tab.s[rr / p.G];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(p.q + ((size_t)sq.x * p.HQ + (size_t)s.g * p.G + rr % p.G) * kHeadDim) + lane), v);
+      }
+      float am = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(v[e]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(kAllLanes, am, o));
+      const int k = row_shift(am);
+      const float mul = pow2i(k);
+      sts128(c.sb + kSmQ + (lane >> 3) * 16384 + row * 128 + (((lane & 7) ^ (row & 7)) << 4),
+             pack_f16x2(v[0] * mul, v[1] * mul), pack_f16x2(v[2] * mul, v[3] * mul), pack_f16x2(v[4] * mul, v[5] * mul),
+             pack_f16x2(v[6] * mul, v[7] * mul));
+      if (lane == 0) rowc[row] = row < s.rows ? pow2i(-k) * p.sm_scale_log2 : 0.f;
+    }
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(c.bar(B_QF));
+
+    const int nt = s.t1 - s.t0;
+    for (int t = 0; t < nt; ++t, ++n_tile) {
+      if (((t + 1) & 3) == 0) {  // the next tile's pages are in the next window
+        pg = pg_next;
+        pg_next = group_page(p, s.grp, b0 + 8 * (t + 1) + 32 + lane);
+      }
+      const bool more = t + 1 < nt;
+      const int t4 = (t + 1) & 3;
+#pragma unroll
+      for (int ch = 0; ch < 2; ++ch) {
+        if (!c.wait(B_KE + ch, n_tile + 1)) return;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int row = 32 * n + (i >> 3), u = i & 7;
+          widen16(r.k[ch][n], c.sb + kSmK + ch * kChunkBytes + (u >> 2) * 16384 + row * 128, row, u, u >= 4);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c.bar(B_KF + ch));
+        if (more) load_k(ch, t4);
+      }
+#pragma unroll
+      for (int ch = 0; ch < 2; ++ch) {
+        if (!c.wait(B_VE + ch, n_tile + 1)) return;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int row = 16 * n + (i >> 4), u = i & 15;
+          widen16(r.v[ch][n], c.sb + kSmV + ch * kChunkBytes + (u >> 2) * 8192 + row * 128, row, u, (u & 4) != 0);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c.bar(B_VF + ch));
+        if (more) load_v(ch, t4);
+      }
+    }
+    x += nt;
+  }
+}
+
+// ---- scales of every tile's keys, V's normalised by a running power of two.
+__device__ __forceinline__ void role_scales(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
+  const int lane = threadIdx.x & 31;
+  uint32_t n_tile = 0;
+  for (long long x = c.x0; x < c.x1;) {
+    const Segment s = segment_at(p, tab, x, c.x1);
+    int ev = -100;
+    // lane: keys 4 lane .. + 3 of a tile, in block lane / 4
+    float ks[4], vs[4];
+    bool valid = false;
+    auto load = [&](int t) {
+      const int b = t * kTileBlocks + (lane >> 2);
+      const int page = group_page(p, s.grp, b);
+      valid = page >= 0;
+      if (!valid && b < s.grp.n_blk && (lane & 3) == 0) atomicCAS(p.err, 0, DEV_ERR_BAD_PAGE);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const size_t at = ((size_t)(valid ? page : 0) * kPage + 4 * (lane & 3) + e) * p.HKV + s.g;
+        ks[e] = valid ? __ldg(p.k_scale + at) : 0.f;
+        vs[e] = valid ? __ldg(p.v_scale + at) : 0.f;
+      }
+    };
+    load(s.t0);
+    for (int t = s.t0; t < s.t1; ++t, ++n_tile) {
+      const int b = n_tile & 1;
+      float mv = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mv = fmaxf(mv, __shfl_xor_sync(kAllLanes, mv, o));
+      ev = max(ev, exp_above(mv));
+      const float vn = pow2i(-ev);
+      const uint32_t ok = __ballot_sync(kAllLanes, valid);
+      if (!c.wait(B_SCE + b, (n_tile >> 1) + 1)) return;
+      const uint32_t at = c.sb + kSmScale + b * kScaleSlot;
+      sts128(at + 16 * lane, __float_as_uint(ks[0]), __float_as_uint(ks[1]), __float_as_uint(ks[2]), __float_as_uint(ks[3]));
+      sts128(at + 512 + 16 * lane, __float_as_uint(vs[0] * vn), __float_as_uint(vs[1] * vn), __float_as_uint(vs[2] * vn),
+             __float_as_uint(vs[3] * vn));
+      if (lane == 0) {
+        uint32_t m8 = 0;
+#pragma unroll
+        for (int e = 0; e < kTileBlocks; ++e) m8 |= ((ok >> (4 * e)) & 1u) << e;
+        sts128(at + 1024, m8, (uint32_t)ev, 0, 0);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c.bar(B_SCF + b));
+      if (t + 1 < s.t1) load(t + 1);
+    }
+    x += s.t1 - s.t0;
+  }
+}
+
+// ---- the products, one thread.  Q K^T of tile t + 1 goes before P V of tile t.
+__device__ __forceinline__ void role_issue(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
+  uint32_t n_tile = 0, n_seg = 0;
+  bool ok = true;
+  auto wait = [&](int i, uint32_t parity) { return mbar_wait(c.bar(i), parity & 1u, c.wc, 80 + i); };
+  // n: the tile's number in the CTA's order
+  auto pv = [&](uint32_t n, bool first) {
+    const uint32_t ptm = c.tm + kTmemS + 128 * (n & 1);
+    if (!wait(B_PF + (n & 1), n >> 1)) return false;
+    for (int ch = 0; ch < 2; ++ch) {
+      if (!wait(B_VF + ch, n)) return false;
+      tc_fence_after();
+      const uint32_t vb = c.sb + kSmV + ch * kChunkBytes;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mma_ts(c.tm + kTmemO, ptm + 8 * (4 * ch + k), sdesc_v(vb + 2048 * k), kIdescPV, !(first && ch == 0 && k == 0));
+      mma_commit(c.bar(B_VE + ch));
+    }
+    mma_commit(c.bar(B_OD));
+    return true;
+  };
+  for (long long x = c.x0; ok && x < c.x1; ++n_seg) {
+    const Segment s = segment_at(p, tab, x, c.x1);
+    const int nt = s.t1 - s.t0;
+    ok = wait(B_QF, n_seg);
+    for (int t = 0; ok && t < nt; ++t, ++n_tile) {
+      const uint32_t stm = c.tm + kTmemS + 128 * (n_tile & 1);
+      for (int ch = 0; ok && ch < 2; ++ch) {
+        ok = wait(B_KF + ch, n_tile);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rgn = 2 * ch + (k >> 2);
+          const uint64_t a = sdesc_k_sw128(c.sb + kSmQ + rgn * 16384 + 32 * (k & 3));
+          const uint64_t b = sdesc_k_sw128(c.sb + kSmK + rgn * 16384 + 32 * (k & 3));
+          mma_ss(stm, a, b, kIdescQK, !(ch == 0 && k == 0));
+        }
+        mma_commit(c.bar(B_KE + ch));
+      }
+      if (!ok) break;
+      mma_commit(c.bar(B_SF + (n_tile & 1)));
+      if (t == nt - 1) mma_commit(c.bar(B_QE));
+      if (t > 0) {
+        if (t == 1 && n_seg > 0) ok = wait(B_OE, n_seg - 1);
+        ok = ok && pv(n_tile - 1, t == 1);
+      }
+    }
+    if (ok && nt == 1 && n_seg > 0) ok = wait(B_OE, n_seg - 1);
+    ok = ok && pv(n_tile - 1, nt == 1);
+    x += nt;
+  }
+  // nothing may be in flight when the CTA frees its TMEM
+  mma_commit(c.bar(B_DRAIN));
+  (void)mbar_wait_drain(c.bar(B_DRAIN), 0, kShDrainNs);
+}
+
+// ---- softmax: thread = row.
+__device__ __forceinline__ void role_softmax(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
+  const int row = threadIdx.x, lane = threadIdx.x & 31;
+  const uint32_t lane_tm = (uint32_t)(threadIdx.x & ~31) << 16;
+  const uint32_t otm = c.tm + kTmemO + lane_tm;
+  uint32_t n_tile = 0, n_seg = 0;
+  for (long long x = c.x0; x < c.x1; ++n_seg) {
+    const Segment s = segment_at(p, tab, x, c.x1);
+    const int nt = s.t1 - s.t0;
+    const int win_lo = p.W > 0 && row < s.rows ? tab.s[(s.rg * kRows + row) / p.G].w : 0;
+    float cr = 0.f, m = -INFINITY;  // the row's factor, its reference in log2 units
+    float2 l2 = make_float2(0.f, 0.f);
+    int ev = -100;
+    for (int t = 0; t < nt; ++t, ++n_tile) {
+      const int b = n_tile & 1;
+      const uint32_t stm = c.tm + kTmemS + 128 * b + lane_tm;
+      if (!c.wait(B_SF + b, n_tile >> 1) || !c.wait(B_SCF + b, n_tile >> 1)) return;
+      tc_fence_after();
+      if (t == 0) {
+        float v;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(c.sb + kSmRow + (n_seg & 1) * 512 + 4 * row));
+        cr = v;
+      }
+      const uint32_t sc = c.sb + kSmScale + b * kScaleSlot;
+      const float4 meta = lds_f32x4(sc + 1024);
+      uint32_t seen = __float_as_uint(meta.x);  // blocks of the tile this row sees
+      const int ev_t = (int)__float_as_uint(meta.y);
+      if (p.W > 0) {
+#pragma unroll
+        for (int e = 0; e < kTileBlocks; ++e) {
+          const int lb = group_block(s.grp, (s.t0 + t) * kTileBlocks + e);
+          if (lb >= p.S && lb < win_lo) seen &= ~(1u << e);
+        }
+      }
+      // 1. the row's maximum
+      float zm = -INFINITY;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t r[32];
+        tmem_ld32(stm + 32 * h, r);
+        tmem_wait_ld(r);
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk) {
+          float bm = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = 16 * blk + 4 * e;
+            const float4 ks = lds_f32x4(sc + 4 * (32 * h + k));
+            const float2 z0 = mul2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), make_float2(ks.x, ks.y));
+            const float2 z1 = mul2(make_float2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), make_float2(ks.z, ks.w));
+            bm = max3(max3(bm, z0.x, z0.y), z1.x, z1.y);
+          }
+          if (seen >> (2 * h + blk) & 1u) zm = fmaxf(zm, bm);
+        }
+      }
+      const float mz = zm == -INFINITY ? -INFINITY : zm * cr;
+      float f = 1.f;  // what earlier sums shrink by (they are zero while m is -inf)
+      if (m == -INFINITY) {
+        m = mz;
+      } else if (mz > m + kMaxLift) {
+        f = ex2f(m - mz);
+        m = mz;
+      }
+      l2 = mul2(l2, make_float2(f, f));
+      const float fo = f * (ev_t > ev ? pow2i(max(-126, ev - ev_t)) : 1.f);
+      ev = ev_t;
+      if (t > 0 && __any_sync(kAllLanes, fo != 1.f)) {
+        if (!c.wait(B_OD, n_tile - 1)) return;
+        tc_fence_after();
+#pragma unroll 1
+        for (int h = 0; h < 8; ++h) {
+          uint32_t r[32];
+          tmem_ld32(otm + 32 * h, r);
+          tmem_wait_ld(r);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * fo);
+          tmem_st32(otm + 32 * h, r);
+        }
+      }
+      // 2. p = 2^(z c - m), P' = p v_scale 2^-ev in fp16 over the scores
+      const float neg = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t r[32], ph[16];
+        tmem_ld32(stm + 32 * h, r);
+        tmem_wait_ld(r);
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk) {
+          const float nb = (seen >> (2 * h + blk) & 1u) ? neg : -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = 16 * blk + 4 * e;
+            const float4 ks = lds_f32x4(sc + 4 * (32 * h + k)), vs = lds_f32x4(sc + 512 + 4 * (32 * h + k));
+            float2 z0 = mul2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), make_float2(ks.x, ks.y));
+            float2 z1 = mul2(make_float2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), make_float2(ks.z, ks.w));
+            z0 = fma2(z0, make_float2(cr, cr), make_float2(nb, nb));
+            z1 = fma2(z1, make_float2(cr, cr), make_float2(nb, nb));
+            z0 = make_float2(ex2f(z0.x), ex2f(z0.y));
+            z1 = make_float2(ex2f(z1.x), ex2f(z1.y));
+            l2 = add2(l2, add2(z0, z1));
+            z0 = mul2(z0, make_float2(vs.x, vs.y));
+            z1 = mul2(z1, make_float2(vs.z, vs.w));
+            ph[k / 2] = pack_f16x2(z0.x, z0.y);
+            ph[k / 2 + 1] = pack_f16x2(z1.x, z1.y);
+          }
+        }
+        tmem_st16(stm + 16 * h, ph);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(c.bar(B_PF + b));
+        mbar_arrive(c.bar(B_SCE + b));
+      }
+    }
+    // the segment's partial
+    if (!c.wait(B_OD, n_tile - 1)) return;
+    tc_fence_after();
+    const int id = (int)blockIdx.x + s.j;
+    const float up = pow2i(ev);
+    float4* dst = p.pre_o + (size_t)id * 64 * kRows + row;
+#pragma unroll 1
+    for (int h = 0; h < 8; ++h) {
+      uint32_t r[32];
+      tmem_ld32(otm + 32 * h, r);
+      tmem_wait_ld(r);
+      if (row < s.rows) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          dst[(size_t)(8 * h + e) * kRows] =
+              make_float4(__uint_as_float(r[4 * e]) * up, __uint_as_float(r[4 * e + 1]) * up,
+                          __uint_as_float(r[4 * e + 2]) * up, __uint_as_float(r[4 * e + 3]) * up);
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(c.bar(B_OE));
+    if (row < s.rows) p.pre_ml[(size_t)id * kRows + row] = make_float2(m, l2.x + l2.y);
+    x += nt;
+  }
+}
+
+__global__ void __launch_bounds__(kPreThreads, 1) prefix_kernel(const __grid_constant__ SharedParams p,
+                                                                const __grid_constant__ SharedSeqs tab) {
+  extern __shared__ uint8_t raw[];
+  PreCtx c;
+  c.sb = (smem_u32(raw) + 1023u) & ~1023u;
+  c.wc = WaitCtl{p.err, p.wait_ns};
+  const long long T = (long long)p.HKV * p.tiles_head;
+  c.x0 = shared_cut((int)blockIdx.x, T, p.n_cta);
+  c.x1 = shared_cut((int)blockIdx.x + 1, T, p.n_cta);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(c.bar(B_KF + i), kConvWarps);
+      mbar_init(c.bar(B_VF + i), kConvWarps);
+      mbar_init(c.bar(B_KE + i), 1);
+      mbar_init(c.bar(B_VE + i), 1);
+      mbar_init(c.bar(B_SF + i), 1);
+      mbar_init(c.bar(B_PF + i), kSoftWarps);
+      mbar_init(c.bar(B_SCF + i), 1);
+      mbar_init(c.bar(B_SCE + i), kSoftWarps);
+    }
+    mbar_init(c.bar(B_OD), 1);
+    mbar_init(c.bar(B_QF), kConvWarps);
+    mbar_init(c.bar(B_QE), 1);
+    mbar_init(c.bar(B_OE), kSoftWarps);
+    mbar_init(c.bar(B_DRAIN), 1);
+    fence_mbar_init();
+  }
+  if (warp == kIssueWarp) {
+    tmem_alloc(c.sb + kSmTmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c.tm) : "r"(c.sb + kSmTmem));
+  dependents_may_start();
+  if (warp < kSoftWarps) role_softmax(p, tab, c);
+  else if (warp < kIssueWarp) role_convert(p, tab, c);
+  else if (warp == kIssueWarp) {
+    if ((threadIdx.x & 31) == 0) role_issue(p, tab, c);
+    __syncwarp();
+  } else {
+    role_scales(p, tab, c);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kIssueWarp) tmem_dealloc(c.tm, 512);
+}
+
+// ====================================================================
+// Each sequence's own keys
+// ====================================================================
+// CTA = (sequence, kv head, chunk of its visible blocks); its four warps take
+// the blocks in turn.  Products as in the decode kernel, on mma.sync in the
+// transposed orientation, S^T = K Q^T and O^T = V^T P^T: keys and dims fill M,
+// the G <= 8 query rows N.  A thread's operand bytes are whole 16-byte pieces of
+// the pool's rows (the dims are permuted, Q and O alike), so they are loaded
+// from global memory straight into registers.
+constexpr int kOwnWarps = 4;
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__global__ void __launch_bounds__(kOwnWarps * 32) own_kernel(const __grid_constant__ SharedParams p,
+                                                             const __grid_constant__ SharedSeqs tab) {
+  __shared__ uint2 qf[16 * 32];
+  __shared__ float comb[kOwnWarps][8][kHeadDim + 4];
+  __shared__ float rowc[8], wm[kOwnWarps][8], wl[kOwnWarps][8];
+  dependents_may_start();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+  // the CTA's sequence, kv head and chunk
+  int lo = 0, hi = p.n_seq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.HKV * tab.s[mid].z <= (int)blockIdx.x) lo = mid;
+    else hi = mid - 1;
+  }
+  const int4 sq = tab.s[lo];
+  const int t = sq.y - 1;
+  const ShOwn own = shared_own(sq.y, sq.w, p.first_blk, p.S, p.W);
+  const int n_ch = (own.n + p.chunk - 1) / p.chunk;
+  const int at = (int)blockIdx.x - p.HKV * sq.z;
+  const int g = at / n_ch, ch = at - g * n_ch;
+  const int b0 = ch * p.chunk, b1 = min(own.n, b0 + p.chunk);
+  // this warp's pages, one per lane (at most 32 blocks a warp)
+  auto block_of = [&](int b) { return b < own.sink ? p.first_blk + b : own.lo + (b - own.sink); };
+  const int mine = b0 + warp + kOwnWarps * lane;
+  int page = -1;
+  if (mine < b1) {
+    const int lb = block_of(mine);
+    page = __ldg(p.block_table + (lb < p.prefix_blk ? 0 : (size_t)(p.bt_row0 + lo) * p.bt_stride) + lb);
+    if (page < 0 || page >= p.n_pool) {
+      page = -1;
+      atomicCAS(p.err, 0, DEV_ERR_BAD_PAGE);
+    }
+  }
+  {  // the G query rows as B fragments: thread row r, dims [16 c, 16 c + 16)
+    const int r = threadIdx.x >> 4, cc = threadIdx.x & 15;
+    float v[16];
+    float am = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = 0.f;
+    if (r < p.G) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + ((size_t)sq.x * p.HQ + (size_t)g * p.G + r) * kHeadDim + 16 * cc);
+      float a[8], b[8];
+      unpack8(__ldg(src), a);
+      unpack8(__ldg(src + 1), b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = a[e], v[8 + e] = b[e], am = fmaxf(am, fmaxf(fabsf(a[e]), fabsf(b[e])));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(kAllLanes, am, o));
+    const int k = row_shift(am);
+    const float mul = pow2i(k);
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      qf[(4 * (cc >> 2) + m) * 32 + 4 * r + (cc & 3)] =
+          make_uint2(pack_f16x2(v[4 * m] * mul, v[4 * m + 1] * mul), pack_f16x2(v[4 * m + 2] * mul, v[4 * m + 3] * mul));
+    if (cc == 0) rowc[r] = r < p.G ? pow2i(-k) * p.sm_scale_log2 : 0.f;
+  }
+  __syncthreads();
+  const float c_lo = rowc[2 * tq], c_hi = rowc[2 * tq + 1];
+  float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;
+  int ev = -100;
+  float o[16][4];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  const size_t tok = (size_t)p.HKV * kHeadDim;
+  for (int it = 0; b0 + warp + kOwnWarps * it < b1; ++it) {
+    const int b = b0 + warp + kOwnWarps * it;
+    const int phys = __shfl_sync(kAllLanes, page, it);
+    if (phys < 0) continue;
+    const int8_t* kp = p.k_pool + (size_t)phys * kPage * tok + (size_t)g * kHeadDim;
+    const int8_t* vp = p.v_pool + (size_t)phys * kPage * tok + (size_t)g * kHeadDim;
+    // K: rows gq and gq + 8, dims 64 j + 16 tq; V: keys 2tq, 2tq+1, 2tq+8, 2tq+9, dims 32 gq
+    uint4 kr[4][2], vr[2][4];
+    const int key[4] = {2 * tq, 2 * tq + 1, 2 * tq + 8, 2 * tq + 9};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      kr[j][0] = ldg_stream(kp + (size_t)gq * tok + 64 * j + 16 * tq);
+      kr[j][1] = ldg_stream(kp + (size_t)(gq + 8) * tok + 64 * j + 16 * tq);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      vr[0][k] = __ldg(reinterpret_cast<const uint4*>(vp + (size_t)key[k] * tok + 32 * gq));
+      vr[1][k] = __ldg(reinterpret_cast<const uint4*>(vp + (size_t)key[k] * tok + 32 * gq + 16));
+    }
+    const size_t s0 = ((size_t)phys * kPage + gq) * p.HKV + g, s1 = s0 + 8 * (size_t)p.HKV;
+    const float ks0 = __ldg(p.k_scale + s0), ks1 = __ldg(p.k_scale + s1);
+    const float vr0 = __ldg(p.v_scale + s0), vr1 = __ldg(p.v_scale + s1);
+    float sacc[4][4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) sacc[m][0] = sacc[m][1] = sacc[m][2] = sacc[m][3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w0[4] = {kr[j][0].x, kr[j][0].y, kr[j][0].z, kr[j][0].w};
+      const uint32_t w1[4] = {kr[j][1].x, kr[j][1].y, kr[j][1].z, kr[j][1].w};
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const uint32_t x0 = w0[m] ^ 0x80808080u, x1 = w1[m] ^ 0x80808080u;
+        const uint32_t a[4] = {lo_pair(x0), lo_pair(x1), hi_pair(x0), hi_pair(x1)};
+        const uint2 bq = qf[(4 * j + m) * 32 + lane];
+        mma16816(sacc[m], a, bq.x, bq.y);
+      }
+    }
+    float sc[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sc[e] = (sacc[0][e] + sacc[1][e]) + (sacc[2][e] + sacc[3][e]);
+    const int lb = block_of(b);
+    const bool v0 = lb * kPage + gq <= t, v1 = lb * kPage + gq + 8 <= t;
+    const float y0 = v0 ? sc[0] * ks0 * c_lo : -INFINITY, y1 = v0 ? sc[1] * ks0 * c_hi : -INFINITY;
+    const float y2 = v1 ? sc[2] * ks1 * c_lo : -INFINITY, y3 = v1 ? sc[3] * ks1 * c_hi : -INFINITY;
+    float bm_lo = fmaxf(y0, y2), bm_hi = fmaxf(y1, y3);
+    float bv = fmaxf(v0 ? vr0 : 0.f, v1 ? vr1 : 0.f);
+#pragma unroll
+    for (int sh = 4; sh < 32; sh <<= 1) {
+      bm_lo = fmaxf(bm_lo, __shfl_xor_sync(kAllLanes, bm_lo, sh));
+      bm_hi = fmaxf(bm_hi, __shfl_xor_sync(kAllLanes, bm_hi, sh));
+      bv = fmaxf(bv, __shfl_xor_sync(kAllLanes, bv, sh));
+    }
+    const float mn_lo = fmaxf(m_lo, bm_lo), mn_hi = fmaxf(m_hi, bm_hi);  // finite: key 0 of a block is visible
+    const int ev_n = max(ev, exp_above(bv));
+    const float vfix = ev_n > ev ? (ev_n - ev > 126 ? 0.f : pow2i(ev - ev_n)) : 1.f;
+    ev = ev_n;
+    const float vnorm = pow2i(-ev);
+    const float al_lo = ex2f(m_lo - mn_lo), al_hi = ex2f(m_hi - mn_hi);
+    m_lo = mn_lo;
+    m_hi = mn_hi;
+    const float p0 = ex2f(y0 - mn_lo), p1 = ex2f(y1 - mn_hi), p2 = ex2f(y2 - mn_lo), p3 = ex2f(y3 - mn_hi);
+    l_lo = l_lo * al_lo + (p0 + p2);
+    l_hi = l_hi * al_hi + (p1 + p3);
+    if (__any_sync(kAllLanes, al_lo != 1.f || al_hi != 1.f || vfix != 1.f)) {
+      const float f_lo = al_lo * vfix, f_hi = al_hi * vfix;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        o[i][0] *= f_lo;
+        o[i][1] *= f_hi;
+        o[i][2] *= f_lo;
+        o[i][3] *= f_hi;
+      }
+    }
+    const float vs0 = v0 ? vr0 * vnorm : 0.f, vs1 = v1 ? vr1 * vnorm : 0.f;
+    const uint32_t pb0 = transpose8x8(pack_f16x2(v0 ? p0 * vs0 : 0.f, v0 ? p1 * vs0 : 0.f));
+    const uint32_t pb1 = transpose8x8(pack_f16x2(v1 ? p2 * vs1 : 0.f, v1 ? p3 * vs1 : 0.f));
+    // dims 32 gq + 2 mt (row gq of m-tile mt) and + 1 (row gq + 8)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k][0] = vr[h][k].x, w[k][1] = vr[h][k].y, w[k][2] = vr[h][k].z, w[k][3] = vr[h][k].w;
+#pragma unroll
+      for (int ii = 0; ii < 4; ++ii) {
+        const int i = 4 * h + ii;
+        const uint32_t lo01 = __byte_perm(w[0][ii], w[1][ii], 0x5140) ^ 0x80808080u;
+        const uint32_t hi01 = __byte_perm(w[0][ii], w[1][ii], 0x7362) ^ 0x80808080u;
+        const uint32_t lo89 = __byte_perm(w[2][ii], w[3][ii], 0x5140) ^ 0x80808080u;
+        const uint32_t hi89 = __byte_perm(w[2][ii], w[3][ii], 0x7362) ^ 0x80808080u;
+        const uint32_t a0[4] = {lo_pair(lo01), hi_pair(lo01), lo_pair(lo89), hi_pair(lo89)};
+        mma16816(o[2 * i], a0, pb0, pb1);
+        const uint32_t a1[4] = {lo_pair(hi01), hi_pair(hi01), lo_pair(hi89), hi_pair(hi89)};
+        mma16816(o[2 * i + 1], a1, pb0, pb1);
+      }
+    }
+  }
+#pragma unroll
+  for (int sh = 4; sh < 32; sh <<= 1) {
+    l_lo += __shfl_xor_sync(kAllLanes, l_lo, sh);
+    l_hi += __shfl_xor_sync(kAllLanes, l_hi, sh);
+  }
+  if (gq == 0) {
+    wm[warp][2 * tq] = m_lo;
+    wm[warp][2 * tq + 1] = m_hi;
+    wl[warp][2 * tq] = l_lo;
+    wl[warp][2 * tq + 1] = l_hi;
+  }
+  const float up = pow2i(max(ev, -126));
+#pragma unroll
+  for (int mt = 0; mt < 16; ++mt) {  // rows 2tq, 2tq+1; dims 32 gq + 2 mt, + 1
+    const int d = 32 * gq + 2 * mt;
+    *reinterpret_cast<float2*>(&comb[warp][2 * tq][d]) = make_float2(o[mt][0] * up, o[mt][2] * up);
+    *reinterpret_cast<float2*>(&comb[warp][2 * tq + 1][d]) = make_float2(o[mt][1] * up, o[mt][3] * up);
+  }
+  __syncthreads();
+  // the warps' parts, in a fixed order; thread (row i % 8, dims 4 (i / 8 + 16 n))
+  const int r = threadIdx.x & 7;
+  float mx = -INFINITY, ls = 0.f, f[kOwnWarps];
+#pragma unroll
+  for (int w = 0; w < kOwnWarps; ++w) mx = fmaxf(mx, wm[w][r]);
+#pragma unroll
+  for (int w = 0; w < kOwnWarps; ++w) {
+    f[w] = wm[w][r] == -INFINITY ? 0.f : ex2f(wm[w][r] - mx);
+    ls += f[w] * wl[w][r];
+  }
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int dq = (threadIdx.x >> 3) + 16 * n;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kOwnWarps; ++w) {
+      const float4 v = *reinterpret_cast<const float4*>(&comb[w][r][4 * dq]);
+      acc.x = fmaf(f[w], v.x, acc.x);
+      acc.y = fmaf(f[w], v.y, acc.y);
+      acc.z = fmaf(f[w], v.z, acc.z);
+      acc.w = fmaf(f[w], v.w, acc.w);
+    }
+    p.own_o[((size_t)blockIdx.x * 64 + dq) * 8 + r] = acc;
+  }
+  if (threadIdx.x < 8) p.own_ml[(size_t)blockIdx.x * 8 + r] = make_float2(mx, ls);
+  wait_for_previous();  // this grid's end then means that the prefix pass has ended too
+}
+
+// ====================================================================
+// Merge
+// ====================================================================
+// CTA = (sequence, kv head); thread (row i % G, dims 4 (i / G)).
+__global__ void __launch_bounds__(512) merge_kernel(const __grid_constant__ SharedParams p,
+                                                    const __grid_constant__ SharedSeqs tab) {
+  const int s = blockIdx.x / p.HKV, g = blockIdx.x % p.HKV;
+  const int r = threadIdx.x % p.G, dq = threadIdx.x / p.G;
+  const int4 sq = tab.s[s];
+  const ShOwn own = shared_own(sq.y, sq.w, p.first_blk, p.S, p.W);
+  const int n_own = (own.n + p.chunk - 1) / p.chunk, own0 = p.HKV * sq.z + g * n_own;
+  int n_pre = 0, pre0 = 0, prow = 0;
+  if (p.n_grp > 0) {
+    const int rg = (s * p.G) / kRows;
+    const ShGroup grp = tab.grp[rg];
+    if (grp.n_blk > 0) {
+      const long long T = (long long)p.HKV * p.tiles_head;
+      const long long a = (long long)g * p.tiles_head + grp.x0;
+      const long long b = a + (grp.n_blk + kTileBlocks - 1) / kTileBlocks;
+      const int c0 = shared_cta_of(a, T, p.n_cta), c1 = shared_cta_of(b - 1, T, p.n_cta);
+      n_pre = c1 - c0 + 1;
+      pre0 = c0 + g * p.n_grp + rg;
+      prow = s * p.G - rg * kRows + r;
+    }
+  }
+  wait_for_previous();
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto part = [&](const float2 ml, const float4 v) {
+    if (ml.x == -INFINITY) return;  // no visible key
+    const float mn = fmaxf(m, ml.x);
+    const float f = m == -INFINITY ? 0.f : ex2f(m - mn), w = ex2f(ml.x - mn);
+    m = mn;
+    l = fmaf(w, ml.y, l * f);
+    acc.x = fmaf(w, v.x, acc.x * f);
+    acc.y = fmaf(w, v.y, acc.y * f);
+    acc.z = fmaf(w, v.z, acc.z * f);
+    acc.w = fmaf(w, v.w, acc.w * f);
+  };
+#pragma unroll 4
+  for (int i = 0; i < n_pre; ++i)
+    part(__ldcg(p.pre_ml + (size_t)(pre0 + i) * kRows + prow),
+         __ldcg(p.pre_o + ((size_t)(pre0 + i) * 64 + dq) * kRows + prow));
+#pragma unroll 4
+  for (int i = 0; i < n_own; ++i)
+    part(__ldcg(p.own_ml + (size_t)(own0 + i) * 8 + r), __ldcg(p.own_o + ((size_t)(own0 + i) * 64 + dq) * 8 + r));
+  const float il = l > 0.f ? 1.f / l : 0.f;
+  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * il, acc.y * il), b = __floats2bfloat162_rn(acc.z * il, acc.w * il);
+  *reinterpret_cast<uint2*>(p.out + ((size_t)sq.x * p.HQ + (size_t)g * p.G + r) * kHeadDim + 4 * dq) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+template <typename K>
+cudaError_t launch_after(K* kernel, int grid, int threads, const SharedParams& p, const SharedSeqs& t, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, t);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, cudaStream_t st) {
+  cudaError_t e;
+  const int own_grid = p.HKV * p.chunks_head;
+  if (p.n_grp > 0 && p.tiles_head > 0) {
+    if ((e = cudaFuncSetAttribute(prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem)) != cudaSuccess)
+      return e;
+    prefix_kernel<<<p.n_cta, kPreThreads, kPreSmem, st>>>(p, t);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_after(own_kernel, own_grid, kOwnWarps * 32, p, t, st)) != cudaSuccess) return e;
+  } else {
+    own_kernel<<<own_grid, kOwnWarps * 32, 0, st>>>(p, t);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  return launch_after(merge_kernel, p.n_seq * p.HKV, p.G * 64, p, t, st);
+}
+
+}  // namespace pa

@@ -1,0 +1,80 @@
+// Declarations shared by the C-ABI host code and the shared-prefix decode
+// kernels (pa_shared.cu).  Not part of the public interface.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "pa_tiles.cuh"
+
+namespace pa {
+
+constexpr int kShSeqs = 512;                        // sequences per launch, their table in its parameters
+constexpr int kShGroups = kShSeqs * 8 / kRows;      // row groups of one kv head at most (8 q heads a kv head)
+
+// Blocks of the prefix that some row of a group of 128 query rows sees: the
+// sink run [0, sink) and the run [lo, prefix blocks).
+struct ShGroup {
+  int x0;    // tiles of the head's earlier groups
+  int sink;
+  int lo;
+  int n_blk; // sink + prefix blocks - lo
+};
+
+struct SharedSeqs {
+  // {row in q / out, context length, chunks of the earlier sequences (per kv head), first block of its window}
+  int4 s[kShSeqs];
+  ShGroup grp[kShGroups];
+};
+
+struct SharedParams {
+  const __nv_bfloat16* q;  // [rows][HQ][256]
+  __nv_bfloat16* out;
+  const int8_t* k_pool;    // [n_pool][16][HKV][256]
+  const int8_t* v_pool;
+  const float* k_scale;    // [n_pool][16][HKV]
+  const float* v_scale;
+  const int32_t* block_table;
+  int bt_stride, n_pool, bt_row0;
+  int n_seq, HQ, HKV, G, S, W;
+  int prefix_blk;          // blocks of the shared prefix; their pages are block_table row 0's
+  int first_blk;           // the per-sequence pass starts at this block: prefix_blk, or 0 without a prefix pass
+  int n_grp;               // row groups per kv head (0: no prefix pass)
+  int tiles_head;          // 128-key tiles of all groups of one kv head
+  int n_cta;               // CTAs of the prefix pass
+  int chunk;               // blocks per CTA of the per-sequence pass
+  int chunks_head;         // its CTAs per kv head
+  float sm_scale_log2;
+  // Partials: per row the reference (log2 units) and sum of its softmax, and
+  // its unnormalised output, 4 dims x rows side by side.  Prefix: the partial
+  // of CTA c for group j (head-major) is number c + j; own keys: the CTA's number.
+  float4* pre_o;           // [c + j][64][128]
+  float2* pre_ml;          // [c + j][128]
+  float4* own_o;           // [cta][64][8]
+  float2* own_ml;          // [cta][8]
+  int* err;
+  unsigned long long wait_ns;
+};
+
+// Blocks of a sequence that the per-sequence pass visits, from block `first` on.
+struct ShOwn {
+  int sink, lo, n;  // sink blocks first .. first + sink, then blocks from lo on; n in all
+};
+PA_HD ShOwn shared_own(int n_ctx, int win_lo, int first, int S, int W) {
+  ShOwn o;
+  o.sink = W > 0 ? imax(0, imin(S, win_lo) - first) : 0;
+  o.lo = imax(win_lo, first);
+  o.n = o.sink + (n_ctx - 1) / kPage + 1 - o.lo;
+  return o;
+}
+PA_HD int shared_win_lo(int n_ctx, int W) { return W > 0 ? imax(0, (n_ctx - 1) / kPage + 1 - W) : 0; }
+
+// The prefix pass's tiles, head-major and group-major, laid end to end are cut
+// evenly: CTA c computes tiles [c T / C, (c + 1) T / C) of T.
+PA_HD long long shared_cut(int c, long long T, int C) { return c * T / C; }
+// The CTA that computes tile x.
+PA_HD int shared_cta_of(long long x, long long T, int C) { return (int)(((x + 1) * C - 1) / T); }
+
+cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, cudaStream_t st);
+
+}  // namespace pa
