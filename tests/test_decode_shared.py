@@ -207,6 +207,30 @@ def test_calls_back_to_back_of_changing_sizes():
             assert torch.equal(o.view(torch.int16), alone.view(torch.int16))
 
 
+def test_first_calls_on_cold_memory_repeat_bit_for_bit():
+    """Fresh handles, fresh copies of the inputs, other data in the freed memory in between: codes that arrive
+    late must not let any part of the kernel run ahead of another."""
+    import torch
+
+    import windowed_prefill_attention_gb300 as pa
+    b = CASES["long_prefix"].make()
+    first = None
+    for i in range(150):
+        d = to_device(b)
+        with Handle(b) as h:
+            out = call(h, b, d)
+            assert pa.pa_last_error(h) == 0
+        if first is None:
+            first = out
+            check(b, out)
+        assert torch.equal(out.view(torch.int16), first.view(torch.int16)), i
+        if i % 7 == 6:
+            del d
+            junk = torch.empty(1 << 27, dtype=torch.uint8, device="cuda").random_()
+            del junk
+            torch.cuda.empty_cache()
+
+
 def test_append_then_shared_decode():
     """A layer's step as a serving loop runs it: the prefix appended once, each sequence's own tokens in one batched
     append, a decode step of the batch, against the definition on the pool the calls wrote."""

@@ -33,6 +33,7 @@ namespace {
 
 constexpr unsigned kAllLanes = 0xffffffffu;
 constexpr float kMaxLift = 8.f;  // the softmax reference moves when a row's maximum passes it by more than 2^8
+constexpr int DEV_ERR_LAYOUT = 0x400;  // shared memory's base is not aligned as the operands need (reported as PA_ECUDA)
 constexpr uint64_t kShDrainNs = 200000000ull;
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -43,6 +44,14 @@ __device__ __forceinline__ float ex2f(float x) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int N>
+__device__ __forceinline__ void more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 // Four codes (bytes) -> two words of fp16 pairs: (b ^ 0x80) in the low byte of
 // 0x64__ is 1152 + b, and the subtraction is exact.
@@ -64,6 +73,21 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 }
 __device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// 16 TMEM lanes x 32 columns in the 16x256b shape (see pa_ptx.cuh).
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 // e with 2^(e-1) <= x < 2^e, in [-100, 100]; -100 for x <= 0.
@@ -90,22 +114,28 @@ constexpr int kSoftWarps = 4;                       // warps 0-3: softmax, one r
 constexpr int kConvWarps = 8;                       // warps 4-11: codes -> fp16 operands, and the queries
 constexpr int kIssueWarp = kSoftWarps + kConvWarps; // warp 12: TMEM, the MMAs
 constexpr int kScaleWarp = kIssueWarp + 1;          // warp 13: the tiles' scales
-constexpr int kPreThreads = 32 * (kScaleWarp + 1);
+constexpr int kPreThreads = 512;                    // whole warpgroups, for the register split below
+// Registers a thread, of the 128 each is launched with; 512 of 512 in all.
+constexpr int kSoftRegs = 144, kConvRegs = 136, kMiscRegs = 96;
+static_assert(kSoftRegs + 2 * kConvRegs + kMiscRegs <= 4 * 128, "register split: above it the increases wait forever");
+static_assert(kSoftRegs >= 128 && kConvRegs >= 128 && kMiscRegs <= 128, "increases and decreases from the launch's 128");
 
 constexpr int kChunkBytes = 32768;                  // half a tile of K (128 keys x 128 dims) or V (64 keys x 256 dims)
-// Shared memory from a 1024-byte aligned base.
+// Shared memory from its base, which is 1024-byte aligned (checked).  The total
+// stays under 195 KB: the SM then keeps 60 KB of its 256 KB as L1, where the
+// converters' loads in flight live.
 constexpr int kSmQ = 0;                             // 4 regions [128 rows][64 dims]
 constexpr int kSmK = 65536;                         // 2 chunks, each 2 regions [128 keys][64 dims]
 constexpr int kSmV = kSmK + 2 * kChunkBytes;        // 2 chunks, each 4 regions [64 keys][64 dims]
 constexpr int kSmScale = kSmV + 2 * kChunkBytes;    // [2] x {K scales 128, V scales 128, valid blocks, exponent}
 constexpr int kScaleSlot = 2 * 512 + 16;
-constexpr int kSmRow = kSmScale + 2 * kScaleSlot;   // [2][128] row factors, by segment parity
-constexpr int kSmBar = kSmRow + 2 * 512;
+constexpr int kSmRow = kSmScale + 2 * kScaleSlot;   // [2][128] int8 exponents of the rows' factors, by segment parity
+constexpr int kSmBar = kSmRow + 2 * kRows;
 enum : int {
   B_KF = 0,    // [2] K chunk written
-  B_KE = 2,    // [2] K chunk's products done
-  B_VF = 4,    // [2]
-  B_VE = 6,    // [2]
+  B_KE = 2,    // K chunk 0's products done (chunk 1's: the tile's scores are)
+  B_VF = 4,    // [2] V chunk written
+  B_VE = 6,    // V chunk 0's products done (chunk 1's: the tile's P V is)
   B_SF = 8,    // [2] scores of a tile in TMEM, by tile parity
   B_PF = 10,   // [2] P' of a tile in TMEM
   B_OD = 12,   // a tile's P V done
@@ -118,8 +148,8 @@ enum : int {
   kPreBars = 21
 };
 constexpr int kSmTmem = kSmBar + kPreBars * 8;
-constexpr int kPreSmem = kSmTmem + 16 + 1024;
-static_assert(kPreSmem <= 227 * 1024, "shared memory");
+constexpr int kPreSmem = kSmTmem + 16;
+static_assert(kPreSmem <= 195 * 1024, "shared memory");
 
 constexpr uint32_t kTmemO = 0, kTmemS = 256;        // O [0, 256), S of even / odd tiles [256, 384) / [384, 512)
 
@@ -181,70 +211,63 @@ struct PreCtx {
   }
 };
 
-// ---- converters.  Thread i of 256 holds its share of one whole tile of codes
-// in registers (64 KB a CTA in flight): chunk by chunk it widens what has
-// arrived, then loads the same chunk of the next tile.
-// K chunk c (dims [128 c, +128)): 16 bytes of keys 32 n + i / 8, dims 16 (i % 8).
-// V chunk c (keys [64 c, +64)): 16 bytes of keys 16 n + i / 16, dims 16 (i % 16).
-struct Codes {
-  uint4 k[2][4], v[2][4];
-};
-
-// 16 codes of one row as 32 bytes at 16-byte pieces 2 (u % 4) and + 1 of a
-// 128-byte swizzled row.  Threads u = 4..7 write their pieces in the other
-// order, so that the eight threads of a row hit eight different pieces.
-__device__ __forceinline__ void widen16(const uint4 c, uint32_t row_addr, int row, int u, bool swap) {
+// ---- converters.  Two warps for each chunk of a tile (K dims [0, 128), K dims
+// [128, 256), V keys [0, 64), V keys [64, 128)).  A warp keeps its share of a
+// tile's codes in registers, 16 bytes x 16 a thread: it widens what has
+// arrived and then loads the same part of the next tile, which has a whole
+// tile's time to arrive (64 KB a CTA in flight).
+// 16 codes of one row as 32 bytes: pieces 2 (u % 4) and + 1 of a 128-byte
+// swizzled row.  Of the eight threads whose stores go together four have an
+// even and four the next, odd row, whose pieces are swizzled to odd places:
+// eight different ones.
+__device__ __forceinline__ void widen16(const uint4 c, uint32_t row_addr, int row, int u) {
   const uint32_t w[4] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u, c.z ^ 0x80808080u, c.w ^ 0x80808080u};
   uint32_t h[8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) h[2 * e] = lo_pair(w[e]), h[2 * e + 1] = hi_pair(w[e]);
-  const int c0 = 2 * (u & 3);
-  const uint32_t a0 = row_addr + (uint32_t)(((c0) ^ (row & 7)) << 4), a1 = row_addr + (uint32_t)(((c0 + 1) ^ (row & 7)) << 4);
-  if (swap) {
-    sts128(a1, h[4], h[5], h[6], h[7]);
-    sts128(a0, h[0], h[1], h[2], h[3]);
-  } else {
-    sts128(a0, h[0], h[1], h[2], h[3]);
-    sts128(a1, h[4], h[5], h[6], h[7]);
-  }
+  const uint32_t at = row_addr + (uint32_t)(((2 * (u & 3)) ^ (row & 7)) << 4);
+  sts128(at, h[0], h[1], h[2], h[3]);
+  sts128(at ^ 16u, h[4], h[5], h[6], h[7]);
 }
 
+template <bool kV>
 __device__ __forceinline__ void role_convert(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
-  const int i = threadIdx.x - 32 * kSoftWarps, lane = threadIdx.x & 31, warp = i >> 5;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kSoftWarps;
+  const int ch = (warp >> 1) & 1, half = warp & 1;  // chunk, and which of its two warps
   uint32_t n_tile = 0, n_seg = 0;
   const size_t tok = (size_t)p.HKV * kHeadDim;  // bytes from a token to the next
+  // A load takes four keys x 128 bytes of K (two keys x 256 of V): lane bit 2
+  // (and 4) the key, the others the 16 bytes.  Load n of 16: keys kStep n on of
+  // the warp's 64 K keys (32 V keys).
+  const int u = kV ? (lane & 3) | (lane >> 3) << 2 : (lane & 3) | (lane >> 1 & 4);
+  const int sub = kV ? lane >> 2 & 1 : (lane >> 2 & 1) | (lane >> 4) << 1;
+  const int key0 = (kV ? 32 : 64) * half + sub;                 // the lane's key of load 0 in the chunk
+  constexpr int kStep = kV ? 2 : 4, kPerBlock = kPage / kStep;  // keys per load, loads per block
+  const uint32_t row0 = c.sb + (kV ? kSmV + ch * kChunkBytes + (u >> 2) * 8192 : kSmK + ch * kChunkBytes + (u >> 2) * 16384);
+  const int blk0 = kV ? 4 * ch + 2 * half : 4 * half;           // first block of the tile it loads
   for (long long x = c.x0; x < c.x1; ++n_seg) {
     const Segment s = segment_at(p, tab, x, c.x1);
-    const int8_t* kp = p.k_pool + (size_t)s.g * kHeadDim;
-    const int8_t* vp = p.v_pool + (size_t)s.g * kHeadDim;
+    const int8_t* src = (kV ? p.v_pool : p.k_pool) + (size_t)s.g * kHeadDim + (kV ? 16 * u : 128 * ch + 16 * u) +
+                        (size_t)sub * tok;
     // pages of the segment's blocks, 32 (four tiles) at a time, one per lane
     const int b0 = s.t0 * kTileBlocks;
     int pg = group_page(p, s.grp, b0 + lane), pg_next = group_page(p, s.grp, b0 + 32 + lane);
-    Codes r;
-    auto load_k = [&](int ch, int t4) {
+    uint4 r[16];
+    // a block past the list or of a bad page loads page 0's codes: whatever finite values they widen to,
+    // the softmax gives those keys no weight
+    auto load = [&](int t4) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int page = __shfl_sync(kAllLanes, pg, t4 * kTileBlocks + 2 * n + (i >> 7));
-        r.k[ch][n] = make_uint4(0, 0, 0, 0);
-        if (page >= 0)
-          r.k[ch][n] = ldg_stream(kp + ((size_t)page * kPage + ((i >> 3) & 15)) * tok + 128 * ch + 16 * (i & 7));
+      for (int b = 0; b < 16 / kPerBlock; ++b) {
+        const int page = max(0, __shfl_sync(kAllLanes, pg, t4 * kTileBlocks + blk0 + b));
+        const int8_t* at = src + (size_t)page * (kPage * tok);
+#pragma unroll
+        for (int n = 0; n < kPerBlock; ++n, at += kStep * tok) r[b * kPerBlock + n] = ldg_stream(at);
       }
     };
-    auto load_v = [&](int ch, int t4) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int page = __shfl_sync(kAllLanes, pg, t4 * kTileBlocks + 4 * ch + n);
-        r.v[ch][n] = make_uint4(0, 0, 0, 0);
-        if (page >= 0) r.v[ch][n] = ldg_stream(vp + ((size_t)page * kPage + (i >> 4)) * tok + 16 * (i & 15));
-      }
-    };
-    load_k(0, 0);
-    load_k(1, 0);
-    load_v(0, 0);
-    load_v(1, 0);
+    load(0);
     // the group's queries: a warp takes a row at a time
     if (n_seg > 0 && !c.wait(B_QE, n_seg - 1)) return;
-    float* rowc = reinterpret_cast<float*>(__cvta_shared_to_generic(c.sb + kSmRow + (n_seg & 1) * 512));
+    const uint32_t rowc = c.sb + kSmRow + (n_seg & 1) * kRows;
     for (int row = warp; row < kRows; row += kConvWarps) {
       float v[8];
 #pragma unroll
@@ -264,7 +287,7 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
       sts128(c.sb + kSmQ + (lane >> 3) * 16384 + row * 128 + (((lane & 7) ^ (row & 7)) << 4),
              pack_f16x2(v[0] * mul, v[1] * mul), pack_f16x2(v[2] * mul, v[3] * mul), pack_f16x2(v[4] * mul, v[5] * mul),
              pack_f16x2(v[6] * mul, v[7] * mul));
-      if (lane == 0) rowc[row] = row < s.rows ? pow2i(-k) * p.sm_scale_log2 : 0.f;
+      if (lane == 0) asm volatile("st.shared.u8 [%0], %1;" ::"r"(rowc + row), "r"(-k) : "memory");
     }
     fence_proxy_async_shared();
     __syncwarp();
@@ -276,34 +299,21 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
         pg = pg_next;
         pg_next = group_page(p, s.grp, b0 + 8 * (t + 1) + 32 + lane);
       }
-      const bool more = t + 1 < nt;
-      const int t4 = (t + 1) & 3;
+      // the chunk's products of the tile before are done
+      bool ok;
+      if (kV) ok = c.wait(ch == 0 ? B_VE : B_OD, n_tile + 1);
+      else if (ch == 0) ok = c.wait(B_KE, n_tile + 1);
+      else ok = n_tile == 0 || c.wait(B_SF + ((n_tile - 1) & 1), (n_tile - 1) >> 1);
+      if (!ok) return;
 #pragma unroll
-      for (int ch = 0; ch < 2; ++ch) {
-        if (!c.wait(B_KE + ch, n_tile + 1)) return;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int row = 32 * n + (i >> 3), u = i & 7;
-          widen16(r.k[ch][n], c.sb + kSmK + ch * kChunkBytes + (u >> 2) * 16384 + row * 128, row, u, u >= 4);
-        }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(c.bar(B_KF + ch));
-        if (more) load_k(ch, t4);
+      for (int n = 0; n < 16; ++n) {
+        const int row = key0 + kStep * n;
+        widen16(r[n], row0 + row * 128, row, u);
       }
-#pragma unroll
-      for (int ch = 0; ch < 2; ++ch) {
-        if (!c.wait(B_VE + ch, n_tile + 1)) return;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int row = 16 * n + (i >> 4), u = i & 15;
-          widen16(r.v[ch][n], c.sb + kSmV + ch * kChunkBytes + (u >> 2) * 8192 + row * 128, row, u, (u & 4) != 0);
-        }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(c.bar(B_VF + ch));
-        if (more) load_v(ch, t4);
-      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c.bar((kV ? B_VF : B_KF) + ch));
+      if (t + 1 < nt) load((t + 1) & 3);
     }
     x += nt;
   }
@@ -359,56 +369,96 @@ __device__ __forceinline__ void role_scales(const SharedParams& p, const SharedS
   }
 }
 
-// ---- the products, one thread.  Q K^T of tile t + 1 goes before P V of tile t.
+// ---- the products, one thread.  The eight (four) instructions of a chunk go
+// out of one asm block with the operands' offsets added inside it: instructions
+// between them, a branch above all, leave the tensor pipe waiting.
+// S (+)= Q K^T over 128 dims: two regions of 64 dims, four k-steps of 32 bytes each.
+__device__ __forceinline__ void mma_qk_chunk(uint32_t d, uint64_t qd, uint64_t kd, uint32_t acc0) {
+  asm volatile(
+      "{\n\t.reg .pred p0, pt;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 pt, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p0;\n\t"
+      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, pt;\n\t"
+      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, pt;\n\t"
+      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, pt;\n\t"
+      "add.s64 a, %1, 1024;\n\tadd.s64 b, %2, 1024;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, pt;\n\t"
+      "add.s64 a, %1, 1026;\n\tadd.s64 b, %2, 1026;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, pt;\n\t"
+      "add.s64 a, %1, 1028;\n\tadd.s64 b, %2, 1028;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, pt;\n\t"
+      "add.s64 a, %1, 1030;\n\tadd.s64 b, %2, 1030;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, pt;\n\t"
+      "}" ::"r"(d), "l"(qd), "l"(kd), "r"(kIdescQK), "r"(acc0)
+      : "memory");
+}
+// O (+)= P V over 64 keys: four k-steps of 16 keys, 8 TMEM columns of P' and 2048 bytes of V each.
+__device__ __forceinline__ void mma_pv_chunk(uint32_t d, uint32_t ptm, uint64_t vd, uint32_t acc0) {
+  asm volatile(
+      "{\n\t.reg .pred p0, pt;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 pt, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p0;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, pt;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, pt;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, pt;\n\t"
+      "}" ::"r"(d), "r"(ptm), "l"(vd), "r"(kIdescPV), "r"(acc0)
+      : "memory");
+}
+static_assert((16384 >> 4) == 1024 && (2048 >> 4) == 128, "descriptor steps of the blocks above");
+
+// Q K^T of tile t + 1 goes before P V of tile t, so that the tensor core has
+// the next scores to compute while the softmax handles these.
 __device__ __forceinline__ void role_issue(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
   uint32_t n_tile = 0, n_seg = 0;
   bool ok = true;
+  const uint64_t qd0 = sdesc_k_sw128(c.sb + kSmQ), qd1 = sdesc_k_sw128(c.sb + kSmQ + kChunkBytes);
+  const uint64_t kd0 = sdesc_k_sw128(c.sb + kSmK), kd1 = sdesc_k_sw128(c.sb + kSmK + kChunkBytes);
+  const uint64_t vd0 = sdesc_v(c.sb + kSmV), vd1 = sdesc_v(c.sb + kSmV + kChunkBytes);
   auto wait = [&](int i, uint32_t parity) { return mbar_wait(c.bar(i), parity & 1u, c.wc, 80 + i); };
-  // n: the tile's number in the CTA's order
-  auto pv = [&](uint32_t n, bool first) {
+  auto pv = [&](uint32_t n, uint32_t acc) {  // n: the tile's number in the CTA's order
     const uint32_t ptm = c.tm + kTmemS + 128 * (n & 1);
-    if (!wait(B_PF + (n & 1), n >> 1)) return false;
-    for (int ch = 0; ch < 2; ++ch) {
-      if (!wait(B_VF + ch, n)) return false;
-      tc_fence_after();
-      const uint32_t vb = c.sb + kSmV + ch * kChunkBytes;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        mma_ts(c.tm + kTmemO, ptm + 8 * (4 * ch + k), sdesc_v(vb + 2048 * k), kIdescPV, !(first && ch == 0 && k == 0));
-      mma_commit(c.bar(B_VE + ch));
-    }
+    if (!wait(B_VF, n) || !wait(B_PF + (n & 1), n >> 1)) return false;
+    tc_fence_after();
+    mma_pv_chunk(c.tm + kTmemO, ptm, vd0, acc);
+    mma_commit(c.bar(B_VE));
+    if (!wait(B_VF + 1, n)) return false;
+    tc_fence_after();
+    mma_pv_chunk(c.tm + kTmemO, ptm + 32, vd1, 1u);
     mma_commit(c.bar(B_OD));
+    return true;
+  };
+  auto qk = [&](uint32_t n) {
+    const uint32_t stm = c.tm + kTmemS + 128 * (n & 1);
+    if (!wait(B_KF, n)) return false;
+    tc_fence_after();
+    mma_qk_chunk(stm, qd0, kd0, 0u);
+    mma_commit(c.bar(B_KE));
+    if (!wait(B_KF + 1, n)) return false;
+    tc_fence_after();
+    mma_qk_chunk(stm, qd1, kd1, 1u);
+    mma_commit(c.bar(B_SF + (n & 1)));
     return true;
   };
   for (long long x = c.x0; ok && x < c.x1; ++n_seg) {
     const Segment s = segment_at(p, tab, x, c.x1);
     const int nt = s.t1 - s.t0;
-    ok = wait(B_QF, n_seg);
-    for (int t = 0; ok && t < nt; ++t, ++n_tile) {
-      const uint32_t stm = c.tm + kTmemS + 128 * (n_tile & 1);
-      for (int ch = 0; ok && ch < 2; ++ch) {
-        ok = wait(B_KF + ch, n_tile);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int rgn = 2 * ch + (k >> 2);
-          const uint64_t a = sdesc_k_sw128(c.sb + kSmQ + rgn * 16384 + 32 * (k & 3));
-          const uint64_t b = sdesc_k_sw128(c.sb + kSmK + rgn * 16384 + 32 * (k & 3));
-          mma_ss(stm, a, b, kIdescQK, !(ch == 0 && k == 0));
-        }
-        mma_commit(c.bar(B_KE + ch));
-      }
-      if (!ok) break;
-      mma_commit(c.bar(B_SF + (n_tile & 1)));
+    ok = wait(B_QF, n_seg) && qk(n_tile);
+    if (nt == 1) mma_commit(c.bar(B_QE));
+    // the epilogue has read the segment before's O
+    ok = ok && (n_seg == 0 || wait(B_OE, n_seg - 1));
+    for (int t = 1; ok && t < nt; ++t) {
+      ok = qk(n_tile + t);
       if (t == nt - 1) mma_commit(c.bar(B_QE));
-      if (t > 0) {
-        if (t == 1 && n_seg > 0) ok = wait(B_OE, n_seg - 1);
-        ok = ok && pv(n_tile - 1, t == 1);
-      }
+      ok = ok && pv(n_tile + t - 1, t > 1);
     }
-    if (ok && nt == 1 && n_seg > 0) ok = wait(B_OE, n_seg - 1);
-    ok = ok && pv(n_tile - 1, nt == 1);
+    ok = ok && pv(n_tile + nt - 1, nt > 1);
+    n_tile += nt;
     x += nt;
   }
   // nothing may be in flight when the CTA frees its TMEM
@@ -416,114 +466,169 @@ __device__ __forceinline__ void role_issue(const SharedParams& p, const SharedSe
   (void)mbar_wait_drain(c.bar(B_DRAIN), 0, kShDrainNs);
 }
 
-// ---- softmax: thread = row.
+// ---- softmax.  A warp owns 32 rows as two slices of 16, one after the other,
+// read in the 16-lane TMEM shape: a thread holds rows t / 4 and t / 4 + 8 and,
+// of every eight keys, keys 2 (t % 4) and + 1, so that each scale it loads from
+// shared memory serves two rows (with one row a thread, each lane loading every
+// key's scales, those loads alone took half of the shared-memory bandwidth).
+struct SliceRows {
+  float c[2], m[2];  // the rows' factors, their references in log2 units
+  float2 l[2];       // their sums, this thread's keys
+  int win_lo[2];
+};
+
+// z = score * k_scale, and the rows' maxima.
+template <bool kMasked>
+__device__ __forceinline__ void scale_and_max(uint32_t (&s)[64], uint32_t ks_at, uint32_t seen0, uint32_t seen1,
+                                              float& z0, float& z1) {
+  float za = -INFINITY, zb = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    float2 ks;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks.x), "=f"(ks.y) : "r"(ks_at + 32 * k));
+    float2 a = mul2(make_float2(__uint_as_float(s[4 * k]), __uint_as_float(s[4 * k + 1])), ks);
+    float2 b = mul2(make_float2(__uint_as_float(s[4 * k + 2]), __uint_as_float(s[4 * k + 3])), ks);
+    if (kMasked) {
+      if (!(seen0 >> (k >> 1) & 1u)) a = make_float2(-INFINITY, -INFINITY);
+      if (!(seen1 >> (k >> 1) & 1u)) b = make_float2(-INFINITY, -INFINITY);
+    }
+    s[4 * k] = __float_as_uint(a.x);
+    s[4 * k + 1] = __float_as_uint(a.y);
+    s[4 * k + 2] = __float_as_uint(b.x);
+    s[4 * k + 3] = __float_as_uint(b.y);
+    za = max3(za, a.x, a.y);
+    zb = max3(zb, b.x, b.y);
+  }
+  z0 = za;
+  z1 = zb;
+}
+
+// One tile of one slice: P' over its scores.  `first`: no O to rescale yet.
+__device__ __forceinline__ bool softmax_slice(const SharedParams& p, const PreCtx& c, const ShGroup& grp, int blk0,
+                                              uint32_t stm, uint32_t otm, uint32_t sc, uint32_t valid, float fe,
+                                              bool first, uint32_t pv_before, SliceRows& r) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t ks_at = sc + 8 * (lane & 3);
+  uint32_t s[64];
+  tmem_ld_16x256b_x16(stm, s);
+  uint32_t seen[2] = {valid, valid};  // blocks of the tile that the rows see
+  if (p.W > 0) {
+#pragma unroll
+    for (int e = 0; e < kTileBlocks; ++e) {
+      const int lb = group_block(grp, blk0 + e);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (lb >= p.S && lb < r.win_lo[i]) seen[i] &= ~(1u << e);
+    }
+  }
+  tmem_wait_ld(s);
+  float z[2];
+  if (__all_sync(kAllLanes, (seen[0] & seen[1]) == 0xffu)) scale_and_max<false>(s, ks_at, 0, 0, z[0], z[1]);
+  else scale_and_max<true>(s, ks_at, seen[0], seen[1], z[0], z[1]);
+  float f[2];  // what earlier sums shrink by (they are zero while m is -inf)
+  bool moved = false;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    z[i] = fmaxf(z[i], __shfl_xor_sync(kAllLanes, z[i], 1));
+    z[i] = fmaxf(z[i], __shfl_xor_sync(kAllLanes, z[i], 2));
+    const float mz = z[i] == -INFINITY ? -INFINITY : z[i] * r.c[i];
+    f[i] = 1.f;
+    if (r.m[i] == -INFINITY) {
+      r.m[i] = mz;
+    } else if (mz > r.m[i] + kMaxLift) {
+      f[i] = ex2f(r.m[i] - mz);
+      r.m[i] = mz;
+    }
+    r.l[i] = mul2(r.l[i], make_float2(f[i], f[i]));
+    f[i] *= fe;
+    moved |= f[i] != 1.f;
+  }
+  if (!first && __any_sync(kAllLanes, moved)) {
+    if (!c.wait(B_OD, pv_before)) return false;
+    tc_fence_after();
+#pragma unroll 1
+    for (int h = 0; h < 8; ++h) {  // 32 columns
+      uint32_t o[16];
+      tmem_ld_16x256b_x4(otm + 32 * h, o);
+      tmem_wait_ld(o);
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        o[e] = __float_as_uint(__uint_as_float(o[e]) * f[0]);
+        o[e + 1] = __float_as_uint(__uint_as_float(o[e + 1]) * f[0]);
+        o[e + 2] = __float_as_uint(__uint_as_float(o[e + 2]) * f[1]);
+        o[e + 3] = __float_as_uint(__uint_as_float(o[e + 3]) * f[1]);
+      }
+      tmem_st_16x256b_x4(otm + 32 * h, o);
+    }
+  }
+  // p = 2^(z c - m), P' = p v_scale 2^-ev in fp16.  A hidden key's z is -inf,
+  // and a row's factor may be 0: keep the product -inf.
+  const float n0 = r.m[0] == -INFINITY ? 0.f : -r.m[0], n1 = r.m[1] == -INFINITY ? 0.f : -r.m[1];
+  const float c0 = fmaxf(r.c[0], 1e-30f), c1 = fmaxf(r.c[1], 1e-30f);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // 64 keys
+    uint32_t ph[16];
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      const int k = 8 * h + kk;
+      float2 vs;
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(vs.x), "=f"(vs.y) : "r"(ks_at + 512 + 32 * k));
+      const float2 ya = fma2(make_float2(__uint_as_float(s[4 * k]), __uint_as_float(s[4 * k + 1])), make_float2(c0, c0), make_float2(n0, n0));
+      const float2 yb = fma2(make_float2(__uint_as_float(s[4 * k + 2]), __uint_as_float(s[4 * k + 3])), make_float2(c1, c1), make_float2(n1, n1));
+      const float2 ea = make_float2(ex2f(ya.x), ex2f(ya.y)), eb = make_float2(ex2f(yb.x), ex2f(yb.y));
+      r.l[0] = add2(r.l[0], ea);
+      r.l[1] = add2(r.l[1], eb);
+      const float2 wa = mul2(ea, vs), wb = mul2(eb, vs);
+      ph[2 * kk] = pack_f16x2(wa.x, wa.y);
+      ph[2 * kk + 1] = pack_f16x2(wb.x, wb.y);
+    }
+    tmem_st_16x128b_x8(stm + 32 * h, ph);
+  }
+  return true;
+}
+
 __device__ __forceinline__ void role_softmax(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
-  const int row = threadIdx.x, lane = threadIdx.x & 31;
-  const uint32_t lane_tm = (uint32_t)(threadIdx.x & ~31) << 16;
-  const uint32_t otm = c.tm + kTmemO + lane_tm;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t quad = (uint32_t)(32 * warp) << 16, slice = 16u << 16;
+  const uint32_t otm = c.tm + kTmemO + quad;
+  const int row0 = 32 * warp + (lane >> 2);  // rows row0, + 8 (slice 0), + 16, + 24 (slice 1)
   uint32_t n_tile = 0, n_seg = 0;
   for (long long x = c.x0; x < c.x1; ++n_seg) {
     const Segment s = segment_at(p, tab, x, c.x1);
     const int nt = s.t1 - s.t0;
-    const int win_lo = p.W > 0 && row < s.rows ? tab.s[(s.rg * kRows + row) / p.G].w : 0;
-    float cr = 0.f, m = -INFINITY;  // the row's factor, its reference in log2 units
-    float2 l2 = make_float2(0.f, 0.f);
+    SliceRows r[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = row0 + 8 * i;
+      r[i >> 1].m[i & 1] = -INFINITY;
+      r[i >> 1].l[i & 1] = make_float2(0.f, 0.f);
+      r[i >> 1].win_lo[i & 1] = p.W > 0 && row < s.rows ? tab.s[(s.rg * kRows + row) / p.G].w : 0;
+    }
     int ev = -100;
     for (int t = 0; t < nt; ++t, ++n_tile) {
       const int b = n_tile & 1;
-      const uint32_t stm = c.tm + kTmemS + 128 * b + lane_tm;
-      if (!c.wait(B_SF + b, n_tile >> 1) || !c.wait(B_SCF + b, n_tile >> 1)) return;
+      const uint32_t stm = c.tm + kTmemS + 128 * b + quad;
+      if (!c.wait(B_SCF + b, n_tile >> 1) || !c.wait(B_SF + b, n_tile >> 1)) return;
       tc_fence_after();
       if (t == 0) {
-        float v;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(c.sb + kSmRow + (n_seg & 1) * 512 + 4 * row));
-        cr = v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          int e;
+          asm volatile("ld.shared.s8 %0, [%1];" : "=r"(e) : "r"(c.sb + kSmRow + (n_seg & 1) * kRows + row0 + 8 * i));
+          r[i >> 1].c[i & 1] = pow2i(e) * p.sm_scale_log2;
+        }
       }
       const uint32_t sc = c.sb + kSmScale + b * kScaleSlot;
       const float4 meta = lds_f32x4(sc + 1024);
-      uint32_t seen = __float_as_uint(meta.x);  // blocks of the tile this row sees
       const int ev_t = (int)__float_as_uint(meta.y);
-      if (p.W > 0) {
-#pragma unroll
-        for (int e = 0; e < kTileBlocks; ++e) {
-          const int lb = group_block(s.grp, (s.t0 + t) * kTileBlocks + e);
-          if (lb >= p.S && lb < win_lo) seen &= ~(1u << e);
-        }
-      }
-      // 1. the row's maximum
-      float zm = -INFINITY;
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        uint32_t r[32];
-        tmem_ld32(stm + 32 * h, r);
-        tmem_wait_ld(r);
-#pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {
-          float bm = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = 16 * blk + 4 * e;
-            const float4 ks = lds_f32x4(sc + 4 * (32 * h + k));
-            const float2 z0 = mul2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), make_float2(ks.x, ks.y));
-            const float2 z1 = mul2(make_float2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), make_float2(ks.z, ks.w));
-            bm = max3(max3(bm, z0.x, z0.y), z1.x, z1.y);
-          }
-          if (seen >> (2 * h + blk) & 1u) zm = fmaxf(zm, bm);
-        }
-      }
-      const float mz = zm == -INFINITY ? -INFINITY : zm * cr;
-      float f = 1.f;  // what earlier sums shrink by (they are zero while m is -inf)
-      if (m == -INFINITY) {
-        m = mz;
-      } else if (mz > m + kMaxLift) {
-        f = ex2f(m - mz);
-        m = mz;
-      }
-      l2 = mul2(l2, make_float2(f, f));
-      const float fo = f * (ev_t > ev ? pow2i(max(-126, ev - ev_t)) : 1.f);
+      const float fe = ev_t > ev ? pow2i(max(-126, ev - ev_t)) : 1.f;
       ev = ev_t;
-      if (t > 0 && __any_sync(kAllLanes, fo != 1.f)) {
-        if (!c.wait(B_OD, n_tile - 1)) return;
-        tc_fence_after();
-#pragma unroll 1
-        for (int h = 0; h < 8; ++h) {
-          uint32_t r[32];
-          tmem_ld32(otm + 32 * h, r);
-          tmem_wait_ld(r);
+      const int blk0 = (s.t0 + t) * kTileBlocks;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * fo);
-          tmem_st32(otm + 32 * h, r);
-        }
-      }
-      // 2. p = 2^(z c - m), P' = p v_scale 2^-ev in fp16 over the scores
-      const float neg = m == -INFINITY ? 0.f : -m;
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        uint32_t r[32], ph[16];
-        tmem_ld32(stm + 32 * h, r);
-        tmem_wait_ld(r);
-#pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {
-          const float nb = (seen >> (2 * h + blk) & 1u) ? neg : -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = 16 * blk + 4 * e;
-            const float4 ks = lds_f32x4(sc + 4 * (32 * h + k)), vs = lds_f32x4(sc + 512 + 4 * (32 * h + k));
-            float2 z0 = mul2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), make_float2(ks.x, ks.y));
-            float2 z1 = mul2(make_float2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), make_float2(ks.z, ks.w));
-            z0 = fma2(z0, make_float2(cr, cr), make_float2(nb, nb));
-            z1 = fma2(z1, make_float2(cr, cr), make_float2(nb, nb));
-            z0 = make_float2(ex2f(z0.x), ex2f(z0.y));
-            z1 = make_float2(ex2f(z1.x), ex2f(z1.y));
-            l2 = add2(l2, add2(z0, z1));
-            z0 = mul2(z0, make_float2(vs.x, vs.y));
-            z1 = mul2(z1, make_float2(vs.z, vs.w));
-            ph[k / 2] = pack_f16x2(z0.x, z0.y);
-            ph[k / 2 + 1] = pack_f16x2(z1.x, z1.y);
-          }
-        }
-        tmem_st16(stm + 16 * h, ph);
-      }
+      for (int i = 0; i < 2; ++i)
+        if (!softmax_slice(p, c, s.grp, blk0, stm + i * slice, otm + i * slice, sc, __float_as_uint(meta.x), fe, t == 0,
+                           n_tile - 1, r[i]))
+          return;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -532,49 +637,64 @@ __device__ __forceinline__ void role_softmax(const SharedParams& p, const Shared
         mbar_arrive(c.bar(B_SCE + b));
       }
     }
-    // the segment's partial
-    if (!c.wait(B_OD, n_tile - 1)) return;
+    // The segment's partial, one row a thread, once the last P V is done.  A
+    // parity wait only tells a phase from the one before: the last tile's
+    // scores came after P V of two tiles before, so the one in between is
+    // waited for first.
+    if ((nt > 1 && !c.wait(B_OD, n_tile - 2)) || !c.wait(B_OD, n_tile - 1)) return;
     tc_fence_after();
     const int id = (int)blockIdx.x + s.j;
     const float up = pow2i(ev);
-    float4* dst = p.pre_o + (size_t)id * 64 * kRows + row;
+    float4* dst = p.pre_o + (size_t)id * 64 * kRows + threadIdx.x;
 #pragma unroll 1
     for (int h = 0; h < 8; ++h) {
-      uint32_t r[32];
-      tmem_ld32(otm + 32 * h, r);
-      tmem_wait_ld(r);
-      if (row < s.rows) {
+      uint32_t o[32];
+      tmem_ld32(otm + 32 * h, o);
+      tmem_wait_ld(o);
+      if ((int)threadIdx.x < s.rows) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           dst[(size_t)(8 * h + e) * kRows] =
-              make_float4(__uint_as_float(r[4 * e]) * up, __uint_as_float(r[4 * e + 1]) * up,
-                          __uint_as_float(r[4 * e + 2]) * up, __uint_as_float(r[4 * e + 3]) * up);
+              make_float4(__uint_as_float(o[4 * e]) * up, __uint_as_float(o[4 * e + 1]) * up,
+                          __uint_as_float(o[4 * e + 2]) * up, __uint_as_float(o[4 * e + 3]) * up);
       }
     }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(c.bar(B_OE));
-    if (row < s.rows) p.pre_ml[(size_t)id * kRows + row] = make_float2(m, l2.x + l2.y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = row0 + 8 * i;
+      const float2 l = r[i >> 1].l[i & 1];
+      float sum = l.x + l.y;
+      sum += __shfl_xor_sync(kAllLanes, sum, 1);
+      sum += __shfl_xor_sync(kAllLanes, sum, 2);
+      if ((lane & 3) == 0 && row < s.rows) p.pre_ml[(size_t)id * kRows + row] = make_float2(r[i >> 1].m[i & 1], sum);
+    }
     x += nt;
   }
 }
 
 __global__ void __launch_bounds__(kPreThreads, 1) prefix_kernel(const __grid_constant__ SharedParams p,
                                                                 const __grid_constant__ SharedSeqs tab) {
-  extern __shared__ uint8_t raw[];
+  extern __shared__ __align__(1024) uint8_t raw[];
   PreCtx c;
-  c.sb = (smem_u32(raw) + 1023u) & ~1023u;
+  c.sb = smem_u32(raw);
+  if (c.sb & 1023u) {  // the whole CTA: nothing was started
+    if (threadIdx.x == 0) atomicCAS(p.err, 0, DEV_ERR_LAYOUT);
+    return;
+  }
   c.wc = WaitCtl{p.err, p.wait_ns};
   const long long T = (long long)p.HKV * p.tiles_head;
   c.x0 = shared_cut((int)blockIdx.x, T, p.n_cta);
   c.x1 = shared_cut((int)blockIdx.x + 1, T, p.n_cta);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
+    mbar_init(c.bar(B_KE), 1);
+    mbar_init(c.bar(B_VE), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(c.bar(B_KF + i), kConvWarps);
-      mbar_init(c.bar(B_VF + i), kConvWarps);
-      mbar_init(c.bar(B_KE + i), 1);
-      mbar_init(c.bar(B_VE + i), 1);
+      mbar_init(c.bar(B_KF + i), 2);
+      mbar_init(c.bar(B_VF + i), 2);
       mbar_init(c.bar(B_SF + i), 1);
       mbar_init(c.bar(B_PF + i), kSoftWarps);
       mbar_init(c.bar(B_SCF + i), 1);
@@ -596,13 +716,21 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefix_kernel(const __grid_con
   tc_fence_after();
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c.tm) : "r"(c.sb + kSmTmem));
   dependents_may_start();
-  if (warp < kSoftWarps) role_softmax(p, tab, c);
-  else if (warp < kIssueWarp) role_convert(p, tab, c);
-  else if (warp == kIssueWarp) {
-    if ((threadIdx.x & 31) == 0) role_issue(p, tab, c);
-    __syncwarp();
+  if (warp < kSoftWarps) {
+    more_regs<kSoftRegs>();
+    role_softmax(p, tab, c);
+  } else if (warp < kIssueWarp) {
+    more_regs<kConvRegs>();
+    if (warp < kSoftWarps + kConvWarps / 2) role_convert<false>(p, tab, c);
+    else role_convert<true>(p, tab, c);
   } else {
-    role_scales(p, tab, c);
+    fewer_regs<kMiscRegs>();
+    if (warp == kIssueWarp) {
+      if ((threadIdx.x & 31) == 0) role_issue(p, tab, c);
+      __syncwarp();
+    } else if (warp == kScaleWarp) {
+      role_scales(p, tab, c);
+    }
   }
   tc_fence_before();
   __syncthreads();
