@@ -339,7 +339,7 @@ int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, c
 
 /* Host-only, no GPU needed: how pa_decode_shared splits the work of one launch
  * (the first min(n_seq, 512) sequences) on a GPU of n_sm SMs.  prefix_out (may
- * be NULL) receives *n_prefix_runs entries of int32[8] = {CTA, kv head, first
+ * be NULL) receives *n_prefix_runs entries of int32[8] = {SM pair, kv head, first
  * sequence, sequences, sink, lo, first, last}: entries first .. last - 1 of the
  * list of blocks 0 .. sink - 1, then lo, lo + 1, ... (the prefix's blocks that
  * some of the sequences see) against those sequences' queries of the head.

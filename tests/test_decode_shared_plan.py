@@ -53,8 +53,8 @@ def test_every_visible_block_is_computed_once(pa, case):
         assert 0 < last - first <= 128
         done.setdefault((s, g), []).extend(listed(base, sink, lo, first, last))
     groups = {}
-    for c, g, s0, ns, sink, lo, first, last in pre.tolist():
-        assert 0 <= first < last and first % 8 == 0 and ns * (hq // hkv) <= 128
+    for _, g, s0, ns, sink, lo, first, last in pre.tolist():
+        assert 0 <= first < last and first % 8 == 0 and ns * (hq // hkv) <= 256
         groups.setdefault((g, s0, ns), []).extend(listed(0, sink, lo, first, last))
     seen_by = {}
     for (g, s0, ns), blocks in groups.items():
@@ -78,15 +78,15 @@ def test_every_visible_block_is_computed_once(pa, case):
             assert set(mine) | {b for b in shared if b in set(want)} == set(want)
             for b in want:
                 if b in shared:
-                    union.setdefault((g, s // (128 // (hq // hkv))), set()).add(b)
+                    union.setdefault((g, s // (256 // (hq // hkv))), set()).add(b)
     assert not done
     for (g, s0, ns), blocks in groups.items():  # a block is listed only if some sequence of the group sees it
-        assert set(blocks) == union[g, s0 // (128 // (hq // hkv))]
-    if len(pre):  # one CTA's tiles are consecutive, and no CTA has more than its even share
-        ctas = pre[:, 0]
-        assert np.all(np.diff(ctas) >= 0) and ctas[0] == 0 and ctas[-1] < n_sm
-        tiles = np.zeros(ctas[-1] + 1, int)
-        np.add.at(tiles, ctas, (pre[:, 7] - pre[:, 6] + 7) // 8)
+        assert set(blocks) == union[g, s0 // (256 // (hq // hkv))]
+    if len(pre):  # one pair's tiles are consecutive, and no pair has more than its even share
+        pairs = pre[:, 0]
+        assert np.all(np.diff(pairs) >= 0) and pairs[0] == 0 and pairs[-1] < max(1, n_sm // 2)
+        tiles = np.zeros(pairs[-1] + 1, int)
+        np.add.at(tiles, pairs, (pre[:, 7] - pre[:, 6] + 7) // 8)
         assert tiles.min() >= 1 and tiles.max() <= -(-tiles.sum() // len(tiles))
 
 

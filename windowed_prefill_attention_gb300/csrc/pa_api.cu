@@ -1626,11 +1626,11 @@ int decode_shared_check(int HQ, int HKV, int max_pages, int n_seq, const pa_seq*
 }
 
 // One launch (sequences [s0, s0 + n)) of the shared-prefix decode: its table and split.
-// The prefix pass: the rows of a kv head in groups of 128, per group the
+// The prefix pass: the rows of a kv head in groups of 256, per group the
 // blocks some row sees, in 128-key tiles; all tiles cut evenly over at most
-// n_sm CTAs.  The per-sequence pass: chunks of equal block counts, about two
+// n_sm / 2 SM pairs.  The per-sequence pass: chunks of equal block counts, about two
 // CTAs per SM, four to 128 blocks each.
-void decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, int n, int n_prefix, int S, int W,
+int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, int n, int n_prefix, int S, int W,
                         SharedParams& p, SharedSeqs& t) {
   const int G = HQ / HKV, Pb = n_prefix / kPage;
   p.n_seq = n;
@@ -1641,10 +1641,10 @@ void decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, i
   p.S = S;
   p.W = W;
   p.prefix_blk = Pb;
-  p.n_grp = n < 2 || Pb == 0 ? 0 : (n * G + kRows - 1) / kRows;
+  p.n_grp = n < 2 || Pb == 0 ? 0 : (n * G + kUnitRows - 1) / kUnitRows;
   p.first_blk = p.n_grp > 0 ? Pb : 0;
   p.tiles_head = 0;
-  const int per = kRows / G;  // sequences per group
+  const int per = kUnitRows / G;  // sequences per group
   for (int j = 0; j < p.n_grp; ++j) {
     int lo = Pb;
     for (int s = j * per; s < std::min(n, (j + 1) * per); ++s) lo = std::min(lo, shared_win_lo(seqs[s0 + s].n_ctx, W));
@@ -1655,7 +1655,9 @@ void decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, i
     g.n_blk = g.sink + Pb - lo;
     p.tiles_head += (g.n_blk + kTileBlocks - 1) / kTileBlocks;
   }
-  p.n_cta = (int)std::min<long long>(n_sm, (long long)HKV * p.tiles_head);
+  // at most 16 groups of 2^23 tiles: no overflow before the test
+  if ((long long)HKV * p.tiles_head >= (1ll << 30)) return PA_EINVAL;
+  p.n_pairs = std::min(std::max(1, n_sm / 2), HKV * p.tiles_head);
   long long own = 0;
   for (int s = 0; s < n; ++s) {
     const pa_seq& q = seqs[s0 + s];
@@ -1671,11 +1673,13 @@ void decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, i
     chunks += (shared_own(q.n_ctx, lo, p.first_blk, S, W).n + p.chunk - 1) / p.chunk;
   }
   p.chunks_head = chunks;
+  return PA_OK;
 }
 
-constexpr size_t kPrePartial = (size_t)kHeadDim * kRows * sizeof(float), kPreStats = (size_t)kRows * sizeof(float2);
+constexpr size_t kPrePartial = (size_t)kHeadDim * kUnitRows * sizeof(float);
+constexpr size_t kPreStats = (size_t)kUnitRows * sizeof(float2);
 constexpr size_t kOwnPartial = (size_t)kHeadDim * 8 * sizeof(float), kOwnStats = 8 * sizeof(float2);
-size_t pre_partials(const SharedParams& p) { return p.tiles_head > 0 ? (size_t)p.n_cta + (size_t)p.n_grp * p.HKV : 0; }
+size_t pre_partials(const SharedParams& p) { return p.tiles_head > 0 ? (size_t)p.n_pairs + (size_t)p.n_grp * p.HKV : 0; }
 size_t own_partials(const SharedParams& p) { return (size_t)p.HKV * p.chunks_head; }
 
 int reserve(Workspace& w, size_t need, bool capturing) {
@@ -1706,8 +1710,9 @@ int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, c
   SharedSeqs t;
   size_t pre = 0, own = 0;
   for (int s0 = 0; s0 < n_seq; s0 += kShSeqs) {
-    decode_shared_plan(h->HQ, h->HKV, h->n_sm, seqs, s0, std::min(kShSeqs, n_seq - s0), n_prefix, n_sink_blk,
-                       n_win_blk, p, t);
+    if ((rc = decode_shared_plan(h->HQ, h->HKV, h->n_sm, seqs, s0, std::min(kShSeqs, n_seq - s0), n_prefix, n_sink_blk,
+                                 n_win_blk, p, t)))
+      return rc;
     pre = std::max(pre, pre_partials(p));
     own = std::max(own, own_partials(p));
   }
@@ -1732,8 +1737,8 @@ int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, c
   p.wait_ns = (unsigned long long)h->opt.wait_timeout_ms * 1000000ull;
   for (int s0 = 0; s0 < n_seq; s0 += kShSeqs) {
     if (n_seq > kShSeqs)
-      decode_shared_plan(h->HQ, h->HKV, h->n_sm, seqs, s0, std::min(kShSeqs, n_seq - s0), n_prefix, n_sink_blk,
-                         n_win_blk, p, t);
+      (void)decode_shared_plan(h->HQ, h->HKV, h->n_sm, seqs, s0, std::min(kShSeqs, n_seq - s0), n_prefix, n_sink_blk,
+                               n_win_blk, p, t);
     PA_CUDA(launch_decode_shared(p, t, st));
   }
   return PA_OK;
@@ -1743,29 +1748,30 @@ int pa_decode_shared_plan(int n_q_heads, int n_kv_heads, int max_pages_per_seq, 
                           const pa_seq* seqs, int n_prefix, int n_sink_blk, int n_win_blk, int32_t* prefix_out,
                           int prefix_cap, int* n_prefix_runs, int32_t* own_out, int own_cap, int* n_own_runs) {
   if (n_sm < 1 || max_pages_per_seq < 1 || !n_prefix_runs || !n_own_runs) return PA_EINVAL;
-  const int rc = decode_shared_check(n_q_heads, n_kv_heads, max_pages_per_seq, n_seq, seqs, n_prefix, n_sink_blk, 1.f);
+  int rc = decode_shared_check(n_q_heads, n_kv_heads, max_pages_per_seq, n_seq, seqs, n_prefix, n_sink_blk, 1.f);
   if (rc) return rc;
   SharedParams p{};
   SharedSeqs t;
-  decode_shared_plan(n_q_heads, n_kv_heads, n_sm, seqs, 0, std::min(n_seq, kShSeqs), n_prefix, n_sink_blk, n_win_blk,
-                     p, t);
-  const long long T = (long long)p.HKV * p.tiles_head;
+  if ((rc = decode_shared_plan(n_q_heads, n_kv_heads, n_sm, seqs, 0, std::min(n_seq, kShSeqs), n_prefix, n_sink_blk,
+                               n_win_blk, p, t)))
+    return rc;
+  const int T = p.HKV * p.tiles_head, per = kUnitRows / p.G;
   int np = 0;
   for (int g = 0; g < p.HKV; ++g)
     for (int j = 0; j < p.n_grp; ++j) {
       const ShGroup& gr = t.grp[j];
       const int nt = (gr.n_blk + kTileBlocks - 1) / kTileBlocks;
-      const long long a = (long long)g * p.tiles_head + gr.x0;
+      const int a = g * p.tiles_head + gr.x0;
       for (int t0 = 0; t0 < nt;) {
-        const int c = shared_cta_of(a + t0, T, p.n_cta);
-        const int t1 = (int)std::min<long long>(nt, shared_cut(c + 1, T, p.n_cta) - a);
+        const int c = shared_pair_of(a + t0, T, p.n_pairs);
+        const int t1 = std::min(nt, shared_cut(c + 1, T, p.n_pairs) - a);
         if (prefix_out) {
           if (np >= prefix_cap) return PA_EINVAL;
           int32_t* o = prefix_out + 8 * np;
           o[0] = c;
           o[1] = g;
-          o[2] = j * (kRows / p.G);
-          o[3] = std::min(p.n_seq, (j + 1) * (kRows / p.G)) - o[2];
+          o[2] = j * per;
+          o[3] = std::min(p.n_seq, (j + 1) * per) - o[2];
           o[4] = gr.sink;
           o[5] = gr.lo;
           o[6] = t0 * kTileBlocks;

@@ -12,7 +12,7 @@
 //   own_kernel     each sequence's own keys, as pa_decode splits them
 //   merge_kernel   the partials of both, and the division
 //
-// prefix_kernel.  Groups of 128 query rows x tiles of 128 keys.  The int8
+// prefix_kernel.  Groups of 256 query rows x tiles of 128 keys.  The int8
 // codes are widened to fp16 (exact) on their way into shared memory, K and V
 // alike as [key][64 dims] rows of 128 bytes: a K-major B operand for S = Q K^T
 // and an MN-major one for O = P V, so V needs no transpose.  Scores, softmax
@@ -110,84 +110,97 @@ __device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
 // ====================================================================
 // The prefix
 // ====================================================================
-constexpr int kSoftWarps = 4;                       // warps 0-3: softmax, one row per thread
-constexpr int kConvWarps = 8;                       // warps 4-11: codes -> fp16 operands, and the queries
-constexpr int kIssueWarp = kSoftWarps + kConvWarps; // warp 12: TMEM, the MMAs
-constexpr int kScaleWarp = kIssueWarp + 1;          // warp 13: the tiles' scales
-constexpr int kPreThreads = 512;                    // whole warpgroups, for the register split below
-// Registers a thread, of the 128 each is launched with; 512 of 512 in all.
-constexpr int kSoftRegs = 144, kConvRegs = 136, kMiscRegs = 96;
-static_assert(kSoftRegs + 2 * kConvRegs + kMiscRegs <= 4 * 128, "register split: above it the increases wait forever");
-static_assert(kSoftRegs >= 128 && kConvRegs >= 128 && kMiscRegs <= 128, "increases and decreases from the launch's 128");
+// A pair of SMs (cluster of two CTAs) computes groups of 256 query rows, 128 in
+// each CTA's TMEM, against tiles of 128 keys; one thread of the even CTA issues
+// every product of both (cta_group::2).  The B operands are split: each CTA
+// holds K of 64 of a tile's keys and V of 128 of the 256 dims, so it reads and
+// widens half of every tile's codes, which (with one CTA per tile: 64 KB of
+// codes read, 128 KB of operands written and 192 KB of operands read per tile
+// and SM) would otherwise bound the kernel.
+constexpr int kSoftWarps = 8;                       // warps 0-7: softmax; TMEM quadrant w % 4, 16 rows w / 4 of it
+constexpr int kConvWarps = 8;                       // warps 8-15: codes -> fp16 operands (K: four, V: four), the queries
+constexpr int kIssueWarp = kSoftWarps + kConvWarps; // warp 16: TMEM; even CTA: the products, odd CTA: forwards K
+constexpr int kScaleWarp = kIssueWarp + 1;          // warp 17: the tiles' scales
+constexpr int kVFwdWarp = kIssueWarp + 2;           // warps 18, 19: odd CTA: forward V and the queries
+constexpr int kQFwdWarp = kIssueWarp + 3;
+constexpr int kPreThreads = 32 * (kQFwdWarp + 1);
+// Registers a thread, of the 96 each is launched with (65536 / 640): in units
+// of a warp's, 8 x 120 + 8 x 80 + 4 x 80 = 20 x 96.
+constexpr int kSoftRegs = 120, kConvRegs = 80, kMiscRegs = 80;
+static_assert(8 * kSoftRegs + 8 * kConvRegs + 4 * kMiscRegs <= 20 * 96, "register split: above it the increase waits forever");
+static_assert(kSoftRegs >= 96 && kConvRegs <= 96 && kMiscRegs <= 96, "an increase and two decreases from the launch's 96");
 
-constexpr int kChunkBytes = 32768;                  // half a tile of K (128 keys x 128 dims) or V (64 keys x 256 dims)
 // Shared memory from its base, which is 1024-byte aligned (checked).  The total
 // stays under 195 KB: the SM then keeps 60 KB of its 256 KB as L1, where the
 // converters' loads in flight live.
+constexpr int kStageBytes = 32768;
 constexpr int kSmQ = 0;                             // 4 regions [128 rows][64 dims]
-constexpr int kSmK = 65536;                         // 2 chunks, each 2 regions [128 keys][64 dims]
-constexpr int kSmV = kSmK + 2 * kChunkBytes;        // 2 chunks, each 4 regions [64 keys][64 dims]
-constexpr int kSmScale = kSmV + 2 * kChunkBytes;    // [2] x {K scales 128, V scales 128, valid blocks, exponent}
+constexpr int kSmK = 65536;                         // 2 stages x 4 regions [64 keys][64 dims]
+constexpr int kSmV = kSmK + 2 * kStageBytes;        // 2 stages x 2 regions [128 keys][64 dims]
+constexpr int kSmScale = kSmV + 2 * kStageBytes;    // [2] x {K scales 128, V scales 128, valid blocks, exponent}
 constexpr int kScaleSlot = 2 * 512 + 16;
 constexpr int kSmRow = kSmScale + 2 * kScaleSlot;   // [2][128] int8 exponents of the rows' factors, by segment parity
 constexpr int kSmBar = kSmRow + 2 * kRows;
+// Barriers, at the same offsets in both CTAs; [2]: by tile parity.  "Even": the
+// issuer waits on the even CTA's, which counts both CTAs' arrivals.  "Both":
+// a commit arrives in both CTAs.  A parity wait tells a phase only from the one
+// before it; every wait below comes when the phase before is known to be over.
 enum : int {
-  B_KF = 0,    // [2] K chunk written
-  B_KE = 2,    // K chunk 0's products done (chunk 1's: the tile's scores are)
-  B_VF = 4,    // [2] V chunk written
-  B_VE = 6,    // V chunk 0's products done (chunk 1's: the tile's P V is)
-  B_SF = 8,    // [2] scores of a tile in TMEM, by tile parity
-  B_PF = 10,   // [2] P' of a tile in TMEM
-  B_OD = 12,   // a tile's P V done
-  B_SCF = 13,  // [2] scales written
-  B_SCE = 15,  // [2] scales read
-  B_QF = 17,   // queries written
-  B_QE = 18,   // a segment's last Q K^T done
-  B_OE = 19,   // a segment's O read
-  B_DRAIN = 20,
-  kPreBars = 21
+  B_KF = 0,    // [2] even: a tile's K is written (four warps, and the odd CTA's forward)
+  B_VF = 2,    // [2] even: its V
+  B_KL = 4,    // [2] odd: its own half of K, V (four warps), to be forwarded
+  B_VL = 6,    // [2]
+  B_SF = 8,    // [2] both: scores of a tile in TMEM; its K stage is free
+  B_PF = 10,   // [2] even: P' of a tile in TMEM (every softmax warp of both)
+  B_OD = 12,   // [2] both: P V of a tile is done; its V stage is free
+  B_SCF = 14,  // [2] scales written (own CTA)
+  B_SCE = 16,  // [2] scales read
+  B_QF = 18,   // even: queries written
+  B_QL = 19,   // odd: its own queries, to be forwarded
+  B_QE = 20,   // both: a segment's last Q K^T is done
+  B_OE = 21,   // even: a segment's O is read (every softmax warp of both)
+  B_DRAIN = 22,
+  kPreBars = 23
 };
 constexpr int kSmTmem = kSmBar + kPreBars * 8;
 constexpr int kPreSmem = kSmTmem + 16;
 static_assert(kPreSmem <= 195 * 1024, "shared memory");
-
 constexpr uint32_t kTmemO = 0, kTmemS = 256;        // O [0, 256), S of even / odd tiles [256, 384) / [384, 512)
 
 // The B operand of O = P V: V as [key][64 dims] rows of 128 bytes with the
 // 128-byte swizzle, dims (N) contiguous: 8-key atoms of 1024 bytes along K,
-// regions of 64 keys x 128 bytes along N.
+// regions of 128 keys x 128 bytes along N.
 __device__ __forceinline__ uint64_t sdesc_v(uint32_t saddr) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(8192 >> 4) << 16;      // leading byte offset: the next 64 dims
+  d |= static_cast<uint64_t>(16384 >> 4) << 16;     // leading byte offset: the next 64 dims
   d |= static_cast<uint64_t>(1024 >> 4) << 32;      // stride byte offset: the next 8 keys
   d |= static_cast<uint64_t>(1) << 46;
   d |= static_cast<uint64_t>(2) << 61;
   return d;
 }
-constexpr uint32_t kIdescQK = idesc_f16(128, 128, false, false);
-constexpr uint32_t kIdescPV = idesc_f16(128, 256, false, false) | (1u << 16);  // B is N-major
+constexpr uint32_t kIdescQK = idesc_f16(256, 128, false, false);
+constexpr uint32_t kIdescPV = idesc_f16(256, 256, false, false) | (1u << 16);  // B is N-major
 
-// A run of tiles of one group: a CTA's work is one or more of these.
+// A run of tiles of one group: a pair's work is one or more of these.
 struct Segment {
   int j, g, rg;     // group number (head-major), kv head, row group
   ShGroup grp;
   int t0, t1;       // tiles of the group
-  int rows;         // query rows of the group
+  int row0, rows;   // this CTA's first row (of the kv head's n_seq G) and how many there are
 };
-__device__ __forceinline__ Segment segment_at(const SharedParams& p, const SharedSeqs& tab, long long x,
-                                              long long x_end) {
+__device__ __forceinline__ Segment segment_at(const SharedParams& p, const SharedSeqs& tab, int rank, int x, int x_end) {
   Segment s;
-  s.g = (int)(x / p.tiles_head);
-  const int xh = (int)(x - (long long)s.g * p.tiles_head);
+  s.g = x / p.tiles_head;
+  const int xh = x - s.g * p.tiles_head;
   s.rg = 0;
   while (s.rg + 1 < p.n_grp && tab.grp[s.rg + 1].x0 <= xh) ++s.rg;
   s.j = s.g * p.n_grp + s.rg;
   s.grp = tab.grp[s.rg];
   s.t0 = xh - s.grp.x0;
-  const int nt = (s.grp.n_blk + kTileBlocks - 1) / kTileBlocks;
-  s.t1 = (int)min((long long)nt, s.t0 + (x_end - x));
-  s.rows = min(kRows, p.n_seq * p.G - s.rg * kRows);
+  s.t1 = min((s.grp.n_blk + kTileBlocks - 1) / kTileBlocks, s.t0 + (x_end - x));
+  s.row0 = s.rg * kUnitRows + rank * kRows;
+  s.rows = max(0, min(kRows, p.n_seq * p.G - s.row0));
   return s;
 }
 // Logical block of the b-th visible block of a group.
@@ -200,22 +213,27 @@ __device__ __forceinline__ int group_page(const SharedParams& p, const ShGroup& 
 }
 
 struct PreCtx {
-  uint32_t sb;  // shared base
-  uint32_t tm;  // TMEM base
-  long long x0, x1;
+  uint32_t sb;    // shared base, the same offset in both CTAs
+  uint32_t tm;    // TMEM base, the same in both
+  int rank;       // 0: the even CTA of the pair, 1: the odd one
+  int x0, x1;     // the pair's tiles
   WaitCtl wc;
   __device__ uint32_t bar(int i) const { return sb + kSmBar + 8 * i; }
   // One outcome for the warp.
   __device__ bool wait(int i, uint32_t parity) const {
     return __all_sync(kAllLanes, mbar_wait(bar(i), parity & 1u, wc, 80 + i));
   }
+  // An arrival on the even CTA's barrier that hands over tensor memory (the
+  // caller has waited for its tcgen05 accesses and fenced them).
+  __device__ void arrive_even_tmem(int i) const {
+    if (rank == 0) mbar_arrive(bar(i));
+    else mbar_arrive_remote(cluster_addr(bar(i), 0));
+  }
 };
 
-// ---- converters.  Two warps for each chunk of a tile (K dims [0, 128), K dims
-// [128, 256), V keys [0, 64), V keys [64, 128)).  A warp keeps its share of a
-// tile's codes in registers, 16 bytes x 16 a thread: it widens what has
-// arrived and then loads the same part of the next tile, which has a whole
-// tile's time to arrive (64 KB a CTA in flight).
+// ---- converters.  A warp keeps its share of a tile's codes in registers, 16
+// bytes x 8 a thread: it widens what has arrived into the stage of the tile's
+// parity and then loads its part of the next tile.
 // 16 codes of one row as 32 bytes: pieces 2 (u % 4) and + 1 of a 128-byte
 // swizzled row.  Of the eight threads whose stores go together four have an
 // even and four the next, odd row, whose pieces are swizzled to odd places:
@@ -233,31 +251,31 @@ __device__ __forceinline__ void widen16(const uint4 c, uint32_t row_addr, int ro
 template <bool kV>
 __device__ __forceinline__ void role_convert(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kSoftWarps;
-  const int ch = (warp >> 1) & 1, half = warp & 1;  // chunk, and which of its two warps
+  const int w = warp & 3;
   uint32_t n_tile = 0, n_seg = 0;
   const size_t tok = (size_t)p.HKV * kHeadDim;  // bytes from a token to the next
-  // A load takes four keys x 128 bytes of K (two keys x 256 of V): lane bit 2
-  // (and 4) the key, the others the 16 bytes.  Load n of 16: keys kStep n on of
-  // the warp's 64 K keys (32 V keys).
-  const int u = kV ? (lane & 3) | (lane >> 3) << 2 : (lane & 3) | (lane >> 1 & 4);
-  const int sub = kV ? lane >> 2 & 1 : (lane >> 2 & 1) | (lane >> 4) << 1;
-  const int key0 = (kV ? 32 : 64) * half + sub;                 // the lane's key of load 0 in the chunk
-  constexpr int kStep = kV ? 2 : 4, kPerBlock = kPage / kStep;  // keys per load, loads per block
-  const uint32_t row0 = c.sb + (kV ? kSmV + ch * kChunkBytes + (u >> 2) * 8192 : kSmK + ch * kChunkBytes + (u >> 2) * 16384);
-  const int blk0 = kV ? 4 * ch + 2 * half : 4 * half;           // first block of the tile it loads
-  for (long long x = c.x0; x < c.x1; ++n_seg) {
-    const Segment s = segment_at(p, tab, x, c.x1);
-    const int8_t* src = (kV ? p.v_pool : p.k_pool) + (size_t)s.g * kHeadDim + (kV ? 16 * u : 128 * ch + 16 * u) +
-                        (size_t)sub * tok;
+  // K: warp w the 16 keys 64 rank + 16 w on, all dims; a load takes two keys.
+  // V: warp w keys 32 w on, dims 128 rank on; a load takes four keys.  Lane bit 2
+  // (and 4) the key, the others the 16 bytes.
+  const int u = kV ? (lane & 3) | (lane >> 1 & 4) : (lane & 3) | (lane >> 3) << 2;
+  const int sub = kV ? (lane >> 2 & 1) | (lane >> 4) << 1 : lane >> 2 & 1;
+  constexpr int kStep = kV ? 4 : 2, kPerBlock = kPage / kStep;  // keys per load, loads per block
+  const int row0 = (kV ? 32 : 16) * w + sub;                    // the stage's row of the lane's first load
+  const uint32_t at0 = c.sb + (kV ? kSmV + (u >> 2) * 16384 : kSmK + (u >> 2) * 8192) + row0 * 128;
+  const int blk0 = kV ? 2 * w : 4 * c.rank + w;                 // first block of the tile it loads
+  const int8_t* base = (kV ? p.v_pool + 128 * c.rank : p.k_pool) + 16 * u + (size_t)sub * tok;
+  for (int x = c.x0; x < c.x1; ++n_seg) {
+    const Segment s = segment_at(p, tab, c.rank, x, c.x1);
+    const int8_t* src = base + (size_t)s.g * kHeadDim;
     // pages of the segment's blocks, 32 (four tiles) at a time, one per lane
     const int b0 = s.t0 * kTileBlocks;
     int pg = group_page(p, s.grp, b0 + lane), pg_next = group_page(p, s.grp, b0 + 32 + lane);
-    uint4 r[16];
+    uint4 r[8];
     // a block past the list or of a bad page loads page 0's codes: whatever finite values they widen to,
     // the softmax gives those keys no weight
     auto load = [&](int t4) {
 #pragma unroll
-      for (int b = 0; b < 16 / kPerBlock; ++b) {
+      for (int b = 0; b < 8 / kPerBlock; ++b) {
         const int page = max(0, __shfl_sync(kAllLanes, pg, t4 * kTileBlocks + blk0 + b));
         const int8_t* at = src + (size_t)page * (kPage * tok);
 #pragma unroll
@@ -265,7 +283,7 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
       }
     };
     load(0);
-    // the group's queries: a warp takes a row at a time
+    // the CTA's queries: a warp takes a row at a time
     if (n_seg > 0 && !c.wait(B_QE, n_seg - 1)) return;
     const uint32_t rowc = c.sb + kSmRow + (n_seg & 1) * kRows;
     for (int row = warp; row < kRows; row += kConvWarps) {
@@ -273,7 +291,7 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = 0.f;
       if (row < s.rows) {
-        const int rr = s.rg * kRows + row;
+        const int rr = s.row0 + row;
         const int4 sq = tab.s[rr / p.G];
         unpack8(__ldg(reinterpret_cast<const uint4*>(p.q + ((size_t)sq.x * p.HQ + (size_t)s.g * p.G + rr % p.G) * kHeadDim) + lane), v);
       }
@@ -291,7 +309,7 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
     }
     fence_proxy_async_shared();
     __syncwarp();
-    if (lane == 0) mbar_arrive(c.bar(B_QF));
+    if (lane == 0) mbar_arrive(c.bar(c.rank == 0 ? B_QF : B_QL));
 
     const int nt = s.t1 - s.t0;
     for (int t = 0; t < nt; ++t, ++n_tile) {
@@ -299,23 +317,36 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
         pg = pg_next;
         pg_next = group_page(p, s.grp, b0 + 8 * (t + 1) + 32 + lane);
       }
-      // the chunk's products of the tile before are done
-      bool ok;
-      if (kV) ok = c.wait(ch == 0 ? B_VE : B_OD, n_tile + 1);
-      else if (ch == 0) ok = c.wait(B_KE, n_tile + 1);
-      else ok = n_tile == 0 || c.wait(B_SF + ((n_tile - 1) & 1), (n_tile - 1) >> 1);
-      if (!ok) return;
+      // the stage's products of two tiles before are done
+      const int st = n_tile & 1;
+      if (n_tile > 1 && !c.wait((kV ? B_OD : B_SF) + st, (n_tile >> 1) - 1)) return;
 #pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        const int row = key0 + kStep * n;
-        widen16(r[n], row0 + row * 128, row, u);
-      }
+      for (int n = 0; n < 8; ++n) widen16(r[n], at0 + st * kStageBytes + kStep * n * 128, row0 + kStep * n, u);
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(c.bar((kV ? B_VF : B_KF) + ch));
+      if (lane == 0) mbar_arrive(c.bar((kV ? (c.rank == 0 ? B_VF : B_VL) : (c.rank == 0 ? B_KF : B_KL)) + st));
       if (t + 1 < nt) load((t + 1) & 3);
     }
     x += nt;
+  }
+}
+
+// ---- forwards of the odd CTA: the even CTA's issuer learns that the odd CTA's
+// part of a tile (of a segment's queries) is written.  A cluster-scope release
+// takes ~1100 cycles, so it has a thread of its own.
+__device__ __forceinline__ void role_forward_tiles(const PreCtx& c, int local, int even) {
+  for (int n = 0; n < c.x1 - c.x0; ++n) {
+    if (!mbar_wait(c.bar(local + (n & 1)), (n >> 1) & 1, c.wc, 80 + local)) return;
+    mbar_arrive_cluster(cluster_addr(c.bar(even + (n & 1)), 0));
+  }
+}
+__device__ __forceinline__ void role_forward_queries(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
+  uint32_t n_seg = 0;
+  for (int x = c.x0; x < c.x1; ++n_seg) {
+    const Segment s = segment_at(p, tab, c.rank, x, c.x1);
+    if (!mbar_wait(c.bar(B_QL), n_seg & 1, c.wc, 80 + B_QL)) return;
+    mbar_arrive_cluster(cluster_addr(c.bar(B_QF), 0));
+    x += s.t1 - s.t0;
   }
 }
 
@@ -323,8 +354,8 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
 __device__ __forceinline__ void role_scales(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
   const int lane = threadIdx.x & 31;
   uint32_t n_tile = 0;
-  for (long long x = c.x0; x < c.x1;) {
-    const Segment s = segment_at(p, tab, x, c.x1);
+  for (int x = c.x0; x < c.x1;) {
+    const Segment s = segment_at(p, tab, c.rank, x, c.x1);
     int ev = -100;
     // lane: keys 4 lane .. + 3 of a tile, in block lane / 4
     float ks[4], vs[4];
@@ -350,7 +381,7 @@ __device__ __forceinline__ void role_scales(const SharedParams& p, const SharedS
       ev = max(ev, exp_above(mv));
       const float vn = pow2i(-ev);
       const uint32_t ok = __ballot_sync(kAllLanes, valid);
-      if (!c.wait(B_SCE + b, (n_tile >> 1) + 1)) return;
+      if (n_tile > 1 && !c.wait(B_SCE + b, (n_tile >> 1) - 1)) return;
       const uint32_t at = c.sb + kSmScale + b * kScaleSlot;
       sts128(at + 16 * lane, __float_as_uint(ks[0]), __float_as_uint(ks[1]), __float_as_uint(ks[2]), __float_as_uint(ks[3]));
       sts128(at + 512 + 16 * lane, __float_as_uint(vs[0] * vn), __float_as_uint(vs[1] * vn), __float_as_uint(vs[2] * vn),
@@ -369,108 +400,94 @@ __device__ __forceinline__ void role_scales(const SharedParams& p, const SharedS
   }
 }
 
-// ---- the products, one thread.  The eight (four) instructions of a chunk go
-// out of one asm block with the operands' offsets added inside it: instructions
+// ---- the products, one thread of the even CTA.  A tile's instructions go out
+// of one asm block with the operands' offsets added inside it: instructions
 // between them, a branch above all, leave the tensor pipe waiting.
-// S (+)= Q K^T over 128 dims: two regions of 64 dims, four k-steps of 32 bytes each.
-__device__ __forceinline__ void mma_qk_chunk(uint32_t d, uint64_t qd, uint64_t kd, uint32_t acc0) {
+// S = Q K^T: four regions of 64 dims, four k-steps of 32 bytes each.
+__device__ __forceinline__ void mma_qk_tile(uint32_t d, uint64_t qd, uint64_t kd) {
+#define PA_SH_QK(qo, ko)                          \
+  "add.s64 a, %1, " #qo ";\n\tadd.s64 b, %2, " #ko ";\n\t" \
+  "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, pt;\n\t"
   asm volatile(
-      "{\n\t.reg .pred p0, pt;\n\t.reg .b64 a, b;\n\t"
-      "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 pt, 0, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p0;\n\t"
-      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, pt;\n\t"
-      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, pt;\n\t"
-      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, pt;\n\t"
-      "add.s64 a, %1, 1024;\n\tadd.s64 b, %2, 1024;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, pt;\n\t"
-      "add.s64 a, %1, 1026;\n\tadd.s64 b, %2, 1026;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, pt;\n\t"
-      "add.s64 a, %1, 1028;\n\tadd.s64 b, %2, 1028;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, pt;\n\t"
-      "add.s64 a, %1, 1030;\n\tadd.s64 b, %2, 1030;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, pt;\n\t"
-      "}" ::"r"(d), "l"(qd), "l"(kd), "r"(kIdescQK), "r"(acc0)
+      "{\n\t.reg .pred pf, pt;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 pf, %4, %4;\n\tsetp.eq.b32 pt, %4, %4;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, pf;\n\t"
+      PA_SH_QK(2, 2) PA_SH_QK(4, 4) PA_SH_QK(6, 6)
+      PA_SH_QK(1024, 512) PA_SH_QK(1026, 514) PA_SH_QK(1028, 516) PA_SH_QK(1030, 518)
+      PA_SH_QK(2048, 1024) PA_SH_QK(2050, 1026) PA_SH_QK(2052, 1028) PA_SH_QK(2054, 1030)
+      PA_SH_QK(3072, 1536) PA_SH_QK(3074, 1538) PA_SH_QK(3076, 1540) PA_SH_QK(3078, 1542)
+      "}" ::"r"(d), "l"(qd), "l"(kd), "r"(kIdescQK), "r"(0u)
       : "memory");
+#undef PA_SH_QK
 }
-// O (+)= P V over 64 keys: four k-steps of 16 keys, 8 TMEM columns of P' and 2048 bytes of V each.
-__device__ __forceinline__ void mma_pv_chunk(uint32_t d, uint32_t ptm, uint64_t vd, uint32_t acc0) {
+// O (+)= P V over 128 keys: eight k-steps of 16 keys, 8 TMEM columns of P' and 2048 bytes of V each.
+__device__ __forceinline__ void mma_pv_tile(uint32_t d, uint32_t ptm, uint64_t vd, uint32_t acc0) {
+#define PA_SH_PV(po, vo)                          \
+  "add.u32 a, %1, " #po ";\n\tadd.s64 b, %2, " #vo ";\n\t" \
+  "tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, pt;\n\t"
   asm volatile(
       "{\n\t.reg .pred p0, pt;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
-      "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 pt, 0, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p0;\n\t"
-      "add.u32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, pt;\n\t"
-      "add.u32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, pt;\n\t"
-      "add.u32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, pt;\n\t"
+      "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 pt, %4, %4;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p0;\n\t"
+      PA_SH_PV(8, 128) PA_SH_PV(16, 256) PA_SH_PV(24, 384) PA_SH_PV(32, 512) PA_SH_PV(40, 640) PA_SH_PV(48, 768)
+      PA_SH_PV(56, 896)
       "}" ::"r"(d), "r"(ptm), "l"(vd), "r"(kIdescPV), "r"(acc0)
       : "memory");
+#undef PA_SH_PV
 }
-static_assert((16384 >> 4) == 1024 && (2048 >> 4) == 128, "descriptor steps of the blocks above");
+static_assert((16384 >> 4) == 1024 && (8192 >> 4) == 512 && (2048 >> 4) == 128, "descriptor steps of the blocks above");
 
 // Q K^T of tile t + 1 goes before P V of tile t, so that the tensor core has
-// the next scores to compute while the softmax handles these.
+// the next scores to compute while the softmax handles these.  The parity waits:
+// a tile's K, V, P' and queries are written only after the products that read
+// what was there before.
 __device__ __forceinline__ void role_issue(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
   uint32_t n_tile = 0, n_seg = 0;
   bool ok = true;
-  const uint64_t qd0 = sdesc_k_sw128(c.sb + kSmQ), qd1 = sdesc_k_sw128(c.sb + kSmQ + kChunkBytes);
-  const uint64_t kd0 = sdesc_k_sw128(c.sb + kSmK), kd1 = sdesc_k_sw128(c.sb + kSmK + kChunkBytes);
-  const uint64_t vd0 = sdesc_v(c.sb + kSmV), vd1 = sdesc_v(c.sb + kSmV + kChunkBytes);
+  const uint64_t qd = sdesc_k_sw128(c.sb + kSmQ);
+  const uint64_t kd0 = sdesc_k_sw128(c.sb + kSmK), kd1 = sdesc_k_sw128(c.sb + kSmK + kStageBytes);
+  const uint64_t vd0 = sdesc_v(c.sb + kSmV), vd1 = sdesc_v(c.sb + kSmV + kStageBytes);
+  // K, V and queries of the odd CTA come with a cluster-scope release
+  auto wait_pair = [&](int i, uint32_t parity) { return mbar_wait_cluster(c.bar(i), parity & 1u, c.wc, 80 + i); };
   auto wait = [&](int i, uint32_t parity) { return mbar_wait(c.bar(i), parity & 1u, c.wc, 80 + i); };
-  auto pv = [&](uint32_t n, uint32_t acc) {  // n: the tile's number in the CTA's order
-    const uint32_t ptm = c.tm + kTmemS + 128 * (n & 1);
-    if (!wait(B_VF, n) || !wait(B_PF + (n & 1), n >> 1)) return false;
+  auto qk = [&](uint32_t n) {  // n: the tile's number in the pair's order
+    if (!wait_pair(B_KF + (n & 1), n >> 1)) return false;
     tc_fence_after();
-    mma_pv_chunk(c.tm + kTmemO, ptm, vd0, acc);
-    mma_commit(c.bar(B_VE));
-    if (!wait(B_VF + 1, n)) return false;
-    tc_fence_after();
-    mma_pv_chunk(c.tm + kTmemO, ptm + 32, vd1, 1u);
-    mma_commit(c.bar(B_OD));
+    mma_qk_tile(c.tm + kTmemS + 128 * (n & 1), qd, (n & 1) ? kd1 : kd0);
+    mma_commit_pair(c.bar(B_SF + (n & 1)));
     return true;
   };
-  auto qk = [&](uint32_t n) {
-    const uint32_t stm = c.tm + kTmemS + 128 * (n & 1);
-    if (!wait(B_KF, n)) return false;
+  auto pv = [&](uint32_t n, uint32_t acc) {
+    if (!wait_pair(B_VF + (n & 1), n >> 1) || !wait(B_PF + (n & 1), n >> 1)) return false;
     tc_fence_after();
-    mma_qk_chunk(stm, qd0, kd0, 0u);
-    mma_commit(c.bar(B_KE));
-    if (!wait(B_KF + 1, n)) return false;
-    tc_fence_after();
-    mma_qk_chunk(stm, qd1, kd1, 1u);
-    mma_commit(c.bar(B_SF + (n & 1)));
+    mma_pv_tile(c.tm + kTmemO, c.tm + kTmemS + 128 * (n & 1), (n & 1) ? vd1 : vd0, acc);
+    mma_commit_pair(c.bar(B_OD + (n & 1)));
     return true;
   };
-  for (long long x = c.x0; ok && x < c.x1; ++n_seg) {
-    const Segment s = segment_at(p, tab, x, c.x1);
+  for (int x = c.x0; ok && x < c.x1; ++n_seg) {
+    const Segment s = segment_at(p, tab, c.rank, x, c.x1);
     const int nt = s.t1 - s.t0;
-    ok = wait(B_QF, n_seg) && qk(n_tile);
-    if (nt == 1) mma_commit(c.bar(B_QE));
+    ok = wait_pair(B_QF, n_seg) && qk(n_tile);
+    if (nt == 1) mma_commit_pair(c.bar(B_QE));
     // the epilogue has read the segment before's O
     ok = ok && (n_seg == 0 || wait(B_OE, n_seg - 1));
     for (int t = 1; ok && t < nt; ++t) {
       ok = qk(n_tile + t);
-      if (t == nt - 1) mma_commit(c.bar(B_QE));
+      if (t == nt - 1) mma_commit_pair(c.bar(B_QE));
       ok = ok && pv(n_tile + t - 1, t > 1);
     }
     ok = ok && pv(n_tile + nt - 1, nt > 1);
     n_tile += nt;
     x += nt;
   }
-  // nothing may be in flight when the CTA frees its TMEM
-  mma_commit(c.bar(B_DRAIN));
+  // nothing may be in flight when the CTAs free their TMEM
+  mma_commit_pair(c.bar(B_DRAIN));
   (void)mbar_wait_drain(c.bar(B_DRAIN), 0, kShDrainNs);
 }
 
-// ---- softmax.  A warp owns 32 rows as two slices of 16, one after the other,
-// read in the 16-lane TMEM shape: a thread holds rows t / 4 and t / 4 + 8 and,
-// of every eight keys, keys 2 (t % 4) and + 1, so that each scale it loads from
-// shared memory serves two rows (with one row a thread, each lane loading every
-// key's scales, those loads alone took half of the shared-memory bandwidth).
+// ---- softmax.  A warp owns 16 rows, read in the 16-lane TMEM shape: a thread
+// holds rows t / 4 and t / 4 + 8 and, of every eight keys, keys 2 (t % 4) and
+// + 1, so that each scale it loads from shared memory serves two rows.
 struct SliceRows {
   float c[2], m[2];  // the rows' factors, their references in log2 units
   float2 l[2];       // their sums, this thread's keys
@@ -503,10 +520,10 @@ __device__ __forceinline__ void scale_and_max(uint32_t (&s)[64], uint32_t ks_at,
   z1 = zb;
 }
 
-// One tile of one slice: P' over its scores.  `first`: no O to rescale yet.
-__device__ __forceinline__ bool softmax_slice(const SharedParams& p, const PreCtx& c, const ShGroup& grp, int blk0,
-                                              uint32_t stm, uint32_t otm, uint32_t sc, uint32_t valid, float fe,
-                                              bool first, uint32_t pv_before, SliceRows& r) {
+// One tile of the warp's rows: P' over its scores.  `first`: no O to rescale yet.
+__device__ __forceinline__ bool softmax_tile(const SharedParams& p, const PreCtx& c, const ShGroup& grp, int blk0,
+                                             uint32_t stm, uint32_t otm, uint32_t sc, uint32_t valid, float fe,
+                                             bool first, uint32_t n_before, SliceRows& r) {
   const int lane = threadIdx.x & 31;
   const uint32_t ks_at = sc + 8 * (lane & 3);
   uint32_t s[64];
@@ -544,7 +561,8 @@ __device__ __forceinline__ bool softmax_slice(const SharedParams& p, const PreCt
     moved |= f[i] != 1.f;
   }
   if (!first && __any_sync(kAllLanes, moved)) {
-    if (!c.wait(B_OD, pv_before)) return false;
+    // P V of the tile before (that of two tiles before came ahead of this tile's scores)
+    if (!c.wait(B_OD + (n_before & 1), n_before >> 1)) return false;
     tc_fence_after();
 #pragma unroll 1
     for (int h = 0; h < 8; ++h) {  // 32 columns
@@ -589,33 +607,33 @@ __device__ __forceinline__ bool softmax_slice(const SharedParams& p, const PreCt
 
 __device__ __forceinline__ void role_softmax(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t quad = (uint32_t)(32 * warp) << 16, slice = 16u << 16;
-  const uint32_t otm = c.tm + kTmemO + quad;
-  const int row0 = 32 * warp + (lane >> 2);  // rows row0, + 8 (slice 0), + 16, + 24 (slice 1)
+  const int quad = 32 * (warp & 3), half = warp >> 2;
+  const uint32_t lanes = (uint32_t)(quad + 16 * half) << 16;  // the warp's 16 rows
+  const int row0 = quad + 16 * half + (lane >> 2);            // this thread's: row0, row0 + 8
   uint32_t n_tile = 0, n_seg = 0;
-  for (long long x = c.x0; x < c.x1; ++n_seg) {
-    const Segment s = segment_at(p, tab, x, c.x1);
+  for (int x = c.x0; x < c.x1; ++n_seg) {
+    const Segment s = segment_at(p, tab, c.rank, x, c.x1);
     const int nt = s.t1 - s.t0;
-    SliceRows r[2];
+    SliceRows r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const int row = row0 + 8 * i;
-      r[i >> 1].m[i & 1] = -INFINITY;
-      r[i >> 1].l[i & 1] = make_float2(0.f, 0.f);
-      r[i >> 1].win_lo[i & 1] = p.W > 0 && row < s.rows ? tab.s[(s.rg * kRows + row) / p.G].w : 0;
+      r.m[i] = -INFINITY;
+      r.l[i] = make_float2(0.f, 0.f);
+      r.win_lo[i] = p.W > 0 && row < s.rows ? tab.s[(s.row0 + row) / p.G].w : 0;
     }
     int ev = -100;
     for (int t = 0; t < nt; ++t, ++n_tile) {
       const int b = n_tile & 1;
-      const uint32_t stm = c.tm + kTmemS + 128 * b + quad;
+      const uint32_t stm = c.tm + kTmemS + 128 * b + lanes;
       if (!c.wait(B_SCF + b, n_tile >> 1) || !c.wait(B_SF + b, n_tile >> 1)) return;
       tc_fence_after();
       if (t == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           int e;
           asm volatile("ld.shared.s8 %0, [%1];" : "=r"(e) : "r"(c.sb + kSmRow + (n_seg & 1) * kRows + row0 + 8 * i));
-          r[i >> 1].c[i & 1] = pow2i(e) * p.sm_scale_log2;
+          r.c[i] = pow2i(e) * p.sm_scale_log2;
         }
       }
       const uint32_t sc = c.sb + kSmScale + b * kScaleSlot;
@@ -623,96 +641,91 @@ __device__ __forceinline__ void role_softmax(const SharedParams& p, const Shared
       const int ev_t = (int)__float_as_uint(meta.y);
       const float fe = ev_t > ev ? pow2i(max(-126, ev - ev_t)) : 1.f;
       ev = ev_t;
-      const int blk0 = (s.t0 + t) * kTileBlocks;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (!softmax_slice(p, c, s.grp, blk0, stm + i * slice, otm + i * slice, sc, __float_as_uint(meta.x), fe, t == 0,
-                           n_tile - 1, r[i]))
-          return;
+      if (!softmax_tile(p, c, s.grp, (s.t0 + t) * kTileBlocks, stm, c.tm + kTmemO + lanes, sc, __float_as_uint(meta.x), fe,
+                        t == 0, n_tile - 1, r))
+        return;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(c.bar(B_PF + b));
+        c.arrive_even_tmem(B_PF + b);
         mbar_arrive(c.bar(B_SCE + b));
       }
     }
-    // The segment's partial, one row a thread, once the last P V is done.  A
-    // parity wait only tells a phase from the one before: the last tile's
-    // scores came after P V of two tiles before, so the one in between is
-    // waited for first.
-    if ((nt > 1 && !c.wait(B_OD, n_tile - 2)) || !c.wait(B_OD, n_tile - 1)) return;
+    // the segment's partial: one row a thread, the quadrant's two warps half of the dims each
+    if (!c.wait(B_OD + ((n_tile - 1) & 1), (n_tile - 1) >> 1)) return;
     tc_fence_after();
-    const int id = (int)blockIdx.x + s.j;
+    const int id = (int)(blockIdx.x >> 1) + s.j, row = quad + lane;
     const float up = pow2i(ev);
-    float4* dst = p.pre_o + (size_t)id * 64 * kRows + threadIdx.x;
+    float4* dst = p.pre_o + ((size_t)id * 64 + 32 * half) * kUnitRows + c.rank * kRows + row;
 #pragma unroll 1
-    for (int h = 0; h < 8; ++h) {
+    for (int h = 0; h < 4; ++h) {
       uint32_t o[32];
-      tmem_ld32(otm + 32 * h, o);
+      tmem_ld32(c.tm + kTmemO + 128 * half + 32 * h + ((uint32_t)quad << 16), o);
       tmem_wait_ld(o);
-      if ((int)threadIdx.x < s.rows) {
+      if (row < s.rows) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          dst[(size_t)(8 * h + e) * kRows] =
+          dst[(size_t)(8 * h + e) * kUnitRows] =
               make_float4(__uint_as_float(o[4 * e]) * up, __uint_as_float(o[4 * e + 1]) * up,
                           __uint_as_float(o[4 * e + 2]) * up, __uint_as_float(o[4 * e + 3]) * up);
       }
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(c.bar(B_OE));
+    if (lane == 0) c.arrive_even_tmem(B_OE);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = row0 + 8 * i;
-      const float2 l = r[i >> 1].l[i & 1];
-      float sum = l.x + l.y;
+    for (int i = 0; i < 2; ++i) {
+      float sum = r.l[i].x + r.l[i].y;
       sum += __shfl_xor_sync(kAllLanes, sum, 1);
       sum += __shfl_xor_sync(kAllLanes, sum, 2);
-      if ((lane & 3) == 0 && row < s.rows) p.pre_ml[(size_t)id * kRows + row] = make_float2(r[i >> 1].m[i & 1], sum);
+      if ((lane & 3) == 0 && row0 + 8 * i < s.rows)
+        p.pre_ml[(size_t)id * kUnitRows + c.rank * kRows + row0 + 8 * i] = make_float2(r.m[i], sum);
     }
     x += nt;
   }
 }
 
-__global__ void __launch_bounds__(kPreThreads, 1) prefix_kernel(const __grid_constant__ SharedParams p,
-                                                                const __grid_constant__ SharedSeqs tab) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
+    prefix_kernel(const __grid_constant__ SharedParams p, const __grid_constant__ SharedSeqs tab) {
   extern __shared__ __align__(1024) uint8_t raw[];
   PreCtx c;
   c.sb = smem_u32(raw);
-  if (c.sb & 1023u) {  // the whole CTA: nothing was started
+  if (c.sb & 1023u) {  // every thread of both CTAs: nothing was started
     if (threadIdx.x == 0) atomicCAS(p.err, 0, DEV_ERR_LAYOUT);
     return;
   }
   c.wc = WaitCtl{p.err, p.wait_ns};
-  const long long T = (long long)p.HKV * p.tiles_head;
-  c.x0 = shared_cut((int)blockIdx.x, T, p.n_cta);
-  c.x1 = shared_cut((int)blockIdx.x + 1, T, p.n_cta);
-  const int warp = threadIdx.x >> 5;
+  c.rank = (int)cluster_rank();
+  c.x0 = shared_cut((int)blockIdx.x >> 1, p.HKV * p.tiles_head, p.n_pairs);
+  c.x1 = shared_cut(((int)blockIdx.x >> 1) + 1, p.HKV * p.tiles_head, p.n_pairs);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(c.bar(B_KE), 1);
-    mbar_init(c.bar(B_VE), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(c.bar(B_KF + i), 2);
-      mbar_init(c.bar(B_VF + i), 2);
+      mbar_init(c.bar(B_KF + i), kConvWarps / 2 + 1);
+      mbar_init(c.bar(B_VF + i), kConvWarps / 2 + 1);
+      mbar_init(c.bar(B_KL + i), kConvWarps / 2);
+      mbar_init(c.bar(B_VL + i), kConvWarps / 2);
       mbar_init(c.bar(B_SF + i), 1);
-      mbar_init(c.bar(B_PF + i), kSoftWarps);
+      mbar_init(c.bar(B_PF + i), 2 * kSoftWarps);
+      mbar_init(c.bar(B_OD + i), 1);
       mbar_init(c.bar(B_SCF + i), 1);
       mbar_init(c.bar(B_SCE + i), kSoftWarps);
     }
-    mbar_init(c.bar(B_OD), 1);
-    mbar_init(c.bar(B_QF), kConvWarps);
+    mbar_init(c.bar(B_QF), kConvWarps + 1);
+    mbar_init(c.bar(B_QL), kConvWarps);
     mbar_init(c.bar(B_QE), 1);
-    mbar_init(c.bar(B_OE), kSoftWarps);
+    mbar_init(c.bar(B_OE), 2 * kSoftWarps);
     mbar_init(c.bar(B_DRAIN), 1);
     fence_mbar_init();
   }
   if (warp == kIssueWarp) {
-    tmem_alloc(c.sb + kSmTmem, 512);
-    tmem_relinquish();
+    tmem_alloc_pair(c.sb + kSmTmem, 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist before either may arrive on the other's
   tc_fence_after();
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c.tm) : "r"(c.sb + kSmTmem));
   dependents_may_start();
@@ -720,22 +733,31 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefix_kernel(const __grid_con
     more_regs<kSoftRegs>();
     role_softmax(p, tab, c);
   } else if (warp < kIssueWarp) {
-    more_regs<kConvRegs>();
+    fewer_regs<kConvRegs>();
     if (warp < kSoftWarps + kConvWarps / 2) role_convert<false>(p, tab, c);
     else role_convert<true>(p, tab, c);
   } else {
     fewer_regs<kMiscRegs>();
-    if (warp == kIssueWarp) {
-      if ((threadIdx.x & 31) == 0) role_issue(p, tab, c);
-      __syncwarp();
-    } else if (warp == kScaleWarp) {
+    if (warp == kScaleWarp) {
       role_scales(p, tab, c);
+    } else if (lane == 0) {
+      if (c.rank == 0) {
+        if (warp == kIssueWarp) role_issue(p, tab, c);
+      } else {
+        if (warp == kIssueWarp) role_forward_tiles(c, B_KL, B_KF);
+        else if (warp == kVFwdWarp) role_forward_tiles(c, B_VL, B_VF);
+        else role_forward_queries(p, tab, c);
+        // this CTA's TMEM and shared memory are in use until the pair's last product is done
+        if (warp == kIssueWarp) (void)mbar_wait_drain(c.bar(B_DRAIN), 0, kShDrainNs);
+      }
     }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // no arrival from the other CTA is still on its way
   tc_fence_after();
-  if (warp == kIssueWarp) tmem_dealloc(c.tm, 512);
+  if (warp == kIssueWarp) tmem_dealloc_pair(c.tm, 512);
 }
 
 // ====================================================================
@@ -982,16 +1004,15 @@ __global__ void __launch_bounds__(512) merge_kernel(const __grid_constant__ Shar
   const int n_own = (own.n + p.chunk - 1) / p.chunk, own0 = p.HKV * sq.z + g * n_own;
   int n_pre = 0, pre0 = 0, prow = 0;
   if (p.n_grp > 0) {
-    const int rg = (s * p.G) / kRows;
+    const int rg = (s * p.G) / kUnitRows;
     const ShGroup grp = tab.grp[rg];
     if (grp.n_blk > 0) {
-      const long long T = (long long)p.HKV * p.tiles_head;
-      const long long a = (long long)g * p.tiles_head + grp.x0;
-      const long long b = a + (grp.n_blk + kTileBlocks - 1) / kTileBlocks;
-      const int c0 = shared_cta_of(a, T, p.n_cta), c1 = shared_cta_of(b - 1, T, p.n_cta);
+      const int T = p.HKV * p.tiles_head, a = g * p.tiles_head + grp.x0;
+      const int c0 = shared_pair_of(a, T, p.n_pairs);
+      const int c1 = shared_pair_of(a + (grp.n_blk + kTileBlocks - 1) / kTileBlocks - 1, T, p.n_pairs);
       n_pre = c1 - c0 + 1;
       pre0 = c0 + g * p.n_grp + rg;
-      prow = s * p.G - rg * kRows + r;
+      prow = s * p.G - rg * kUnitRows + r;
     }
   }
   wait_for_previous();
@@ -1010,8 +1031,8 @@ __global__ void __launch_bounds__(512) merge_kernel(const __grid_constant__ Shar
   };
 #pragma unroll 4
   for (int i = 0; i < n_pre; ++i)
-    part(__ldcg(p.pre_ml + (size_t)(pre0 + i) * kRows + prow),
-         __ldcg(p.pre_o + ((size_t)(pre0 + i) * 64 + dq) * kRows + prow));
+    part(__ldcg(p.pre_ml + (size_t)(pre0 + i) * kUnitRows + prow),
+         __ldcg(p.pre_o + ((size_t)(pre0 + i) * 64 + dq) * kUnitRows + prow));
 #pragma unroll 4
   for (int i = 0; i < n_own; ++i)
     part(__ldcg(p.own_ml + (size_t)(own0 + i) * 8 + r), __ldcg(p.own_o + ((size_t)(own0 + i) * 64 + dq) * 8 + r));
@@ -1043,7 +1064,7 @@ cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, cud
   if (p.n_grp > 0 && p.tiles_head > 0) {
     if ((e = cudaFuncSetAttribute(prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem)) != cudaSuccess)
       return e;
-    prefix_kernel<<<p.n_cta, kPreThreads, kPreSmem, st>>>(p, t);
+    prefix_kernel<<<2 * p.n_pairs, kPreThreads, kPreSmem, st>>>(p, t);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = launch_after(own_kernel, own_grid, kOwnWarps * 32, p, t, st)) != cudaSuccess) return e;
   } else {

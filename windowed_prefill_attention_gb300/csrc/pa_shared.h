@@ -10,9 +10,9 @@
 namespace pa {
 
 constexpr int kShSeqs = 512;                        // sequences per launch, their table in its parameters
-constexpr int kShGroups = kShSeqs * 8 / kRows;      // row groups of one kv head at most (8 q heads a kv head)
+constexpr int kShGroups = kShSeqs * 8 / kUnitRows;  // row groups of one kv head at most (8 q heads a kv head)
 
-// Blocks of the prefix that some row of a group of 128 query rows sees: the
+// Blocks of the prefix that some row of a group of 256 query rows sees: the
 // sink run [0, sink) and the run [lo, prefix blocks).
 struct ShGroup {
   int x0;    // tiles of the head's earlier groups
@@ -41,15 +41,15 @@ struct SharedParams {
   int first_blk;           // the per-sequence pass starts at this block: prefix_blk, or 0 without a prefix pass
   int n_grp;               // row groups per kv head (0: no prefix pass)
   int tiles_head;          // 128-key tiles of all groups of one kv head
-  int n_cta;               // CTAs of the prefix pass
+  int n_pairs;             // SM pairs of the prefix pass
   int chunk;               // blocks per CTA of the per-sequence pass
   int chunks_head;         // its CTAs per kv head
   float sm_scale_log2;
   // Partials: per row the reference (log2 units) and sum of its softmax, and
   // its unnormalised output, 4 dims x rows side by side.  Prefix: the partial
-  // of CTA c for group j (head-major) is number c + j; own keys: the CTA's number.
-  float4* pre_o;           // [c + j][64][128]
-  float2* pre_ml;          // [c + j][128]
+  // of pair c for group j (head-major) is number c + j; own keys: the CTA's number.
+  float4* pre_o;           // [c + j][64][256]
+  float2* pre_ml;          // [c + j][256]
   float4* own_o;           // [cta][64][8]
   float2* own_ml;          // [cta][8]
   int* err;
@@ -69,11 +69,11 @@ PA_HD ShOwn shared_own(int n_ctx, int win_lo, int first, int S, int W) {
 }
 PA_HD int shared_win_lo(int n_ctx, int W) { return W > 0 ? imax(0, (n_ctx - 1) / kPage + 1 - W) : 0; }
 
-// The prefix pass's tiles, head-major and group-major, laid end to end are cut
-// evenly: CTA c computes tiles [c T / C, (c + 1) T / C) of T.
-PA_HD long long shared_cut(int c, long long T, int C) { return c * T / C; }
-// The CTA that computes tile x.
-PA_HD int shared_cta_of(long long x, long long T, int C) { return (int)(((x + 1) * C - 1) / T); }
+// The prefix pass's T tiles (fewer than 2^30), head-major and group-major, laid
+// end to end are cut evenly: pair c of n computes tiles [c T / n, (c + 1) T / n).
+PA_HD int shared_cut(int c, int T, int n) { return (int)((long long)c * T / n); }
+// The pair that computes tile x.
+PA_HD int shared_pair_of(int x, int T, int n) { return (int)((((long long)x + 1) * n - 1) / T); }
 
 cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, cudaStream_t st);
 
