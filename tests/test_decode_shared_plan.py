@@ -82,12 +82,15 @@ def test_every_visible_block_is_computed_once(pa, case):
     assert not done
     for (g, s0, ns), blocks in groups.items():  # a block is listed only if some sequence of the group sees it
         assert set(blocks) == union[g, s0 // (256 // (hq // hkv))]
-    if len(pre):  # one pair's tiles are consecutive, and no pair has more than its even share
+    if len(pre):  # one pair's tiles are consecutive, and the costliest pair (4 for every group after its first) is
+        # within one group's charge of the mean
         pairs = pre[:, 0]
         assert np.all(np.diff(pairs) >= 0) and pairs[0] == 0 and pairs[-1] < max(1, n_sm // 2)
-        tiles = np.zeros(pairs[-1] + 1, int)
-        np.add.at(tiles, pairs, (pre[:, 7] - pre[:, 6] + 7) // 8)
-        assert tiles.min() >= 1 and tiles.max() <= -(-tiles.sum() // len(tiles))
+        cost = np.full(pairs[-1] + 1, -4)
+        np.add.at(cost, pairs, (pre[:, 7] - pre[:, 6] + 7) // 8 + 4)
+        assert cost.min() >= 1
+        assert cost.max() <= -(-cost.sum() // max(1, n_sm // 2)) + 5 or len(cost) < max(1, n_sm // 2)
+        assert len(cost) == max(1, n_sm // 2) or cost.max() <= cost.sum() // len(cost) + 5
 
 
 def test_plan_refusals(pa):

@@ -1627,9 +1627,39 @@ int decode_shared_check(int HQ, int HKV, int max_pages, int n_seq, const pa_seq*
 
 // One launch (sequences [s0, s0 + n)) of the shared-prefix decode: its table and split.
 // The prefix pass: the rows of a kv head in groups of 256, per group the
-// blocks some row sees, in 128-key tiles; all tiles cut evenly over at most
-// n_sm / 2 SM pairs.  The per-sequence pass: chunks of equal block counts, about two
+// blocks some row sees, in 128-key tiles; all tiles, group after group, cut
+// into at most n_sm / 2 runs of equal cost, one for each SM pair.  A run costs
+// its tiles plus kShSegCost for every group after its first: the next group's
+// queries are staged and the last one's output stored while no product runs
+// (about 12000 cycles against 3000 to 4000 a tile on GB300).  The per-sequence pass: chunks of equal block counts, about two
 // CTAs per SM, four to 128 blocks each.
+constexpr int kShSegCost = 4;
+// Packs the groups (nt[j] tiles each, laid end to end) into runs of at most
+// `budget` cost; false if they take more than max_pairs.
+bool shared_pack(const int* nt, int n_groups, int budget, int max_pairs, int* cut, int& n_pairs) {
+  int c = 0, cost = 0, x = 0;
+  cut[0] = 0;
+  for (int j = 0; j < n_groups; ++j) {
+    int left = nt[j];
+    while (left > 0) {
+      const int extra = cost > 0 ? kShSegCost : 0;
+      if (cost + extra >= budget) {  // the run is full
+        if (++c >= max_pairs) return false;
+        cut[c] = x;
+        cost = 0;
+        continue;
+      }
+      const int take = std::min(left, budget - cost - extra);
+      cost += extra + take;
+      x += take;
+      left -= take;
+    }
+  }
+  n_pairs = c + 1;
+  cut[n_pairs] = x;
+  return true;
+}
+
 int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, int n, int n_prefix, int S, int W,
                         SharedParams& p, SharedSeqs& t) {
   const int G = HQ / HKV, Pb = n_prefix / kPage;
@@ -1638,6 +1668,7 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
   p.HQ = HQ;
   p.HKV = HKV;
   p.G = G;
+  p.log2_g = G == 8 ? 3 : G == 4 ? 2 : G == 2 ? 1 : 0;
   p.S = S;
   p.W = W;
   p.prefix_blk = Pb;
@@ -1657,7 +1688,29 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
   }
   // at most 16 groups of 2^23 tiles: no overflow before the test
   if ((long long)HKV * p.tiles_head >= (1ll << 30)) return PA_EINVAL;
-  p.n_pairs = std::min(std::max(1, n_sm / 2), HKV * p.tiles_head);
+  const int T = HKV * p.tiles_head, max_pairs = std::min(kShPairs, std::max(1, n_sm / 2));
+  p.n_pairs = 0;
+  if (T > 0) {
+    int nt[8 * kShGroups];
+    const int J = HKV * p.n_grp;
+    for (int j = 0; j < J; ++j) nt[j] = (t.grp[j % p.n_grp].n_blk + kTileBlocks - 1) / kTileBlocks;
+    int lo = (T + max_pairs - 1) / max_pairs, hi = T + kShSegCost * J;
+    while (lo < hi) {  // the smallest budget that packs
+      const int mid = lo + (hi - lo) / 2;
+      if (shared_pack(nt, J, mid, max_pairs, t.cut, p.n_pairs)) hi = mid;
+      else lo = mid + 1;
+    }
+    (void)shared_pack(nt, J, lo, max_pairs, t.cut, p.n_pairs);
+    int x = 0, c = 0;
+    for (int j = 0; j < J; ++j) {
+      while (c + 1 < p.n_pairs && t.cut[c + 1] <= x) ++c;
+      t.first_pair[j] = (uint8_t)c;
+      x += nt[j];
+      int e = c;
+      while (e + 1 < p.n_pairs && t.cut[e + 1] < x) ++e;
+      t.last_pair[j] = (uint8_t)e;
+    }
+  }
   long long own = 0;
   for (int s = 0; s < n; ++s) {
     const pa_seq& q = seqs[s0 + s];
@@ -1755,7 +1808,7 @@ int pa_decode_shared_plan(int n_q_heads, int n_kv_heads, int max_pages_per_seq, 
   if ((rc = decode_shared_plan(n_q_heads, n_kv_heads, n_sm, seqs, 0, std::min(n_seq, kShSeqs), n_prefix, n_sink_blk,
                                n_win_blk, p, t)))
     return rc;
-  const int T = p.HKV * p.tiles_head, per = kUnitRows / p.G;
+  const int per = kUnitRows / p.G;
   int np = 0;
   for (int g = 0; g < p.HKV; ++g)
     for (int j = 0; j < p.n_grp; ++j) {
@@ -1763,8 +1816,8 @@ int pa_decode_shared_plan(int n_q_heads, int n_kv_heads, int max_pages_per_seq, 
       const int nt = (gr.n_blk + kTileBlocks - 1) / kTileBlocks;
       const int a = g * p.tiles_head + gr.x0;
       for (int t0 = 0; t0 < nt;) {
-        const int c = shared_pair_of(a + t0, T, p.n_pairs);
-        const int t1 = std::min(nt, shared_cut(c + 1, T, p.n_pairs) - a);
+        const int c = (int)(std::upper_bound(t.cut, t.cut + p.n_pairs, a + t0) - t.cut) - 1;
+        const int t1 = std::min(nt, t.cut[c + 1] - a);
         if (prefix_out) {
           if (np >= prefix_cap) return PA_EINVAL;
           int32_t* o = prefix_out + 8 * np;

@@ -125,8 +125,8 @@ constexpr int kVFwdWarp = kIssueWarp + 2;           // warps 18, 19: odd CTA: fo
 constexpr int kQFwdWarp = kIssueWarp + 3;
 constexpr int kPreThreads = 32 * (kQFwdWarp + 1);
 // Registers a thread, of the 96 each is launched with (65536 / 640): in units
-// of a warp's, 8 x 120 + 8 x 80 + 4 x 80 = 20 x 96.
-constexpr int kSoftRegs = 120, kConvRegs = 80, kMiscRegs = 80;
+// of a warp's, 8 x 120 + 8 x 88 + 4 x 64 = 20 x 96.
+constexpr int kSoftRegs = 120, kConvRegs = 88, kMiscRegs = 64;
 static_assert(8 * kSoftRegs + 8 * kConvRegs + 4 * kMiscRegs <= 20 * 96, "register split: above it the increase waits forever");
 static_assert(kSoftRegs >= 96 && kConvRegs <= 96 && kMiscRegs <= 96, "an increase and two decreases from the launch's 96");
 
@@ -159,8 +159,9 @@ enum : int {
   B_QL = 19,   // odd: its own queries, to be forwarded
   B_QE = 20,   // both: a segment's last Q K^T is done
   B_OE = 21,   // even: a segment's O is read (every softmax warp of both)
-  B_DRAIN = 22,
-  kPreBars = 23
+  B_RAW = 22,  // the segment's raw queries are read (converter warps)
+  B_DRAIN = 23,
+  kPreBars = 24
 };
 constexpr int kSmTmem = kSmBar + kPreBars * 8;
 constexpr int kPreSmem = kSmTmem + 16;
@@ -248,52 +249,72 @@ __device__ __forceinline__ void widen16(const uint4 c, uint32_t row_addr, int ro
   sts128(at ^ 16u, h[4], h[5], h[6], h[7]);
 }
 
-template <bool kV>
+// One code for K and V warps: the kernel's instructions exceed the caches that
+// feed the schedulers, and every line of it is fetched anew for each tile.
 __device__ __forceinline__ void role_convert(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kSoftWarps;
+  const bool kv = warp >= kConvWarps / 2;  // V
   const int w = warp & 3;
   uint32_t n_tile = 0, n_seg = 0;
   const size_t tok = (size_t)p.HKV * kHeadDim;  // bytes from a token to the next
   // K: warp w the 16 keys 64 rank + 16 w on, all dims; a load takes two keys.
   // V: warp w keys 32 w on, dims 128 rank on; a load takes four keys.  Lane bit 2
   // (and 4) the key, the others the 16 bytes.
-  const int u = kV ? (lane & 3) | (lane >> 1 & 4) : (lane & 3) | (lane >> 3) << 2;
-  const int sub = kV ? (lane >> 2 & 1) | (lane >> 4) << 1 : lane >> 2 & 1;
-  constexpr int kStep = kV ? 4 : 2, kPerBlock = kPage / kStep;  // keys per load, loads per block
-  const int row0 = (kV ? 32 : 16) * w + sub;                    // the stage's row of the lane's first load
-  const uint32_t at0 = c.sb + (kV ? kSmV + (u >> 2) * 16384 : kSmK + (u >> 2) * 8192) + row0 * 128;
-  const int blk0 = kV ? 2 * w : 4 * c.rank + w;                 // first block of the tile it loads
-  const int8_t* base = (kV ? p.v_pool + 128 * c.rank : p.k_pool) + 16 * u + (size_t)sub * tok;
+  const int u = kv ? (lane & 3) | (lane >> 1 & 4) : (lane & 3) | (lane >> 3) << 2;
+  const int sub = kv ? (lane >> 2 & 1) | (lane >> 4) << 1 : lane >> 2 & 1;
+  const int step = kv ? 4 : 2;                                  // keys per load
+  const int row0 = (kv ? 32 : 16) * w + sub;                    // the stage's row of the lane's first load
+  const uint32_t at0 = c.sb + (kv ? kSmV + (u >> 2) * 16384 : kSmK + (u >> 2) * 8192) + row0 * 128;
+  const int blk0 = kv ? 2 * w : 4 * c.rank + w;                 // first block of the tile it loads
+  const size_t step_b = step * tok, half_b = kv ? 0 : 8 * tok;  // from a load to the next; from load 0 to load 4
+  const int blk4 = kv ? blk0 + 1 : blk0;                        // block of load 4
+  const int8_t* base = (kv ? p.v_pool + 128 * c.rank : p.k_pool) + 16 * u + (size_t)sub * tok;
   for (int x = c.x0; x < c.x1; ++n_seg) {
     const Segment s = segment_at(p, tab, c.rank, x, c.x1);
     const int8_t* src = base + (size_t)s.g * kHeadDim;
     // pages of the segment's blocks, 32 (four tiles) at a time, one per lane
     const int b0 = s.t0 * kTileBlocks;
     int pg = group_page(p, s.grp, b0 + lane), pg_next = group_page(p, s.grp, b0 + 32 + lane);
+    // The CTA's queries, 16 rows a warp, copied as they are into the K stages
+    // (free: the segment before's last Q K^T is done), all in flight together,
+    // then widened row by row in a loop that is short for the same reason.
+    if (n_seg > 0 && !c.wait(B_QE, n_seg - 1)) return;
+    const uint32_t rowc = c.sb + kSmRow + (n_seg & 1) * kRows;
+    const uint32_t raw = c.sb + kSmK + warp * (16 * kHeadDim * 2) + 16 * lane;
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      const int row = kConvWarps * i + warp;
+      if (row < s.rows) {
+        const int rr = s.row0 + row;
+        const __nv_bfloat16* q = p.q + ((size_t)tab.s[rr >> p.log2_g].x * p.HQ + (size_t)s.g * p.G + (rr & (p.G - 1))) * kHeadDim;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(raw + i * (kHeadDim * 2)), "l"(q + 8 * lane) : "memory");
+      }
+    }
     uint4 r[8];
     // a block past the list or of a bad page loads page 0's codes: whatever finite values they widen to,
     // the softmax gives those keys no weight
     auto load = [&](int t4) {
+      const int pa = max(0, __shfl_sync(kAllLanes, pg, t4 * kTileBlocks + blk0));
+      const int pb = max(0, __shfl_sync(kAllLanes, pg, t4 * kTileBlocks + blk4));
+      const int8_t* a = src + (size_t)pa * (kPage * tok);
+      const int8_t* b = src + (size_t)pb * (kPage * tok) + half_b;
 #pragma unroll
-      for (int b = 0; b < 8 / kPerBlock; ++b) {
-        const int page = max(0, __shfl_sync(kAllLanes, pg, t4 * kTileBlocks + blk0 + b));
-        const int8_t* at = src + (size_t)page * (kPage * tok);
+      for (int n = 0; n < 4; ++n, a += step_b) r[n] = ldg_stream(a);
 #pragma unroll
-        for (int n = 0; n < kPerBlock; ++n, at += kStep * tok) r[b * kPerBlock + n] = ldg_stream(at);
-      }
+      for (int n = 4; n < 8; ++n, b += step_b) r[n] = ldg_stream(b);
     };
     load(0);
-    // the CTA's queries: a warp takes a row at a time
-    if (n_seg > 0 && !c.wait(B_QE, n_seg - 1)) return;
-    const uint32_t rowc = c.sb + kSmRow + (n_seg & 1) * kRows;
-    for (int row = warp; row < kRows; row += kConvWarps) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      const int row = kConvWarps * i + warp;
       float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
-      if (row < s.rows) {
-        const int rr = s.row0 + row;
-        const int4 sq = tab.s[rr / p.G];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(p.q + ((size_t)sq.x * p.HQ + (size_t)s.g * p.G + rr % p.G) * kHeadDim) + lane), v);
+      {
+        const float4 f = lds_f32x4(raw + i * (kHeadDim * 2));
+        const bool in = row < s.rows;
+        unpack8(make_uint4(in ? __float_as_uint(f.x) : 0, in ? __float_as_uint(f.y) : 0, in ? __float_as_uint(f.z) : 0,
+                           in ? __float_as_uint(f.w) : 0), v);
       }
       float am = 0.f;
 #pragma unroll
@@ -309,7 +330,12 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
     }
     fence_proxy_async_shared();
     __syncwarp();
-    if (lane == 0) mbar_arrive(c.bar(c.rank == 0 ? B_QF : B_QL));
+    if (lane == 0) {
+      mbar_arrive(c.bar(c.rank == 0 ? B_QF : B_QL));
+      mbar_arrive(c.bar(B_RAW));
+    }
+    // every warp has read its raw rows: the K stages may be written
+    if (!c.wait(B_RAW, n_seg)) return;
 
     const int nt = s.t1 - s.t0;
     for (int t = 0; t < nt; ++t, ++n_tile) {
@@ -319,12 +345,12 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
       }
       // the stage's products of two tiles before are done
       const int st = n_tile & 1;
-      if (n_tile > 1 && !c.wait((kV ? B_OD : B_SF) + st, (n_tile >> 1) - 1)) return;
+      if (n_tile > 1 && !c.wait((kv ? B_OD : B_SF) + st, (n_tile >> 1) - 1)) return;
 #pragma unroll
-      for (int n = 0; n < 8; ++n) widen16(r[n], at0 + st * kStageBytes + kStep * n * 128, row0 + kStep * n, u);
+      for (int n = 0; n < 8; ++n) widen16(r[n], at0 + st * kStageBytes + step * n * 128, row0 + step * n, u);
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(c.bar((kV ? (c.rank == 0 ? B_VF : B_VL) : (c.rank == 0 ? B_KF : B_KL)) + st));
+      if (lane == 0) mbar_arrive(c.bar((kv ? (c.rank == 0 ? B_VF : B_VL) : (c.rank == 0 ? B_KF : B_KL)) + st));
       if (t + 1 < nt) load((t + 1) & 3);
     }
     x += nt;
@@ -620,7 +646,7 @@ __device__ __forceinline__ void role_softmax(const SharedParams& p, const Shared
       const int row = row0 + 8 * i;
       r.m[i] = -INFINITY;
       r.l[i] = make_float2(0.f, 0.f);
-      r.win_lo[i] = p.W > 0 && row < s.rows ? tab.s[(s.row0 + row) / p.G].w : 0;
+      r.win_lo[i] = p.W > 0 && row < s.rows ? tab.s[(s.row0 + row) >> p.log2_g].w : 0;
     }
     int ev = -100;
     for (int t = 0; t < nt; ++t, ++n_tile) {
@@ -697,8 +723,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
   }
   c.wc = WaitCtl{p.err, p.wait_ns};
   c.rank = (int)cluster_rank();
-  c.x0 = shared_cut((int)blockIdx.x >> 1, p.HKV * p.tiles_head, p.n_pairs);
-  c.x1 = shared_cut(((int)blockIdx.x >> 1) + 1, p.HKV * p.tiles_head, p.n_pairs);
+  c.x0 = tab.cut[blockIdx.x >> 1];
+  c.x1 = tab.cut[(blockIdx.x >> 1) + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -714,6 +740,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
     }
     mbar_init(c.bar(B_QF), kConvWarps + 1);
     mbar_init(c.bar(B_QL), kConvWarps);
+    mbar_init(c.bar(B_RAW), kConvWarps);
     mbar_init(c.bar(B_QE), 1);
     mbar_init(c.bar(B_OE), 2 * kSoftWarps);
     mbar_init(c.bar(B_DRAIN), 1);
@@ -734,8 +761,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
     role_softmax(p, tab, c);
   } else if (warp < kIssueWarp) {
     fewer_regs<kConvRegs>();
-    if (warp < kSoftWarps + kConvWarps / 2) role_convert<false>(p, tab, c);
-    else role_convert<true>(p, tab, c);
+    role_convert(p, tab, c);
   } else {
     fewer_regs<kMiscRegs>();
     if (warp == kScaleWarp) {
@@ -848,28 +874,47 @@ __global__ void __launch_bounds__(kOwnWarps * 32) own_kernel(const __grid_consta
 #pragma unroll
   for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   const size_t tok = (size_t)p.HKV * kHeadDim;
-  for (int it = 0; b0 + warp + kOwnWarps * it < b1; ++it) {
-    const int b = b0 + warp + kOwnWarps * it;
-    const int phys = __shfl_sync(kAllLanes, page, it);
-    if (phys < 0) continue;
-    const int8_t* kp = p.k_pool + (size_t)phys * kPage * tok + (size_t)g * kHeadDim;
-    const int8_t* vp = p.v_pool + (size_t)phys * kPage * tok + (size_t)g * kHeadDim;
-    // K: rows gq and gq + 8, dims 64 j + 16 tq; V: keys 2tq, 2tq+1, 2tq+8, 2tq+9, dims 32 gq
-    uint4 kr[4][2], vr[2][4];
-    const int key[4] = {2 * tq, 2 * tq + 1, 2 * tq + 8, 2 * tq + 9};
+  // K: rows gq and gq + 8, dims 64 j + 16 tq; V: keys 2tq, 2tq+1, 2tq+8, 2tq+9,
+  // dims 32 gq.  The next block's K is loaded as soon as this block's scores are
+  // done with the registers, its V after this block's products: a block's loads
+  // are in flight during the other half of the work.
+  uint4 kr[4][2], vr[2][4];
+  float ks0 = 0.f, ks1 = 0.f, vr0 = 0.f, vr1 = 0.f;
+  const int n_it = b1 > b0 + warp ? (b1 - b0 - warp + kOwnWarps - 1) / kOwnWarps : 0;
+  // a block of a bad page (skipped below) loads page 0
+  auto page_of = [&](int it) { return max(0, __shfl_sync(kAllLanes, page, it)); };
+  auto load_k = [&](int it) {
+    const int phys = page_of(it);
+    const int8_t* kp = p.k_pool + (size_t)phys * kPage * tok + (size_t)g * kHeadDim + 16 * tq;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      kr[j][0] = ldg_stream(kp + (size_t)gq * tok + 64 * j + 16 * tq);
-      kr[j][1] = ldg_stream(kp + (size_t)(gq + 8) * tok + 64 * j + 16 * tq);
+      kr[j][0] = ldg_stream(kp + (size_t)gq * tok + 64 * j);
+      kr[j][1] = ldg_stream(kp + (size_t)(gq + 8) * tok + 64 * j);
     }
+    const size_t s0 = ((size_t)phys * kPage + gq) * p.HKV + g;
+    ks0 = __ldg(p.k_scale + s0);
+    ks1 = __ldg(p.k_scale + s0 + 8 * (size_t)p.HKV);
+  };
+  auto load_v = [&](int it) {
+    const int phys = page_of(it);
+    const int8_t* vp = p.v_pool + (size_t)phys * kPage * tok + (size_t)g * kHeadDim + 32 * gq;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      vr[0][k] = __ldg(reinterpret_cast<const uint4*>(vp + (size_t)key[k] * tok + 32 * gq));
-      vr[1][k] = __ldg(reinterpret_cast<const uint4*>(vp + (size_t)key[k] * tok + 32 * gq + 16));
+      const int8_t* at = vp + (size_t)(2 * tq + (k & 1) + 8 * (k >> 1)) * tok;
+      vr[0][k] = __ldg(reinterpret_cast<const uint4*>(at));
+      vr[1][k] = __ldg(reinterpret_cast<const uint4*>(at + 16));
     }
-    const size_t s0 = ((size_t)phys * kPage + gq) * p.HKV + g, s1 = s0 + 8 * (size_t)p.HKV;
-    const float ks0 = __ldg(p.k_scale + s0), ks1 = __ldg(p.k_scale + s1);
-    const float vr0 = __ldg(p.v_scale + s0), vr1 = __ldg(p.v_scale + s1);
+    const size_t s0 = ((size_t)phys * kPage + gq) * p.HKV + g;
+    vr0 = __ldg(p.v_scale + s0);
+    vr1 = __ldg(p.v_scale + s0 + 8 * (size_t)p.HKV);
+  };
+  if (n_it > 0) {
+    load_k(0);
+    load_v(0);
+  }
+  for (int it = 0; it < n_it; ++it) {
+    const int b = b0 + warp + kOwnWarps * it;
+    const bool good = __shfl_sync(kAllLanes, page, it) >= 0;
     float sacc[4][4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) sacc[m][0] = sacc[m][1] = sacc[m][2] = sacc[m][3] = 0.f;
@@ -889,9 +934,10 @@ __global__ void __launch_bounds__(kOwnWarps * 32) own_kernel(const __grid_consta
 #pragma unroll
     for (int e = 0; e < 4; ++e) sc[e] = (sacc[0][e] + sacc[1][e]) + (sacc[2][e] + sacc[3][e]);
     const int lb = block_of(b);
-    const bool v0 = lb * kPage + gq <= t, v1 = lb * kPage + gq + 8 <= t;
+    const bool v0 = good && lb * kPage + gq <= t, v1 = good && lb * kPage + gq + 8 <= t;
     const float y0 = v0 ? sc[0] * ks0 * c_lo : -INFINITY, y1 = v0 ? sc[1] * ks0 * c_hi : -INFINITY;
     const float y2 = v1 ? sc[2] * ks1 * c_lo : -INFINITY, y3 = v1 ? sc[3] * ks1 * c_hi : -INFINITY;
+    if (it + 1 < n_it) load_k(it + 1);
     float bm_lo = fmaxf(y0, y2), bm_hi = fmaxf(y1, y3);
     float bv = fmaxf(v0 ? vr0 : 0.f, v1 ? vr1 : 0.f);
 #pragma unroll
@@ -900,15 +946,16 @@ __global__ void __launch_bounds__(kOwnWarps * 32) own_kernel(const __grid_consta
       bm_hi = fmaxf(bm_hi, __shfl_xor_sync(kAllLanes, bm_hi, sh));
       bv = fmaxf(bv, __shfl_xor_sync(kAllLanes, bv, sh));
     }
-    const float mn_lo = fmaxf(m_lo, bm_lo), mn_hi = fmaxf(m_hi, bm_hi);  // finite: key 0 of a block is visible
+    const float mn_lo = fmaxf(m_lo, bm_lo), mn_hi = fmaxf(m_hi, bm_hi);  // -inf only while every page was bad
+    const float ml = mn_lo == -INFINITY ? 0.f : mn_lo, mh = mn_hi == -INFINITY ? 0.f : mn_hi;
     const int ev_n = max(ev, exp_above(bv));
     const float vfix = ev_n > ev ? (ev_n - ev > 126 ? 0.f : pow2i(ev - ev_n)) : 1.f;
     ev = ev_n;
     const float vnorm = pow2i(-ev);
-    const float al_lo = ex2f(m_lo - mn_lo), al_hi = ex2f(m_hi - mn_hi);
+    const float al_lo = ex2f(m_lo - ml), al_hi = ex2f(m_hi - mh);
     m_lo = mn_lo;
     m_hi = mn_hi;
-    const float p0 = ex2f(y0 - mn_lo), p1 = ex2f(y1 - mn_hi), p2 = ex2f(y2 - mn_lo), p3 = ex2f(y3 - mn_hi);
+    const float p0 = ex2f(y0 - ml), p1 = ex2f(y1 - mh), p2 = ex2f(y2 - ml), p3 = ex2f(y3 - mh);
     l_lo = l_lo * al_lo + (p0 + p2);
     l_hi = l_hi * al_hi + (p1 + p3);
     if (__any_sync(kAllLanes, al_lo != 1.f || al_hi != 1.f || vfix != 1.f)) {
@@ -943,6 +990,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32) own_kernel(const __grid_consta
         mma16816(o[2 * i + 1], a1, pb0, pb1);
       }
     }
+    if (it + 1 < n_it) load_v(it + 1);
   }
 #pragma unroll
   for (int sh = 4; sh < 32; sh <<= 1) {
@@ -994,11 +1042,20 @@ __global__ void __launch_bounds__(kOwnWarps * 32) own_kernel(const __grid_consta
 // ====================================================================
 // Merge
 // ====================================================================
-// CTA = (sequence, kv head); thread (row i % G, dims 4 (i / G)).
-__global__ void __launch_bounds__(512) merge_kernel(const __grid_constant__ SharedParams p,
-                                                    const __grid_constant__ SharedSeqs tab) {
+// CTA = (sequence, kv head, 64 of the dims); thread (row i % G, dims 4 (i / G %
+// 16), every kMergeWays-th partial from i / (16 G) on), then the ways' parts
+// through shared memory in a fixed order.  Bound by the latency of the partials'
+// loads: the ways and four loads a thread keep them in flight together.
+constexpr int kMergeWays = 8;
+constexpr int kMergeDims = 64;
+
+__global__ void __launch_bounds__(8 * 16 * kMergeWays) merge_kernel(const __grid_constant__ SharedParams p,
+                                                                    const __grid_constant__ SharedSeqs tab) {
+  __shared__ float4 acc_sh[kMergeWays - 1][16 * 8];
+  __shared__ float2 ml_sh[kMergeWays - 1][16 * 8];
   const int s = blockIdx.x / p.HKV, g = blockIdx.x % p.HKV;
-  const int r = threadIdx.x % p.G, dq = threadIdx.x / p.G;
+  const int slot = threadIdx.x % (16 * p.G), way = threadIdx.x / (16 * p.G);
+  const int r = slot & (p.G - 1), dq = blockIdx.y * (kMergeDims / 4) + (slot >> p.log2_g);
   const int4 sq = tab.s[s];
   const ShOwn own = shared_own(sq.y, sq.w, p.first_blk, p.S, p.W);
   const int n_own = (own.n + p.chunk - 1) / p.chunk, own0 = p.HKV * sq.z + g * n_own;
@@ -1007,18 +1064,22 @@ __global__ void __launch_bounds__(512) merge_kernel(const __grid_constant__ Shar
     const int rg = (s * p.G) / kUnitRows;
     const ShGroup grp = tab.grp[rg];
     if (grp.n_blk > 0) {
-      const int T = p.HKV * p.tiles_head, a = g * p.tiles_head + grp.x0;
-      const int c0 = shared_pair_of(a, T, p.n_pairs);
-      const int c1 = shared_pair_of(a + (grp.n_blk + kTileBlocks - 1) / kTileBlocks - 1, T, p.n_pairs);
+      const int c0 = tab.first_pair[g * p.n_grp + rg], c1 = tab.last_pair[g * p.n_grp + rg];
       n_pre = c1 - c0 + 1;
       pre0 = c0 + g * p.n_grp + rg;
       prow = s * p.G - rg * kUnitRows + r;
     }
   }
+  // partial i of the row: the prefix's, then its own keys'
+  const int n = n_pre + n_own;
+  const float2* pm = p.pre_ml + (size_t)pre0 * kUnitRows + prow;
+  const float4* po = p.pre_o + ((size_t)pre0 * 64 + dq) * kUnitRows + prow;
+  const float2* om = p.own_ml + (size_t)own0 * 8 + r;
+  const float4* oo = p.own_o + ((size_t)own0 * 64 + dq) * 8 + r;
   wait_for_previous();
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto part = [&](const float2 ml, const float4 v) {
+  auto add = [&](const float2 ml, const float4 v) {
     if (ml.x == -INFINITY) return;  // no visible key
     const float mn = fmaxf(m, ml.x);
     const float f = m == -INFINITY ? 0.f : ex2f(m - mn), w = ex2f(ml.x - mn);
@@ -1029,13 +1090,33 @@ __global__ void __launch_bounds__(512) merge_kernel(const __grid_constant__ Shar
     acc.z = fmaf(w, v.z, acc.z * f);
     acc.w = fmaf(w, v.w, acc.w * f);
   };
-#pragma unroll 4
-  for (int i = 0; i < n_pre; ++i)
-    part(__ldcg(p.pre_ml + (size_t)(pre0 + i) * kUnitRows + prow),
-         __ldcg(p.pre_o + ((size_t)(pre0 + i) * 64 + dq) * kUnitRows + prow));
-#pragma unroll 4
-  for (int i = 0; i < n_own; ++i)
-    part(__ldcg(p.own_ml + (size_t)(own0 + i) * 8 + r), __ldcg(p.own_o + ((size_t)(own0 + i) * 64 + dq) * 8 + r));
+  for (int i0 = way; i0 < n; i0 += 4 * kMergeWays) {
+    float2 ml[4];
+    float4 v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + e * kMergeWays;
+      ml[e] = make_float2(-INFINITY, 0.f);
+      v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n_pre) {
+        ml[e] = __ldcg(pm + (size_t)i * kUnitRows);
+        v[e] = __ldcg(po + (size_t)i * 64 * kUnitRows);
+      } else if (i < n) {
+        ml[e] = __ldcg(om + (size_t)(i - n_pre) * 8);
+        v[e] = __ldcg(oo + (size_t)(i - n_pre) * 64 * 8);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) add(ml[e], v[e]);
+  }
+  if (way > 0) {
+    acc_sh[way - 1][slot] = acc;
+    ml_sh[way - 1][slot] = make_float2(m, l);
+  }
+  __syncthreads();
+  if (way > 0) return;
+#pragma unroll
+  for (int w = 0; w < kMergeWays - 1; ++w) add(ml_sh[w][slot], acc_sh[w][slot]);
   const float il = l > 0.f ? 1.f / l : 0.f;
   const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * il, acc.y * il), b = __floats2bfloat162_rn(acc.z * il, acc.w * il);
   *reinterpret_cast<uint2*>(p.out + ((size_t)sq.x * p.HQ + (size_t)g * p.G + r) * kHeadDim + 4 * dq) =
@@ -1043,9 +1124,9 @@ __global__ void __launch_bounds__(512) merge_kernel(const __grid_constant__ Shar
 }
 
 template <typename K>
-cudaError_t launch_after(K* kernel, int grid, int threads, const SharedParams& p, const SharedSeqs& t, cudaStream_t st) {
+cudaError_t launch_after(K* kernel, dim3 grid, int threads, const SharedParams& p, const SharedSeqs& t, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = st;
   cudaLaunchAttribute at{};
@@ -1066,12 +1147,12 @@ cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, cud
       return e;
     prefix_kernel<<<2 * p.n_pairs, kPreThreads, kPreSmem, st>>>(p, t);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_after(own_kernel, own_grid, kOwnWarps * 32, p, t, st)) != cudaSuccess) return e;
+    if ((e = launch_after(own_kernel, dim3((unsigned)own_grid), kOwnWarps * 32, p, t, st)) != cudaSuccess) return e;
   } else {
     own_kernel<<<own_grid, kOwnWarps * 32, 0, st>>>(p, t);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  return launch_after(merge_kernel, p.n_seq * p.HKV, p.G * 64, p, t, st);
+  return launch_after(merge_kernel, dim3((unsigned)(p.n_seq * p.HKV), kHeadDim / kMergeDims), 16 * p.G * kMergeWays, p, t, st);
 }
 
 }  // namespace pa

@@ -21,10 +21,17 @@ struct ShGroup {
   int n_blk; // sink + prefix blocks - lo
 };
 
+constexpr int kShPairs = 128;  // SM pairs of a launch at most
+
 struct SharedSeqs {
   // {row in q / out, context length, chunks of the earlier sequences (per kv head), first block of its window}
   int4 s[kShSeqs];
   ShGroup grp[kShGroups];
+  // The prefix pass's tiles (fewer than 2^30), head-major and group-major, laid
+  // end to end: pair c computes tiles [cut[c], cut[c + 1]); group j (head-major)
+  // lies in pairs first_pair[j] .. last_pair[j].
+  int cut[kShPairs + 1];
+  uint8_t first_pair[8 * kShGroups], last_pair[8 * kShGroups];
 };
 
 struct SharedParams {
@@ -37,6 +44,7 @@ struct SharedParams {
   const int32_t* block_table;
   int bt_stride, n_pool, bt_row0;
   int n_seq, HQ, HKV, G, S, W;
+  int log2_g;              // G = q heads per kv head is 1, 2, 4 or 8
   int prefix_blk;          // blocks of the shared prefix; their pages are block_table row 0's
   int first_blk;           // the per-sequence pass starts at this block: prefix_blk, or 0 without a prefix pass
   int n_grp;               // row groups per kv head (0: no prefix pass)
@@ -68,12 +76,6 @@ PA_HD ShOwn shared_own(int n_ctx, int win_lo, int first, int S, int W) {
   return o;
 }
 PA_HD int shared_win_lo(int n_ctx, int W) { return W > 0 ? imax(0, (n_ctx - 1) / kPage + 1 - W) : 0; }
-
-// The prefix pass's T tiles (fewer than 2^30), head-major and group-major, laid
-// end to end are cut evenly: pair c of n computes tiles [c T / n, (c + 1) T / n).
-PA_HD int shared_cut(int c, int T, int n) { return (int)((long long)c * T / n); }
-// The pair that computes tile x.
-PA_HD int shared_pair_of(int x, int T, int n) { return (int)((((long long)x + 1) * n - 1) / T); }
 
 cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, cudaStream_t st);
 
