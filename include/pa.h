@@ -218,11 +218,13 @@ typedef struct {
   uint8_t axis[128];  /* pair i: the axis whose position turns it */
 } pa_rope;
 
-/* bf16 rows [token][head][256] in device memory: strides in elements, each a
+/* bf16 rows [n_tok][head][256] in device memory: strides in elements, each a
  * multiple of 8 and >= 0; the 256 values of a row are contiguous; data 16-byte
- * aligned.  So the rows may be slices of one fused projection buffer. */
+ * aligned.  So the rows may be slices of one fused projection buffer.  A call
+ * that would read past n_tok tokens is PA_EINVAL. */
 typedef struct {
   const void* data;
+  long long n_tok;
   long long tok_stride;
   long long head_stride;
 } pa_rows;
@@ -324,6 +326,7 @@ int pa_decode_plan(int n_kv_heads, int slots, int n_seq, const pa_seq* seqs, int
  * sums and the roundings of P' to fp16.
  *   block_table   row s holds sequence s's pages; the prefix's pages are those
  *                 of row 0, and the other rows' entries for it are not read
+ *   n_rows        rows of q and out; a sequence's row outside them is PA_EINVAL
  *   others        as pa_decode; sequences must not share a row of q / out (PA_EINVAL)
  * A prefix page outside the pool is skipped for all sequences, one of a
  * sequence's own pages for that sequence (PA_EBADPAGE through pa_last_error).
@@ -333,8 +336,8 @@ int pa_decode_plan(int n_kv_heads, int slots, int n_seq, const pa_seq* seqs, int
  * capturing stream that would have to grow them returns PA_ENOMEM (make a call
  * of that size before the capture).  They are freed with the handle only, so a
  * graph stays valid while its handle lives. */
-int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, const void* q, const int8_t* k_pool,
-                     const int8_t* v_pool, const float* k_scale, const float* v_scale, const int32_t* block_table,
+int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, int n_rows, const void* q,
+                     const int8_t* k_pool, const int8_t* v_pool, const float* k_scale, const float* v_scale, const int32_t* block_table,
                      int n_sink_blk, int n_win_blk, float sm_scale, void* out, void* stream);
 
 /* Host-only, no GPU needed: how pa_decode_shared splits the work of one launch

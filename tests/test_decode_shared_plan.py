@@ -117,5 +117,5 @@ def test_plan_refusals(pa):
 
 
 def test_null_handle_is_refused(pa):
-    assert pa._lib.pa_decode_shared(None, 1, pa._seqs([(0, 99, 1, 100)]), 64, *[None] * 6, 1, 0, 0.1, None,
+    assert pa._lib.pa_decode_shared(None, 1, pa._seqs([(0, 99, 1, 100)]), 64, 1, *[None] * 6, 1, 0, 0.1, None,
                                     None) == pa.PA_EINVAL

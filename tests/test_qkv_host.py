@@ -56,8 +56,8 @@ def test_rope_init_refuses(pa):
     assert pa._lib.pa_rope_init(None, 0, 0, 1, None, None) == pa.PA_EINVAL
 
 
-def rows(pa, data, ts, hs):
-    return C.byref(pa.pa_rows(data, ts, hs))
+def rows(pa, data, ts, hs, n_tok=10):
+    return C.byref(pa.pa_rows(data, n_tok, ts, hs))
 
 
 # addresses only: the checks read no memory behind them
@@ -80,6 +80,7 @@ def test_norm_rope_argument_checks(pa):
     no = lambda **k: rope_args(pa, **k) == pa.PA_EINVAL      # noqa: E731
     assert ok()
     assert ok(n=0, q=None)                                    # nothing to do
+    assert no(n=11, ps=11) and ok(n=9)                        # past the rows there are
     assert ok(q=None, qo=None) and ok(k=None, ko=None)
     assert no(q=None) and no(k=None) and no(q=None, qo=None, k=None, ko=None) and no(qo=None) and no(ko=None)
     assert no(n=-1) and no(n=2 ** 30 + 1)
@@ -133,8 +134,9 @@ def test_append_argument_checks(pa):
     assert no(seqs=[(0, 5, 4, 8)])                                     # past its own context
     assert ok(seqs=[(0, 60, 4, 64)]) and no(seqs=[(0, 60, 5, 65)])     # past max_pages_per_seq pages
     assert no(seqs=[(2 ** 30 - 1, 0, 3, 3)])
+    assert no(seqs=[(0, 5, 3, 8), (4, 0, 7, 7)]) and no(v=(B + (1 << 20), 512, 256, 9))  # past the rows there are
     assert no(seqs=[(0, 5, 3, 8), (2, 0, 7, 7)])                       # a row of two sequences
-    assert no(seqs=[(6, 0, 7, 7), (0, 5, 7, 12)]) and ok(seqs=[(7, 0, 7, 7), (0, 5, 7, 12)])
+    assert no(seqs=[(4, 0, 6, 6), (0, 5, 5, 10)]) and ok(seqs=[(5, 0, 5, 5), (0, 5, 5, 10)])
     assert no(qo=B) and no(qo=B + (1 << 20)) and ok(qo=A) and no(qo=A, q=(A, 9216, 256))
     two = pa.pa_rope_init(np.ones(32), pair_axis=np.arange(32) % 2)
     assert ok(rope=two, pos=1 << 20, ps=10) and no(rope=two, pos=1 << 20, ps=9)

@@ -54,7 +54,8 @@ class pa_rope(C.Structure):
 
 
 class pa_rows(C.Structure):
-    _fields_ = [("data", C.c_void_p), ("tok_stride", C.c_longlong), ("head_stride", C.c_longlong)]
+    _fields_ = [("data", C.c_void_p), ("n_tok", C.c_longlong), ("tok_stride", C.c_longlong),
+                ("head_stride", C.c_longlong)]
 
 
 _vp, _i, _f = C.c_void_p, C.c_int, C.c_float
@@ -72,12 +73,12 @@ _ll = C.c_longlong
 _lib.pa_rope_init.argtypes = [C.POINTER(pa_rope), _i, _i, _i, _vp, _vp]
 _lib.pa_qk_norm_rope.argtypes = [_vp, _i, C.POINTER(pa_rows), C.POINTER(pa_rows), _vp, _vp, _f, _f, C.POINTER(pa_rope),
                                  _vp, _ll, _vp, _vp, _vp]
-_lib.pa_qkv_append.argtypes = ([_vp, _i, C.POINTER(pa_seq)] + [C.POINTER(pa_rows)] * 3
+_lib.pa_qkv_append.argtypes = ([_vp, _i, _vp] + [C.POINTER(pa_rows)] * 3
                                + [_vp, _vp, _f, _f, C.POINTER(pa_rope), _vp, _ll] + [_vp] * 7)
 _lib.pa_debug_qk_norm_rope_check.argtypes = [_i, _i] + _lib.pa_qk_norm_rope.argtypes[1:-1]
 _lib.pa_debug_qkv_append_check.argtypes = [_i, _i, _i] + _lib.pa_qkv_append.argtypes[1:-1]
 _lib.pa_decode.argtypes = _lib.pa_prefill_batch.argtypes
-_lib.pa_decode_shared.argtypes = [_vp, _i, C.POINTER(pa_seq), _i] + [_vp] * 6 + [_i, _i, _f, _vp, _vp]
+_lib.pa_decode_shared.argtypes = [_vp, _i, _vp, _i, _i] + [_vp] * 6 + [_i, _i, _f, _vp, _vp]
 _lib.pa_decode_shared_plan.argtypes = ([_i] * 5 + [C.POINTER(pa_seq)] + [_i] * 3
                                        + [_vp, _i, C.POINTER(_i), _vp, _i, C.POINTER(_i)])
 _lib.pa_last_error.argtypes = [_vp, _vp]
@@ -153,16 +154,30 @@ def _stream(stream):
     return C.c_void_p(stream.cuda_stream)
 
 
+_torch_names = None
+
+
 def _torch():
-    import torch
-    return torch
+    """(bfloat16, float32, int8, int32, current raw stream of a device index): looked up once, since the calls of
+    a single decode step cost more on the host than on the GPU."""
+    global _torch_names
+    if _torch_names is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _torch_names = (torch.bfloat16, torch.float32, torch.int8, torch.int32, raw)
+    return _torch_names
 
 
-def _stream_of(t, stream):
-    """The given stream, or the current one of the tensor's device."""
-    if stream is None:
-        stream = _torch().cuda.current_stream(t.device)
-    return C.c_void_p(stream.cuda_stream)
+def _seq_array(seqs):
+    """Sequences as the library reads them, and their number: an int32 array [n, 4] is taken as it is."""
+    if not (type(seqs) is np.ndarray and seqs.dtype == np.int32 and seqs.ndim == 2 and seqs.shape[1] == 4
+            and seqs.flags.c_contiguous):
+        wide = np.asarray(seqs, dtype=np.int64).reshape(-1, 4)
+        seqs = np.ascontiguousarray(wide, dtype=np.int32)
+        if not np.array_equal(seqs, wide):
+            raise ValueError("sequence fields must fit int32")
+    return seqs, seqs.shape[0]
 
 
 def pa_default_options() -> pa_options:
@@ -176,10 +191,10 @@ _geometry = {}
 
 
 def _geometry_of(h):
-    g = _geometry.get(h.value) if isinstance(h, C.c_void_p) else None
-    if g is None:
-        raise ValueError("not a live handle")
-    return g
+    try:
+        return _geometry[h.value]
+    except (AttributeError, KeyError):
+        raise ValueError("not a live handle") from None
 
 
 def pa_create(n_q_heads, n_kv_heads, n_pool_pages, max_pages_per_seq, head_dim=256, page_size=16,
@@ -241,18 +256,17 @@ def pa_decode(h, seqs, q, k_pool, v_pool, k_scale, v_scale, block_table, n_sink_
 
 def pa_decode_shared(h, seqs, n_prefix, q, k_pool, v_pool, k_scale, v_scale, block_table, n_sink_blk, n_win_blk,
                      sm_scale, out, stream=None) -> None:
-    """pa_decode for sequences that share their first n_prefix tokens (the pages of block_table row 0)."""
+    """pa_decode for sequences that share their first n_prefix tokens (the pages of block_table row 0).  seqs as
+    pa_qkv_append takes them; stream None: the current one of q's device."""
     geometry = _geometry_of(h)
-    bf16, s = _torch().bfloat16, _seqs(seqs)
-    if q.dim() != 3 or q.size(1) != geometry[0] or q.size(2) != 256:
-        raise ValueError("q must be [rows, %d, 256]" % geometry[0])
-    if len(s) and max(e.q_off for e in s) >= q.size(0):
-        raise ValueError("a sequence's row is outside q")
+    bf16, _, _, _, raw_stream = _torch()
+    s, n_seq = _seq_array(seqs)
+    rows = (q.shape[0], geometry[0], 256)
+    bt, kp, vp, ks, vs = _pool_args(geometry, n_seq, block_table, k_pool, v_pool, k_scale, v_scale)
     _check(_lib.pa_decode_shared(
-        h, len(s), s, n_prefix, _dev(q, bf16, "q"),
-        *_pool_args(geometry, len(s), block_table, k_pool, v_pool, k_scale, v_scale)[1:],
-        C.c_void_p(block_table.data_ptr()), n_sink_blk, n_win_blk, sm_scale, _shaped(out, q.shape, bf16, "out"),
-        _stream_of(q, stream)), "pa_decode_shared")
+        h, n_seq, s.ctypes.data, n_prefix, rows[0], _array(q, bf16, rows, "q"), kp, vp, ks, vs, bt, n_sink_blk,
+        n_win_blk, sm_scale, _array(out, bf16, rows, "out"),
+        raw_stream(q.get_device()) if stream is None else stream.cuda_stream), "pa_decode_shared")
 
 
 def pa_kv_append(h, k_new, v_new, tok_start, block_table_row, k_pool, v_pool, k_scale, v_scale,
@@ -281,99 +295,108 @@ def pa_rope_init(inv_freq, pairing=PA_ROPE_HALF, pair_axis=None) -> pa_rope:
     return r
 
 
-def _rows(t, name, heads, tokens):
+def _wrong(t, dtype, shape, name, what="contiguous"):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        return TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    return ValueError("%s must be %s and %s, got %s with strides %s" % (name, what, tuple(shape), tuple(t.shape), t.stride()))
+
+
+def _array(t, dtype, shape, name):
+    """Address of a contiguous CUDA tensor of this type and shape."""
+    try:
+        if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise _wrong(t, dtype, shape, name)
+
+
+def _rows(t, bf16, shape, name):
     """bf16 rows [token, head, 256] at any strides (the 256 values of a row contiguous)."""
-    if not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype != _torch().bfloat16:
-        raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
-    if t.shape != (tokens, heads, 256) or t.stride(2) != 1:
-        raise ValueError("%s must be [%d, %d, 256] with contiguous rows, got %s" % (name, tokens, heads, tuple(t.shape)))
-    return C.byref(pa_rows(t.data_ptr(), t.stride(0), t.stride(1)))
+    try:
+        if t.dtype is bf16 and t.is_cuda and t.shape == shape:
+            ts, hs, one = t.stride()
+            if one == 1:
+                return pa_rows(t.data_ptr(), shape[0], ts, hs)
+    except AttributeError:
+        pass
+    raise _wrong(t, bf16, shape, name, "with contiguous rows")
 
 
-def _gain(w, name):
-    if w is None:
-        return None
-    if w.numel() != 256:
-        raise ValueError("%s must have 256 entries" % name)
-    return _dev(w, _torch().bfloat16, name)
+def _gain(w, bf16, name):
+    return None if w is None else _array(w, bf16, (256,), name)
 
 
-def _positions(positions, rope, tokens):
-    """int32 [tokens] or [axes, tokens] -> pointer and row stride."""
+def _positions(positions, rope, tokens, int32):
+    """int32 [tokens] or [axes, tokens] -> address and row stride."""
     if positions is None:
         return None, 0
-    if not positions.is_cuda or positions.dtype != _torch().int32:
+    shape, stride = positions.shape, positions.stride()
+    if positions.dtype is not int32 or not positions.is_cuda:
         raise TypeError("positions must be a CUDA int32 tensor")
-    if positions.stride(-1) != 1 and positions.size(-1) > 1:
-        raise ValueError("positions must be contiguous along the tokens")
-    n_axes = positions.size(0) if positions.dim() == 2 else 1
-    if positions.dim() not in (1, 2) or positions.size(-1) < tokens:
-        raise ValueError("positions must be [tokens] or [axes, tokens]")
+    n_axes = shape[0] if len(shape) == 2 else 1
+    if len(shape) not in (1, 2) or shape[-1] < tokens or (stride[-1] != 1 and shape[-1] > 1):
+        raise ValueError("positions must be [tokens] or [axes, tokens], contiguous along the tokens")
     if rope is not None and rope.rot_dim > 0 and n_axes < rope.n_axes:
         raise ValueError("positions must have %d axes, got %d" % (rope.n_axes, n_axes))
-    return C.c_void_p(positions.data_ptr()), positions.stride(0) if n_axes > 1 else positions.size(-1)
-
-
-def _shaped(t, shape, dtype, name):
-    p = _dev(t, dtype, name)
-    if t.shape != shape:
-        raise ValueError("%s must be %s, got %s" % (name, shape, tuple(t.shape)))
-    return p
+    return positions.data_ptr(), stride[0] if n_axes > 1 else shape[-1]
 
 
 def _pool_args(geometry, n_seq, block_table, k_pool, v_pool, k_scale, v_scale):
-    """Block table, pools and scales of the handle's shapes."""
-    torch = _torch()
+    """Addresses of the block table, pools and scales, of the handle's shapes."""
+    _, f32, int8, int32, _ = _torch()
     _, hkv, n_pool, max_pages = geometry
-    if block_table.dim() != 2 or block_table.size(0) < n_seq or block_table.size(1) != max_pages:
-        raise ValueError("block_table must have a row of %d pages for each sequence" % max_pages)
-    rows = (n_pool, 16, hkv)
-    return (_dev(block_table, torch.int32, "block_table"), _shaped(k_pool, rows + (256,), torch.int8, "k_pool"),
-            _shaped(v_pool, rows + (256,), torch.int8, "v_pool"), _shaped(k_scale, rows, torch.float32, "k_scale"),
-            _shaped(v_scale, rows, torch.float32, "v_scale"))
+    if block_table.shape[0] < n_seq:
+        raise ValueError("block_table must have a row for each sequence")
+    rows, scales = (n_pool, 16, hkv, 256), (n_pool, 16, hkv)
+    return (_array(block_table, int32, (block_table.shape[0], max_pages), "block_table"),
+            _array(k_pool, int8, rows, "k_pool"), _array(v_pool, int8, rows, "v_pool"),
+            _array(k_scale, f32, scales, "k_scale"), _array(v_scale, f32, scales, "v_scale"))
 
 
 def pa_qk_norm_rope(h, q, k, q_weight, k_weight, eps, rope, positions, q_out, k_out, weight_offset=0.0,
                     stream=None) -> None:
     """Norm and rotate query rows q [tokens, HQ, 256] into q_out and key rows k [tokens, HKV, 256] into k_out
     (contiguous; q or k None leaves that kind out).  rope: a pa_rope, or None for the norm alone; positions
-    int32 [tokens] or [axes, tokens]."""
+    int32 [tokens] or [axes, tokens].  stream None: the current one of the rows' device."""
     some = k if q is None else q
     if some is None:
         raise ValueError("q or k is needed")
-    hq, hkv = _geometry_of(h)[:2]
-    bf16, n = _torch().bfloat16, some.size(0)
-    pos, pos_stride = _positions(positions, rope, n)
+    hq, hkv, _, _ = _geometry_of(h)
+    bf16, _, _, int32, raw_stream = _torch()
+    n = some.shape[0]
+    qs, ks = (n, hq, 256), (n, hkv, 256)
+    pos, pos_stride = _positions(positions, rope, n, int32)
     _check(_lib.pa_qk_norm_rope(
-        h, n, None if q is None else _rows(q, "q", hq, n), None if k is None else _rows(k, "k", hkv, n),
-        _gain(q_weight, "q_weight"), _gain(k_weight, "k_weight"), weight_offset, eps,
-        None if rope is None else C.byref(rope), pos, pos_stride,
-        None if q is None else _shaped(q_out, (n, hq, 256), bf16, "q_out"),
-        None if k is None else _shaped(k_out, (n, hkv, 256), bf16, "k_out"), _stream_of(some, stream)),
-        "pa_qk_norm_rope")
+        h, n, None if q is None else _rows(q, bf16, qs, "q"), None if k is None else _rows(k, bf16, ks, "k"),
+        _gain(q_weight, bf16, "q_weight"), _gain(k_weight, bf16, "k_weight"), weight_offset, eps, rope, pos,
+        pos_stride, None if q is None else _array(q_out, bf16, qs, "q_out"),
+        None if k is None else _array(k_out, bf16, ks, "k_out"),
+        raw_stream(some.get_device()) if stream is None else stream.cuda_stream), "pa_qk_norm_rope")
 
 
 def pa_qkv_append(h, seqs, q, k, v, q_weight, k_weight, eps, rope, positions, block_table, k_pool, v_pool, k_scale,
                   v_scale, q_out, weight_offset=0.0, stream=None) -> None:
-    """The new tokens of a batch of sequences (rows q_off .. q_off + n_q of q, k, v): queries normed and rotated
-    into q_out, keys normed, rotated and quantised, values quantised into the pool.  positions None: the tokens'
-    own; q None (with q_out None): keys and values only."""
+    """The new tokens of a batch of sequences (seqs: (q_off, q_start, n_q, n_ctx) each, an int32 array is taken as it
+    is; rows q_off .. q_off + n_q of q, k, v): queries normed and rotated into q_out, keys normed, rotated and
+    quantised, values quantised into the pool.  positions None: the tokens' own; q None (with q_out None): keys and
+    values only."""
     geometry = _geometry_of(h)
-    hq, hkv = geometry[:2]
-    s = _seqs(seqs)
-    n = k.size(0)
-    if len(s) and max(e.q_off + e.n_q for e in s) > n:
-        raise ValueError("a sequence's rows are outside k")
-    pos, pos_stride = _positions(positions, rope, n)
+    hq, hkv, _, _ = geometry
+    bf16, _, _, int32, raw_stream = _torch()
+    s, n_seq = _seq_array(seqs)
+    n = k.shape[0]
+    pos, pos_stride = _positions(positions, rope, n, int32)
     _check(_lib.pa_qkv_append(
-        h, len(s), s, None if q is None else _rows(q, "q", hq, n), _rows(k, "k", hkv, n), _rows(v, "v", hkv, n),
-        _gain(q_weight, "q_weight"), _gain(k_weight, "k_weight"), weight_offset, eps,
-        None if rope is None else C.byref(rope), pos, pos_stride,
-        *_pool_args(geometry, len(s), block_table, k_pool, v_pool, k_scale, v_scale),
-        None if q is None else _shaped(q_out, (n, hq, 256), _torch().bfloat16, "q_out"), _stream_of(k, stream)),
-        "pa_qkv_append")
+        h, n_seq, s.ctypes.data, None if q is None else _rows(q, bf16, (n, hq, 256), "q"),
+        _rows(k, bf16, (n, hkv, 256), "k"), _rows(v, bf16, (n, hkv, 256), "v"),
+        _gain(q_weight, bf16, "q_weight"), _gain(k_weight, bf16, "k_weight"), weight_offset, eps, rope, pos,
+        pos_stride, *_pool_args(geometry, n_seq, block_table, k_pool, v_pool, k_scale, v_scale),
+        None if q is None else _array(q_out, bf16, (n, hq, 256), "q_out"),
+        raw_stream(k.get_device()) if stream is None else stream.cuda_stream), "pa_qkv_append")
 
 
 def pa_prefill_host(h, seqs, q, k_pool, v_pool, k_scale, v_scale, block_table, n_sink_blk, n_win_blk, sm_scale,

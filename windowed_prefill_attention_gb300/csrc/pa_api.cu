@@ -1122,7 +1122,7 @@ Span span_of(const void* p, size_t bytes) {
 // Checks a host description of `tokens` rows of `heads` heads (row indexes
 // below `tokens`) and fills the kernel's form and the bytes they lie in.
 bool rows_ok(const pa_rows* r, long long tokens, int heads, RowsIn& in, Span& span) {
-  if (!r || !r->data || !aligned(r->data, 16)) return false;
+  if (!r || !r->data || !aligned(r->data, 16) || r->n_tok < tokens) return false;
   const long long ts = r->tok_stride, hs = r->head_stride;
   if (ts < 0 || hs < 0 || ts % 8 || hs % 8) return false;
   const long long most = 1ll << 46;  // elements: far above any device's memory, and no product below overflows
@@ -1716,15 +1716,22 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
     const pa_seq& q = seqs[s0 + s];
     own += shared_own(q.n_ctx, shared_win_lo(q.n_ctx, W), p.first_blk, S, W).n;
   }
+  // chunks of equal size, four to 128 blocks, as small as one wave of two CTAs per SM allows
   const long long even = (own * HKV + 2 * n_sm - 1) / (2 * n_sm);
-  p.chunk = (int)std::min<long long>(128, (std::max(4ll, even) + 3) / 4 * 4);
   int chunks = 0;
-  for (int s = 0; s < n; ++s) {
-    const pa_seq& q = seqs[s0 + s];
-    const int lo = shared_win_lo(q.n_ctx, W);
-    t.s[s] = make_int4(q.q_off, q.n_ctx, chunks, lo);
-    chunks += (shared_own(q.n_ctx, lo, p.first_blk, S, W).n + p.chunk - 1) / p.chunk;
+  for (p.chunk = (int)std::min<long long>(128, (std::max(4ll, even) + 3) / 4 * 4);; p.chunk += 4) {
+    chunks = 0;
+    for (int s = 0; s < n; ++s) {
+      const pa_seq& q = seqs[s0 + s];
+      const int lo = shared_win_lo(q.n_ctx, W);
+      t.s[s] = make_int4(q.q_off, q.n_ctx, chunks, lo);
+      chunks += (shared_own(q.n_ctx, lo, p.first_blk, S, W).n + p.chunk - 1) / p.chunk;
+    }
+    if (p.chunk >= 128 || (long long)chunks * HKV <= 2 * n_sm || chunks == n) break;
   }
+  for (int s = 0; s < n; ++s)
+    for (int c = HKV * t.s[s].z, e = HKV * (s + 1 < n ? t.s[s + 1].z : chunks); c < e && c < kShOwnListed; ++c)
+      t.own_seq[c] = (uint16_t)s;
   p.chunks_head = chunks;
   return PA_OK;
 }
@@ -1748,12 +1755,14 @@ int reserve(Workspace& w, size_t need, bool capturing) {
 }
 }  // namespace
 
-int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, const void* q, const int8_t* k_pool,
-                     const int8_t* v_pool, const float* k_scale, const float* v_scale, const int32_t* block_table,
+int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, int n_rows, const void* q,
+                     const int8_t* k_pool, const int8_t* v_pool, const float* k_scale, const float* v_scale, const int32_t* block_table,
                      int n_sink_blk, int n_win_blk, float sm_scale, void* out, void* stream) {
   int rc = check_inputs(h, q, k_pool, v_pool, k_scale, v_scale, block_table, out);
   if (rc) return rc;
   if ((rc = decode_shared_check(h->HQ, h->HKV, h->max_pages, n_seq, seqs, n_prefix, n_sink_blk, sm_scale))) return rc;
+  for (int s = 0; s < n_seq; ++s)
+    if (seqs[s].q_off >= n_rows) return PA_EINVAL;
   OnDevice dev(h->device);
   if (!dev.ok) return PA_ECUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -32,7 +32,9 @@ namespace pa {
 namespace {
 
 constexpr unsigned kAllLanes = 0xffffffffu;
-constexpr float kMaxLift = 8.f;  // the softmax reference moves when a row's maximum passes it by more than 2^8
+// The softmax reference moves when a row's maximum passes it by more than 2^14
+// (moving it rescales O, ~1500 cycles); P' <= 2^14 then, inside fp16's range.
+constexpr float kMaxLift = 14.f;
 constexpr int DEV_ERR_LAYOUT = 0x400;  // shared memory's base is not aligned as the operands need (reported as PA_ECUDA)
 constexpr uint64_t kShDrainNs = 200000000ull;
 
@@ -281,12 +283,14 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
     if (n_seg > 0 && !c.wait(B_QE, n_seg - 1)) return;
     const uint32_t rowc = c.sb + kSmRow + (n_seg & 1) * kRows;
     const uint32_t raw = c.sb + kSmK + warp * (16 * kHeadDim * 2) + 16 * lane;
+    const int my = kConvWarps * (lane & 15) + warp;  // lane i: the row of q of the warp's i-th row
+    const int my_q = my < s.rows ? tab.s[(s.row0 + my) >> p.log2_g].x : 0;
 #pragma unroll 1
     for (int i = 0; i < 16; ++i) {
       const int row = kConvWarps * i + warp;
+      const int q_row = __shfl_sync(kAllLanes, my_q, i);
       if (row < s.rows) {
-        const int rr = s.row0 + row;
-        const __nv_bfloat16* q = p.q + ((size_t)tab.s[rr >> p.log2_g].x * p.HQ + (size_t)s.g * p.G + (rr & (p.G - 1))) * kHeadDim;
+        const __nv_bfloat16* q = p.q + ((size_t)q_row * p.HQ + (size_t)s.g * p.G + ((s.row0 + row) & (p.G - 1))) * kHeadDim;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(raw + i * (kHeadDim * 2)), "l"(q + 8 * lane) : "memory");
       }
     }
@@ -306,7 +310,7 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
     load(0);
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
-#pragma unroll 1
+#pragma unroll 4
     for (int i = 0; i < 16; ++i) {
       const int row = kConvWarps * i + warp;
       float v[8];
@@ -568,25 +572,32 @@ __device__ __forceinline__ bool softmax_tile(const SharedParams& p, const PreCtx
   float z[2];
   if (__all_sync(kAllLanes, (seen[0] & seen[1]) == 0xffu)) scale_and_max<false>(s, ks_at, 0, 0, z[0], z[1]);
   else scale_and_max<true>(s, ks_at, seen[0], seen[1], z[0], z[1]);
-  float f[2];  // what earlier sums shrink by (they are zero while m is -inf)
-  bool moved = false;
+  // The rows' references.  Mostly no row passes its own by enough to move it,
+  // which each thread sees from its own keys; only else are the rows' maxima
+  // put together.
+  float f[2] = {fe, fe};  // what earlier P V shrink by
+  bool need = false;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    z[i] = fmaxf(z[i], __shfl_xor_sync(kAllLanes, z[i], 1));
-    z[i] = fmaxf(z[i], __shfl_xor_sync(kAllLanes, z[i], 2));
-    const float mz = z[i] == -INFINITY ? -INFINITY : z[i] * r.c[i];
-    f[i] = 1.f;
-    if (r.m[i] == -INFINITY) {
-      r.m[i] = mz;
-    } else if (mz > r.m[i] + kMaxLift) {
-      f[i] = ex2f(r.m[i] - mz);
-      r.m[i] = mz;
+  for (int i = 0; i < 2; ++i)
+    need |= z[i] != -INFINITY && (r.m[i] == -INFINITY || z[i] * r.c[i] > r.m[i] + kMaxLift);
+  need = __any_sync(kAllLanes, need);
+  if (need) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      z[i] = fmaxf(z[i], __shfl_xor_sync(kAllLanes, z[i], 1));
+      z[i] = fmaxf(z[i], __shfl_xor_sync(kAllLanes, z[i], 2));
+      const float mz = z[i] == -INFINITY ? -INFINITY : z[i] * r.c[i];
+      if (r.m[i] == -INFINITY) {  // sums and products so far are zero
+        r.m[i] = mz;
+      } else if (mz > r.m[i] + kMaxLift) {
+        const float g = ex2f(r.m[i] - mz);
+        r.m[i] = mz;
+        r.l[i] = mul2(r.l[i], make_float2(g, g));
+        f[i] *= g;
+      }
     }
-    r.l[i] = mul2(r.l[i], make_float2(f[i], f[i]));
-    f[i] *= fe;
-    moved |= f[i] != 1.f;
   }
-  if (!first && __any_sync(kAllLanes, moved)) {
+  if (!first && (fe != 1.f || (need && __any_sync(kAllLanes, f[0] != 1.f || f[1] != 1.f)))) {
     // P V of the tile before (that of two tiles before came ahead of this tile's scores)
     if (!c.wait(B_OD + (n_before & 1), n_before >> 1)) return false;
     tc_fence_after();
@@ -750,6 +761,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
     tmem_alloc_pair(c.sb + kSmTmem, 512);
     tmem_relinquish_pair();
   }
+  {  // the table's lines that the roles read first come in while the CTAs set up
+    const Segment s = segment_at(p, tab, c.rank, c.x0, c.x1);
+    const int row = min(s.row0 + (int)threadIdx.x % kRows, p.n_seq * p.G - 1);
+    asm volatile("" ::"r"(s.t1), "r"(tab.s[row >> p.log2_g].x));
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers exist before either may arrive on the other's
@@ -816,8 +832,9 @@ __global__ void __launch_bounds__(kOwnWarps * 32) own_kernel(const __grid_consta
   __shared__ float rowc[8], wm[kOwnWarps][8], wl[kOwnWarps][8];
   dependents_may_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-  // the CTA's sequence, kv head and chunk
+  // the CTA's sequence (listed for the launch's first CTAs), kv head and chunk
   int lo = 0, hi = p.n_seq - 1;
+  if ((int)blockIdx.x < kShOwnListed) lo = hi = tab.own_seq[blockIdx.x];
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (p.HKV * tab.s[mid].z <= (int)blockIdx.x) lo = mid;

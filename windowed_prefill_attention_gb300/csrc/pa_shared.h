@@ -23,6 +23,8 @@ struct ShGroup {
 
 constexpr int kShPairs = 128;  // SM pairs of a launch at most
 
+constexpr int kShOwnListed = 1024;
+
 struct SharedSeqs {
   // {row in q / out, context length, chunks of the earlier sequences (per kv head), first block of its window}
   int4 s[kShSeqs];
@@ -32,6 +34,7 @@ struct SharedSeqs {
   // lies in pairs first_pair[j] .. last_pair[j].
   int cut[kShPairs + 1];
   uint8_t first_pair[8 * kShGroups], last_pair[8 * kShGroups];
+  uint16_t own_seq[kShOwnListed];  // sequence of the per-sequence pass's first CTAs (a search finds the others')
 };
 
 struct SharedParams {
