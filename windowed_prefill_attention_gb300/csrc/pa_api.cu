@@ -1634,6 +1634,8 @@ int decode_shared_check(int HQ, int HKV, int max_pages, int n_seq, const pa_seq*
 // (about 12000 cycles against 3000 to 4000 a tile on GB300).  The per-sequence pass: chunks of equal block counts, about two
 // CTAs per SM, four to 128 blocks each.
 constexpr int kShSegCost = 4;
+constexpr double kShPairUs = 11.0, kShTileUs = 2.1;  // a pair's set-up, queries and epilogue; a tile
+constexpr double kShOwnBlockUs = 0.25, kShOwnCtaUs = 2.0, kShOwnTailUs = 5.0;
 // Packs the groups (nt[j] tiles each, laid end to end) into runs of at most
 // `budget` cost; false if they take more than max_pairs.
 bool shared_pack(const int* nt, int n_groups, int budget, int max_pairs, int* cut, int& n_pairs) {
@@ -1688,20 +1690,53 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
   }
   // at most 16 groups of 2^23 tiles: no overflow before the test
   if ((long long)HKV * p.tiles_head >= (1ll << 30)) return PA_EINVAL;
-  const int T = HKV * p.tiles_head, max_pairs = std::min(kShPairs, std::max(1, n_sm / 2));
+  // Blocks of the per-sequence pass, and its CTAs for a chunk size.
+  long long own = 0;
+  for (int s = 0; s < n; ++s) {
+    const pa_seq& q = seqs[s0 + s];
+    const int lo = shared_win_lo(q.n_ctx, W), own_n = shared_own(q.n_ctx, lo, p.first_blk, S, W).n;
+    t.s[s] = make_int4(q.q_off, q.n_ctx, own_n, lo);  // .z: the blocks until the chunks are counted
+    own += own_n;
+  }
+  auto own_ctas = [&](int chunk) {
+    long long c = 0;
+    for (int s = 0; s < n; ++s) c += (t.s[s].z + chunk - 1) / chunk;
+    return c * HKV;
+  };
+  auto own_chunk = [&](int slots) {  // the smallest of 4, 8, ... 128 whose CTAs fit one wave of `slots`
+    const long long even = (own * HKV + slots - 1) / slots;
+    int c = (int)std::min<long long>(128, (std::max(4ll, even) + 3) / 4 * 4);
+    for (long long k; c < 128 && (k = own_ctas(c)) > slots && k > (long long)n * HKV;) c = std::min(128, c + c / 8 / 4 * 4 + 4);
+    return c;
+  };
+  // The prefix pass's pairs.  Both passes can run at once: the pairs left out
+  // leave their SMs to the per-sequence pass, whose CTAs otherwise start when the
+  // prefix pass ends.  Of a few numbers of pairs the one that ends first, by what
+  // GB300 measures (microseconds; an own block and CTA as the SM time they take).
+  const int T = HKV * p.tiles_head, max_pairs = std::min(kShPairs, std::max(1, n_sm / 2)), J = HKV * p.n_grp;
   p.n_pairs = 0;
+  p.chunk = own_chunk(kShOwnPerSm * n_sm);
   if (T > 0) {
     int nt[8 * kShGroups];
-    const int J = HKV * p.n_grp;
     for (int j = 0; j < J; ++j) nt[j] = (t.grp[j % p.n_grp].n_blk + kTileBlocks - 1) / kTileBlocks;
-    int lo = (T + max_pairs - 1) / max_pairs, hi = T + kShSegCost * J;
-    while (lo < hi) {  // the smallest budget that packs
-      const int mid = lo + (hi - lo) / 2;
-      if (shared_pack(nt, J, mid, max_pairs, t.cut, p.n_pairs)) hi = mid;
-      else lo = mid + 1;
+    double best = 1e30;
+    int pairs = max_pairs;
+    const double own_us = kShOwnBlockUs * own * HKV + kShOwnCtaUs * own_ctas(p.chunk);
+    for (int left = 0; left < max_pairs; left += 4) {
+      const int use = std::min(max_pairs - left, T), free_sm = n_sm - 2 * use;
+      // a pair's cost when all are equal: its tiles, and its share of the groups' changes
+      const int budget = (T + kShSegCost * std::max(0, J - use) + use - 1) / use + (J > 1 && J < use && use % J ? 1 : 0);
+      const double prefix_us = kShPairUs + kShTileUs * budget, rest = std::max(0.0, own_us - free_sm * prefix_us);
+      const double end = prefix_us + (rest > 0.0 ? rest / n_sm + kShOwnTailUs : 0.0);
+      if (end < best) {
+        best = end;
+        pairs = use;
+      }
+      if (rest <= 0.0) break;  // fewer pairs only make the prefix pass longer
     }
-    (void)shared_pack(nt, J, lo, max_pairs, t.cut, p.n_pairs);
-    int x = 0, c = 0;
+    int budget = (T + pairs - 1) / pairs;
+    while (!shared_pack(nt, J, budget, pairs, t.cut, p.n_pairs)) ++budget;
+    int x = 0, c = 0, most = 0;
     for (int j = 0; j < J; ++j) {
       while (c + 1 < p.n_pairs && t.cut[c + 1] <= x) ++c;
       t.first_pair[j] = (uint8_t)c;
@@ -1709,29 +1744,19 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
       int e = c;
       while (e + 1 < p.n_pairs && t.cut[e + 1] < x) ++e;
       t.last_pair[j] = (uint8_t)e;
+      most = std::max(most, e - c + 1);
     }
+    p.merge_ways = most;
   }
-  long long own = 0;
+  int chunks = 0, most = 0;
   for (int s = 0; s < n; ++s) {
-    const pa_seq& q = seqs[s0 + s];
-    own += shared_own(q.n_ctx, shared_win_lo(q.n_ctx, W), p.first_blk, S, W).n;
+    const int c = (t.s[s].z + p.chunk - 1) / p.chunk;
+    t.s[s].z = chunks;
+    for (int i = HKV * chunks; i < HKV * (chunks + c) && i < kShOwnListed; ++i) t.own_seq[i] = (uint16_t)s;
+    chunks += c;
+    most = std::max(most, c);
   }
-  // chunks of equal size, four to 128 blocks, as small as one wave of two CTAs per SM allows
-  const long long even = (own * HKV + 2 * n_sm - 1) / (2 * n_sm);
-  int chunks = 0;
-  for (p.chunk = (int)std::min<long long>(128, (std::max(4ll, even) + 3) / 4 * 4);; p.chunk += 4) {
-    chunks = 0;
-    for (int s = 0; s < n; ++s) {
-      const pa_seq& q = seqs[s0 + s];
-      const int lo = shared_win_lo(q.n_ctx, W);
-      t.s[s] = make_int4(q.q_off, q.n_ctx, chunks, lo);
-      chunks += (shared_own(q.n_ctx, lo, p.first_blk, S, W).n + p.chunk - 1) / p.chunk;
-    }
-    if (p.chunk >= 128 || (long long)chunks * HKV <= 2 * n_sm || chunks == n) break;
-  }
-  for (int s = 0; s < n; ++s)
-    for (int c = HKV * t.s[s].z, e = HKV * (s + 1 < n ? t.s[s + 1].z : chunks); c < e && c < kShOwnListed; ++c)
-      t.own_seq[c] = (uint16_t)s;
+  p.merge_ways = std::min(8, (p.merge_ways + most + 3) / 4);
   p.chunks_head = chunks;
   return PA_OK;
 }

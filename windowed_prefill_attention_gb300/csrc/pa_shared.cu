@@ -75,20 +75,14 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 }
 __device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// 16 TMEM lanes x 32 columns in the 16x256b shape (see pa_ptx.cuh).
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+// 16 TMEM lanes x 128 columns in the 16x256b shape (see pa_ptx.cuh).
+__device__ __forceinline__ void tmem_st_16x256b_x16(uint32_t taddr, const uint32_t (&r)[64]) {
+#define PA_SH_W8(i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.st.sync.aligned.16x256b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,%64};" ::"r"(taddr),
+      PA_SH_W8(0), PA_SH_W8(8), PA_SH_W8(16), PA_SH_W8(24), PA_SH_W8(32), PA_SH_W8(40), PA_SH_W8(48), PA_SH_W8(56)
       : "memory");
+#undef PA_SH_W8
 }
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
@@ -123,12 +117,12 @@ constexpr int kSoftWarps = 8;                       // warps 0-7: softmax; TMEM 
 constexpr int kConvWarps = 8;                       // warps 8-15: codes -> fp16 operands (K: four, V: four), the queries
 constexpr int kIssueWarp = kSoftWarps + kConvWarps; // warp 16: TMEM; even CTA: the products, odd CTA: forwards K
 constexpr int kScaleWarp = kIssueWarp + 1;          // warp 17: the tiles' scales
-constexpr int kVFwdWarp = kIssueWarp + 2;           // warps 18, 19: odd CTA: forward V and the queries
-constexpr int kQFwdWarp = kIssueWarp + 3;
-constexpr int kPreThreads = 32 * (kQFwdWarp + 1);
+// warp 18: odd CTA: forwards V
+constexpr int kQueryWarp = kIssueWarp + 3;          // warp 19: copies the queries in; odd CTA: forwards them
+constexpr int kPreThreads = 32 * (kQueryWarp + 1);
 // Registers a thread, of the 96 each is launched with (65536 / 640): in units
-// of a warp's, 8 x 120 + 8 x 88 + 4 x 64 = 20 x 96.
-constexpr int kSoftRegs = 120, kConvRegs = 88, kMiscRegs = 64;
+// of a warp's, 8 x 112 + 8 x 96 + 4 x 64 = 20 x 96.
+constexpr int kSoftRegs = 112, kConvRegs = 96, kMiscRegs = 64;
 static_assert(8 * kSoftRegs + 8 * kConvRegs + 4 * kMiscRegs <= 20 * 96, "register split: above it the increase waits forever");
 static_assert(kSoftRegs >= 96 && kConvRegs <= 96 && kMiscRegs <= 96, "an increase and two decreases from the launch's 96");
 
@@ -162,8 +156,9 @@ enum : int {
   B_QE = 20,   // both: a segment's last Q K^T is done
   B_OE = 21,   // even: a segment's O is read (every softmax warp of both)
   B_RAW = 22,  // the segment's raw queries are read (converter warps)
-  B_DRAIN = 23,
-  kPreBars = 24
+  B_RAWF = 23, // the segment's raw queries have landed
+  B_DRAIN = 24,
+  kPreBars = 25
 };
 constexpr int kSmTmem = kSmBar + kPreBars * 8;
 constexpr int kPreSmem = kSmTmem + 16;
@@ -277,23 +272,6 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
     // pages of the segment's blocks, 32 (four tiles) at a time, one per lane
     const int b0 = s.t0 * kTileBlocks;
     int pg = group_page(p, s.grp, b0 + lane), pg_next = group_page(p, s.grp, b0 + 32 + lane);
-    // The CTA's queries, 16 rows a warp, copied as they are into the K stages
-    // (free: the segment before's last Q K^T is done), all in flight together,
-    // then widened row by row in a loop that is short for the same reason.
-    if (n_seg > 0 && !c.wait(B_QE, n_seg - 1)) return;
-    const uint32_t rowc = c.sb + kSmRow + (n_seg & 1) * kRows;
-    const uint32_t raw = c.sb + kSmK + warp * (16 * kHeadDim * 2) + 16 * lane;
-    const int my = kConvWarps * (lane & 15) + warp;  // lane i: the row of q of the warp's i-th row
-    const int my_q = my < s.rows ? tab.s[(s.row0 + my) >> p.log2_g].x : 0;
-#pragma unroll 1
-    for (int i = 0; i < 16; ++i) {
-      const int row = kConvWarps * i + warp;
-      const int q_row = __shfl_sync(kAllLanes, my_q, i);
-      if (row < s.rows) {
-        const __nv_bfloat16* q = p.q + ((size_t)q_row * p.HQ + (size_t)s.g * p.G + ((s.row0 + row) & (p.G - 1))) * kHeadDim;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(raw + i * (kHeadDim * 2)), "l"(q + 8 * lane) : "memory");
-      }
-    }
     uint4 r[8];
     // a block past the list or of a bad page loads page 0's codes: whatever finite values they widen to,
     // the softmax gives those keys no weight
@@ -308,29 +286,42 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
       for (int n = 4; n < 8; ++n, b += step_b) r[n] = ldg_stream(b);
     };
     load(0);
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncwarp();
-#pragma unroll 4
-    for (int i = 0; i < 16; ++i) {
-      const int row = kConvWarps * i + warp;
-      float v[8];
-      {
-        const float4 f = lds_f32x4(raw + i * (kHeadDim * 2));
-        const bool in = row < s.rows;
-        unpack8(make_uint4(in ? __float_as_uint(f.x) : 0, in ? __float_as_uint(f.y) : 0, in ? __float_as_uint(f.z) : 0,
-                           in ? __float_as_uint(f.w) : 0), v);
+    // The CTA's queries, 16 rows a warp, from the raw copies in the K stages:
+    // each row scaled by a power of two and rounded to fp16, exactly.  Four rows
+    // at a time, their chains of shuffles side by side; a row's largest magnitude
+    // from the bf16 bit patterns, two rows to a word.
+    if (!c.wait(B_RAWF, n_seg)) return;
+    const uint32_t rowc = c.sb + kSmRow + (n_seg & 1) * kRows;
+#pragma unroll 1
+    for (int i0 = 16 * warp; i0 < 16 * warp + 16; i0 += 4) {
+      uint4 q[4];
+      uint32_t m[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 f = lds_f32x4(c.sb + kSmK + (i0 + i) * (kHeadDim * 2) + 16 * lane);
+        const bool in = i0 + i < s.rows;
+        q[i] = make_uint4(in ? __float_as_uint(f.x) : 0, in ? __float_as_uint(f.y) : 0, in ? __float_as_uint(f.z) : 0,
+                          in ? __float_as_uint(f.w) : 0);
+        uint32_t a = __vmaxu2(__vmaxu2(q[i].x & 0x7fff7fffu, q[i].y & 0x7fff7fffu), __vmaxu2(q[i].z & 0x7fff7fffu, q[i].w & 0x7fff7fffu));
+        a = max(a & 0xffffu, a >> 16);
+        m[i >> 1] = i & 1 ? m[i >> 1] | a << 16 : a;
       }
-      float am = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(v[e]));
+      for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(kAllLanes, am, o));
-      const int k = row_shift(am);
-      const float mul = pow2i(k);
-      sts128(c.sb + kSmQ + (lane >> 3) * 16384 + row * 128 + (((lane & 7) ^ (row & 7)) << 4),
-             pack_f16x2(v[0] * mul, v[1] * mul), pack_f16x2(v[2] * mul, v[3] * mul), pack_f16x2(v[4] * mul, v[5] * mul),
-             pack_f16x2(v[6] * mul, v[7] * mul));
-      if (lane == 0) asm volatile("st.shared.u8 [%0], %1;" ::"r"(rowc + row), "r"(-k) : "memory");
+        for (int i = 0; i < 2; ++i) m[i] = __vmaxu2(m[i], __shfl_xor_sync(kAllLanes, m[i], o));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = i0 + i;
+        const int k = row_shift(__uint_as_float(i & 1 ? m[i >> 1] & 0xffff0000u : m[i >> 1] << 16));
+        const float mul = pow2i(k);
+        float v[8];
+        unpack8(q[i], v);
+        sts128(c.sb + kSmQ + (lane >> 3) * 16384 + row * 128 + (((lane & 7) ^ (row & 7)) << 4),
+               pack_f16x2(v[0] * mul, v[1] * mul), pack_f16x2(v[2] * mul, v[3] * mul), pack_f16x2(v[4] * mul, v[5] * mul),
+               pack_f16x2(v[6] * mul, v[7] * mul));
+        if (lane == 0) asm volatile("st.shared.u8 [%0], %1;" ::"r"(rowc + row), "r"(-k) : "memory");
+      }
     }
     fence_proxy_async_shared();
     __syncwarp();
@@ -370,14 +361,31 @@ __device__ __forceinline__ void role_forward_tiles(const PreCtx& c, int local, i
     mbar_arrive_cluster(cluster_addr(c.bar(even + (n & 1)), 0));
   }
 }
-__device__ __forceinline__ void role_forward_queries(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
-  uint32_t n_seg = 0;
+// The segments' query rows, copied as they are into the K stages (free: the
+// segment before's last Q K^T is done): the G rows of a sequence lie together.
+// In the odd CTA also the forward of its queries.
+__device__ __forceinline__ void role_queries(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
+  const int lane = threadIdx.x & 31;
+  uint32_t n_seg = 0, copied = 0;
   for (int x = c.x0; x < c.x1; ++n_seg) {
     const Segment s = segment_at(p, tab, c.rank, x, c.x1);
-    if (!mbar_wait(c.bar(B_QL), n_seg & 1, c.wc, 80 + B_QL)) return;
-    mbar_arrive_cluster(cluster_addr(c.bar(B_QF), 0));
+    if (n_seg > 0 && !c.wait(B_QE, n_seg - 1)) break;
+    if (lane == 0) mbar_expect_tx(c.bar(B_RAWF), s.rows * (kHeadDim * 2));
+    __syncwarp();
+    const int n = s.rows >> p.log2_g, s0 = s.row0 >> p.log2_g;  // whole sequences: 128 is a multiple of G
+    for (int i = lane; i < n; i += 32)
+      bulk_load(c.sb + kSmK + i * p.G * (kHeadDim * 2),
+                p.q + ((size_t)tab.s[s0 + i].x * p.HQ + (size_t)s.g * p.G) * kHeadDim, p.G * (kHeadDim * 2), c.bar(B_RAWF));
+    ++copied;
+    if (c.rank == 1) {
+      if (!c.wait(B_QL, n_seg)) break;
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(c.bar(B_QF), 0));
+    }
     x += s.t1 - s.t0;
   }
+  // no copy is in flight when the CTA leaves, whatever gave up
+  if (copied > 0) (void)mbar_wait_drain(c.bar(B_RAWF), (copied - 1) & 1u, kShDrainNs);
+  __syncwarp();
 }
 
 // ---- scales of every tile's keys, V's normalised by a running power of two.
@@ -597,25 +605,6 @@ __device__ __forceinline__ bool softmax_tile(const SharedParams& p, const PreCtx
       }
     }
   }
-  if (!first && (fe != 1.f || (need && __any_sync(kAllLanes, f[0] != 1.f || f[1] != 1.f)))) {
-    // P V of the tile before (that of two tiles before came ahead of this tile's scores)
-    if (!c.wait(B_OD + (n_before & 1), n_before >> 1)) return false;
-    tc_fence_after();
-#pragma unroll 1
-    for (int h = 0; h < 8; ++h) {  // 32 columns
-      uint32_t o[16];
-      tmem_ld_16x256b_x4(otm + 32 * h, o);
-      tmem_wait_ld(o);
-#pragma unroll
-      for (int e = 0; e < 16; e += 4) {
-        o[e] = __float_as_uint(__uint_as_float(o[e]) * f[0]);
-        o[e + 1] = __float_as_uint(__uint_as_float(o[e + 1]) * f[0]);
-        o[e + 2] = __float_as_uint(__uint_as_float(o[e + 2]) * f[1]);
-        o[e + 3] = __float_as_uint(__uint_as_float(o[e + 3]) * f[1]);
-      }
-      tmem_st_16x256b_x4(otm + 32 * h, o);
-    }
-  }
   // p = 2^(z c - m), P' = p v_scale 2^-ev in fp16.  A hidden key's z is -inf,
   // and a row's factor may be 0: keep the product -inf.
   const float n0 = r.m[0] == -INFINITY ? 0.f : -r.m[0], n1 = r.m[1] == -INFINITY ? 0.f : -r.m[1];
@@ -638,6 +627,28 @@ __device__ __forceinline__ bool softmax_tile(const SharedParams& p, const PreCtx
       ph[2 * kk + 1] = pack_f16x2(wb.x, wb.y);
     }
     tmem_st_16x128b_x8(stm + 32 * h, ph);
+  }
+  // O takes the same factors; last, when the scores' registers are free for it
+  if (!first && (fe != 1.f || (need && __any_sync(kAllLanes, f[0] != 1.f || f[1] != 1.f)))) {
+    // P V of the tile before (that of two tiles before came ahead of this tile's scores)
+    if (!c.wait(B_OD + (n_before & 1), n_before >> 1)) return false;
+    tc_fence_after();
+    uint32_t o[64];  // 128 columns
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      tmem_ld_16x256b_x16(otm + 128 * h, o);
+      tmem_wait_ld(o);
+#pragma unroll
+      for (int e = 0; e < 64; e += 4) {
+        const float2 a = mul2(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), make_float2(f[0], f[0]));
+        const float2 b = mul2(make_float2(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])), make_float2(f[1], f[1]));
+        o[e] = __float_as_uint(a.x);
+        o[e + 1] = __float_as_uint(a.y);
+        o[e + 2] = __float_as_uint(b.x);
+        o[e + 3] = __float_as_uint(b.y);
+      }
+      tmem_st_16x256b_x16(otm + 128 * h, o);
+    }
   }
   return true;
 }
@@ -696,16 +707,21 @@ __device__ __forceinline__ void role_softmax(const SharedParams& p, const Shared
     const float up = pow2i(ev);
     float4* dst = p.pre_o + ((size_t)id * 64 + 32 * half) * kUnitRows + c.rank * kRows + row;
 #pragma unroll 1
-    for (int h = 0; h < 4; ++h) {
-      uint32_t o[32];
-      tmem_ld32(c.tm + kTmemO + 128 * half + 32 * h + ((uint32_t)quad << 16), o);
-      tmem_wait_ld(o);
+    for (int h = 0; h < 2; ++h) {  // 64 columns
+      uint32_t o[2][32];
+      const uint32_t at = c.tm + kTmemO + 128 * half + 64 * h + ((uint32_t)quad << 16);
+      tmem_ld32(at, o[0]);
+      tmem_ld32(at + 32, o[1]);
+      tmem_wait_ld(o[0]);
+      reg_fence(o[1]);
       if (row < s.rows) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          dst[(size_t)(8 * h + e) * kUnitRows] =
-              make_float4(__uint_as_float(o[4 * e]) * up, __uint_as_float(o[4 * e + 1]) * up,
-                          __uint_as_float(o[4 * e + 2]) * up, __uint_as_float(o[4 * e + 3]) * up);
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t* v = o[e >> 3] + 4 * (e & 7);
+          dst[(size_t)(16 * h + e) * kUnitRows] =
+              make_float4(__uint_as_float(v[0]) * up, __uint_as_float(v[1]) * up, __uint_as_float(v[2]) * up,
+                          __uint_as_float(v[3]) * up);
+        }
       }
     }
     tc_fence_before();
@@ -752,6 +768,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
     mbar_init(c.bar(B_QF), kConvWarps + 1);
     mbar_init(c.bar(B_QL), kConvWarps);
     mbar_init(c.bar(B_RAW), kConvWarps);
+    mbar_init(c.bar(B_RAWF), 1);
     mbar_init(c.bar(B_QE), 1);
     mbar_init(c.bar(B_OE), 2 * kSoftWarps);
     mbar_init(c.bar(B_DRAIN), 1);
@@ -782,13 +799,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
     fewer_regs<kMiscRegs>();
     if (warp == kScaleWarp) {
       role_scales(p, tab, c);
+    } else if (warp == kQueryWarp) {
+      role_queries(p, tab, c);
     } else if (lane == 0) {
       if (c.rank == 0) {
         if (warp == kIssueWarp) role_issue(p, tab, c);
       } else {
         if (warp == kIssueWarp) role_forward_tiles(c, B_KL, B_KF);
-        else if (warp == kVFwdWarp) role_forward_tiles(c, B_VL, B_VF);
-        else role_forward_queries(p, tab, c);
+        else role_forward_tiles(c, B_VL, B_VF);
         // this CTA's TMEM and shared memory are in use until the pair's last product is done
         if (warp == kIssueWarp) (void)mbar_wait_drain(c.bar(B_DRAIN), 0, kShDrainNs);
       }
@@ -825,7 +843,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-__global__ void __launch_bounds__(kOwnWarps * 32) own_kernel(const __grid_constant__ SharedParams p,
+__global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const __grid_constant__ SharedParams p,
                                                              const __grid_constant__ SharedSeqs tab) {
   __shared__ uint2 qf[16 * 32];
   __shared__ float comb[kOwnWarps][8][kHeadDim + 4];
@@ -1053,23 +1071,26 @@ __global__ void __launch_bounds__(kOwnWarps * 32) own_kernel(const __grid_consta
     p.own_o[((size_t)blockIdx.x * 64 + dq) * 8 + r] = acc;
   }
   if (threadIdx.x < 8) p.own_ml[(size_t)blockIdx.x * 8 + r] = make_float2(mx, ls);
-  wait_for_previous();  // this grid's end then means that the prefix pass has ended too
+  // This grid's end has to mean that the prefix pass has ended too.  One CTA
+  // waits for it, the last: the others leave their places to those still to come.
+  if (blockIdx.x == gridDim.x - 1) wait_for_previous();
 }
 
 // ====================================================================
 // Merge
 // ====================================================================
 // CTA = (sequence, kv head, 64 of the dims); thread (row i % G, dims 4 (i / G %
-// 16), every kMergeWays-th partial from i / (16 G) on), then the ways' parts
+// 16), every merge_ways-th partial from i / (16 G) on), then the ways' parts
 // through shared memory in a fixed order.  Bound by the latency of the partials'
-// loads: the ways and four loads a thread keep them in flight together.
-constexpr int kMergeWays = 8;
+// loads: the ways (as many as give a thread about four partials) and four loads
+// a thread keep them in flight together.
+constexpr int kMergeMostWays = 8;
 constexpr int kMergeDims = 64;
 
-__global__ void __launch_bounds__(8 * 16 * kMergeWays) merge_kernel(const __grid_constant__ SharedParams p,
+__global__ void __launch_bounds__(8 * 16 * kMergeMostWays) merge_kernel(const __grid_constant__ SharedParams p,
                                                                     const __grid_constant__ SharedSeqs tab) {
-  __shared__ float4 acc_sh[kMergeWays - 1][16 * 8];
-  __shared__ float2 ml_sh[kMergeWays - 1][16 * 8];
+  __shared__ float4 acc_sh[kMergeMostWays - 1][16 * 8];
+  __shared__ float2 ml_sh[kMergeMostWays - 1][16 * 8];
   const int s = blockIdx.x / p.HKV, g = blockIdx.x % p.HKV;
   const int slot = threadIdx.x % (16 * p.G), way = threadIdx.x / (16 * p.G);
   const int r = slot & (p.G - 1), dq = blockIdx.y * (kMergeDims / 4) + (slot >> p.log2_g);
@@ -1107,12 +1128,12 @@ __global__ void __launch_bounds__(8 * 16 * kMergeWays) merge_kernel(const __grid
     acc.z = fmaf(w, v.z, acc.z * f);
     acc.w = fmaf(w, v.w, acc.w * f);
   };
-  for (int i0 = way; i0 < n; i0 += 4 * kMergeWays) {
+  for (int i0 = way; i0 < n; i0 += 4 * p.merge_ways) {
     float2 ml[4];
     float4 v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int i = i0 + e * kMergeWays;
+      const int i = i0 + e * p.merge_ways;
       ml[e] = make_float2(-INFINITY, 0.f);
       v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < n_pre) {
@@ -1132,8 +1153,7 @@ __global__ void __launch_bounds__(8 * 16 * kMergeWays) merge_kernel(const __grid
   }
   __syncthreads();
   if (way > 0) return;
-#pragma unroll
-  for (int w = 0; w < kMergeWays - 1; ++w) add(ml_sh[w][slot], acc_sh[w][slot]);
+  for (int w = 0; w < p.merge_ways - 1; ++w) add(ml_sh[w][slot], acc_sh[w][slot]);
   const float il = l > 0.f ? 1.f / l : 0.f;
   const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * il, acc.y * il), b = __floats2bfloat162_rn(acc.z * il, acc.w * il);
   *reinterpret_cast<uint2*>(p.out + ((size_t)sq.x * p.HQ + (size_t)g * p.G + r) * kHeadDim + 4 * dq) =
@@ -1169,7 +1189,7 @@ cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, cud
     own_kernel<<<own_grid, kOwnWarps * 32, 0, st>>>(p, t);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  return launch_after(merge_kernel, dim3((unsigned)(p.n_seq * p.HKV), kHeadDim / kMergeDims), 16 * p.G * kMergeWays, p, t, st);
+  return launch_after(merge_kernel, dim3((unsigned)(p.n_seq * p.HKV), kHeadDim / kMergeDims), 16 * p.G * p.merge_ways, p, t, st);
 }
 
 }  // namespace pa

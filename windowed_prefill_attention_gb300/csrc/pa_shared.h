@@ -24,6 +24,7 @@ struct ShGroup {
 constexpr int kShPairs = 128;  // SM pairs of a launch at most
 
 constexpr int kShOwnListed = 1024;
+constexpr int kShOwnPerSm = 3;  // CTAs of the per-sequence pass on an SM at a time
 
 struct SharedSeqs {
   // {row in q / out, context length, chunks of the earlier sequences (per kv head), first block of its window}
@@ -55,6 +56,7 @@ struct SharedParams {
   int n_pairs;             // SM pairs of the prefix pass
   int chunk;               // blocks per CTA of the per-sequence pass
   int chunks_head;         // its CTAs per kv head
+  int merge_ways;          // threads that share a row's partials in the merge, 1 to 8
   float sm_scale_log2;
   // Partials: per row the reference (log2 units) and sum of its softmax, and
   // its unnormalised output, 4 dims x rows side by side.  Prefix: the partial
