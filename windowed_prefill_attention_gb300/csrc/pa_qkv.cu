@@ -29,168 +29,272 @@ namespace pa {
 namespace {
 
 constexpr int kQkvWarps = 8;
+constexpr int kQkvPerSm = 3;  // CTAs: 24 warps with four rows (2 KB) each in flight cover the loads' latency
 constexpr int kMaxPairs = kHeadDim / 2;
 constexpr unsigned kAll = 0xffffffffu;
+enum : int { TURN_NONE, TURN_HALVES, TURN_ADJACENT };
 
-__device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
+// A lane holds dims [8 lane, 8 lane + 8) of a row, as four pairs.
+struct Vals {
+  float2 v[4];
+};
+__device__ __forceinline__ Vals unpack8(const uint4 w) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  Vals x;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x[2 * j] = __uint_as_float(u[j] << 16);
-    x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-  }
+  for (int j = 0; j < 4; ++j) x.v[j] = make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
+  return x;
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+__device__ __forceinline__ uint4 pack8(const Vals& x) {
   uint32_t u[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+    const __nv_bfloat162 b = __float22bfloat162_rn(x.v[j]);
     u[j] = *reinterpret_cast<const uint32_t*>(&b);
   }
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  return v;
+
+// One value of each of N rows a lane, reduced over the warp's lanes.  Rows are
+// halved among the lanes as the distance halves (4 rows: 2 + 1 + 3 shuffles, and
+// one each to bring the results back to all lanes, in place of 5 each).
+template <bool kMax>
+__device__ __forceinline__ float combine(float a, float b) {
+  return kMax ? fmaxf(a, b) : a + b;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int N, bool kMax>
+__device__ __forceinline__ void warp_reduce(float (&v)[N], int lane) {
+  static_assert(N == 1 || N == 2 || N == 4, "rows of a batch");
+  if (N == 4) {
+    const bool up = lane & 16;
+    const float s0 = up ? v[0] : v[2 % N], s1 = up ? v[1 % N] : v[3 % N];
+    const float k0 = up ? v[2 % N] : v[0], k1 = up ? v[3 % N] : v[1 % N];
+    v[0] = combine<kMax>(k0, __shfl_xor_sync(kAll, s0, 16));
+    v[1 % N] = combine<kMax>(k1, __shfl_xor_sync(kAll, s1, 16));
+  }
+  if (N >= 2) {
+    const int d = N == 4 ? 8 : 16;
+    const bool up = lane & d;
+    const float s = up ? v[0] : v[1 % N], k = up ? v[1 % N] : v[0];
+    v[0] = combine<kMax>(k, __shfl_xor_sync(kAll, s, d));
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
+  for (int o = N == 4 ? 4 : (N == 2 ? 8 : 16); o > 0; o >>= 1) v[0] = combine<kMax>(v[0], __shfl_xor_sync(kAll, v[0], o));
+  if (N > 1) {
+    const float mine = v[0];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(kAll, mine, N == 4 ? 8 * i : 16 * i);
+  }
 }
 
-// Where a lane's rotation partners are.  The lane holds dims [8 lane, 8 lane +
-// 8).  Halves: dim i < R/2 pairs with i + R/2, a whole lane R/16 lanes away (R
-// is a multiple of 16).  Neighbours: dims 2i and 2i + 1, in the same word.
-struct Partner {
-  int lane;
-  bool halves;
-  __device__ __forceinline__ uint32_t word(uint32_t w) const {
-    return halves ? __shfl_sync(kAll, w, lane) : __byte_perm(w, w, 0x1032);
+// Where a lane's rotation partners are.  Halves: dim i < R/2 pairs with i + R/2,
+// a whole lane R/16 lanes away (R is a multiple of 16).  Neighbours: dims 2i and
+// 2i + 1, the two of a pair.
+template <int kTurn>
+__device__ __forceinline__ Vals partners(const uint4 raw, const Vals& x, int from) {
+  Vals p;
+  if (kTurn == TURN_HALVES) {
+    p = unpack8(make_uint4(__shfl_sync(kAll, raw.x, from), __shfl_sync(kAll, raw.y, from), __shfl_sync(kAll, raw.z, from),
+                           __shfl_sync(kAll, raw.w, from)));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p.v[j] = make_float2(x.v[j].y, x.v[j].x);
   }
-  __device__ __forceinline__ uint4 words(const uint4 w) const {
-    return make_uint4(word(w.x), word(w.y), word(w.z), word(w.w));
-  }
-};
+  return p;
+}
 
 // A and B of the lane's eight dims for one set of gains.
 struct Turn {
-  float a[8], b[8];
+  float2 a[4], b[4];
 };
-__device__ __forceinline__ void make_turn(const QkvParams& p, const __nv_bfloat16* w, const float2* cs, int lane,
-                                          const Partner& pt, Turn& t) {
-  float g[8], gp[8];
+template <int kTurn>
+__device__ __forceinline__ void make_turn(const QkvParams& p, const __nv_bfloat16* w, const float2* cs, int lane, int from,
+                                          Turn& t) {
+  Vals g, gp;
   if (w) {
     const uint4 raw = __ldg(reinterpret_cast<const uint4*>(w) + lane);
-    unpack8(raw, g);
-    unpack8(pt.words(raw), gp);
+    g = unpack8(raw);
+    if (kTurn != TURN_NONE) gp = partners<kTurn>(raw, g, from);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] += p.w_off, gp[e] += p.w_off;
+    for (int j = 0; j < 4; ++j) {
+      g.v[j] = add2(g.v[j], make_float2(p.w_off, p.w_off));
+      if (kTurn != TURN_NONE) gp.v[j] = add2(gp.v[j], make_float2(p.w_off, p.w_off));
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] = gp[e] = 1.f;
+    for (int j = 0; j < 4; ++j) g.v[j] = gp.v[j] = make_float2(1.f, 1.f);
   }
   const int d0 = 8 * lane, R = p.rope.rot_dim;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) t.a[e] = g[e], t.b[e] = 0.f;
-  if (d0 < R) {
+  for (int j = 0; j < 4; ++j) t.a[j] = g.v[j], t.b[j] = make_float2(0.f, 0.f);
+  if (kTurn != TURN_NONE && d0 < R) {
     const int half = R / 2;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const bool first = pt.halves ? d0 < half : (e & 1) == 0;
-      const float2 c = cs[pt.halves ? (d0 < half ? d0 : d0 - half) + e : (d0 + e) >> 1];
-      t.a[e] = g[e] * c.x;
-      t.b[e] = first ? -gp[e] * c.y : gp[e] * c.y;
+    for (int j = 0; j < 4; ++j) {
+      if (kTurn == TURN_HALVES) {
+        const bool first = d0 < half;
+        const float2 c0 = cs[(first ? d0 : d0 - half) + 2 * j], c1 = cs[(first ? d0 : d0 - half) + 2 * j + 1];
+        t.a[j] = mul2(g.v[j], make_float2(c0.x, c1.x));
+        t.b[j] = mul2(gp.v[j], first ? make_float2(-c0.y, -c1.y) : make_float2(c0.y, c1.y));
+      } else {
+        const float2 c = cs[(d0 >> 1) + j];
+        t.a[j] = mul2(g.v[j], make_float2(c.x, c.x));
+        t.b[j] = mul2(gp.v[j], make_float2(-c.y, c.y));
+      }
     }
   }
 }
 
-// The lane's eight values of a row, normed and turned.
-__device__ __forceinline__ void norm_turn(const uint4 raw, const Turn& t, const Partner& pt, bool rotate, float eps,
-                                          float (&y)[8]) {
-  float x[8];
-  unpack8(raw, x);
-  float ss = 0.f;
+// N rows into the pool: scale = absmax / 127, codes rint(x / scale) half to
+// even, decided on the IEEE quotients as kv_append_kernel decides them.  The
+// scale is Markstein's division by a constant (a product with RN(1/127) and one
+// correction by the exact remainder).  x * rcp, rcp the hardware reciprocal, is
+// within 3.1e-5 of x / scale (|quotient| <= 127.5), so only quotients within
+// 1e-4 of a half-integer take the division; adding 1.5 * 2^23 rounds the others
+// and leaves the code in the sum's low byte.  Rows with a subnormal scale, which
+// the approximate reciprocal flushes, take the division too.
+template <int N>
+__device__ __forceinline__ void store_codes(const Vals (&x)[N], int lane, int8_t* codes, float* scale_out) {
+  float am[N];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-  const float ms = warp_sum(ss) * (1.f / kHeadDim) + eps;
-  const float r = ms > 0.f ? rsqrtf(ms) : 0.f;  // an all-zero row with eps 0 stays zero
-  if (rotate) {
-    float xp[8];
-    unpack8(pt.words(raw), xp);
+  for (int i = 0; i < N; ++i) {
+    am[i] = fabsf(x[i].v[0].x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = r * fmaf(xp[e], t.b[e], x[e] * t.a[e]);
+    for (int j = 0; j < 4; ++j) am[i] = max3(am[i], fabsf(x[i].v[j].x), fabsf(x[i].v[j].y));
+  }
+  warp_reduce<N, true>(am, lane);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    constexpr float kInv127 = 1.0f / 127.0f;
+    const float q0 = __fmul_rn(am[i], kInv127);
+    const float scale = __fmaf_rn(__fmaf_rn(-q0, 127.f, am[i]), kInv127, q0);
+    constexpr float kRound = 12582912.f;  // 1.5 * 2^23
+    float rcp = 0.f;
+    if (scale > 0.f) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rcp) : "f"(scale));
+    uint32_t f[8];
+    float dmax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 q = mul2(x[i].v[j], make_float2(rcp, rcp));
+      const float2 s = add2(q, make_float2(kRound, kRound));
+      const float2 d = fma2(add2(s, make_float2(-kRound, -kRound)), make_float2(-1.f, -1.f), q);
+      dmax = max3(dmax, fabsf(d.x), fabsf(d.y));
+      f[2 * j] = __float_as_uint(s.x);
+      f[2 * j + 1] = __float_as_uint(s.y);
+    }
+    if (dmax > 0.4999f || (scale > 0.f && scale < 1.17549435e-38f)) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __float_as_uint(rintf(__fdiv_rn(x[i].v[j].x, scale)) + kRound);
+        f[2 * j + 1] = __float_as_uint(rintf(__fdiv_rn(x[i].v[j].y, scale)) + kRound);
+      }
+    }
+    const uint32_t lo = __byte_perm(__byte_perm(f[0], f[1], 0x0040), __byte_perm(f[2], f[3], 0x0040), 0x5410);
+    const uint32_t hi = __byte_perm(__byte_perm(f[4], f[5], 0x0040), __byte_perm(f[6], f[7], 0x0040), 0x5410);
+    reinterpret_cast<uint2*>(codes + i * kHeadDim)[lane] = make_uint2(lo, hi);
+    if (lane == 0) scale_out[i] = scale;
+  }
+}
+
+// N rows: loaded together, normed and turned (kNorm), stored as bf16 (kCodes
+// false; dst: the lane's 16 bytes of the first row) or as codes.
+template <int N, int kTurn, bool kNorm, bool kCodes>
+__device__ __forceinline__ void do_rows(const uint4* src, size_t step, const Turn& t, int from, float eps, int lane,
+                                        uint4* dst, int8_t* codes, float* scales, bool store) {
+  uint4 raw[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) raw[i] = src[i * step];
+  Vals y[N];
+  if (kNorm) {
+    float ss[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      y[i] = unpack8(raw[i]);
+      float2 s = mul2(y[i].v[0], y[i].v[0]);
+#pragma unroll
+      for (int j = 1; j < 4; ++j) s = fma2(y[i].v[j], y[i].v[j], s);
+      ss[i] = s.x + s.y;
+    }
+    warp_reduce<N, false>(ss, lane);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float ms = fmaf(ss[i], 1.f / kHeadDim, eps);
+      const float r = ms > 0.f ? rsqrtf(ms) : 0.f;  // an all-zero row with eps 0 stays zero
+      Vals xp;
+      if (kTurn != TURN_NONE) xp = partners<kTurn>(raw[i], y[i], from);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float2 v = mul2(y[i].v[j], t.a[j]);
+        if (kTurn != TURN_NONE) v = fma2(xp.v[j], t.b[j], v);
+        y[i].v[j] = mul2(v, make_float2(r, r));
+      }
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = r * (x[e] * t.a[e]);
+    for (int i = 0; i < N; ++i) y[i] = unpack8(raw[i]);
+  }
+  if (kCodes) {
+    if (store) store_codes<N>(y, lane, codes, scales);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) dst[i * (kHeadDim / 8)] = pack8(y[i]);
   }
 }
 
-// One row into the pool: scale = absmax / 127, codes rint(x / scale) half to
-// even, decided on the IEEE quotient as kv_append_kernel decides them.  x *
-// rcp, rcp the hardware reciprocal, is within 3.1e-5 of that quotient
-// (|quotient| <= 127.5), so only quotients within 1e-4 of a half-integer take
-// the division; adding 1.5 * 2^23 rounds the others and leaves the code in the
-// sum's low byte.  Rows with a subnormal scale, which the approximate
-// reciprocal flushes, take the division too.
-__device__ __forceinline__ void store_codes(const float (&x)[8], int lane, int8_t* codes, float* scale_out) {
-  float am = 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(x[e]));
-  am = warp_max(am);
-  const float scale = __fdiv_rn(am, 127.f);
-  constexpr float kRound = 12582912.f;  // 1.5 * 2^23
-  float rcp = 0.f;
-  if (scale > 0.f) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rcp) : "f"(scale));
-  uint32_t f[8];
-  float dmax = 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float q = x[e] * rcp, s = q + kRound;
-    dmax = fmaxf(dmax, fabsf(q - (s - kRound)));
-    f[e] = __float_as_uint(s);
+// Heads [a, b) of one kind of row of a token.
+template <int kTurn, bool kNorm, bool kCodes>
+__device__ __forceinline__ void do_heads(const RowsIn& in, size_t row, int a, int b, const Turn& t, int from, float eps,
+                                         int lane, __nv_bfloat16* out, int8_t* codes, float* scales, bool store) {
+  const size_t step = (size_t)in.hs / 8;
+  const uint4* src = reinterpret_cast<const uint4*>(in.p + row * in.ts + (size_t)a * in.hs) + lane;
+  uint4* dst = reinterpret_cast<uint4*>(out + (size_t)a * kHeadDim) + lane;
+  if (kCodes) codes += a * kHeadDim, scales += a;
+  int h = a;
+#pragma unroll 1
+  for (; h + 4 <= b; h += 4) {
+    do_rows<4, kTurn, kNorm, kCodes>(src, step, t, from, eps, lane, dst, codes, scales, store);
+    src += 4 * step;
+    dst += 4 * (kHeadDim / 8);
+    if (kCodes) codes += 4 * kHeadDim, scales += 4;
   }
-  if (dmax > 0.4999f || (scale > 0.f && scale < 1.17549435e-38f)) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = __float_as_uint(rintf(__fdiv_rn(x[e], scale)) + kRound);
+  if (h + 2 <= b) {
+    do_rows<2, kTurn, kNorm, kCodes>(src, step, t, from, eps, lane, dst, codes, scales, store);
+    h += 2;
+    src += 2 * step;
+    dst += 2 * (kHeadDim / 8);
+    if (kCodes) codes += 2 * kHeadDim, scales += 2;
   }
-  const uint32_t lo = __byte_perm(__byte_perm(f[0], f[1], 0x0040), __byte_perm(f[2], f[3], 0x0040), 0x5410);
-  const uint32_t hi = __byte_perm(__byte_perm(f[4], f[5], 0x0040), __byte_perm(f[6], f[7], 0x0040), 0x5410);
-  reinterpret_cast<uint2*>(codes)[lane] = make_uint2(lo, hi);
-  if (lane == 0) *scale_out = scale;
+  if (h < b) do_rows<1, kTurn, kNorm, kCodes>(src, step, t, from, eps, lane, dst, codes, scales, store);
 }
 
-enum : int { KIND_Q, KIND_K, KIND_V };
-
-// A warp takes items (token, part of its rows) with a grid stride.  Rows go
-// four at a time, all their loads before the first is used.
-constexpr int kBatch = 4;
-
-template <bool kAppend, int kCap>
-__global__ void __launch_bounds__(kQkvWarps * 32) qkv_kernel(const __grid_constant__ QkvParams p,
-                                                             const __grid_constant__ QkvSeqs<kCap> tab) {
+// A warp takes items (token, part of its rows: queries, keys, values in turn)
+// with a grid stride, rows four at a time, all their loads before the first is
+// used.
+template <bool kAppend, int kCap, int kTurn>
+__global__ void __launch_bounds__(kQkvWarps * 32, kQkvPerSm) qkv_kernel(const __grid_constant__ QkvParams p,
+                                                                        const __grid_constant__ QkvSeqs<kCap> tab) {
   __shared__ uint64_t turn[kMaxPairs];
   __shared__ int axis[kMaxPairs];
   __shared__ float2 cs_all[kQkvWarps][kMaxPairs];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pairs = p.rope.rot_dim / 2;
-  for (int i = threadIdx.x; i < pairs; i += kQkvWarps * 32) {
-    turn[i] = p.rope.turn[i];
-    axis[i] = p.rope.axis[i];
+  const int pairs = kTurn == TURN_NONE ? 0 : p.rope.rot_dim / 2;
+  if (kTurn != TURN_NONE) {
+    for (int i = threadIdx.x; i < pairs; i += kQkvWarps * 32) {
+      turn[i] = p.rope.turn[i];
+      axis[i] = p.rope.axis[i];
+    }
+    __syncthreads();
   }
-  __syncthreads();
   float2* cs = cs_all[warp];
-  Partner pt;
-  pt.halves = p.rope.pairing == PA_ROPE_HALF;
   const int hl = p.rope.rot_dim / 16;  // lanes of half the rotated dims
-  pt.lane = lane < hl ? lane + hl : (lane < 2 * hl ? lane - hl : lane);
+  const int from = lane < hl ? lane + hl : (lane < 2 * hl ? lane - hl : lane);
   const int n_rows = p.n_q + p.n_k + p.n_v;
   const long long n_items = (long long)p.n_tok * p.parts;
   for (long long item = (long long)blockIdx.x * kQkvWarps + warp; item < n_items;
        item += (long long)gridDim.x * kQkvWarps) {
-    const int i = (int)(item / p.parts);
-    const int r0 = (int)(item % p.parts) * p.rows_per_part, r1 = min(n_rows, r0 + p.rows_per_part);
+    const int i = p.parts == 1 ? (int)item : (int)(item / p.parts);
+    const int r0 = p.parts == 1 ? 0 : (int)(item - (long long)i * p.parts) * p.rows_per_part;
+    const int r1 = min(n_rows, r0 + p.rows_per_part);
     int row = i, tok = i, seq = 0;
     if (kAppend) {  // the launch's i-th token: its sequence, row and position
       if (p.same_len > 0) {
@@ -208,9 +312,17 @@ __global__ void __launch_bounds__(kQkvWarps * 32) qkv_kernel(const __grid_consta
       row = s.x + (i - s.z);
       tok = s.y + (i - s.z);
     }
+    int phys = -1;
+    if (kAppend && r1 > p.n_q) {
+      phys = __ldg(p.block_table + (size_t)(p.bt_row0 + seq) * p.bt_stride + tok / kPage);
+      if (phys < 0 || phys >= p.n_pool) {  // never dereferenced
+        if (lane == 0) atomicCAS(p.err, 0, DEV_ERR_BAD_PAGE);
+        phys = -1;
+      }
+    }
     // cosine and sine of the token's angles, one per pair
-    const bool turned = pairs > 0 && r0 < p.n_q + p.n_k;
-    if (turned) {
+    if (kTurn != TURN_NONE && r0 < p.n_q + p.n_k) {
+      __syncwarp();  // every lane has read cs before
       for (int j = lane; j < pairs; j += 32) {
         const int pos = p.pos ? __ldg(p.pos + (size_t)axis[j] * p.pos_stride + row) : tok;
         const uint64_t frac = turn[j] * (uint64_t)(int64_t)pos;
@@ -221,73 +333,48 @@ __global__ void __launch_bounds__(kQkvWarps * 32) qkv_kernel(const __grid_consta
       }
       __syncwarp();
     }
-    int phys = -1;
-    if (kAppend && r1 > p.n_q) {
-      phys = __ldg(p.block_table + (size_t)(p.bt_row0 + seq) * p.bt_stride + tok / kPage);
-      if (phys < 0 || phys >= p.n_pool) {  // never dereferenced
-        if (lane == 0) atomicCAS(p.err, 0, DEV_ERR_BAD_PAGE);
-        phys = -1;
-      }
-    }
     Turn t;
-    for (int kind = KIND_Q; kind <= (kAppend ? KIND_V : KIND_K); ++kind) {
-      const int base = kind == KIND_Q ? 0 : (kind == KIND_K ? p.n_q : p.n_q + p.n_k);
-      const int cnt = kind == KIND_Q ? p.n_q : (kind == KIND_K ? p.n_k : p.n_v);
-      const int a = max(r0 - base, 0), b = min(r1 - base, cnt);  // heads of this kind
-      if (a >= b) continue;
-      const RowsIn in = kind == KIND_Q ? p.q : (kind == KIND_K ? p.k : p.v);
-      const uint4* src = reinterpret_cast<const uint4*>(in.p + (size_t)row * in.ts) + lane;
-      const size_t hstep = (size_t)in.hs / 8;
-      bool made = kind == KIND_V;
-      for (int h0 = a; h0 < b; h0 += kBatch) {
-        uint4 raw[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          if (h0 + u < b) raw[u] = src[(size_t)(h0 + u) * hstep];
-        if (!made) {
-          make_turn(p, kind == KIND_Q ? p.qw : p.kw, cs, lane, pt, t);
-          made = true;
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          if (h0 + u >= b) break;
-          const int h = h0 + u;
-          float y[8];
-          if (kind == KIND_V) unpack8(raw[u], y);
-          else norm_turn(raw[u], t, pt, pairs > 0, p.eps, y);
-          if (kind == KIND_Q) {
-            reinterpret_cast<uint4*>(p.q_out + ((size_t)row * p.n_q + h) * kHeadDim)[lane] = pack8(y);
-          } else if (!kAppend) {
-            reinterpret_cast<uint4*>(p.k_out + ((size_t)row * p.n_k + h) * kHeadDim)[lane] = pack8(y);
-          } else if (phys >= 0) {
-            const size_t slot = ((size_t)phys * kPage + tok % kPage) * p.HKV + h;
-            if (kind == KIND_K) store_codes(y, lane, p.k_pool + slot * kHeadDim, p.k_scale + slot);
-            else store_codes(y, lane, p.v_pool + slot * kHeadDim, p.v_scale + slot);
-          }
-        }
-      }
+    if (r0 < p.n_q) {
+      make_turn<kTurn>(p, p.qw, cs, lane, from, t);
+      do_heads<kTurn, true, false>(p.q, row, r0, min(r1, p.n_q), t, from, p.eps, lane,
+                                   p.q_out + (size_t)row * p.n_q * kHeadDim, nullptr, nullptr, true);
     }
-    if (turned) __syncwarp();  // every lane has read cs before the next item's
+    const size_t slot = kAppend ? ((size_t)max(phys, 0) * kPage + tok % kPage) * p.HKV : 0;
+    const int ka = max(r0 - p.n_q, 0), kb = min(r1 - p.n_q, p.n_k);
+    if (ka < kb) {
+      make_turn<kTurn>(p, p.kw, cs, lane, from, t);
+      do_heads<kTurn, true, kAppend>(p.k, row, ka, kb, t, from, p.eps, lane, p.k_out + (size_t)row * p.n_k * kHeadDim,
+                                     p.k_pool + slot * kHeadDim, p.k_scale + slot, phys >= 0);
+    }
+    if (kAppend) {
+      const int va = max(r0 - p.n_q - p.n_k, 0), vb = r1 - p.n_q - p.n_k;
+      if (va < vb)
+        do_heads<TURN_NONE, false, true>(p.v, row, va, vb, t, from, 0.f, lane, p.k_out, p.v_pool + slot * kHeadDim,
+                                         p.v_scale + slot, phys >= 0);
+    }
   }
 }
 
 template <bool kAppend, int kCap>
 cudaError_t launch(const QkvParams& p, const QkvSeqs<kCap>& tab, int n_sm, cudaStream_t st) {
   const long long items = (long long)p.n_tok * p.parts;
-  const long long want = (items + kQkvWarps - 1) / kQkvWarps;
-  const int grid = (int)(want < (long long)n_sm * 8 ? want : (long long)n_sm * 8);
-  qkv_kernel<kAppend, kCap><<<grid, kQkvWarps * 32, 0, st>>>(p, tab);
+  const long long want = (items + kQkvWarps - 1) / kQkvWarps, most = (long long)n_sm * kQkvPerSm;
+  const int grid = (int)(want < most ? want : most);
+  if (p.rope.rot_dim == 0) qkv_kernel<kAppend, kCap, TURN_NONE><<<grid, kQkvWarps * 32, 0, st>>>(p, tab);
+  else if (p.rope.pairing == PA_ROPE_HALF) qkv_kernel<kAppend, kCap, TURN_HALVES><<<grid, kQkvWarps * 32, 0, st>>>(p, tab);
+  else qkv_kernel<kAppend, kCap, TURN_ADJACENT><<<grid, kQkvWarps * 32, 0, st>>>(p, tab);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 int qkv_rows_per_part(long long n_tok, int rows, int n_sm) {
-  const long long warps = (long long)n_sm * 16;
-  const long long per = (n_tok * rows + warps - 1) / warps;
-  const int want = (int)(per < rows ? (per < 1 ? 1 : per) : rows);
-  const int parts = (rows + want - 1) / want;
-  return (rows + parts - 1) / parts;
+  const long long warps = (long long)n_sm * kQkvPerSm * kQkvWarps;
+  // few tokens: as many warps as there are rows, up to a full GPU; then whole
+  // batches of four rows, until there are four items a warp to even out the end
+  long long per = (n_tok * rows + warps - 1) / warps;
+  if (per > 4) per = n_tok >= 4 * warps ? rows : (per + 15) / 16 * 4;
+  return (int)(per < rows ? per : rows);
 }
 
 cudaError_t launch_qk_norm_rope(const QkvParams& p, int n_sm, cudaStream_t st) {
