@@ -146,15 +146,16 @@ __device__ __forceinline__ void make_turn(const QkvParams& p, const __nv_bfloat1
 }
 
 // N rows into the pool: scale = absmax / 127, codes rint(x / scale) half to
-// even, decided on the IEEE quotients as kv_append_kernel decides them.  The
-// scale is Markstein's division by a constant (a product with RN(1/127) and one
-// correction by the exact remainder).  x * rcp, rcp the hardware reciprocal, is
-// within 3.1e-5 of x / scale (|quotient| <= 127.5), so only quotients within
-// 1e-4 of a half-integer take the division; adding 1.5 * 2^23 rounds the others
-// and leaves the code in the sum's low byte.  Rows with a subnormal scale, which
-// the approximate reciprocal flushes, take the division too.
+// even, decided on the IEEE quotients as kv_append_kernel decides them.  Both
+// divisions by Markstein's correction of an approximate quotient: with r near
+// 1/b, q0 = RN(a r), the remainder a - q0 b is exact in one FMA and RN(q0 +
+// remainder r) is RN(a / b).  For the scale r = RN(1/127); for the codes r is the
+// hardware reciprocal after one Newton step (checked for every bf16 absmax and
+// value, with a reciprocal up to an ulp off).  Adding 1.5 * 2^23 rounds a quotient
+// to an integer, half to even, and leaves the code in the sum's low byte.  A row
+// whose remainders could be subnormal is raised by 2^64 first, its scale too.
 template <int N>
-__device__ __forceinline__ void store_codes(const Vals (&x)[N], int lane, int8_t* codes, float* scale_out) {
+__device__ __forceinline__ void store_codes(Vals (&x)[N], int lane, int8_t* codes, float* scale_out) {
   float am[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -169,25 +170,24 @@ __device__ __forceinline__ void store_codes(const Vals (&x)[N], int lane, int8_t
     const float q0 = __fmul_rn(am[i], kInv127);
     const float scale = __fmaf_rn(__fmaf_rn(-q0, 127.f, am[i]), kInv127, q0);
     constexpr float kRound = 12582912.f;  // 1.5 * 2^23
-    float rcp = 0.f;
-    if (scale > 0.f) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rcp) : "f"(scale));
+    float b = scale;
+    if (scale < 8.077935669463161e-28f) {  // 2^-90
+      b *= 18446744073709551616.f;         // 2^64
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[i].v[j] = mul2(x[i].v[j], make_float2(18446744073709551616.f, 18446744073709551616.f));
+    }
+    float r = 0.f;
+    if (b > 0.f) {
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b));
+      r = __fmaf_rn(r, __fmaf_rn(-r, b, 1.f), r);
+    }
     uint32_t f[8];
-    float dmax = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 q = mul2(x[i].v[j], make_float2(rcp, rcp));
-      const float2 s = add2(q, make_float2(kRound, kRound));
-      const float2 d = fma2(add2(s, make_float2(-kRound, -kRound)), make_float2(-1.f, -1.f), q);
-      dmax = max3(dmax, fabsf(d.x), fabsf(d.y));
+      const float2 q = mul2(x[i].v[j], make_float2(r, r));
+      const float2 s = add2(fma2(fma2(q, make_float2(-b, -b), x[i].v[j]), make_float2(r, r), q), make_float2(kRound, kRound));
       f[2 * j] = __float_as_uint(s.x);
       f[2 * j + 1] = __float_as_uint(s.y);
-    }
-    if (dmax > 0.4999f || (scale > 0.f && scale < 1.17549435e-38f)) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[2 * j] = __float_as_uint(rintf(__fdiv_rn(x[i].v[j].x, scale)) + kRound);
-        f[2 * j + 1] = __float_as_uint(rintf(__fdiv_rn(x[i].v[j].y, scale)) + kRound);
-      }
     }
     const uint32_t lo = __byte_perm(__byte_perm(f[0], f[1], 0x0040), __byte_perm(f[2], f[3], 0x0040), 0x5410);
     const uint32_t hi = __byte_perm(__byte_perm(f[4], f[5], 0x0040), __byte_perm(f[6], f[7], 0x0040), 0x5410);
@@ -369,11 +369,12 @@ cudaError_t launch(const QkvParams& p, const QkvSeqs<kCap>& tab, int n_sm, cudaS
 }  // namespace
 
 int qkv_rows_per_part(long long n_tok, int rows, int n_sm) {
-  const long long warps = (long long)n_sm * kQkvPerSm * kQkvWarps;
-  // few tokens: as many warps as there are rows, up to a full GPU; then whole
-  // batches of four rows, until there are four items a warp to even out the end
-  long long per = (n_tok * rows + warps - 1) / warps;
-  if (per > 4) per = n_tok >= 4 * warps ? rows : (per + 15) / 16 * 4;
+  const long long warps = (long long)n_sm * kQkvPerSm * kQkvWarps, total = n_tok * rows;
+  // few rows: as many warps as there are rows, up to a full GPU; more: whole
+  // batches of four rows, about eight items a warp to even out the end (with
+  // four, 9776 tokens of 24 rows took 65 us instead of 57)
+  long long per = (total + warps - 1) / warps;
+  if (per > 4) per = (total + 32 * warps - 1) / (32 * warps) * 4;
   return (int)(per < rows ? per : rows);
 }
 
