@@ -322,7 +322,8 @@ int pa_decode_plan(int n_kv_heads, int slots, int n_seq, const pa_seq* seqs, int
  * many questions.  The prefix's keys are read once for all sequences (up to
  * 512 a launch) and multiplied with all their queries on the tensor cores;
  * each sequence's own keys are computed as pa_decode does, and the parts are
- * merged.  The result is pa_decode's on the same keys, but for the order of
+ * merged.  Where few sequences or a short prefix make that the slower way, by
+ * sizes alone, each sequence reads the prefix too.  The result is pa_decode's on the same keys, but for the order of
  * sums and the roundings of P' to fp16.
  *   block_table   row s holds sequence s's pages; the prefix's pages are those
  *                 of row 0, and the other rows' entries for it are not read
@@ -330,7 +331,7 @@ int pa_decode_plan(int n_kv_heads, int slots, int n_seq, const pa_seq* seqs, int
  *   others        as pa_decode; sequences must not share a row of q / out (PA_EINVAL)
  * A prefix page outside the pool is skipped for all sequences, one of a
  * sequence's own pages for that sequence (PA_EBADPAGE through pa_last_error).
- * Three kernel launches per 512 sequences, asynchronous on `stream`.  Calls on
+ * Two or three kernel launches per 512 sequences, asynchronous on `stream`.  Calls on
  * one handle share its work buffers: issue them, and replay graphs captured
  * from them, one after another.  The buffers grow by allocation; a call on a
  * capturing stream that would have to grow them returns PA_ENOMEM (make a call
@@ -341,7 +342,8 @@ int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, i
                      int n_sink_blk, int n_win_blk, float sm_scale, void* out, void* stream);
 
 /* Host-only, no GPU needed: how pa_decode_shared splits the work of one launch
- * (the first min(n_seq, 512) sequences) on a GPU of n_sm SMs.  prefix_out (may
+ * (the first min(n_seq, 512) sequences) on a GPU of n_sm SMs; prefix_pass as in
+ * pa_debug_decode_shared_pass (-1: what a call does).  prefix_out (may
  * be NULL) receives *n_prefix_runs entries of int32[8] = {SM pair, kv head, first
  * sequence, sequences, sink, lo, first, last}: entries first .. last - 1 of the
  * list of blocks 0 .. sink - 1, then lo, lo + 1, ... (the prefix's blocks that
@@ -352,8 +354,14 @@ int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, i
  * for what pa_decode_shared refuses of these arguments, or a list that does
  * not fit its cap. */
 int pa_decode_shared_plan(int n_q_heads, int n_kv_heads, int max_pages_per_seq, int n_sm, int n_seq,
-                          const pa_seq* seqs, int n_prefix, int n_sink_blk, int n_win_blk, int32_t* prefix_out,
-                          int prefix_cap, int* n_prefix_runs, int32_t* own_out, int own_cap, int* n_own_runs);
+                          const pa_seq* seqs, int n_prefix, int n_sink_blk, int n_win_blk, int prefix_pass,
+                          int32_t* prefix_out, int prefix_cap, int* n_prefix_runs, int32_t* own_out, int own_cap,
+                          int* n_own_runs);
+
+/* Test hook: whether the handle's pa_decode_shared calls compute the prefix once
+ * for all sequences: 1 always (where two sequences or more share one they see),
+ * 0 never, -1 by sizes (the default). */
+int pa_debug_decode_shared_pass(pa_handle h, int prefix_pass);
 
 /* Query rows per work unit: the G = n_q_heads / n_kv_heads q heads of one kv
  * head times PA_UNIT_ROWS / G consecutive tokens starting on a multiple of

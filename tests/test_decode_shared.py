@@ -20,9 +20,12 @@ def to_device(b):
 
 
 class Handle:
-    def __init__(self, b, **opts):
+    """A handle whose calls compute the prefix once (most batches here are so small that by size they would not)."""
+
+    def __init__(self, b, prefix_pass=1, **opts):
         import windowed_prefill_attention_gb300 as pa
         self.pa, self.h = pa, pa.pa_create(b.hq, b.hkv, b.n_pool, b.max_pages, **opts)
+        pa.pa_debug_decode_shared_pass(self.h, prefix_pass)
 
     def __enter__(self):
         return self.h
@@ -77,17 +80,39 @@ CASES = {
 }
 
 
+@pytest.mark.parametrize("prefix_pass", (1, 0))
 @pytest.mark.parametrize("case", sorted(CASES))
-def test_matches_the_definition(case):
+def test_matches_the_definition(case, prefix_pass):
     import windowed_prefill_attention_gb300 as pa
     b = CASES[case].make()
-    with Handle(b) as h:
+    with Handle(b, prefix_pass) as h:
         out = call(h, b, to_device(b))
         assert pa.pa_last_error(h) == 0
     check(b, out)
 
 
-def test_scales_of_every_magnitude():
+def test_passes_by_size_agree():
+    """Batches on both sides of the rule, each call's bits those of the pass that the rule names."""
+    import torch
+
+    import windowed_prefill_attention_gb300 as pa
+    for b, by_size in ((Batch(16, 2, 1024, (5, 40, 17), 1, 0, 31), 0),
+                       (Batch(8, 4, 4096, tuple(1 + 3 * i for i in range(40)), 1, 0, 32), 1)):
+        b.make()
+        d = to_device(b)
+        runs, _ = pa.pa_decode_shared_plan(b.hq, b.hkv, b.max_pages, 152, b.seqs, b.prefix, b.S, b.W)
+        assert (len(runs) > 0) == by_size
+        outs = []
+        for prefix_pass in (-1, by_size):
+            with Handle(b, prefix_pass) as h:
+                outs.append(call(h, b, d))
+                assert pa.pa_last_error(h) == 0
+        check(b, outs[0])
+        assert torch.equal(*(o.view(torch.int16) for o in outs))
+
+
+@pytest.mark.parametrize("prefix_pass", (1, 0))
+def test_scales_of_every_magnitude(prefix_pass):
     """K and V scales over many powers of two (falling and rising along the keys, zero among them)."""
     import windowed_prefill_attention_gb300 as pa
     b = Batch(8, 2, 1536, (40, 5, 333), 1, 0, 30).make()
@@ -97,7 +122,7 @@ def test_scales_of_every_magnitude():
             s *= (2.0 ** rng.integers(-9, 3, s.shape)).astype(np.float32)
     b.v_scale[b.block_table[0, 5]] = 0
     b.v_scale[b.block_table[0, :4]] *= np.float32(2.0 ** -40)
-    with Handle(b) as h:
+    with Handle(b, prefix_pass) as h:
         out = call(h, b, to_device(b))
         assert pa.pa_last_error(h) == 0
     check(b, out)
@@ -129,14 +154,15 @@ def test_equals_decode_and_repeats_bit_for_bit():
     assert np.all(diff <= 2 * bound)
 
 
-def test_bad_pages_are_skipped_and_reported():
+@pytest.mark.parametrize("prefix_pass", (1, 0))
+def test_bad_pages_are_skipped_and_reported(prefix_pass):
     """A prefix entry outside the pool: its keys leave every sequence's softmax; an own entry: that sequence's."""
     import windowed_prefill_attention_gb300 as pa
     b = CASES["ragged_tile"].make()
     d = to_device(b)
     gone = [int(b.block_table[0, 3]), int(b.block_table[1, b.prefix // 16 + 2])]
     b.block_table[0, 3], b.block_table[1, b.prefix // 16 + 2] = b.n_pool, -1
-    with Handle(b) as h:
+    with Handle(b, prefix_pass) as h:
         out = call(h, b, d, bt=dev(b.block_table))
         assert pa.pa_last_error(h) == pa.PA_EBADPAGE
         assert pa.pa_last_error(h) == 0
@@ -231,7 +257,8 @@ def test_first_calls_on_cold_memory_repeat_bit_for_bit():
             torch.cuda.empty_cache()
 
 
-def test_append_then_shared_decode():
+@pytest.mark.parametrize("prefix_pass", (1, 0))
+def test_append_then_shared_decode(prefix_pass):
     """A layer's step as a serving loop runs it: the prefix appended once, each sequence's own tokens in one batched
     append, a decode step of the batch, against the definition on the pool the calls wrote."""
     import torch
@@ -250,7 +277,7 @@ def test_append_then_shared_decode():
     ks, vs = (torch.full((b.n_pool, 16, 2), float("nan"), device="cuda") for _ in range(2))
     bt, qo = dev(b.block_table), torch.empty(tok, 16, 256, dtype=torch.bfloat16, device="cuda")
     out = torch.full_like(qo, float("nan"))
-    with Handle(b) as h:
+    with Handle(b, prefix_pass) as h:
         for seqs in ([(0, 0, b.prefix, b.prefix)], [(f, b.prefix, m, c) for f, m, c in zip(first, own, ctx)]):
             pa.pa_qkv_append(h, seqs, q, k, v, w, w, 1e-6, rope, None, bt, kp, vp, ks, vs, qo)
         last = first + own - 1

@@ -42,11 +42,13 @@ CASES = [
 ]
 
 
+@pytest.mark.parametrize("prefix_pass", (1, 0, -1))
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(x) for x in (c[0], c[1], c[2], c[3], len(c[4]), c[6])))
-def test_every_visible_block_is_computed_once(pa, case):
+def test_every_visible_block_is_computed_once(pa, case, prefix_pass):
     hq, hkv, n_sm, prefix, suffix, S, W = case
     seqs = np.array([(i, prefix + x - 1, 1, prefix + x) for i, x in enumerate(suffix)], np.int32)
-    pre, own = pa.pa_decode_shared_plan(hq, hkv, 1 << 20, n_sm, seqs, prefix, S, W)
+    pre, own = pa.pa_decode_shared_plan(hq, hkv, 1 << 20, n_sm, seqs, prefix, S, W, prefix_pass)
+    assert prefix_pass or not len(pre)
     n, pb = min(512, len(suffix)), prefix // 16
     done = {}  # (sequence, head) -> blocks of its own passes
     for s, g, base, sink, lo, first, last in own.tolist():
@@ -93,11 +95,22 @@ def test_every_visible_block_is_computed_once(pa, case):
         assert len(cost) == max(1, n_sm // 2) or cost.max() <= cost.sum() // len(cost) + 5
 
 
+def test_prefix_pass_by_size(pa):
+    """Few sequences or a short prefix: every sequence reads it; many on a long one: once for all."""
+    def runs(n, prefix, **kw):
+        seqs = [(i, prefix + 9, 1, prefix + 10) for i in range(n)]
+        return len(pa.pa_decode_shared_plan(16, 2, 1 << 20, 152, seqs, prefix, 1, 0, **kw)[0])
+    assert runs(3, 1024) == 0 < runs(3, 1024, prefix_pass=1)
+    assert runs(250, 16) == 0
+    assert runs(64, 32768) > 0 == runs(64, 32768, prefix_pass=0)
+    assert runs(1, 32768, prefix_pass=1) == 0
+
+
 def test_plan_refusals(pa):
     ok = [(0, 99, 1, 100), (1, 119, 1, 120)]
 
-    def plan(hq=8, hkv=2, pages=100, n_sm=152, seqs=ok, prefix=64, S=1, W=0):
-        return pa.pa_decode_shared_plan(hq, hkv, pages, n_sm, seqs, prefix, S, W)
+    def plan(hq=8, hkv=2, pages=100, n_sm=152, seqs=ok, prefix=64, S=1, W=0, prefix_pass=-1):
+        return pa.pa_decode_shared_plan(hq, hkv, pages, n_sm, seqs, prefix, S, W, prefix_pass)
     plan()
     plan(prefix=96)
     plan(W=-1)
@@ -105,15 +118,17 @@ def test_plan_refusals(pa):
                 dict(prefix=-16), dict(prefix=60), dict(prefix=112), dict(prefix=1 << 20), dict(S=-1), dict(seqs=[]),
                 dict(seqs=[(0, 99, 2, 101)]), dict(seqs=[(0, 98, 1, 100)]), dict(seqs=[(-1, 99, 1, 100)]),
                 dict(seqs=[(0, 99, 1, 100), (0, 119, 1, 120)]), dict(seqs=[(0, 2 ** 31 - 2, 1, 2 ** 31 - 1)]),
-                dict(seqs=[(2 ** 30, 99, 1, 100)])):
+                dict(seqs=[(2 ** 30, 99, 1, 100)]), dict(prefix_pass=2), dict(prefix_pass=-2)):
         with pytest.raises(pa.PAError):
             plan(**bad)
     n = C.c_int()
-    assert pa._lib.pa_decode_shared_plan(8, 2, 100, 152, 2, pa._seqs(ok), 64, 1, 0, None, 0, None, None, 0,
-                                         C.byref(n)) == pa.PA_EINVAL
+    assert pa._lib.pa_decode_shared_plan(8, 2, 100, 152, 2, pa._seqs(ok), 64, 1, 0, 1, None, 0, None, None,
+                                         0, C.byref(n)) == pa.PA_EINVAL
     buf = np.zeros(8, np.int32)
-    assert pa._lib.pa_decode_shared_plan(8, 2, 100, 152, 2, pa._seqs(ok), 64, 1, 0, buf.ctypes.data, 1, C.byref(n),
-                                         None, 0, C.byref(n)) == pa.PA_EINVAL
+    for prefix_pass, pre, own in ((1, buf.ctypes.data, None), (1, None, buf.ctypes.data), (0, None, buf.ctypes.data)):
+        assert pa._lib.pa_decode_shared_plan(8, 2, 100, 152, 2, pa._seqs(ok), 64, 1, 0, prefix_pass, pre, 1, C.byref(n),
+                                             own, 1, C.byref(n)) == pa.PA_EINVAL
+    assert pa._lib.pa_debug_decode_shared_pass(None, 1) == pa.PA_EINVAL
 
 
 def test_null_handle_is_refused(pa):

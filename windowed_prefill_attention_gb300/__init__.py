@@ -36,7 +36,8 @@ EXPORTED = ("pa_default_options", "pa_create", "pa_destroy", "pa_prefill", "pa_p
             "pa_last_error", "pa_timing", "pa_strerror", "pa_plan", "pa_plan_pairs", "pa_host_chunks", "pa_decode_plan",
             "pa_debug_gather",
             "pa_debug_maskset", "pa_debug_qcodes", "pa_debug_copy_streams_idle", "pa_prefill_noalloc",
-            "pa_debug_noalloc_units", "pa_debug_qk_norm_rope_check", "pa_debug_qkv_append_check")
+            "pa_debug_noalloc_units", "pa_debug_qk_norm_rope_check", "pa_debug_qkv_append_check",
+            "pa_debug_decode_shared_pass")
 
 
 class pa_options(C.Structure):
@@ -79,8 +80,9 @@ _lib.pa_debug_qk_norm_rope_check.argtypes = [_i, _i] + _lib.pa_qk_norm_rope.argt
 _lib.pa_debug_qkv_append_check.argtypes = [_i, _i, _i] + _lib.pa_qkv_append.argtypes[1:-1]
 _lib.pa_decode.argtypes = _lib.pa_prefill_batch.argtypes
 _lib.pa_decode_shared.argtypes = [_vp, _i, _vp, _i, _i] + [_vp] * 6 + [_i, _i, _f, _vp, _vp]
-_lib.pa_decode_shared_plan.argtypes = ([_i] * 5 + [C.POINTER(pa_seq)] + [_i] * 3
+_lib.pa_decode_shared_plan.argtypes = ([_i] * 5 + [C.POINTER(pa_seq)] + [_i] * 4
                                        + [_vp, _i, C.POINTER(_i), _vp, _i, C.POINTER(_i)])
+_lib.pa_debug_decode_shared_pass.argtypes = [_vp, _i]
 _lib.pa_last_error.argtypes = [_vp, _vp]
 _lib.pa_timing.argtypes = [_vp, _i, C.POINTER(C.c_double), C.POINTER(C.c_double), C.POINTER(_i)]
 _lib.pa_strerror.argtypes = [_i]
@@ -497,12 +499,18 @@ def pa_decode_plan(n_kv_heads, slots, seqs, n_sink_blk, n_win_blk):
     return runs, per_cta.value, max_slots.value, bool(listed.value), total.value
 
 
-def pa_decode_shared_plan(n_q_heads, n_kv_heads, max_pages_per_seq, n_sm, seqs, n_prefix, n_sink_blk, n_win_blk):
+def pa_debug_decode_shared_pass(h, prefix_pass) -> None:
+    """Test hook: 1 / 0 / -1, whether pa_decode_shared computes the prefix once for all sequences (see include/pa.h)."""
+    _check(_lib.pa_debug_decode_shared_pass(h, prefix_pass), "pa_debug_decode_shared_pass")
+
+
+def pa_decode_shared_plan(n_q_heads, n_kv_heads, max_pages_per_seq, n_sm, seqs, n_prefix, n_sink_blk, n_win_blk,
+                          prefix_pass=-1):
     """Host-only: pa_decode_shared's work split of one launch (see include/pa.h): (prefix runs int32 [n, 8],
     own runs int32 [m, 7])."""
     s = _seqs(seqs)
     n, m = C.c_int(), C.c_int()
-    args = (n_q_heads, n_kv_heads, max_pages_per_seq, n_sm, len(s), s, n_prefix, n_sink_blk, n_win_blk)
+    args = (n_q_heads, n_kv_heads, max_pages_per_seq, n_sm, len(s), s, n_prefix, n_sink_blk, n_win_blk, prefix_pass)
     _check(_lib.pa_decode_shared_plan(*args, None, 0, C.byref(n), None, 0, C.byref(m)), "pa_decode_shared_plan")
     pre, own = np.zeros((n.value, 8), dtype=np.int32), np.zeros((m.value, 7), dtype=np.int32)
     _check(_lib.pa_decode_shared_plan(*args, pre.ctypes.data_as(C.c_void_p), n.value, C.byref(n),

@@ -250,6 +250,7 @@ struct pa_ctx {
   // shared-prefix decode: partials of the prefix and of the sequences' own keys.  A buffer that became too
   // small is kept until the handle goes, since a captured graph may still write it.
   Workspace sh_pre, sh_own;
+  int sh_pass = -1;  // pa_debug_decode_shared_pass
 
   // host-buffer path staging
   void* hb[7] = {nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
@@ -1524,6 +1525,17 @@ int pa_decode_plan(int n_kv_heads, int slots, int n_seq, const pa_seq* seqs, int
   return PA_OK;
 }
 
+namespace {
+// The pool as uint8 [n_pool * 16][HKV][256]; a box is one kv head's 16 token rows of half the dims.
+int pool_maps(pa_handle h, const int8_t* k_pool, const int8_t* v_pool, DecodeMaps& m) {
+  const uint64_t dims[3] = {(uint64_t)kHeadDim, (uint64_t)h->HKV, (uint64_t)h->n_pool * kPage};
+  const uint64_t strides[2] = {(uint64_t)kHeadDim, (uint64_t)h->HKV * kHeadDim};
+  const uint32_t box[3] = {128, 1, (uint32_t)kPage};
+  const int rc = encode(&m.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, k_pool, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  return rc ? rc : encode(&m.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, v_pool, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+}  // namespace
+
 int pa_decode(pa_handle h, int n_seq, const pa_seq* seqs, const void* q, const int8_t* k_pool, const int8_t* v_pool,
               const float* k_scale, const float* v_scale, const int32_t* block_table, int n_sink_blk, int n_win_blk,
               float sm_scale, void* out, void* stream) {
@@ -1554,16 +1566,8 @@ int pa_decode(pa_handle h, int n_seq, const pa_seq* seqs, const void* q, const i
     PA_CUDA(cudaMemsetAsync(h->d_tickets, 0, (size_t)h->tickets_cap * sizeof(unsigned long long), st));
   }
   if (k_pool != h->dec_kp || v_pool != h->dec_vp) {
-    // the pool as uint8 [n_pool * 16][HKV][256]; a box is one kv head's 16 token rows of half the dims
-    const uint64_t dims[3] = {(uint64_t)kHeadDim, (uint64_t)h->HKV, (uint64_t)h->n_pool * kPage};
-    const uint64_t strides[2] = {(uint64_t)kHeadDim, (uint64_t)h->HKV * kHeadDim};
-    const uint32_t box[3] = {128, 1, (uint32_t)kPage};
     h->dec_kp = h->dec_vp = nullptr;
-    if ((rc = encode(&h->dec_maps.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, k_pool, dims, strides, box,
-                     CU_TENSOR_MAP_SWIZZLE_128B)) ||
-        (rc = encode(&h->dec_maps.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, v_pool, dims, strides, box,
-                     CU_TENSOR_MAP_SWIZZLE_128B)))
-      return rc;
+    if ((rc = pool_maps(h, k_pool, v_pool, h->dec_maps))) return rc;
     h->dec_kp = k_pool;
     h->dec_vp = v_pool;
   }
@@ -1663,7 +1667,7 @@ bool shared_pack(const int* nt, int n_groups, int budget, int max_pairs, int* cu
 }
 
 int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, int n, int n_prefix, int S, int W,
-                        SharedParams& p, SharedSeqs& t) {
+                       int prefix_pass, SharedParams& p, SharedSeqs& t) {
   const int G = HQ / HKV, Pb = n_prefix / kPage;
   p.n_seq = n;
   p.bt_row0 = s0;
@@ -1692,12 +1696,16 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
   if ((long long)HKV * p.tiles_head >= (1ll << 30)) return PA_EINVAL;
   // Blocks of the per-sequence pass, and its CTAs for a chunk size.
   long long own = 0;
-  for (int s = 0; s < n; ++s) {
-    const pa_seq& q = seqs[s0 + s];
-    const int lo = shared_win_lo(q.n_ctx, W), own_n = shared_own(q.n_ctx, lo, p.first_blk, S, W).n;
-    t.s[s] = make_int4(q.q_off, q.n_ctx, own_n, lo);  // .z: the blocks until the chunks are counted
-    own += own_n;
-  }
+  auto count_own = [&] {
+    own = 0;
+    for (int s = 0; s < n; ++s) {
+      const pa_seq& q = seqs[s0 + s];
+      const int lo = shared_win_lo(q.n_ctx, W), own_n = shared_own(q.n_ctx, lo, p.first_blk, S, W).n;
+      t.s[s] = make_int4(q.q_off, q.n_ctx, own_n, lo);  // .z: the blocks until the chunks are counted
+      own += own_n;
+    }
+  };
+  count_own();
   auto own_ctas = [&](int chunk) {
     long long c = 0;
     for (int s = 0; s < n; ++s) c += (t.s[s].z + chunk - 1) / chunk;
@@ -1715,12 +1723,12 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
   // GB300 measures (microseconds; an own block and CTA as the SM time they take).
   const int T = HKV * p.tiles_head, max_pairs = std::min(kShPairs, std::max(1, n_sm / 2)), J = HKV * p.n_grp;
   p.n_pairs = 0;
+  p.merge_ways = 0;
   p.chunk = own_chunk(kShOwnPerSm * n_sm);
+  int nt[8 * kShGroups], pairs = max_pairs;
   if (T > 0) {
-    int nt[8 * kShGroups];
     for (int j = 0; j < J; ++j) nt[j] = (t.grp[j % p.n_grp].n_blk + kTileBlocks - 1) / kTileBlocks;
     double best = 1e30;
-    int pairs = max_pairs;
     const double own_us = kShOwnBlockUs * own * HKV + kShOwnCtaUs * own_ctas(p.chunk);
     for (int left = 0; left < max_pairs; left += 4) {
       const int use = std::min(max_pairs - left, T), free_sm = n_sm - 2 * use;
@@ -1734,6 +1742,16 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
       }
       if (rest <= 0.0) break;  // fewer pairs only make the prefix pass longer
     }
+    // With few sequences or a short prefix it is quicker that each reads the prefix too.
+    long long all = own * HKV;
+    for (int s = 0; s < n; ++s) all += (long long)HKV * t.grp[s / per].n_blk;
+    if (prefix_pass < 0 ? kShOwnTailUs + kShOwnBlockUs * all / n_sm < best : prefix_pass == 0) {
+      p.n_grp = p.tiles_head = p.first_blk = 0;
+      count_own();
+      p.chunk = own_chunk(kShOwnPerSm * n_sm);
+    }
+  }
+  if (p.tiles_head > 0) {
     int budget = (T + pairs - 1) / pairs;
     while (!shared_pack(nt, J, budget, pairs, t.cut, p.n_pairs)) ++budget;
     int x = 0, c = 0, most = 0;
@@ -1798,11 +1816,13 @@ int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, i
   size_t pre = 0, own = 0;
   for (int s0 = 0; s0 < n_seq; s0 += kShSeqs) {
     if ((rc = decode_shared_plan(h->HQ, h->HKV, h->n_sm, seqs, s0, std::min(kShSeqs, n_seq - s0), n_prefix, n_sink_blk,
-                                 n_win_blk, p, t)))
+                                 n_win_blk, h->sh_pass, p, t)))
       return rc;
     pre = std::max(pre, pre_partials(p));
     own = std::max(own, own_partials(p));
   }
+  DecodeMaps maps;
+  if ((rc = pool_maps(h, k_pool, v_pool, maps))) return rc;
   const bool capturing = capture != cudaStreamCaptureStatusNone;
   if ((rc = reserve(h->sh_pre, pre * (kPrePartial + kPreStats), capturing))) return rc;
   if ((rc = reserve(h->sh_own, own * (kOwnPartial + kOwnStats), capturing))) return rc;
@@ -1825,22 +1845,29 @@ int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, i
   for (int s0 = 0; s0 < n_seq; s0 += kShSeqs) {
     if (n_seq > kShSeqs)
       (void)decode_shared_plan(h->HQ, h->HKV, h->n_sm, seqs, s0, std::min(kShSeqs, n_seq - s0), n_prefix, n_sink_blk,
-                               n_win_blk, p, t);
-    PA_CUDA(launch_decode_shared(p, t, st));
+                               n_win_blk, h->sh_pass, p, t);
+    PA_CUDA(launch_decode_shared(p, t, maps, st));
   }
   return PA_OK;
 }
 
+int pa_debug_decode_shared_pass(pa_handle h, int prefix_pass) {
+  if (!h || prefix_pass < -1 || prefix_pass > 1) return PA_EINVAL;
+  h->sh_pass = prefix_pass;
+  return PA_OK;
+}
+
 int pa_decode_shared_plan(int n_q_heads, int n_kv_heads, int max_pages_per_seq, int n_sm, int n_seq,
-                          const pa_seq* seqs, int n_prefix, int n_sink_blk, int n_win_blk, int32_t* prefix_out,
-                          int prefix_cap, int* n_prefix_runs, int32_t* own_out, int own_cap, int* n_own_runs) {
-  if (n_sm < 1 || max_pages_per_seq < 1 || !n_prefix_runs || !n_own_runs) return PA_EINVAL;
+                          const pa_seq* seqs, int n_prefix, int n_sink_blk, int n_win_blk, int prefix_pass,
+                          int32_t* prefix_out, int prefix_cap, int* n_prefix_runs, int32_t* own_out, int own_cap,
+                          int* n_own_runs) {
+  if (n_sm < 1 || prefix_pass < -1 || prefix_pass > 1 || max_pages_per_seq < 1 || !n_prefix_runs || !n_own_runs) return PA_EINVAL;
   int rc = decode_shared_check(n_q_heads, n_kv_heads, max_pages_per_seq, n_seq, seqs, n_prefix, n_sink_blk, 1.f);
   if (rc) return rc;
   SharedParams p{};
   SharedSeqs t;
   if ((rc = decode_shared_plan(n_q_heads, n_kv_heads, n_sm, seqs, 0, std::min(n_seq, kShSeqs), n_prefix, n_sink_blk,
-                               n_win_blk, p, t)))
+                               n_win_blk, prefix_pass, p, t)))
     return rc;
   const int per = kUnitRows / p.G;
   int np = 0;

@@ -73,6 +73,12 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+// Volatile, so that it stays behind the wait that made the data visible.
+__device__ __forceinline__ uint4 lds_u32x4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // 16 TMEM lanes x 128 columns in the 16x256b shape (see pa_ptx.cuh).
@@ -826,10 +832,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
 // CTA = (sequence, kv head, chunk of its visible blocks); its four warps take
 // the blocks in turn.  Products as in the decode kernel, on mma.sync in the
 // transposed orientation, S^T = K Q^T and O^T = V^T P^T: keys and dims fill M,
-// the G <= 8 query rows N.  A thread's operand bytes are whole 16-byte pieces of
-// the pool's rows (the dims are permuted, Q and O alike), so they are loaded
-// from global memory straight into registers.
+// the G <= 8 query rows N.  A warp's blocks come by TMA into two stages of its
+// own, K and V with a barrier each, a stage's K filled again as soon as its
+// scores are done: one to two blocks a warp are always on their way.  Which dims
+// a thread's operands hold is free as long as Q and O agree: chosen so that its
+// 16-byte reads of the 128-byte swizzled rows have no bank conflicts.
 constexpr int kOwnWarps = 4;
+constexpr int kOwnStage = 8192;                              // K and V of a block, each two halves of [16][128]
+constexpr int kOwnRing = 2 * kOwnStage;                      // a warp's; at the end its partial output [8][kOwnPitch]
+constexpr int kOwnPitch = kHeadDim + 4;
+constexpr int kOwnQ = kOwnWarps * kOwnRing;                  // [16][32] uint2: Q's fragments
+constexpr int kOwnRow = kOwnQ + 16 * 32 * 8;                 // [8] the rows' factors
+constexpr int kOwnML = kOwnRow + 8 * 4;                      // [2][warps][8] the warps' references and sums
+constexpr int kOwnBar = kOwnML + 2 * kOwnWarps * 8 * 4;      // [warps][stage][K, V]
+constexpr int kOwnSmem = kOwnBar + kOwnWarps * 4 * 8;
+static_assert(kOwnSmem * kShOwnPerSm <= 224 * 1024 && 8 * kOwnPitch * 4 <= kOwnRing && kOwnBar % 8 == 0, "shared memory");
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -844,11 +861,19 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 
 __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const __grid_constant__ SharedParams p,
-                                                             const __grid_constant__ SharedSeqs tab) {
-  __shared__ uint2 qf[16 * 32];
-  __shared__ float comb[kOwnWarps][8][kHeadDim + 4];
-  __shared__ float rowc[8], wm[kOwnWarps][8], wl[kOwnWarps][8];
+                                                             const __grid_constant__ SharedSeqs tab,
+                                                             const __grid_constant__ DecodeMaps maps) {
+  extern __shared__ __align__(1024) uint8_t raw[];
   dependents_may_start();
+  const uint32_t sb = smem_u32(raw);
+  if (sb & 1023u) {  // every thread: nothing was started
+    if (threadIdx.x == 0) atomicCAS(p.err, 0, DEV_ERR_LAYOUT);
+    return;
+  }
+  uint2* qf = reinterpret_cast<uint2*>(raw + kOwnQ);
+  float* rowc = reinterpret_cast<float*>(raw + kOwnRow);
+  float (*wm)[8] = reinterpret_cast<float(*)[8]>(raw + kOwnML);
+  float (*wl)[8] = wm + kOwnWarps;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
   // the CTA's sequence (listed for the launch's first CTAs), kv head and chunk
   int lo = 0, hi = p.n_seq - 1;
@@ -877,6 +902,29 @@ __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const 
       atomicCAS(p.err, 0, DEV_ERR_BAD_PAGE);
     }
   }
+  const int n_it = b1 > b0 + warp ? (b1 - b0 - warp + kOwnWarps - 1) / kOwnWarps : 0;
+  const uint32_t ring = sb + warp * kOwnRing, bars = sb + kOwnBar + 32 * warp;
+  // a block of a bad page (skipped below) loads page 0
+  auto page_of = [&](int it) { return max(0, __shfl_sync(kAllLanes, page, it)); };
+  auto load = [&](int it, int v) {  // K or V of block it into its stage
+    const int phys = page_of(it);
+    if (lane == 0) {
+      const uint32_t dst = ring + (it & 1) * kOwnStage + v * (kOwnStage / 2), bar = bars + 16 * (it & 1) + 8 * v;
+      const CUtensorMap* map = v ? &maps.v : &maps.k;
+      mbar_expect_tx(bar, kOwnStage / 2);
+      tma_load_3d(dst, map, bar, 0, g, phys * kPage);
+      tma_load_3d(dst + kOwnStage / 4, map, bar, 128, g, phys * kPage);
+    }
+  };
+  if (lane == 0) {
+    for (int i = 0; i < 4; ++i) mbar_init(bars + 8 * i, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  for (int it = 0; it < 2 && it < n_it; ++it) {
+    load(it, 0);
+    load(it, 1);
+  }
   {  // the G query rows as B fragments: thread row r, dims [16 c, 16 c + 16)
     const int r = threadIdx.x >> 4, cc = threadIdx.x & 15;
     float v[16];
@@ -897,7 +945,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const 
     const float mul = pow2i(k);
 #pragma unroll
     for (int m = 0; m < 4; ++m)
-      qf[(4 * (cc >> 2) + m) * 32 + 4 * r + (cc & 3)] =
+      qf[(4 * (2 * (cc >> 3) + (cc & 1)) + m) * 32 + 4 * r + (cc >> 1 & 3)] =
           make_uint2(pack_f16x2(v[4 * m] * mul, v[4 * m + 1] * mul), pack_f16x2(v[4 * m + 2] * mul, v[4 * m + 3] * mul));
     if (cc == 0) rowc[r] = r < p.G ? pow2i(-k) * p.sm_scale_log2 : 0.f;
   }
@@ -908,55 +956,35 @@ __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const 
   float o[16][4];
 #pragma unroll
   for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  const size_t tok = (size_t)p.HKV * kHeadDim;
-  // K: rows gq and gq + 8, dims 64 j + 16 tq; V: keys 2tq, 2tq+1, 2tq+8, 2tq+9,
-  // dims 32 gq.  The next block's K is loaded as soon as this block's scores are
-  // done with the registers, its V after this block's products: a block's loads
-  // are in flight during the other half of the work.
-  uint4 kr[4][2], vr[2][4];
+  // the scales of keys gq and gq + 8, a block ahead
   float ks0 = 0.f, ks1 = 0.f, vr0 = 0.f, vr1 = 0.f;
-  const int n_it = b1 > b0 + warp ? (b1 - b0 - warp + kOwnWarps - 1) / kOwnWarps : 0;
-  // a block of a bad page (skipped below) loads page 0
-  auto page_of = [&](int it) { return max(0, __shfl_sync(kAllLanes, page, it)); };
-  auto load_k = [&](int it) {
-    const int phys = page_of(it);
-    const int8_t* kp = p.k_pool + (size_t)phys * kPage * tok + (size_t)g * kHeadDim + 16 * tq;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      kr[j][0] = ldg_stream(kp + (size_t)gq * tok + 64 * j);
-      kr[j][1] = ldg_stream(kp + (size_t)(gq + 8) * tok + 64 * j);
-    }
-    const size_t s0 = ((size_t)phys * kPage + gq) * p.HKV + g;
+  auto load_scales = [&](int it) {
+    const size_t s0 = ((size_t)page_of(it) * kPage + gq) * p.HKV + g;
     ks0 = __ldg(p.k_scale + s0);
     ks1 = __ldg(p.k_scale + s0 + 8 * (size_t)p.HKV);
-  };
-  auto load_v = [&](int it) {
-    const int phys = page_of(it);
-    const int8_t* vp = p.v_pool + (size_t)phys * kPage * tok + (size_t)g * kHeadDim + 32 * gq;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int8_t* at = vp + (size_t)(2 * tq + (k & 1) + 8 * (k >> 1)) * tok;
-      vr[0][k] = __ldg(reinterpret_cast<const uint4*>(at));
-      vr[1][k] = __ldg(reinterpret_cast<const uint4*>(at + 16));
-    }
-    const size_t s0 = ((size_t)phys * kPage + gq) * p.HKV + g;
     vr0 = __ldg(p.v_scale + s0);
     vr1 = __ldg(p.v_scale + s0 + 8 * (size_t)p.HKV);
   };
-  if (n_it > 0) {
-    load_k(0);
-    load_v(0);
-  }
-  for (int it = 0; it < n_it; ++it) {
+  if (n_it > 0) load_scales(0);
+  const WaitCtl wc{p.err, p.wait_ns};
+  int it = 0, n_k = min(n_it, 2), n_v = n_k;  // copies issued
+  for (; it < n_it; ++it) {
     const int b = b0 + warp + kOwnWarps * it;
+    const uint32_t stage = ring + (it & 1) * kOwnStage, bar = bars + 16 * (it & 1);
     const bool good = __shfl_sync(kAllLanes, page, it) >= 0;
     float sacc[4][4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) sacc[m][0] = sacc[m][1] = sacc[m][2] = sacc[m][3] = 0.f;
+    const float s_k0 = ks0, s_k1 = ks1, s_v0 = vr0, s_v1 = vr1;
+    if (it + 1 < n_it) load_scales(it + 1);
+    if (!__all_sync(kAllLanes, mbar_wait(bar, (it >> 1) & 1, wc, 120))) break;
+    // K: rows gq and gq + 8, dims 128 (j / 2) + 32 tq + 16 (j % 2)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t w0[4] = {kr[j][0].x, kr[j][0].y, kr[j][0].z, kr[j][0].w};
-      const uint32_t w1[4] = {kr[j][1].x, kr[j][1].y, kr[j][1].z, kr[j][1].w};
+      const uint32_t at = stage + (j >> 1) * 2048 + gq * 128 + (((2 * tq + (j & 1)) ^ gq) << 4);
+      const uint4 u0 = lds_u32x4(at), u1 = lds_u32x4(at + 1024);
+      const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w};
+      const uint32_t w1[4] = {u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const uint32_t x0 = w0[m] ^ 0x80808080u, x1 = w1[m] ^ 0x80808080u;
@@ -965,16 +993,17 @@ __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const 
         mma16816(sacc[m], a, bq.x, bq.y);
       }
     }
+    __syncwarp();
+    if (n_k < n_it) load(n_k++, 0);
     float sc[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) sc[e] = (sacc[0][e] + sacc[1][e]) + (sacc[2][e] + sacc[3][e]);
     const int lb = block_of(b);
     const bool v0 = good && lb * kPage + gq <= t, v1 = good && lb * kPage + gq + 8 <= t;
-    const float y0 = v0 ? sc[0] * ks0 * c_lo : -INFINITY, y1 = v0 ? sc[1] * ks0 * c_hi : -INFINITY;
-    const float y2 = v1 ? sc[2] * ks1 * c_lo : -INFINITY, y3 = v1 ? sc[3] * ks1 * c_hi : -INFINITY;
-    if (it + 1 < n_it) load_k(it + 1);
+    const float y0 = v0 ? sc[0] * s_k0 * c_lo : -INFINITY, y1 = v0 ? sc[1] * s_k0 * c_hi : -INFINITY;
+    const float y2 = v1 ? sc[2] * s_k1 * c_lo : -INFINITY, y3 = v1 ? sc[3] * s_k1 * c_hi : -INFINITY;
     float bm_lo = fmaxf(y0, y2), bm_hi = fmaxf(y1, y3);
-    float bv = fmaxf(v0 ? vr0 : 0.f, v1 ? vr1 : 0.f);
+    float bv = fmaxf(v0 ? s_v0 : 0.f, v1 ? s_v1 : 0.f);
 #pragma unroll
     for (int sh = 4; sh < 32; sh <<= 1) {
       bm_lo = fmaxf(bm_lo, __shfl_xor_sync(kAllLanes, bm_lo, sh));
@@ -1003,15 +1032,20 @@ __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const 
         o[i][3] *= f_hi;
       }
     }
-    const float vs0 = v0 ? vr0 * vnorm : 0.f, vs1 = v1 ? vr1 * vnorm : 0.f;
+    const float vs0 = v0 ? s_v0 * vnorm : 0.f, vs1 = v1 ? s_v1 * vnorm : 0.f;
     const uint32_t pb0 = transpose8x8(pack_f16x2(v0 ? p0 * vs0 : 0.f, v0 ? p1 * vs0 : 0.f));
     const uint32_t pb1 = transpose8x8(pack_f16x2(v1 ? p2 * vs1 : 0.f, v1 ? p3 * vs1 : 0.f));
-    // dims 32 gq + 2 mt (row gq of m-tile mt) and + 1 (row gq + 8)
+    if (!__all_sync(kAllLanes, mbar_wait(bar + 8, (it >> 1) & 1, wc, 121))) break;
+    // V: keys 2tq, + 1, + 8, + 9, dims 128 h + 16 gq + 2 (mt % 8) (row gq of m-tile mt = 8 h ..) and + 1 (row gq + 8)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t w[4][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w[k][0] = vr[h][k].x, w[k][1] = vr[h][k].y, w[k][2] = vr[h][k].z, w[k][3] = vr[h][k].w;
+      for (int k = 0; k < 4; ++k) {
+        const int r = 2 * tq + (k & 1);
+        const uint4 u = lds_u32x4(stage + 4096 + h * 2048 + (k >> 1) * 1024 + r * 128 + ((gq ^ r) << 4));
+        w[k][0] = u.x, w[k][1] = u.y, w[k][2] = u.z, w[k][3] = u.w;
+      }
 #pragma unroll
       for (int ii = 0; ii < 4; ++ii) {
         const int i = 4 * h + ii;
@@ -1025,7 +1059,14 @@ __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const 
         mma16816(o[2 * i + 1], a1, pb0, pb1);
       }
     }
-    if (it + 1 < n_it) load_v(it + 1);
+    __syncwarp();
+    if (n_v < n_it) load(n_v++, 1);
+  }
+  if (it < n_it) {  // a wait gave up: no copy may be in flight when the CTA leaves
+    for (int v = 0; v < 2; ++v)
+      for (int n = v ? n_v : n_k, i = max(0, n - 2); i < n; ++i)  // the last of each stage
+        (void)mbar_wait_drain(bars + 16 * (i & 1) + 8 * v, (i >> 1) & 1, kShDrainNs);
+    __syncwarp();
   }
 #pragma unroll
   for (int sh = 4; sh < 32; sh <<= 1) {
@@ -1039,11 +1080,13 @@ __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const 
     wl[warp][2 * tq + 1] = l_hi;
   }
   const float up = pow2i(max(ev, -126));
+  float* part = reinterpret_cast<float*>(raw + warp * kOwnRing);  // over the stages: all copies have landed and are read
+  __syncwarp();
 #pragma unroll
-  for (int mt = 0; mt < 16; ++mt) {  // rows 2tq, 2tq+1; dims 32 gq + 2 mt, + 1
-    const int d = 32 * gq + 2 * mt;
-    *reinterpret_cast<float2*>(&comb[warp][2 * tq][d]) = make_float2(o[mt][0] * up, o[mt][2] * up);
-    *reinterpret_cast<float2*>(&comb[warp][2 * tq + 1][d]) = make_float2(o[mt][1] * up, o[mt][3] * up);
+  for (int mt = 0; mt < 16; ++mt) {  // rows 2tq, 2tq+1
+    const int d = 128 * (mt >> 3) + 16 * gq + 2 * (mt & 7);
+    *reinterpret_cast<float2*>(part + 2 * tq * kOwnPitch + d) = make_float2(o[mt][0] * up, o[mt][2] * up);
+    *reinterpret_cast<float2*>(part + (2 * tq + 1) * kOwnPitch + d) = make_float2(o[mt][1] * up, o[mt][3] * up);
   }
   __syncthreads();
   // the warps' parts, in a fixed order; thread (row i % 8, dims 4 (i / 8 + 16 n))
@@ -1062,7 +1105,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const 
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kOwnWarps; ++w) {
-      const float4 v = *reinterpret_cast<const float4*>(&comb[w][r][4 * dq]);
+      const float4 v = *reinterpret_cast<const float4*>(raw + w * kOwnRing + 4 * (r * kOwnPitch + 4 * dq));
       acc.x = fmaf(f[w], v.x, acc.x);
       acc.y = fmaf(f[w], v.y, acc.y);
       acc.z = fmaf(f[w], v.z, acc.z);
@@ -1160,36 +1203,40 @@ __global__ void __launch_bounds__(8 * 16 * kMergeMostWays) merge_kernel(const __
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-template <typename K>
-cudaError_t launch_after(K* kernel, dim3 grid, int threads, const SharedParams& p, const SharedSeqs& t, cudaStream_t st) {
+template <typename... Params>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t st, const Params&... params) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, t);
+  return cudaLaunchKernelEx(&cfg, kernel, params...);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, cudaStream_t st) {
+cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, const DecodeMaps& maps, cudaStream_t st) {
   cudaError_t e;
   const int own_grid = p.HKV * p.chunks_head;
+  if ((e = cudaFuncSetAttribute(own_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwnSmem)) != cudaSuccess) return e;
   if (p.n_grp > 0 && p.tiles_head > 0) {
     if ((e = cudaFuncSetAttribute(prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem)) != cudaSuccess)
       return e;
     prefix_kernel<<<2 * p.n_pairs, kPreThreads, kPreSmem, st>>>(p, t);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_after(own_kernel, dim3((unsigned)own_grid), kOwnWarps * 32, p, t, st)) != cudaSuccess) return e;
+    if ((e = launch_after(own_kernel, dim3((unsigned)own_grid), kOwnWarps * 32, kOwnSmem, st, p, t, maps)) != cudaSuccess)
+      return e;
   } else {
-    own_kernel<<<own_grid, kOwnWarps * 32, 0, st>>>(p, t);
+    own_kernel<<<own_grid, kOwnWarps * 32, kOwnSmem, st>>>(p, t, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  return launch_after(merge_kernel, dim3((unsigned)(p.n_seq * p.HKV), kHeadDim / kMergeDims), 16 * p.G * p.merge_ways, p, t, st);
+  return launch_after(merge_kernel, dim3((unsigned)(p.n_seq * p.HKV), kHeadDim / kMergeDims), 16 * p.G * p.merge_ways, 0, st,
+                      p, t);
 }
 
 }  // namespace pa

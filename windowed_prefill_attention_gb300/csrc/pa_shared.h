@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "pa_internal.h"
 #include "pa_tiles.cuh"
 
 namespace pa {
@@ -82,6 +83,7 @@ PA_HD ShOwn shared_own(int n_ctx, int win_lo, int first, int S, int W) {
 }
 PA_HD int shared_win_lo(int n_ctx, int W) { return W > 0 ? imax(0, (n_ctx - 1) / kPage + 1 - W) : 0; }
 
-cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, cudaStream_t st);
+// maps: the pool as uint8 [n_pool * 16][HKV][256], boxes of 16 tokens, one head, 128 dims, 128-byte swizzle.
+cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, const DecodeMaps& maps, cudaStream_t st);
 
 }  // namespace pa
