@@ -1635,11 +1635,19 @@ int decode_shared_check(int HQ, int HKV, int max_pages, int n_seq, const pa_seq*
 // into at most n_sm / 2 runs of equal cost, one for each SM pair.  A run costs
 // its tiles plus kShSegCost for every group after its first: the next group's
 // queries are staged and the last one's output stored while no product runs
-// (about 12000 cycles against 3000 to 4000 a tile on GB300).  The per-sequence pass: chunks of equal block counts, about two
-// CTAs per SM, four to 128 blocks each.
-constexpr int kShSegCost = 4;
-constexpr double kShPairUs = 11.0, kShTileUs = 2.1;  // a pair's set-up, queries and epilogue; a tile
-constexpr double kShOwnBlockUs = 0.25, kShOwnCtaUs = 2.0, kShOwnTailUs = 5.0;
+// (about 12000 cycles against 3000 to 4000 a tile on GB300).  The per-sequence
+// pass: chunks of equal block counts, one wave of CTAs on the SMs it has, four to
+// 128 blocks each.
+constexpr int kShSegCost = 4, kShOwnWaves = 2;
+// Microseconds on GB300, fitted to 15 batches at 11 numbers of pairs each: a
+// pair's set-up, queries and epilogue, its first ten tiles, the others; the SM
+// time of an own block, of a prefix block that a sequence reads again (from L2)
+// and of an own CTA, what the per-sequence pass takes to get going, what it adds
+// when it ends after the prefix pass, and how full it keeps its SMs when not even
+// a CTA for every sequence fits them at once.
+constexpr double kShPairUs = 11.0, kShTileUs = 2.1, kShLateTileUs = 1.65;
+constexpr double kShOwnBlockUs = 0.215, kShAgainBlockUs = 0.165, kShOwnCtaUs = 0.25;
+constexpr double kShOwnStartUs = 4.5, kShOwnTailUs = 4.0, kShOwnFull = 0.85;
 // Packs the groups (nt[j] tiles each, laid end to end) into runs of at most
 // `budget` cost; false if they take more than max_pairs.
 bool shared_pack(const int* nt, int n_groups, int budget, int max_pairs, int* cut, int& n_pairs) {
@@ -1719,22 +1727,26 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
   };
   // The prefix pass's pairs.  Both passes can run at once: the pairs left out
   // leave their SMs to the per-sequence pass, whose CTAs otherwise start when the
-  // prefix pass ends.  Of a few numbers of pairs the one that ends first, by what
-  // GB300 measures (microseconds; an own block and CTA as the SM time they take).
+  // prefix pass ends.  Of a few numbers of pairs the one that ends first.
   const int T = HKV * p.tiles_head, max_pairs = std::min(kShPairs, std::max(1, n_sm / 2)), J = HKV * p.n_grp;
   p.n_pairs = 0;
   p.merge_ways = 0;
-  p.chunk = own_chunk(kShOwnPerSm * n_sm);
   int nt[8 * kShGroups], pairs = max_pairs;
   if (T > 0) {
     for (int j = 0; j < J; ++j) nt[j] = (t.grp[j % p.n_grp].n_blk + kTileBlocks - 1) / kTileBlocks;
     double best = 1e30;
-    const double own_us = kShOwnBlockUs * own * HKV + kShOwnCtaUs * own_ctas(p.chunk);
+    const double own_blk = (double)own * HKV, least_ctas = (double)n * HKV;
     for (int left = 0; left < max_pairs; left += 4) {
       const int use = std::min(max_pairs - left, T), free_sm = n_sm - 2 * use;
       // a pair's cost when all are equal: its tiles, and its share of the groups' changes
       const int budget = (T + kShSegCost * std::max(0, J - use) + use - 1) / use + (J > 1 && J < use && use % J ? 1 : 0);
-      const double prefix_us = kShPairUs + kShTileUs * budget, rest = std::max(0.0, own_us - free_sm * prefix_us);
+      const double prefix_us = kShPairUs + kShTileUs * std::min(budget, 10) + kShLateTileUs * std::max(0, budget - 10);
+      const double slots = kShOwnPerSm * free_sm, ctas = std::max(least_ctas, std::min(own_blk / 4, kShOwnWaves * slots));
+      const double own_us = (kShOwnBlockUs * own_blk + kShOwnCtaUs * ctas) / (least_ctas > slots ? kShOwnFull : 1.0);
+      // SM time before the prefix pass ends: that of the SMs left out; if none is, of the pairs with a tile less
+      const double idle = free_sm > 1 ? free_sm * std::max(0.0, prefix_us - kShOwnStartUs)
+                                      : 2.0 * kShLateTileUs * std::max(0, budget * use - T);
+      const double rest = std::max(0.0, own_us - idle);
       const double end = prefix_us + (rest > 0.0 ? rest / n_sm + kShOwnTailUs : 0.0);
       if (end < best) {
         best = end;
@@ -1743,13 +1755,18 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
       if (rest <= 0.0) break;  // fewer pairs only make the prefix pass longer
     }
     // With few sequences or a short prefix it is quicker that each reads the prefix too.
-    long long all = own * HKV;
-    for (int s = 0; s < n; ++s) all += (long long)HKV * t.grp[s / per].n_blk;
-    if (prefix_pass < 0 ? kShOwnTailUs + kShOwnBlockUs * all / n_sm < best : prefix_pass == 0) {
+    double again = 0.0;
+    for (int s = 0; s < n; ++s) again += (double)HKV * t.grp[s / per].n_blk;
+    const double each = kShOwnStartUs + (kShOwnBlockUs * own_blk + kShAgainBlockUs * again) / n_sm;
+    if (prefix_pass < 0 ? each < best : prefix_pass == 0) {
       p.n_grp = p.tiles_head = p.first_blk = 0;
       count_own();
-      p.chunk = own_chunk(kShOwnPerSm * n_sm);
     }
+  }
+  {  // Two waves keep the SMs full beside a prefix pass (48 sequences, windowed, 12104 blocks: 33.4 us, with one 37.3);
+    // alone one is quicker (40 sequences, 16408 blocks: 29.5 us, with two 32.1).
+    const int free_sm = p.tiles_head > 0 ? n_sm - 2 * pairs : n_sm, wave = kShOwnPerSm * (free_sm > 0 ? free_sm : n_sm);
+    p.chunk = own_chunk(wave * std::max(p.tiles_head > 0 ? kShOwnWaves : 1, (n * HKV + n * HKV / 4) / wave));
   }
   if (p.tiles_head > 0) {
     int budget = (T + pairs - 1) / pairs;
@@ -1899,8 +1916,8 @@ int pa_decode_shared_plan(int n_q_heads, int n_kv_heads, int max_pages_per_seq, 
   for (int s = 0; s < p.n_seq; ++s) {
     const ShOwn o = shared_own(t.s[s].y, t.s[s].w, p.first_blk, p.S, p.W);
     const int n_ch = (o.n + p.chunk - 1) / p.chunk;
-    for (int g = 0; g < p.HKV; ++g)
-      for (int c = 0; c < n_ch; ++c) {
+    for (int c = 0; c < n_ch; ++c)
+      for (int g = 0; g < p.HKV; ++g) {
         if (own_out) {
           if (no >= own_cap) return PA_EINVAL;
           int32_t* r = own_out + 7 * no;

@@ -886,9 +886,8 @@ __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const 
   const int4 sq = tab.s[lo];
   const int t = sq.y - 1;
   const ShOwn own = shared_own(sq.y, sq.w, p.first_blk, p.S, p.W);
-  const int n_ch = (own.n + p.chunk - 1) / p.chunk;
   const int at = (int)blockIdx.x - p.HKV * sq.z;
-  const int g = at / n_ch, ch = at - g * n_ch;
+  const int ch = at / p.HKV, g = at - ch * p.HKV;  // the heads of a chunk side by side: they read the same DRAM pages
   const int b0 = ch * p.chunk, b1 = min(own.n, b0 + p.chunk);
   // this warp's pages, one per lane (at most 32 blocks a warp)
   auto block_of = [&](int b) { return b < own.sink ? p.first_blk + b : own.lo + (b - own.sink); };
@@ -1139,7 +1138,7 @@ __global__ void __launch_bounds__(8 * 16 * kMergeMostWays) merge_kernel(const __
   const int r = slot & (p.G - 1), dq = blockIdx.y * (kMergeDims / 4) + (slot >> p.log2_g);
   const int4 sq = tab.s[s];
   const ShOwn own = shared_own(sq.y, sq.w, p.first_blk, p.S, p.W);
-  const int n_own = (own.n + p.chunk - 1) / p.chunk, own0 = p.HKV * sq.z + g * n_own;
+  const int n_own = (own.n + p.chunk - 1) / p.chunk, own0 = p.HKV * sq.z + g;
   int n_pre = 0, pre0 = 0, prow = 0;
   if (p.n_grp > 0) {
     const int rg = (s * p.G) / kUnitRows;
@@ -1183,8 +1182,8 @@ __global__ void __launch_bounds__(8 * 16 * kMergeMostWays) merge_kernel(const __
         ml[e] = __ldcg(pm + (size_t)i * kUnitRows);
         v[e] = __ldcg(po + (size_t)i * 64 * kUnitRows);
       } else if (i < n) {
-        ml[e] = __ldcg(om + (size_t)(i - n_pre) * 8);
-        v[e] = __ldcg(oo + (size_t)(i - n_pre) * 64 * 8);
+        ml[e] = __ldcg(om + (size_t)(i - n_pre) * p.HKV * 8);
+        v[e] = __ldcg(oo + (size_t)(i - n_pre) * p.HKV * 64 * 8);
       }
     }
 #pragma unroll
