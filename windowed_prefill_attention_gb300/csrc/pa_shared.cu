@@ -79,6 +79,8 @@ __device__ __forceinline__ uint4 lds_u32x4(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // 16 TMEM lanes x 128 columns in the 16x256b shape (see pa_ptx.cuh).
@@ -163,8 +165,9 @@ enum : int {
   B_OE = 21,   // even: a segment's O is read (every softmax warp of both)
   B_RAW = 22,  // the segment's raw queries are read (converter warps)
   B_RAWF = 23, // the segment's raw queries have landed
-  B_DRAIN = 24,
-  kPreBars = 25
+  B_HELP = 24, // the softmax warps' rows of the first segment's queries are written
+  B_DRAIN = 25,
+  kPreBars = 26
 };
 constexpr int kSmTmem = kSmBar + kPreBars * 8;
 constexpr int kPreSmem = kSmTmem + 16;
@@ -252,6 +255,62 @@ __device__ __forceinline__ void widen16(const uint4 c, uint32_t row_addr, int ro
   sts128(at ^ 16u, h[4], h[5], h[6], h[7]);
 }
 
+// ---- queries.  Rows [first, end) of the CTA's, from their raw copies: each row
+// scaled by a power of two and rounded to fp16, exactly.  Four rows at a time,
+// their chains of shuffles side by side; a row's largest magnitude from the bf16
+// bit patterns, two rows to a word.
+__device__ __forceinline__ void stage_queries(const PreCtx& c, const Segment& s, uint32_t raw, uint32_t rowc, int first, int end) {
+  const int lane = threadIdx.x & 31;
+  const int last = max(0, s.rows - 1);  // rows past the last hold anything: no one reads their results
+#pragma unroll 1
+  for (int i0 = first; i0 < end; i0 += 4) {
+    uint4 q[4];
+    uint32_t m[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      q[i] = lds_u32x4(raw + min(i0 + i, last) * (kHeadDim * 2) + 16 * lane);
+      uint32_t a = __vmaxu2(__vmaxu2(q[i].x & 0x7fff7fffu, q[i].y & 0x7fff7fffu), __vmaxu2(q[i].z & 0x7fff7fffu, q[i].w & 0x7fff7fffu));
+      a = max(a & 0xffffu, a >> 16);
+      m[i >> 1] = i & 1 ? m[i >> 1] | a << 16 : a;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) m[i] = __vmaxu2(m[i], __shfl_xor_sync(kAllLanes, m[i], o));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = i0 + i;
+      const int k = row_shift(__uint_as_float(i & 1 ? m[i >> 1] & 0xffff0000u : m[i >> 1] << 16));
+      const float mul = pow2i(k);
+      const uint32_t u[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+      uint32_t h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = mul2(make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u)), make_float2(mul, mul));
+        h[e] = pack_f16x2(v.x, v.y);
+      }
+      sts128(c.sb + kSmQ + (lane >> 3) * 16384 + row * 128 + (((lane & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+      if (lane == 0) asm volatile("st.shared.u8 [%0], %1;" ::"r"(rowc + row), "r"(-k) : "memory");
+    }
+  }
+  fence_proxy_async_shared();
+  __syncwarp();
+}
+// The first segment's raw rows lie in the V stages, the others' in the K stages:
+// the first ones' staging, by the idle softmax warps and the V warps, then runs
+// beside the widening of the first K tile, while a later segment's must not wait
+// for the last P V of the one before.
+constexpr int kHelpRows = 12;  // each softmax warp's; the four V warps share the others
+static_assert(kSoftWarps * kHelpRows + 4 * 8 == kRows, "rows of the first segment");
+__device__ __forceinline__ bool help_stage(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
+  const int warp = threadIdx.x >> 5;
+  const Segment s = segment_at(p, tab, c.rank, c.x0, c.x1);
+  if (!c.wait(B_RAWF, 0)) return false;
+  stage_queries(c, s, c.sb + kSmV, c.sb + kSmRow, kHelpRows * warp, kHelpRows * (warp + 1));
+  if ((threadIdx.x & 31) == 0) mbar_arrive(c.bar(B_HELP));
+  return true;
+}
+
 // One code for K and V warps: the kernel's instructions exceed the caches that
 // feed the schedulers, and every line of it is fetched anew for each tile.
 __device__ __forceinline__ void role_convert(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
@@ -292,51 +351,19 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
       for (int n = 4; n < 8; ++n, b += step_b) r[n] = ldg_stream(b);
     };
     load(0);
-    // The CTA's queries, 16 rows a warp, from the raw copies in the K stages:
-    // each row scaled by a power of two and rounded to fp16, exactly.  Four rows
-    // at a time, their chains of shuffles side by side; a row's largest magnitude
-    // from the bf16 bit patterns, two rows to a word.
-    if (!c.wait(B_RAWF, n_seg)) return;
-    const uint32_t rowc = c.sb + kSmRow + (n_seg & 1) * kRows;
-#pragma unroll 1
-    for (int i0 = 16 * warp; i0 < 16 * warp + 16; i0 += 4) {
-      uint4 q[4];
-      uint32_t m[2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 f = lds_f32x4(c.sb + kSmK + (i0 + i) * (kHeadDim * 2) + 16 * lane);
-        const bool in = i0 + i < s.rows;
-        q[i] = make_uint4(in ? __float_as_uint(f.x) : 0, in ? __float_as_uint(f.y) : 0, in ? __float_as_uint(f.z) : 0,
-                          in ? __float_as_uint(f.w) : 0);
-        uint32_t a = __vmaxu2(__vmaxu2(q[i].x & 0x7fff7fffu, q[i].y & 0x7fff7fffu), __vmaxu2(q[i].z & 0x7fff7fffu, q[i].w & 0x7fff7fffu));
-        a = max(a & 0xffffu, a >> 16);
-        m[i >> 1] = i & 1 ? m[i >> 1] | a << 16 : a;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) m[i] = __vmaxu2(m[i], __shfl_xor_sync(kAllLanes, m[i], o));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = i0 + i;
-        const int k = row_shift(__uint_as_float(i & 1 ? m[i >> 1] & 0xffff0000u : m[i >> 1] << 16));
-        const float mul = pow2i(k);
-        float v[8];
-        unpack8(q[i], v);
-        sts128(c.sb + kSmQ + (lane >> 3) * 16384 + row * 128 + (((lane & 7) ^ (row & 7)) << 4),
-               pack_f16x2(v[0] * mul, v[1] * mul), pack_f16x2(v[2] * mul, v[3] * mul), pack_f16x2(v[4] * mul, v[5] * mul),
-               pack_f16x2(v[6] * mul, v[7] * mul));
-        if (lane == 0) asm volatile("st.shared.u8 [%0], %1;" ::"r"(rowc + row), "r"(-k) : "memory");
-      }
+    if (n_seg > 0 || kv) {
+      if (!c.wait(B_RAWF, n_seg)) return;
+      const int first = n_seg > 0 ? 16 * warp : kSoftWarps * kHelpRows + 8 * w;
+      stage_queries(c, s, c.sb + (n_seg > 0 ? kSmK : kSmV), c.sb + kSmRow + (n_seg & 1) * kRows, first,
+                    first + (n_seg > 0 ? 16 : 8));
+      if (n_seg == 0 && !c.wait(B_HELP, 0)) return;
     }
-    fence_proxy_async_shared();
-    __syncwarp();
     if (lane == 0) {
-      mbar_arrive(c.bar(c.rank == 0 ? B_QF : B_QL));
       mbar_arrive(c.bar(B_RAW));
+      mbar_arrive(c.bar(c.rank == 0 ? B_QF : B_QL));
     }
-    // every warp has read its raw rows: the K stages may be written
-    if (!c.wait(B_RAW, n_seg)) return;
+    // every warp has read its raw rows: the stages that held them may be written
+    if ((n_seg > 0 || kv) && !c.wait(B_RAW, n_seg)) return;
 
     const int nt = s.t1 - s.t0;
     for (int t = 0; t < nt; ++t, ++n_tile) {
@@ -367,22 +394,30 @@ __device__ __forceinline__ void role_forward_tiles(const PreCtx& c, int local, i
     mbar_arrive_cluster(cluster_addr(c.bar(even + (n & 1)), 0));
   }
 }
-// The segments' query rows, copied as they are into the K stages (free: the
+// The segments' query rows, copied as they are (into the K stages: free, the
 // segment before's last Q K^T is done): the G rows of a sequence lie together.
-// In the odd CTA also the forward of its queries.
+__device__ __forceinline__ void copy_queries(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c, const Segment& s,
+                                             uint32_t raw) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) mbar_expect_tx(c.bar(B_RAWF), s.rows * (kHeadDim * 2));
+  __syncwarp();
+  const int n = s.rows >> p.log2_g, s0 = s.row0 >> p.log2_g;  // whole sequences: 128 is a multiple of G
+  for (int i = lane; i < n; i += 32)
+    bulk_load(raw + i * p.G * (kHeadDim * 2), p.q + ((size_t)tab.s[s0 + i].x * p.HQ + (size_t)s.g * p.G) * kHeadDim,
+              p.G * (kHeadDim * 2), c.bar(B_RAWF));
+}
+// The first segment's copies have been issued.  In the odd CTA also the forward
+// of its queries.
 __device__ __forceinline__ void role_queries(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
   const int lane = threadIdx.x & 31;
-  uint32_t n_seg = 0, copied = 0;
+  uint32_t n_seg = 0, copied = 1;
   for (int x = c.x0; x < c.x1; ++n_seg) {
     const Segment s = segment_at(p, tab, c.rank, x, c.x1);
-    if (n_seg > 0 && !c.wait(B_QE, n_seg - 1)) break;
-    if (lane == 0) mbar_expect_tx(c.bar(B_RAWF), s.rows * (kHeadDim * 2));
-    __syncwarp();
-    const int n = s.rows >> p.log2_g, s0 = s.row0 >> p.log2_g;  // whole sequences: 128 is a multiple of G
-    for (int i = lane; i < n; i += 32)
-      bulk_load(c.sb + kSmK + i * p.G * (kHeadDim * 2),
-                p.q + ((size_t)tab.s[s0 + i].x * p.HQ + (size_t)s.g * p.G) * kHeadDim, p.G * (kHeadDim * 2), c.bar(B_RAWF));
-    ++copied;
+    if (n_seg > 0) {
+      if (!c.wait(B_QE, n_seg - 1)) break;
+      copy_queries(p, tab, c, s, c.sb + kSmK);
+      ++copied;
+    }
     if (c.rank == 1) {
       if (!c.wait(B_QL, n_seg)) break;
       if (lane == 0) mbar_arrive_cluster(cluster_addr(c.bar(B_QF), 0));
@@ -390,7 +425,7 @@ __device__ __forceinline__ void role_queries(const SharedParams& p, const Shared
     x += s.t1 - s.t0;
   }
   // no copy is in flight when the CTA leaves, whatever gave up
-  if (copied > 0) (void)mbar_wait_drain(c.bar(B_RAWF), (copied - 1) & 1u, kShDrainNs);
+  (void)mbar_wait_drain(c.bar(B_RAWF), (copied - 1) & 1u, kShDrainNs);
   __syncwarp();
 }
 
@@ -759,62 +794,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
   c.x0 = tab.cut[blockIdx.x >> 1];
   c.x1 = tab.cut[(blockIdx.x >> 1) + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(c.bar(B_KF + i), kConvWarps / 2 + 1);
-      mbar_init(c.bar(B_VF + i), kConvWarps / 2 + 1);
-      mbar_init(c.bar(B_KL + i), kConvWarps / 2);
-      mbar_init(c.bar(B_VL + i), kConvWarps / 2);
-      mbar_init(c.bar(B_SF + i), 1);
-      mbar_init(c.bar(B_PF + i), 2 * kSoftWarps);
-      mbar_init(c.bar(B_OD + i), 1);
-      mbar_init(c.bar(B_SCF + i), 1);
-      mbar_init(c.bar(B_SCE + i), kSoftWarps);
-    }
-    mbar_init(c.bar(B_QF), kConvWarps + 1);
-    mbar_init(c.bar(B_QL), kConvWarps);
-    mbar_init(c.bar(B_RAW), kConvWarps);
-    mbar_init(c.bar(B_RAWF), 1);
-    mbar_init(c.bar(B_QE), 1);
-    mbar_init(c.bar(B_OE), 2 * kSoftWarps);
-    mbar_init(c.bar(B_DRAIN), 1);
+  if (threadIdx.x < kPreBars) {
+    const int i = threadIdx.x;
+    int n = 1;
+    if (i < B_KL) n = kConvWarps / 2 + 1;
+    if (i >= B_KL && i < B_SF) n = kConvWarps / 2;
+    if (i == B_QF) n = kConvWarps + 1;
+    if (i == B_QL || i == B_RAW) n = kConvWarps;
+    if ((i >= B_SCE && i < B_QF) || i == B_HELP) n = kSoftWarps;
+    if ((i >= B_PF && i < B_OD) || i == B_OE) n = 2 * kSoftWarps;
+    mbar_init(c.bar(i), n);
     fence_mbar_init();
   }
+  __syncthreads();
+  // The first segment's queries come in and are staged, and its first K tile is
+  // widened, while the pair's tensor memory is allocated and the CTAs meet: only
+  // what reaches into the other CTA or tensor memory waits for that.
+  if (warp == kQueryWarp) copy_queries(p, tab, c, segment_at(p, tab, c.rank, c.x0, c.x1), c.sb + kSmV);
   if (warp == kIssueWarp) {
     tmem_alloc_pair(c.sb + kSmTmem, 512);
     tmem_relinquish_pair();
   }
-  {  // the table's lines that the roles read first come in while the CTAs set up
-    const Segment s = segment_at(p, tab, c.rank, c.x0, c.x1);
-    const int row = min(s.row0 + (int)threadIdx.x % kRows, p.n_seq * p.G - 1);
-    asm volatile("" ::"r"(s.t1), "r"(tab.s[row >> p.log2_g].x));
-  }
   tc_fence_before();
-  __syncthreads();
-  cluster_sync_all();  // both CTAs' barriers exist before either may arrive on the other's
-  tc_fence_after();
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c.tm) : "r"(c.sb + kSmTmem));
+  cluster_arrive();
   dependents_may_start();
+  auto meet = [&] {  // both CTAs have their barriers and tensor memory; once in every thread
+    cluster_wait();
+    tc_fence_after();
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c.tm) : "r"(c.sb + kSmTmem));
+  };
   if (warp < kSoftWarps) {
     more_regs<kSoftRegs>();
-    role_softmax(p, tab, c);
+    const bool ok = help_stage(p, tab, c);
+    meet();
+    if (ok) role_softmax(p, tab, c);
   } else if (warp < kIssueWarp) {
     fewer_regs<kConvRegs>();
     role_convert(p, tab, c);
+    meet();
   } else {
     fewer_regs<kMiscRegs>();
     if (warp == kScaleWarp) {
       role_scales(p, tab, c);
-    } else if (warp == kQueryWarp) {
-      role_queries(p, tab, c);
-    } else if (lane == 0) {
-      if (c.rank == 0) {
-        if (warp == kIssueWarp) role_issue(p, tab, c);
-      } else {
-        if (warp == kIssueWarp) role_forward_tiles(c, B_KL, B_KF);
-        else role_forward_tiles(c, B_VL, B_VF);
-        // this CTA's TMEM and shared memory are in use until the pair's last product is done
-        if (warp == kIssueWarp) (void)mbar_wait_drain(c.bar(B_DRAIN), 0, kShDrainNs);
+      meet();
+    } else {
+      meet();
+      if (warp == kQueryWarp) {
+        role_queries(p, tab, c);
+      } else if (lane == 0) {
+        if (c.rank == 0) {
+          if (warp == kIssueWarp) role_issue(p, tab, c);
+        } else {
+          if (warp == kIssueWarp) role_forward_tiles(c, B_KL, B_KF);
+          else role_forward_tiles(c, B_VL, B_VF);
+          // this CTA's TMEM and shared memory are in use until the pair's last product is done
+          if (warp == kIssueWarp) (void)mbar_wait_drain(c.bar(B_DRAIN), 0, kShDrainNs);
+        }
       }
     }
     __syncwarp();
