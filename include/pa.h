@@ -344,10 +344,11 @@ int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, i
 /* Host-only, no GPU needed: how pa_decode_shared splits the work of one launch
  * (the first min(n_seq, 512) sequences) on a GPU of n_sm SMs; prefix_pass as in
  * pa_debug_decode_shared_pass (-1: what a call does).  prefix_out (may
- * be NULL) receives *n_prefix_runs entries of int32[8] = {SM pair, kv head, first
+ * be NULL) receives *n_prefix_runs entries of int32[8] = {unit, kv head, first
  * sequence, sequences, sink, lo, first, last}: entries first .. last - 1 of the
  * list of blocks 0 .. sink - 1, then lo, lo + 1, ... (the prefix's blocks that
- * some of the sequences see) against those sequences' queries of the head.
+ * some of the sequences see) against those sequences' queries of the head; a
+ * unit is a pair of SMs, or with up to 128 query rows a kv head one SM.
  * own_out (may be NULL): *n_own_runs entries, one CTA each, of int32[7] =
  * {sequence, kv head, base, sink, lo, first, last}: entries first .. last - 1 of
  * the list of blocks base .. base + sink - 1, then lo, lo + 1, ...  PA_EINVAL

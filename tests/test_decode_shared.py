@@ -54,14 +54,18 @@ def check(b, out, skip_pages=()):
     assert np.isnan(got[others]).all(), "a row of no sequence was written"
 
 
+# Up to 128 query rows a kv head (sequences x q heads a kv head) are one CTA's, more a pair's in groups of 256.
 CASES = {
     "two_blocks": Batch(8, 1, 16, (1, 1), 1, 0, 1),
     "one_tile": Batch(8, 2, 128, (5, 17, 40), 1, 0, 2),
     "ragged_tile": Batch(16, 2, 144, (1, 300, 16, 31), 1, 0, 3),
     "full_group": Batch(8, 1, 2048, tuple(range(1, 17)), 0, 0, 4),
-    "two_groups": Batch(16, 2, 1040, tuple(1 + 7 * i for i in range(17)), 1, 0, 5),
+    "one_row_too_many": Batch(8, 1, 2048, tuple(range(1, 18)), 0, 0, 23),
+    "two_ctas": Batch(16, 2, 1040, tuple(1 + 7 * i for i in range(17)), 1, 0, 5),
     "many_rows": Batch(8, 2, 4096, tuple(1 + (37 * i) % 90 for i in range(130)), 1, 0, 6),
     "long_prefix": Batch(8, 1, 20000, (1, 100, 2000), 1, 0, 7),
+    "long_prefix_pair": Batch(8, 1, 20000, tuple(1 + 19 * i for i in range(33)), 1, 0, 24),
+    "ragged_pair": Batch(2, 2, 1232, tuple(1 + i % 37 for i in range(129)), 1, 0, 25),
     "gqa1": Batch(4, 4, 1600, (3, 33, 64), 1, 0, 8),
     "gqa2": Batch(4, 2, 800, tuple(2 + i for i in range(70)), 1, 0, 9),
     "gqa4_windowed": Batch(8, 2, 3200, tuple(1 + 53 * i for i in range(40)), 1, 64, 10),
@@ -77,6 +81,7 @@ CASES = {
     "over_512": Batch(2, 1, 320, tuple(1 + (13 * i) % 40 for i in range(1030)), 1, 0, 20),
     "cold_softmax": Batch(8, 1, 1024, (9, 90, 3), 1, 0, 21, outliers=0.0, sm_scale=0.0),
     "steep_softmax": Batch(8, 1, 1024, (9, 90, 3), 1, 0, 22, outliers=0.05, sm_scale=2.0),
+    "steep_softmax_pair": Batch(8, 1, 2560, tuple(1 + i for i in range(40)), 1, 0, 26, outliers=0.05, sm_scale=2.0),
 }
 
 
@@ -97,7 +102,8 @@ def test_passes_by_size_agree():
 
     import windowed_prefill_attention_gb300 as pa
     for b, by_size in ((Batch(16, 2, 1024, (5, 40, 17), 1, 0, 31), 0),
-                       (Batch(8, 4, 4096, tuple(1 + 3 * i for i in range(40)), 1, 0, 32), 1)):
+                       (Batch(8, 4, 4096, tuple(1 + 3 * i for i in range(40)), 1, 0, 32), 1),
+                       (Batch(8, 4, 2048, tuple(1 + 3 * i for i in range(80)), 1, 0, 33), 1)):
         b.make()
         d = to_device(b)
         runs, _ = pa.pa_decode_shared_plan(b.hq, b.hkv, b.max_pages, 152, b.seqs, b.prefix, b.S, b.W)
@@ -134,7 +140,7 @@ def test_equals_decode_and_repeats_bit_for_bit():
     import torch
 
     import windowed_prefill_attention_gb300 as pa
-    b = CASES["two_groups"].make()
+    b = CASES["two_ctas"].make()
     d = to_device(b)
     with Handle(b) as h:
         first = call(h, b, d)
@@ -233,15 +239,16 @@ def test_calls_back_to_back_of_changing_sizes():
             assert torch.equal(o.view(torch.int16), alone.view(torch.int16))
 
 
-def test_first_calls_on_cold_memory_repeat_bit_for_bit():
+@pytest.mark.parametrize("case", ("long_prefix", "long_prefix_pair"))
+def test_first_calls_on_cold_memory_repeat_bit_for_bit(case):
     """Fresh handles, fresh copies of the inputs, other data in the freed memory in between: codes that arrive
     late must not let any part of the kernel run ahead of another."""
     import torch
 
     import windowed_prefill_attention_gb300 as pa
-    b = CASES["long_prefix"].make()
+    b = CASES[case].make()
     first = None
-    for i in range(150):
+    for i in range(100):
         d = to_device(b)
         with Handle(b) as h:
             out = call(h, b, d)

@@ -50,13 +50,15 @@ def test_every_visible_block_is_computed_once(pa, case, prefix_pass):
     pre, own = pa.pa_decode_shared_plan(hq, hkv, 1 << 20, n_sm, seqs, prefix, S, W, prefix_pass)
     assert prefix_pass or not len(pre)
     n, pb = min(512, len(suffix)), prefix // 16
+    n_cta = 1 if n * (hq // hkv) <= 128 else 2  # CTAs of a unit of the prefix pass
+    tile, rows = 4 * n_cta, 128 * n_cta         # blocks of a tile; rows of a group
     done = {}  # (sequence, head) -> blocks of its own passes
     for s, g, base, sink, lo, first, last in own.tolist():
         assert 0 < last - first <= 128
         done.setdefault((s, g), []).extend(listed(base, sink, lo, first, last))
     groups = {}
     for _, g, s0, ns, sink, lo, first, last in pre.tolist():
-        assert 0 <= first < last and first % 8 == 0 and ns * (hq // hkv) <= 256
+        assert 0 <= first < last and first % tile == 0 and ns * (hq // hkv) <= rows
         groups.setdefault((g, s0, ns), []).extend(listed(0, sink, lo, first, last))
     seen_by = {}
     for (g, s0, ns), blocks in groups.items():
@@ -80,19 +82,19 @@ def test_every_visible_block_is_computed_once(pa, case, prefix_pass):
             assert set(mine) | {b for b in shared if b in set(want)} == set(want)
             for b in want:
                 if b in shared:
-                    union.setdefault((g, s // (256 // (hq // hkv))), set()).add(b)
+                    union.setdefault((g, s // (rows // (hq // hkv))), set()).add(b)
     assert not done
     for (g, s0, ns), blocks in groups.items():  # a block is listed only if some sequence of the group sees it
-        assert set(blocks) == union[g, s0 // (256 // (hq // hkv))]
-    if len(pre):  # one pair's tiles are consecutive, and the costliest pair (4 for every group after its first) is
+        assert set(blocks) == union[g, s0 // (rows // (hq // hkv))]
+    if len(pre):  # one unit's tiles are consecutive, and the costliest unit (4 for every group after its first) is
         # within one group's charge of the mean
-        pairs = pre[:, 0]
-        assert np.all(np.diff(pairs) >= 0) and pairs[0] == 0 and pairs[-1] < max(1, n_sm // 2)
-        cost = np.full(pairs[-1] + 1, -4)
-        np.add.at(cost, pairs, (pre[:, 7] - pre[:, 6] + 7) // 8 + 4)
+        units, most = pre[:, 0], max(1, n_sm // n_cta)
+        assert np.all(np.diff(units) >= 0) and units[0] == 0 and units[-1] < most
+        cost = np.full(units[-1] + 1, -4)
+        np.add.at(cost, units, (pre[:, 7] - pre[:, 6] + tile - 1) // tile + 4)
         assert cost.min() >= 1
-        assert cost.max() <= -(-cost.sum() // max(1, n_sm // 2)) + 5 or len(cost) < max(1, n_sm // 2)
-        assert len(cost) == max(1, n_sm // 2) or cost.max() <= cost.sum() // len(cost) + 5
+        assert cost.max() <= -(-cost.sum() // most) + 5 or len(cost) < most
+        assert len(cost) == most or cost.max() <= cost.sum() // len(cost) + 5
 
 
 def test_prefix_pass_by_size(pa):

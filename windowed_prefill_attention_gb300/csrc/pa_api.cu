@@ -1630,14 +1630,14 @@ int decode_shared_check(int HQ, int HKV, int max_pages, int n_seq, const pa_seq*
 }
 
 // One launch (sequences [s0, s0 + n)) of the shared-prefix decode: its table and split.
-// The prefix pass: the rows of a kv head in groups of 256, per group the
-// blocks some row sees, in 128-key tiles; all tiles, group after group, cut
-// into at most n_sm / 2 runs of equal cost, one for each SM pair.  A run costs
-// its tiles plus kShSegCost for every group after its first: the next group's
-// queries are staged and the last one's output stored while no product runs
-// (about 12000 cycles against 3000 to 4000 a tile on GB300).  The per-sequence
-// pass: chunks of equal block counts, one wave of CTAs on the SMs it has, four to
-// 128 blocks each.
+// The prefix pass: up to 128 rows of a kv head (n sequences x G) are one CTA's, in
+// 64-key tiles; more are worked on by pairs of CTAs, in groups of 256 and 128-key
+// tiles.  Per group the blocks some row sees; all tiles, group after group, cut
+// into runs of equal cost, one for each unit (a CTA or a pair, one CTA an SM).  A
+// run costs its tiles plus kShSegCost for every group after its first: the next
+// group's queries are staged and the last one's output stored while no product
+// runs (about 12000 cycles against 3000 to 4000 a pair's tile on GB300).  The
+// per-sequence pass: chunks of equal block counts, four to 128 blocks each.
 constexpr int kShSegCost = 4, kShOwnWaves = 2;
 // Microseconds on GB300, fitted to 15 batches at 11 numbers of pairs each: a
 // pair's set-up, queries and epilogue, its first ten tiles, the others; the SM
@@ -1645,12 +1645,16 @@ constexpr int kShSegCost = 4, kShOwnWaves = 2;
 // and of an own CTA, what the per-sequence pass takes to get going, what it adds
 // when it ends after the prefix pass, and how full it keeps its SMs when not even
 // a CTA for every sequence fits them at once.
-constexpr double kShPairUs = 11.0, kShTileUs = 2.1, kShLateTileUs = 1.65;
+struct ShCost {
+  double unit, tile, late;
+  int early;
+};
+constexpr ShCost kShCost[2] = {{9.5, 1.5, 1.45, 10}, {11.0, 2.1, 1.65, 10}};
 constexpr double kShOwnBlockUs = 0.215, kShAgainBlockUs = 0.165, kShOwnCtaUs = 0.25;
 constexpr double kShOwnStartUs = 4.5, kShOwnTailUs = 4.0, kShOwnFull = 0.85;
 // Packs the groups (nt[j] tiles each, laid end to end) into runs of at most
-// `budget` cost; false if they take more than max_pairs.
-bool shared_pack(const int* nt, int n_groups, int budget, int max_pairs, int* cut, int& n_pairs) {
+// `budget` cost; false if they take more than max_units.
+bool shared_pack(const int* nt, int n_groups, int budget, int max_units, int* cut, int& n_units) {
   int c = 0, cost = 0, x = 0;
   cut[0] = 0;
   for (int j = 0; j < n_groups; ++j) {
@@ -1658,7 +1662,7 @@ bool shared_pack(const int* nt, int n_groups, int budget, int max_pairs, int* cu
     while (left > 0) {
       const int extra = cost > 0 ? kShSegCost : 0;
       if (cost + extra >= budget) {  // the run is full
-        if (++c >= max_pairs) return false;
+        if (++c >= max_units) return false;
         cut[c] = x;
         cost = 0;
         continue;
@@ -1669,8 +1673,8 @@ bool shared_pack(const int* nt, int n_groups, int budget, int max_pairs, int* cu
       left -= take;
     }
   }
-  n_pairs = c + 1;
-  cut[n_pairs] = x;
+  n_units = c + 1;
+  cut[n_units] = x;
   return true;
 }
 
@@ -1686,10 +1690,12 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
   p.S = S;
   p.W = W;
   p.prefix_blk = Pb;
-  p.n_grp = n < 2 || Pb == 0 ? 0 : (n * G + kUnitRows - 1) / kUnitRows;
+  p.n_cta = n * G <= kRows ? 1 : 2;
+  const int unit_rows = kRows * p.n_cta, tile_blk = kTileBlocks / 2 * p.n_cta;
+  p.n_grp = n < 2 || Pb == 0 ? 0 : (n * G + unit_rows - 1) / unit_rows;
   p.first_blk = p.n_grp > 0 ? Pb : 0;
   p.tiles_head = 0;
-  const int per = kUnitRows / G;  // sequences per group
+  const int per = unit_rows / G;  // sequences per group
   for (int j = 0; j < p.n_grp; ++j) {
     int lo = Pb;
     for (int s = j * per; s < std::min(n, (j + 1) * per); ++s) lo = std::min(lo, shared_win_lo(seqs[s0 + s].n_ctx, W));
@@ -1698,7 +1704,7 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
     g.lo = lo;
     g.sink = W > 0 ? std::min(S, lo) : 0;
     g.n_blk = g.sink + Pb - lo;
-    p.tiles_head += (g.n_blk + kTileBlocks - 1) / kTileBlocks;
+    p.tiles_head += (g.n_blk + tile_blk - 1) / tile_blk;
   }
   // at most 16 groups of 2^23 tiles: no overflow before the test
   if ((long long)HKV * p.tiles_head >= (1ll << 30)) return PA_EINVAL;
@@ -1725,34 +1731,35 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
     for (long long k; c < 128 && (k = own_ctas(c)) > slots && k > (long long)n * HKV;) c = std::min(128, c + c / 8 / 4 * 4 + 4);
     return c;
   };
-  // The prefix pass's pairs.  Both passes can run at once: the pairs left out
+  // The prefix pass's units.  Both passes can run at once: the units left out
   // leave their SMs to the per-sequence pass, whose CTAs otherwise start when the
-  // prefix pass ends.  Of a few numbers of pairs the one that ends first.
-  const int T = HKV * p.tiles_head, max_pairs = std::min(kShPairs, std::max(1, n_sm / 2)), J = HKV * p.n_grp;
-  p.n_pairs = 0;
+  // prefix pass ends.  Of a few numbers of units the one that ends first.
+  const int T = HKV * p.tiles_head, max_units = std::min(kShUnits, std::max(1, n_sm / p.n_cta)), J = HKV * p.n_grp;
+  const ShCost& cost = kShCost[p.n_cta - 1];
+  p.n_units = 0;
   p.merge_ways = 0;
-  int nt[8 * kShGroups], pairs = max_pairs;
+  int nt[8 * kShGroups], units = max_units;
   if (T > 0) {
-    for (int j = 0; j < J; ++j) nt[j] = (t.grp[j % p.n_grp].n_blk + kTileBlocks - 1) / kTileBlocks;
+    for (int j = 0; j < J; ++j) nt[j] = (t.grp[j % p.n_grp].n_blk + tile_blk - 1) / tile_blk;
     double best = 1e30;
     const double own_blk = (double)own * HKV, least_ctas = (double)n * HKV;
-    for (int left = 0; left < max_pairs; left += 4) {
-      const int use = std::min(max_pairs - left, T), free_sm = n_sm - 2 * use;
-      // a pair's cost when all are equal: its tiles, and its share of the groups' changes
+    for (int left = 0; left < max_units; left += 8 / p.n_cta) {
+      const int use = std::min(max_units - left, T), free_sm = n_sm - p.n_cta * use;
+      // a unit's cost when all are equal: its tiles, and its share of the groups' changes
       const int budget = (T + kShSegCost * std::max(0, J - use) + use - 1) / use + (J > 1 && J < use && use % J ? 1 : 0);
-      const double prefix_us = kShPairUs + kShTileUs * std::min(budget, 10) + kShLateTileUs * std::max(0, budget - 10);
+      const double prefix_us = cost.unit + cost.tile * std::min(budget, cost.early) + cost.late * std::max(0, budget - cost.early);
       const double slots = kShOwnPerSm * free_sm, ctas = std::max(least_ctas, std::min(own_blk / 4, kShOwnWaves * slots));
       const double own_us = (kShOwnBlockUs * own_blk + kShOwnCtaUs * ctas) / (least_ctas > slots ? kShOwnFull : 1.0);
-      // SM time before the prefix pass ends: that of the SMs left out; if none is, of the pairs with a tile less
+      // SM time before the prefix pass ends: that of the SMs left out; if none is, of the units with a tile less
       const double idle = free_sm > 1 ? free_sm * std::max(0.0, prefix_us - kShOwnStartUs)
-                                      : 2.0 * kShLateTileUs * std::max(0, budget * use - T);
+                                      : p.n_cta * cost.late * std::max(0, budget * use - T);
       const double rest = std::max(0.0, own_us - idle);
       const double end = prefix_us + (rest > 0.0 ? rest / n_sm + kShOwnTailUs : 0.0);
       if (end < best) {
         best = end;
-        pairs = use;
+        units = use;
       }
-      if (rest <= 0.0) break;  // fewer pairs only make the prefix pass longer
+      if (rest <= 0.0) break;  // fewer units only make the prefix pass longer
     }
     // With few sequences or a short prefix it is quicker that each reads the prefix too.
     double again = 0.0;
@@ -1765,20 +1772,20 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
   }
   {  // Two waves keep the SMs full beside a prefix pass (48 sequences, windowed, 12104 blocks: 33.4 us, with one 37.3);
     // alone one is quicker (40 sequences, 16408 blocks: 29.5 us, with two 32.1).
-    const int free_sm = p.tiles_head > 0 ? n_sm - 2 * pairs : n_sm, wave = kShOwnPerSm * (free_sm > 0 ? free_sm : n_sm);
+    const int free_sm = p.tiles_head > 0 ? n_sm - p.n_cta * units : n_sm, wave = kShOwnPerSm * (free_sm > 0 ? free_sm : n_sm);
     p.chunk = own_chunk(wave * std::max(p.tiles_head > 0 ? kShOwnWaves : 1, (n * HKV + n * HKV / 4) / wave));
   }
   if (p.tiles_head > 0) {
-    int budget = (T + pairs - 1) / pairs;
-    while (!shared_pack(nt, J, budget, pairs, t.cut, p.n_pairs)) ++budget;
+    int budget = (T + units - 1) / units;
+    while (!shared_pack(nt, J, budget, units, t.cut, p.n_units)) ++budget;
     int x = 0, c = 0, most = 0;
     for (int j = 0; j < J; ++j) {
-      while (c + 1 < p.n_pairs && t.cut[c + 1] <= x) ++c;
-      t.first_pair[j] = (uint8_t)c;
+      while (c + 1 < p.n_units && t.cut[c + 1] <= x) ++c;
+      t.first_unit[j] = (uint8_t)c;
       x += nt[j];
       int e = c;
-      while (e + 1 < p.n_pairs && t.cut[e + 1] < x) ++e;
-      t.last_pair[j] = (uint8_t)e;
+      while (e + 1 < p.n_units && t.cut[e + 1] < x) ++e;
+      t.last_unit[j] = (uint8_t)e;
       most = std::max(most, e - c + 1);
     }
     p.merge_ways = most;
@@ -1791,15 +1798,15 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
     chunks += c;
     most = std::max(most, c);
   }
-  p.merge_ways = std::min(8, (p.merge_ways + most + 3) / 4);
+  p.merge_ways = std::min(16, (p.merge_ways + most + 3) / 4);
   p.chunks_head = chunks;
   return PA_OK;
 }
 
-constexpr size_t kPrePartial = (size_t)kHeadDim * kUnitRows * sizeof(float);
-constexpr size_t kPreStats = (size_t)kUnitRows * sizeof(float2);
 constexpr size_t kOwnPartial = (size_t)kHeadDim * 8 * sizeof(float), kOwnStats = 8 * sizeof(float2);
-size_t pre_partials(const SharedParams& p) { return p.tiles_head > 0 ? (size_t)p.n_pairs + (size_t)p.n_grp * p.HKV : 0; }
+size_t pre_rows(const SharedParams& p) {  // of the partials
+  return p.tiles_head > 0 ? ((size_t)p.n_units + (size_t)p.n_grp * p.HKV) * p.n_cta * kRows : 0;
+}
 size_t own_partials(const SharedParams& p) { return (size_t)p.HKV * p.chunks_head; }
 
 int reserve(Workspace& w, size_t need, bool capturing) {
@@ -1835,13 +1842,13 @@ int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, i
     if ((rc = decode_shared_plan(h->HQ, h->HKV, h->n_sm, seqs, s0, std::min(kShSeqs, n_seq - s0), n_prefix, n_sink_blk,
                                  n_win_blk, h->sh_pass, p, t)))
       return rc;
-    pre = std::max(pre, pre_partials(p));
+    pre = std::max(pre, pre_rows(p));
     own = std::max(own, own_partials(p));
   }
   DecodeMaps maps;
   if ((rc = pool_maps(h, k_pool, v_pool, maps))) return rc;
   const bool capturing = capture != cudaStreamCaptureStatusNone;
-  if ((rc = reserve(h->sh_pre, pre * (kPrePartial + kPreStats), capturing))) return rc;
+  if ((rc = reserve(h->sh_pre, pre * (kHeadDim * sizeof(float) + sizeof(float2)), capturing))) return rc;
   if ((rc = reserve(h->sh_own, own * (kOwnPartial + kOwnStats), capturing))) return rc;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.out = static_cast<__nv_bfloat16*>(out);
@@ -1854,7 +1861,7 @@ int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, i
   p.n_pool = h->n_pool;
   p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
   p.pre_o = static_cast<float4*>(h->sh_pre.p);
-  p.pre_ml = reinterpret_cast<float2*>(static_cast<char*>(h->sh_pre.p) + pre * kPrePartial);
+  p.pre_ml = reinterpret_cast<float2*>(static_cast<char*>(h->sh_pre.p) + pre * kHeadDim * sizeof(float));
   p.own_o = static_cast<float4*>(h->sh_own.p);
   p.own_ml = reinterpret_cast<float2*>(static_cast<char*>(h->sh_own.p) + own * kOwnPartial);
   p.err = h->d_err;
@@ -1886,15 +1893,15 @@ int pa_decode_shared_plan(int n_q_heads, int n_kv_heads, int max_pages_per_seq, 
   if ((rc = decode_shared_plan(n_q_heads, n_kv_heads, n_sm, seqs, 0, std::min(n_seq, kShSeqs), n_prefix, n_sink_blk,
                                n_win_blk, prefix_pass, p, t)))
     return rc;
-  const int per = kUnitRows / p.G;
+  const int per = kRows * p.n_cta / p.G, tile_blk = kTileBlocks / 2 * p.n_cta;
   int np = 0;
   for (int g = 0; g < p.HKV; ++g)
     for (int j = 0; j < p.n_grp; ++j) {
       const ShGroup& gr = t.grp[j];
-      const int nt = (gr.n_blk + kTileBlocks - 1) / kTileBlocks;
+      const int nt = (gr.n_blk + tile_blk - 1) / tile_blk;
       const int a = g * p.tiles_head + gr.x0;
       for (int t0 = 0; t0 < nt;) {
-        const int c = (int)(std::upper_bound(t.cut, t.cut + p.n_pairs, a + t0) - t.cut) - 1;
+        const int c = (int)(std::upper_bound(t.cut, t.cut + p.n_units, a + t0) - t.cut) - 1;
         const int t1 = std::min(nt, t.cut[c + 1] - a);
         if (prefix_out) {
           if (np >= prefix_cap) return PA_EINVAL;
@@ -1905,8 +1912,8 @@ int pa_decode_shared_plan(int n_q_heads, int n_kv_heads, int max_pages_per_seq, 
           o[3] = std::min(p.n_seq, (j + 1) * per) - o[2];
           o[4] = gr.sink;
           o[5] = gr.lo;
-          o[6] = t0 * kTileBlocks;
-          o[7] = std::min(gr.n_blk, t1 * kTileBlocks);
+          o[6] = t0 * tile_blk;
+          o[7] = std::min(gr.n_blk, t1 * tile_blk);
         }
         ++np;
         t0 = t1;

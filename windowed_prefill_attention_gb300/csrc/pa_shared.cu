@@ -32,9 +32,9 @@ namespace pa {
 namespace {
 
 constexpr unsigned kAllLanes = 0xffffffffu;
-// The softmax reference moves when a row's maximum passes it by more than 2^14
-// (moving it rescales O, ~1500 cycles); P' <= 2^14 then, inside fp16's range.
-constexpr float kMaxLift = 14.f;
+// The softmax reference moves when a row's maximum passes it by more than 2^15
+// (moving it rescales O, ~1500 cycles); P' <= 2^15 then, inside fp16's range.
+constexpr float kMaxLift = 15.f;
 constexpr int DEV_ERR_LAYOUT = 0x400;  // shared memory's base is not aligned as the operands need (reported as PA_ECUDA)
 constexpr uint64_t kShDrainNs = 200000000ull;
 
@@ -167,7 +167,8 @@ enum : int {
   B_RAWF = 23, // the segment's raw queries have landed
   B_HELP = 24, // the softmax warps' rows of the first segment's queries are written
   B_DRAIN = 25,
-  kPreBars = 26
+  B_TMEM = 26, // one CTA alone: its tensor memory is allocated
+  kPreBars = 27
 };
 constexpr int kSmTmem = kSmBar + kPreBars * 8;
 constexpr int kPreSmem = kSmTmem + 16;
@@ -176,18 +177,21 @@ constexpr uint32_t kTmemO = 0, kTmemS = 256;        // O [0, 256), S of even / o
 
 // The B operand of O = P V: V as [key][64 dims] rows of 128 bytes with the
 // 128-byte swizzle, dims (N) contiguous: 8-key atoms of 1024 bytes along K,
-// regions of 128 keys x 128 bytes along N.
+// regions of a tile's keys x 128 bytes along N.
+template <int kN>
 __device__ __forceinline__ uint64_t sdesc_v(uint32_t saddr) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(16384 >> 4) << 16;     // leading byte offset: the next 64 dims
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;      // stride byte offset: the next 8 keys
+  d |= static_cast<uint64_t>(kN * 8192 >> 4) << 16;  // leading byte offset: the next 64 dims
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;       // stride byte offset: the next 8 keys
   d |= static_cast<uint64_t>(1) << 46;
   d |= static_cast<uint64_t>(2) << 61;
   return d;
 }
-constexpr uint32_t kIdescQK = idesc_f16(256, 128, false, false);
-constexpr uint32_t kIdescPV = idesc_f16(256, 256, false, false) | (1u << 16);  // B is N-major
+template <int kN>
+constexpr uint32_t kIdescQK = idesc_f16(kN * 128, kN * 64, false, false);
+template <int kN>
+constexpr uint32_t kIdescPV = idesc_f16(kN * 128, 256, false, false) | (1u << 16);  // B is N-major
 
 // A run of tiles of one group: a pair's work is one or more of these.
 struct Segment {
@@ -196,6 +200,7 @@ struct Segment {
   int t0, t1;       // tiles of the group
   int row0, rows;   // this CTA's first row (of the kv head's n_seq G) and how many there are
 };
+template <int kN>
 __device__ __forceinline__ Segment segment_at(const SharedParams& p, const SharedSeqs& tab, int rank, int x, int x_end) {
   Segment s;
   s.g = x / p.tiles_head;
@@ -205,8 +210,8 @@ __device__ __forceinline__ Segment segment_at(const SharedParams& p, const Share
   s.j = s.g * p.n_grp + s.rg;
   s.grp = tab.grp[s.rg];
   s.t0 = xh - s.grp.x0;
-  s.t1 = min((s.grp.n_blk + kTileBlocks - 1) / kTileBlocks, s.t0 + (x_end - x));
-  s.row0 = s.rg * kUnitRows + rank * kRows;
+  s.t1 = min((s.grp.n_blk + kN * 4 - 1) / (kN * 4), s.t0 + (x_end - x));
+  s.row0 = s.rg * (kN * kRows) + rank * kRows;
   s.rows = max(0, min(kRows, p.n_seq * p.G - s.row0));
   return s;
 }
@@ -302,9 +307,10 @@ __device__ __forceinline__ void stage_queries(const PreCtx& c, const Segment& s,
 // for the last P V of the one before.
 constexpr int kHelpRows = 12;  // each softmax warp's; the four V warps share the others
 static_assert(kSoftWarps * kHelpRows + 4 * 8 == kRows, "rows of the first segment");
+template <int kN>
 __device__ __forceinline__ bool help_stage(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
   const int warp = threadIdx.x >> 5;
-  const Segment s = segment_at(p, tab, c.rank, c.x0, c.x1);
+  const Segment s = segment_at<kN>(p, tab, c.rank, c.x0, c.x1);
   if (!c.wait(B_RAWF, 0)) return false;
   stage_queries(c, s, c.sb + kSmV, c.sb + kSmRow, kHelpRows * warp, kHelpRows * (warp + 1));
   if ((threadIdx.x & 31) == 0) mbar_arrive(c.bar(B_HELP));
@@ -313,36 +319,39 @@ __device__ __forceinline__ bool help_stage(const SharedParams& p, const SharedSe
 
 // One code for K and V warps: the kernel's instructions exceed the caches that
 // feed the schedulers, and every line of it is fetched anew for each tile.
+template <int kN>
 __device__ __forceinline__ void role_convert(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kSoftWarps;
   const bool kv = warp >= kConvWarps / 2;  // V
   const int w = warp & 3;
   uint32_t n_tile = 0, n_seg = 0;
   const size_t tok = (size_t)p.HKV * kHeadDim;  // bytes from a token to the next
-  // K: warp w the 16 keys 64 rank + 16 w on, all dims; a load takes two keys.
-  // V: warp w keys 32 w on, dims 128 rank on; a load takes four keys.  Lane bit 2
+  // Warp w the 16 keys 64 rank + 16 w on, all dims; a load takes two keys.  V of a
+  // pair: keys 32 w on, dims 128 rank on; a load takes four keys.  Lane bit 2
   // (and 4) the key, the others the 16 bytes.
-  const int u = kv ? (lane & 3) | (lane >> 1 & 4) : (lane & 3) | (lane >> 3) << 2;
-  const int sub = kv ? (lane >> 2 & 1) | (lane >> 4) << 1 : lane >> 2 & 1;
-  const int step = kv ? 4 : 2;                                  // keys per load
-  const int row0 = (kv ? 32 : 16) * w + sub;                    // the stage's row of the lane's first load
-  const uint32_t at0 = c.sb + (kv ? kSmV + (u >> 2) * 16384 : kSmK + (u >> 2) * 8192) + row0 * 128;
-  const int blk0 = kv ? 2 * w : 4 * c.rank + w;                 // first block of the tile it loads
-  const size_t step_b = step * tok, half_b = kv ? 0 : 8 * tok;  // from a load to the next; from load 0 to load 4
-  const int blk4 = kv ? blk0 + 1 : blk0;                        // block of load 4
-  const int8_t* base = (kv ? p.v_pool + 128 * c.rank : p.k_pool) + 16 * u + (size_t)sub * tok;
+  const bool wide = kN == 2 && kv;
+  const int u = wide ? (lane & 3) | (lane >> 1 & 4) : (lane & 3) | (lane >> 3) << 2;
+  const int sub = wide ? (lane >> 2 & 1) | (lane >> 4) << 1 : lane >> 2 & 1;
+  const int step = wide ? 4 : 2;                                // keys per load
+  const int row0 = (wide ? 32 : 16) * w + sub;                  // the stage's row of the lane's first load
+  const uint32_t at0 = c.sb + (kv ? kSmV : kSmK) + (u >> 2) * (wide ? 16384 : 8192) + row0 * 128;
+  const int blk0 = wide ? 2 * w : 4 * c.rank + w;               // first block of the tile it loads
+  const size_t step_b = step * tok, half_b = wide ? 0 : 8 * tok;  // from a load to the next; from load 0 to load 4
+  const int blk4 = wide ? blk0 + 1 : blk0;                      // block of load 4
+  const int8_t* base = (kv ? p.v_pool + (wide ? 128 * c.rank : 0) : p.k_pool) + 16 * u + (size_t)sub * tok;
+  constexpr int kBlk = 4 * kN, kWin = 32 / kBlk;                // a tile's blocks; tiles of a window of pages
   for (int x = c.x0; x < c.x1; ++n_seg) {
-    const Segment s = segment_at(p, tab, c.rank, x, c.x1);
+    const Segment s = segment_at<kN>(p, tab, c.rank, x, c.x1);
     const int8_t* src = base + (size_t)s.g * kHeadDim;
-    // pages of the segment's blocks, 32 (four tiles) at a time, one per lane
-    const int b0 = s.t0 * kTileBlocks;
+    // pages of the segment's blocks, 32 at a time, one per lane
+    const int b0 = s.t0 * kBlk;
     int pg = group_page(p, s.grp, b0 + lane), pg_next = group_page(p, s.grp, b0 + 32 + lane);
     uint4 r[8];
     // a block past the list or of a bad page loads page 0's codes: whatever finite values they widen to,
     // the softmax gives those keys no weight
-    auto load = [&](int t4) {
-      const int pa = max(0, __shfl_sync(kAllLanes, pg, t4 * kTileBlocks + blk0));
-      const int pb = max(0, __shfl_sync(kAllLanes, pg, t4 * kTileBlocks + blk4));
+    auto load = [&](int tw) {
+      const int pa = max(0, __shfl_sync(kAllLanes, pg, tw * kBlk + blk0));
+      const int pb = max(0, __shfl_sync(kAllLanes, pg, tw * kBlk + blk4));
       const int8_t* a = src + (size_t)pa * (kPage * tok);
       const int8_t* b = src + (size_t)pb * (kPage * tok) + half_b;
 #pragma unroll
@@ -367,9 +376,9 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
 
     const int nt = s.t1 - s.t0;
     for (int t = 0; t < nt; ++t, ++n_tile) {
-      if (((t + 1) & 3) == 0) {  // the next tile's pages are in the next window
+      if (((t + 1) & (kWin - 1)) == 0) {  // the next tile's pages are in the next window
         pg = pg_next;
-        pg_next = group_page(p, s.grp, b0 + 8 * (t + 1) + 32 + lane);
+        pg_next = group_page(p, s.grp, b0 + kBlk * (t + 1) + 32 + lane);
       }
       // the stage's products of two tiles before are done
       const int st = n_tile & 1;
@@ -379,7 +388,7 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(c.bar((kv ? (c.rank == 0 ? B_VF : B_VL) : (c.rank == 0 ? B_KF : B_KL)) + st));
-      if (t + 1 < nt) load((t + 1) & 3);
+      if (t + 1 < nt) load((t + 1) & (kWin - 1));
     }
     x += nt;
   }
@@ -408,11 +417,12 @@ __device__ __forceinline__ void copy_queries(const SharedParams& p, const Shared
 }
 // The first segment's copies have been issued.  In the odd CTA also the forward
 // of its queries.
+template <int kN>
 __device__ __forceinline__ void role_queries(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
   const int lane = threadIdx.x & 31;
   uint32_t n_seg = 0, copied = 1;
   for (int x = c.x0; x < c.x1; ++n_seg) {
-    const Segment s = segment_at(p, tab, c.rank, x, c.x1);
+    const Segment s = segment_at<kN>(p, tab, c.rank, x, c.x1);
     if (n_seg > 0) {
       if (!c.wait(B_QE, n_seg - 1)) break;
       copy_queries(p, tab, c, s, c.sb + kSmK);
@@ -430,20 +440,22 @@ __device__ __forceinline__ void role_queries(const SharedParams& p, const Shared
 }
 
 // ---- scales of every tile's keys, V's normalised by a running power of two.
+template <int kN>
 __device__ __forceinline__ void role_scales(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
   const int lane = threadIdx.x & 31;
   uint32_t n_tile = 0;
   for (int x = c.x0; x < c.x1;) {
-    const Segment s = segment_at(p, tab, c.rank, x, c.x1);
+    const Segment s = segment_at<kN>(p, tab, c.rank, x, c.x1);
     int ev = -100;
-    // lane: keys 4 lane .. + 3 of a tile, in block lane / 4
+    // lane: keys 4 lane .. + 3 of a tile, in block lane / 4 (one CTA alone: half the lanes)
+    const bool mine = lane < 16 * kN;
     float ks[4], vs[4];
     bool valid = false;
     auto load = [&](int t) {
-      const int b = t * kTileBlocks + (lane >> 2);
-      const int page = group_page(p, s.grp, b);
+      const int b = t * (4 * kN) + (lane >> 2);
+      const int page = mine ? group_page(p, s.grp, b) : -1;
       valid = page >= 0;
-      if (!valid && b < s.grp.n_blk && (lane & 3) == 0) atomicCAS(p.err, 0, DEV_ERR_BAD_PAGE);
+      if (!valid && mine && b < s.grp.n_blk && (lane & 3) == 0) atomicCAS(p.err, 0, DEV_ERR_BAD_PAGE);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const size_t at = ((size_t)(valid ? page : 0) * kPage + 4 * (lane & 3) + e) * p.HKV + s.g;
@@ -468,7 +480,7 @@ __device__ __forceinline__ void role_scales(const SharedParams& p, const SharedS
       if (lane == 0) {
         uint32_t m8 = 0;
 #pragma unroll
-        for (int e = 0; e < kTileBlocks; ++e) m8 |= ((ok >> (4 * e)) & 1u) << e;
+        for (int e = 0; e < 4 * kN; ++e) m8 |= ((ok >> (4 * e)) & 1u) << e;
         sts128(at + 1024, m8, (uint32_t)ev, 0, 0);
       }
       __syncwarp();
@@ -483,76 +495,86 @@ __device__ __forceinline__ void role_scales(const SharedParams& p, const SharedS
 // of one asm block with the operands' offsets added inside it: instructions
 // between them, a branch above all, leave the tensor pipe waiting.
 // S = Q K^T: four regions of 64 dims, four k-steps of 32 bytes each.
+#define PA_SH_QK(G, qo, ko)                                \
+  "add.s64 a, %1, " qo ";\n\tadd.s64 b, %2, " ko ";\n\t" \
+  "tcgen05.mma.cta_group::" G ".kind::f16 [%0], a, b, %3, pt;\n\t"
+#define PA_SH_QK4(G, r)                                                                                           \
+  PA_SH_QK(G, r " * 1024", r " * 512") PA_SH_QK(G, r " * 1024 + 2", r " * 512 + 2") PA_SH_QK(G, r " * 1024 + 4", r " * 512 + 4") \
+      PA_SH_QK(G, r " * 1024 + 6", r " * 512 + 6")
+#define PA_SH_QK_TILE(G)                                                                                          \
+  "{\n\t.reg .pred pf, pt;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 pf, %4, %4;\n\tsetp.eq.b32 pt, %4, %4;\n\t"          \
+  "tcgen05.mma.cta_group::" G ".kind::f16 [%0], %1, %2, %3, pf;\n\t"                                              \
+  PA_SH_QK(G, "2", "2") PA_SH_QK(G, "4", "4") PA_SH_QK(G, "6", "6") PA_SH_QK4(G, "1") PA_SH_QK4(G, "2") PA_SH_QK4(G, "3") "}"
+template <int kN>
 __device__ __forceinline__ void mma_qk_tile(uint32_t d, uint64_t qd, uint64_t kd) {
-#define PA_SH_QK(qo, ko)                          \
-  "add.s64 a, %1, " #qo ";\n\tadd.s64 b, %2, " #ko ";\n\t" \
-  "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, pt;\n\t"
-  asm volatile(
-      "{\n\t.reg .pred pf, pt;\n\t.reg .b64 a, b;\n\t"
-      "setp.ne.b32 pf, %4, %4;\n\tsetp.eq.b32 pt, %4, %4;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, pf;\n\t"
-      PA_SH_QK(2, 2) PA_SH_QK(4, 4) PA_SH_QK(6, 6)
-      PA_SH_QK(1024, 512) PA_SH_QK(1026, 514) PA_SH_QK(1028, 516) PA_SH_QK(1030, 518)
-      PA_SH_QK(2048, 1024) PA_SH_QK(2050, 1026) PA_SH_QK(2052, 1028) PA_SH_QK(2054, 1030)
-      PA_SH_QK(3072, 1536) PA_SH_QK(3074, 1538) PA_SH_QK(3076, 1540) PA_SH_QK(3078, 1542)
-      "}" ::"r"(d), "l"(qd), "l"(kd), "r"(kIdescQK), "r"(0u)
-      : "memory");
-#undef PA_SH_QK
+  if constexpr (kN == 2)
+    asm volatile(PA_SH_QK_TILE("2") ::"r"(d), "l"(qd), "l"(kd), "r"(kIdescQK<2>), "r"(0u) : "memory");
+  else
+    asm volatile(PA_SH_QK_TILE("1") ::"r"(d), "l"(qd), "l"(kd), "r"(kIdescQK<1>), "r"(0u) : "memory");
 }
-// O (+)= P V over 128 keys: eight k-steps of 16 keys, 8 TMEM columns of P' and 2048 bytes of V each.
+// O (+)= P V: k-steps of 16 keys, 8 TMEM columns of P' and 2048 bytes of V each.
+#define PA_SH_PV(G, po, vo)                                \
+  "add.u32 a, %1, " po ";\n\tadd.s64 b, %2, " vo ";\n\t" \
+  "tcgen05.mma.cta_group::" G ".kind::f16 [%0], [a], b, %3, pt;\n\t"
+#define PA_SH_PV_FIRST(G)                                                                                         \
+  "{\n\t.reg .pred p0, pt;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\tsetp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 pt, %4, %4;\n\t" \
+  "tcgen05.mma.cta_group::" G ".kind::f16 [%0], [%1], %2, %3, p0;\n\t"                                            \
+  PA_SH_PV(G, "8", "128") PA_SH_PV(G, "16", "256") PA_SH_PV(G, "24", "384")
+template <int kN>
 __device__ __forceinline__ void mma_pv_tile(uint32_t d, uint32_t ptm, uint64_t vd, uint32_t acc0) {
-#define PA_SH_PV(po, vo)                          \
-  "add.u32 a, %1, " #po ";\n\tadd.s64 b, %2, " #vo ";\n\t" \
-  "tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, pt;\n\t"
-  asm volatile(
-      "{\n\t.reg .pred p0, pt;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
-      "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 pt, %4, %4;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p0;\n\t"
-      PA_SH_PV(8, 128) PA_SH_PV(16, 256) PA_SH_PV(24, 384) PA_SH_PV(32, 512) PA_SH_PV(40, 640) PA_SH_PV(48, 768)
-      PA_SH_PV(56, 896)
-      "}" ::"r"(d), "r"(ptm), "l"(vd), "r"(kIdescPV), "r"(acc0)
-      : "memory");
-#undef PA_SH_PV
+  if constexpr (kN == 2)
+    asm volatile(PA_SH_PV_FIRST("2") PA_SH_PV("2", "32", "512") PA_SH_PV("2", "40", "640") PA_SH_PV("2", "48", "768")
+                 PA_SH_PV("2", "56", "896") "}" ::"r"(d), "r"(ptm), "l"(vd), "r"(kIdescPV<2>), "r"(acc0) : "memory");
+  else
+    asm volatile(PA_SH_PV_FIRST("1") "}" ::"r"(d), "r"(ptm), "l"(vd), "r"(kIdescPV<1>), "r"(acc0) : "memory");
 }
 static_assert((16384 >> 4) == 1024 && (8192 >> 4) == 512 && (2048 >> 4) == 128, "descriptor steps of the blocks above");
+template <int kN>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (kN == 2) mma_commit_pair(bar);
+  else mma_commit(bar);
+}
 
 // Q K^T of tile t + 1 goes before P V of tile t, so that the tensor core has
 // the next scores to compute while the softmax handles these.  The parity waits:
 // a tile's K, V, P' and queries are written only after the products that read
 // what was there before.
+template <int kN>
 __device__ __forceinline__ void role_issue(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
   uint32_t n_tile = 0, n_seg = 0;
   bool ok = true;
   const uint64_t qd = sdesc_k_sw128(c.sb + kSmQ);
   const uint64_t kd0 = sdesc_k_sw128(c.sb + kSmK), kd1 = sdesc_k_sw128(c.sb + kSmK + kStageBytes);
-  const uint64_t vd0 = sdesc_v(c.sb + kSmV), vd1 = sdesc_v(c.sb + kSmV + kStageBytes);
+  const uint64_t vd0 = sdesc_v<kN>(c.sb + kSmV), vd1 = sdesc_v<kN>(c.sb + kSmV + kStageBytes);
   // K, V and queries of the odd CTA come with a cluster-scope release
-  auto wait_pair = [&](int i, uint32_t parity) { return mbar_wait_cluster(c.bar(i), parity & 1u, c.wc, 80 + i); };
+  auto wait_pair = [&](int i, uint32_t parity) {
+    return kN == 2 ? mbar_wait_cluster(c.bar(i), parity & 1u, c.wc, 80 + i) : mbar_wait(c.bar(i), parity & 1u, c.wc, 80 + i);
+  };
   auto wait = [&](int i, uint32_t parity) { return mbar_wait(c.bar(i), parity & 1u, c.wc, 80 + i); };
   auto qk = [&](uint32_t n) {  // n: the tile's number in the pair's order
     if (!wait_pair(B_KF + (n & 1), n >> 1)) return false;
     tc_fence_after();
-    mma_qk_tile(c.tm + kTmemS + 128 * (n & 1), qd, (n & 1) ? kd1 : kd0);
-    mma_commit_pair(c.bar(B_SF + (n & 1)));
+    mma_qk_tile<kN>(c.tm + kTmemS + 128 * (n & 1), qd, (n & 1) ? kd1 : kd0);
+    commit<kN>(c.bar(B_SF + (n & 1)));
     return true;
   };
   auto pv = [&](uint32_t n, uint32_t acc) {
     if (!wait_pair(B_VF + (n & 1), n >> 1) || !wait(B_PF + (n & 1), n >> 1)) return false;
     tc_fence_after();
-    mma_pv_tile(c.tm + kTmemO, c.tm + kTmemS + 128 * (n & 1), (n & 1) ? vd1 : vd0, acc);
-    mma_commit_pair(c.bar(B_OD + (n & 1)));
+    mma_pv_tile<kN>(c.tm + kTmemO, c.tm + kTmemS + 128 * (n & 1), (n & 1) ? vd1 : vd0, acc);
+    commit<kN>(c.bar(B_OD + (n & 1)));
     return true;
   };
   for (int x = c.x0; ok && x < c.x1; ++n_seg) {
-    const Segment s = segment_at(p, tab, c.rank, x, c.x1);
+    const Segment s = segment_at<kN>(p, tab, c.rank, x, c.x1);
     const int nt = s.t1 - s.t0;
     ok = wait_pair(B_QF, n_seg) && qk(n_tile);
-    if (nt == 1) mma_commit_pair(c.bar(B_QE));
+    if (nt == 1) commit<kN>(c.bar(B_QE));
     // the epilogue has read the segment before's O
     ok = ok && (n_seg == 0 || wait(B_OE, n_seg - 1));
     for (int t = 1; ok && t < nt; ++t) {
       ok = qk(n_tile + t);
-      if (t == nt - 1) mma_commit_pair(c.bar(B_QE));
+      if (t == nt - 1) commit<kN>(c.bar(B_QE));
       ok = ok && pv(n_tile + t - 1, t > 1);
     }
     ok = ok && pv(n_tile + nt - 1, nt > 1);
@@ -560,7 +582,7 @@ __device__ __forceinline__ void role_issue(const SharedParams& p, const SharedSe
     x += nt;
   }
   // nothing may be in flight when the CTAs free their TMEM
-  mma_commit_pair(c.bar(B_DRAIN));
+  commit<kN>(c.bar(B_DRAIN));
   (void)mbar_wait_drain(c.bar(B_DRAIN), 0, kShDrainNs);
 }
 
@@ -574,12 +596,12 @@ struct SliceRows {
 };
 
 // z = score * k_scale, and the rows' maxima.
-template <bool kMasked>
-__device__ __forceinline__ void scale_and_max(uint32_t (&s)[64], uint32_t ks_at, uint32_t seen0, uint32_t seen1,
+template <bool kMasked, int kN>
+__device__ __forceinline__ void scale_and_max(uint32_t (&s)[32 * kN], uint32_t ks_at, uint32_t seen0, uint32_t seen1,
                                               float& z0, float& z1) {
   float za = -INFINITY, zb = -INFINITY;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
+  for (int k = 0; k < 8 * kN; ++k) {
     float2 ks;
     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks.x), "=f"(ks.y) : "r"(ks_at + 32 * k));
     float2 a = mul2(make_float2(__uint_as_float(s[4 * k]), __uint_as_float(s[4 * k + 1])), ks);
@@ -600,17 +622,19 @@ __device__ __forceinline__ void scale_and_max(uint32_t (&s)[64], uint32_t ks_at,
 }
 
 // One tile of the warp's rows: P' over its scores.  `first`: no O to rescale yet.
+template <int kN>
 __device__ __forceinline__ bool softmax_tile(const SharedParams& p, const PreCtx& c, const ShGroup& grp, int blk0,
                                              uint32_t stm, uint32_t otm, uint32_t sc, uint32_t valid, float fe,
                                              bool first, uint32_t n_before, SliceRows& r) {
   const int lane = threadIdx.x & 31;
   const uint32_t ks_at = sc + 8 * (lane & 3);
-  uint32_t s[64];
-  tmem_ld_16x256b_x16(stm, s);
+  uint32_t s[32 * kN];
+  if constexpr (kN == 2) tmem_ld_16x256b_x16(stm, s);
+  else tmem_ld_16x256b_x8(stm, s);
   uint32_t seen[2] = {valid, valid};  // blocks of the tile that the rows see
   if (p.W > 0) {
 #pragma unroll
-    for (int e = 0; e < kTileBlocks; ++e) {
+    for (int e = 0; e < 4 * kN; ++e) {
       const int lb = group_block(grp, blk0 + e);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -619,8 +643,8 @@ __device__ __forceinline__ bool softmax_tile(const SharedParams& p, const PreCtx
   }
   tmem_wait_ld(s);
   float z[2];
-  if (__all_sync(kAllLanes, (seen[0] & seen[1]) == 0xffu)) scale_and_max<false>(s, ks_at, 0, 0, z[0], z[1]);
-  else scale_and_max<true>(s, ks_at, seen[0], seen[1], z[0], z[1]);
+  if (__all_sync(kAllLanes, (seen[0] & seen[1]) == (1u << (4 * kN)) - 1u)) scale_and_max<false, kN>(s, ks_at, 0, 0, z[0], z[1]);
+  else scale_and_max<true, kN>(s, ks_at, seen[0], seen[1], z[0], z[1]);
   // The rows' references.  Mostly no row passes its own by enough to move it,
   // which each thread sees from its own keys; only else are the rows' maxima
   // put together.
@@ -651,7 +675,7 @@ __device__ __forceinline__ bool softmax_tile(const SharedParams& p, const PreCtx
   const float n0 = r.m[0] == -INFINITY ? 0.f : -r.m[0], n1 = r.m[1] == -INFINITY ? 0.f : -r.m[1];
   const float c0 = fmaxf(r.c[0], 1e-30f), c1 = fmaxf(r.c[1], 1e-30f);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {  // 64 keys
+  for (int h = 0; h < kN; ++h) {  // 64 keys
     uint32_t ph[16];
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
@@ -694,6 +718,7 @@ __device__ __forceinline__ bool softmax_tile(const SharedParams& p, const PreCtx
   return true;
 }
 
+template <int kN>
 __device__ __forceinline__ void role_softmax(const SharedParams& p, const SharedSeqs& tab, const PreCtx& c) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = 32 * (warp & 3), half = warp >> 2;
@@ -701,7 +726,7 @@ __device__ __forceinline__ void role_softmax(const SharedParams& p, const Shared
   const int row0 = quad + 16 * half + (lane >> 2);            // this thread's: row0, row0 + 8
   uint32_t n_tile = 0, n_seg = 0;
   for (int x = c.x0; x < c.x1; ++n_seg) {
-    const Segment s = segment_at(p, tab, c.rank, x, c.x1);
+    const Segment s = segment_at<kN>(p, tab, c.rank, x, c.x1);
     const int nt = s.t1 - s.t0;
     SliceRows r;
 #pragma unroll
@@ -730,7 +755,7 @@ __device__ __forceinline__ void role_softmax(const SharedParams& p, const Shared
       const int ev_t = (int)__float_as_uint(meta.y);
       const float fe = ev_t > ev ? pow2i(max(-126, ev - ev_t)) : 1.f;
       ev = ev_t;
-      if (!softmax_tile(p, c, s.grp, (s.t0 + t) * kTileBlocks, stm, c.tm + kTmemO + lanes, sc, __float_as_uint(meta.x), fe,
+      if (!softmax_tile<kN>(p, c, s.grp, (s.t0 + t) * (4 * kN), stm, c.tm + kTmemO + lanes, sc, __float_as_uint(meta.x), fe,
                         t == 0, n_tile - 1, r))
         return;
       tmem_wait_st();
@@ -744,9 +769,9 @@ __device__ __forceinline__ void role_softmax(const SharedParams& p, const Shared
     // the segment's partial: one row a thread, the quadrant's two warps half of the dims each
     if (!c.wait(B_OD + ((n_tile - 1) & 1), (n_tile - 1) >> 1)) return;
     tc_fence_after();
-    const int id = (int)(blockIdx.x >> 1) + s.j, row = quad + lane;
+    const int id = (int)blockIdx.x / kN + s.j, row = quad + lane;
     const float up = pow2i(ev);
-    float4* dst = p.pre_o + ((size_t)id * 64 + 32 * half) * kUnitRows + c.rank * kRows + row;
+    float4* dst = p.pre_o + ((size_t)id * 64 + 32 * half) * (kN * kRows) + c.rank * kRows + row;
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {  // 64 columns
       uint32_t o[2][32];
@@ -759,7 +784,7 @@ __device__ __forceinline__ void role_softmax(const SharedParams& p, const Shared
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const uint32_t* v = o[e >> 3] + 4 * (e & 7);
-          dst[(size_t)(16 * h + e) * kUnitRows] =
+          dst[(size_t)(16 * h + e) * (kN * kRows)] =
               make_float4(__uint_as_float(v[0]) * up, __uint_as_float(v[1]) * up, __uint_as_float(v[2]) * up,
                           __uint_as_float(v[3]) * up);
         }
@@ -774,14 +799,14 @@ __device__ __forceinline__ void role_softmax(const SharedParams& p, const Shared
       sum += __shfl_xor_sync(kAllLanes, sum, 1);
       sum += __shfl_xor_sync(kAllLanes, sum, 2);
       if ((lane & 3) == 0 && row0 + 8 * i < s.rows)
-        p.pre_ml[(size_t)id * kUnitRows + c.rank * kRows + row0 + 8 * i] = make_float2(r.m[i], sum);
+        p.pre_ml[(size_t)id * (kN * kRows) + c.rank * kRows + row0 + 8 * i] = make_float2(r.m[i], sum);
     }
     x += nt;
   }
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
-    prefix_kernel(const __grid_constant__ SharedParams p, const __grid_constant__ SharedSeqs tab) {
+template <int kN>
+__device__ __forceinline__ void prefix_pass(const SharedParams& p, const SharedSeqs& tab) {
   extern __shared__ __align__(1024) uint8_t raw[];
   PreCtx c;
   c.sb = smem_u32(raw);
@@ -790,19 +815,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
     return;
   }
   c.wc = WaitCtl{p.err, p.wait_ns};
-  c.rank = (int)cluster_rank();
-  c.x0 = tab.cut[blockIdx.x >> 1];
-  c.x1 = tab.cut[(blockIdx.x >> 1) + 1];
+  c.rank = kN == 2 ? (int)cluster_rank() : 0;
+  c.x0 = tab.cut[blockIdx.x / kN];
+  c.x1 = tab.cut[blockIdx.x / kN + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x < kPreBars) {
     const int i = threadIdx.x;
     int n = 1;
-    if (i < B_KL) n = kConvWarps / 2 + 1;
+    if (i < B_KL) n = kConvWarps / 2 + kN - 1;
     if (i >= B_KL && i < B_SF) n = kConvWarps / 2;
-    if (i == B_QF) n = kConvWarps + 1;
+    if (i == B_QF) n = kConvWarps + kN - 1;
     if (i == B_QL || i == B_RAW) n = kConvWarps;
     if ((i >= B_SCE && i < B_QF) || i == B_HELP) n = kSoftWarps;
-    if ((i >= B_PF && i < B_OD) || i == B_OE) n = 2 * kSoftWarps;
+    if ((i >= B_PF && i < B_OD) || i == B_OE) n = kN * kSoftWarps;
     mbar_init(c.bar(i), n);
     fence_mbar_init();
   }
@@ -810,40 +835,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
   // The first segment's queries come in and are staged, and its first K tile is
   // widened, while the pair's tensor memory is allocated and the CTAs meet: only
   // what reaches into the other CTA or tensor memory waits for that.
-  if (warp == kQueryWarp) copy_queries(p, tab, c, segment_at(p, tab, c.rank, c.x0, c.x1), c.sb + kSmV);
+  if (warp == kQueryWarp) copy_queries(p, tab, c, segment_at<kN>(p, tab, c.rank, c.x0, c.x1), c.sb + kSmV);
   if (warp == kIssueWarp) {
-    tmem_alloc_pair(c.sb + kSmTmem, 512);
-    tmem_relinquish_pair();
+    if constexpr (kN == 2) {
+      tmem_alloc_pair(c.sb + kSmTmem, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(c.sb + kSmTmem, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
-  cluster_arrive();
+  if constexpr (kN == 2) {
+    cluster_arrive();
+  } else {
+    __syncwarp();
+    if (warp == kIssueWarp && lane == 0) mbar_arrive(c.bar(B_TMEM));
+  }
   dependents_may_start();
   auto meet = [&] {  // both CTAs have their barriers and tensor memory; once in every thread
-    cluster_wait();
+    bool ok = true;
+    if constexpr (kN == 2) cluster_wait();
+    else ok = c.wait(B_TMEM, 0);
     tc_fence_after();
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c.tm) : "r"(c.sb + kSmTmem));
+    return ok;
   };
   if (warp < kSoftWarps) {
     more_regs<kSoftRegs>();
-    const bool ok = help_stage(p, tab, c);
-    meet();
-    if (ok) role_softmax(p, tab, c);
+    const bool ok = help_stage<kN>(p, tab, c);
+    if (meet() && ok) role_softmax<kN>(p, tab, c);
   } else if (warp < kIssueWarp) {
     fewer_regs<kConvRegs>();
-    role_convert(p, tab, c);
-    meet();
+    role_convert<kN>(p, tab, c);
+    (void)meet();
   } else {
     fewer_regs<kMiscRegs>();
     if (warp == kScaleWarp) {
-      role_scales(p, tab, c);
-      meet();
+      role_scales<kN>(p, tab, c);
+      (void)meet();
     } else {
-      meet();
+      const bool ok = meet();
       if (warp == kQueryWarp) {
-        role_queries(p, tab, c);
-      } else if (lane == 0) {
+        role_queries<kN>(p, tab, c);
+      } else if (lane == 0 && ok) {
         if (c.rank == 0) {
-          if (warp == kIssueWarp) role_issue(p, tab, c);
+          if (warp == kIssueWarp) role_issue<kN>(p, tab, c);
         } else {
           if (warp == kIssueWarp) role_forward_tiles(c, B_KL, B_KF);
           else role_forward_tiles(c, B_VL, B_VF);
@@ -856,9 +893,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // no arrival from the other CTA is still on its way
+  if constexpr (kN == 2) cluster_sync_all();  // no arrival from the other CTA is still on its way
   tc_fence_after();
-  if (warp == kIssueWarp) tmem_dealloc_pair(c.tm, 512);
+  if (warp == kIssueWarp) {
+    if constexpr (kN == 2) tmem_dealloc_pair(c.tm, 512);
+    else tmem_dealloc(c.tm, 512);
+  }
+}
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
+    prefix_pair_kernel(const __grid_constant__ SharedParams p, const __grid_constant__ SharedSeqs tab) {
+  prefix_pass<2>(p, tab);
+}
+__global__ void __launch_bounds__(kPreThreads, 1)
+    prefix_one_kernel(const __grid_constant__ SharedParams p, const __grid_constant__ SharedSeqs tab) {
+  prefix_pass<1>(p, tab);
 }
 
 // ====================================================================
@@ -1161,34 +1209,35 @@ __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const 
 // through shared memory in a fixed order.  Bound by the latency of the partials'
 // loads: the ways (as many as give a thread about four partials) and four loads
 // a thread keep them in flight together.
-constexpr int kMergeMostWays = 8;
-constexpr int kMergeDims = 64;
+constexpr int kMergeMostWays = 16;
+constexpr int kMergeDims = 32;
 
-__global__ void __launch_bounds__(8 * 16 * kMergeMostWays) merge_kernel(const __grid_constant__ SharedParams p,
+__global__ void __launch_bounds__(8 * kMergeDims / 4 * kMergeMostWays) merge_kernel(const __grid_constant__ SharedParams p,
                                                                     const __grid_constant__ SharedSeqs tab) {
-  __shared__ float4 acc_sh[kMergeMostWays - 1][16 * 8];
-  __shared__ float2 ml_sh[kMergeMostWays - 1][16 * 8];
+  __shared__ float4 acc_sh[kMergeMostWays - 1][kMergeDims / 4 * 8];
+  __shared__ float2 ml_sh[kMergeMostWays - 1][kMergeDims / 4 * 8];
   const int s = blockIdx.x / p.HKV, g = blockIdx.x % p.HKV;
-  const int slot = threadIdx.x % (16 * p.G), way = threadIdx.x / (16 * p.G);
+  const int slot = threadIdx.x % (kMergeDims / 4 * p.G), way = threadIdx.x / (kMergeDims / 4 * p.G);
   const int r = slot & (p.G - 1), dq = blockIdx.y * (kMergeDims / 4) + (slot >> p.log2_g);
   const int4 sq = tab.s[s];
   const ShOwn own = shared_own(sq.y, sq.w, p.first_blk, p.S, p.W);
   const int n_own = (own.n + p.chunk - 1) / p.chunk, own0 = p.HKV * sq.z + g;
-  int n_pre = 0, pre0 = 0, prow = 0;
+  int n_pre = 0, pre0 = 0, prow = 0, rows = 0;
   if (p.n_grp > 0) {
-    const int rg = (s * p.G) / kUnitRows;
+    const int unit = p.n_cta * kRows, rg = (s * p.G) / unit;
     const ShGroup grp = tab.grp[rg];
     if (grp.n_blk > 0) {
-      const int c0 = tab.first_pair[g * p.n_grp + rg], c1 = tab.last_pair[g * p.n_grp + rg];
+      const int c0 = tab.first_unit[g * p.n_grp + rg], c1 = tab.last_unit[g * p.n_grp + rg];
       n_pre = c1 - c0 + 1;
       pre0 = c0 + g * p.n_grp + rg;
-      prow = s * p.G - rg * kUnitRows + r;
+      prow = s * p.G - rg * unit + r;
+      rows = unit;
     }
   }
   // partial i of the row: the prefix's, then its own keys'
   const int n = n_pre + n_own;
-  const float2* pm = p.pre_ml + (size_t)pre0 * kUnitRows + prow;
-  const float4* po = p.pre_o + ((size_t)pre0 * 64 + dq) * kUnitRows + prow;
+  const float2* pm = p.pre_ml + (size_t)pre0 * rows + prow;
+  const float4* po = p.pre_o + ((size_t)pre0 * 64 + dq) * rows + prow;
   const float2* om = p.own_ml + (size_t)own0 * 8 + r;
   const float4* oo = p.own_o + ((size_t)own0 * 64 + dq) * 8 + r;
   wait_for_previous();
@@ -1214,8 +1263,8 @@ __global__ void __launch_bounds__(8 * 16 * kMergeMostWays) merge_kernel(const __
       ml[e] = make_float2(-INFINITY, 0.f);
       v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < n_pre) {
-        ml[e] = __ldcg(pm + (size_t)i * kUnitRows);
-        v[e] = __ldcg(po + (size_t)i * 64 * kUnitRows);
+        ml[e] = __ldcg(pm + (size_t)i * rows);
+        v[e] = __ldcg(po + (size_t)i * 64 * rows);
       } else if (i < n) {
         ml[e] = __ldcg(om + (size_t)(i - n_pre) * p.HKV * 8);
         v[e] = __ldcg(oo + (size_t)(i - n_pre) * p.HKV * 64 * 8);
@@ -1259,9 +1308,9 @@ cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, con
   const int own_grid = p.HKV * p.chunks_head;
   if ((e = cudaFuncSetAttribute(own_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwnSmem)) != cudaSuccess) return e;
   if (p.n_grp > 0 && p.tiles_head > 0) {
-    if ((e = cudaFuncSetAttribute(prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem)) != cudaSuccess)
-      return e;
-    prefix_kernel<<<2 * p.n_pairs, kPreThreads, kPreSmem, st>>>(p, t);
+    auto* kernel = p.n_cta == 2 ? prefix_pair_kernel : prefix_one_kernel;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem)) != cudaSuccess) return e;
+    kernel<<<p.n_cta * p.n_units, kPreThreads, kPreSmem, st>>>(p, t);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = launch_after(own_kernel, dim3((unsigned)own_grid), kOwnWarps * 32, kOwnSmem, st, p, t, maps)) != cudaSuccess)
       return e;
@@ -1269,7 +1318,8 @@ cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, con
     own_kernel<<<own_grid, kOwnWarps * 32, kOwnSmem, st>>>(p, t, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  return launch_after(merge_kernel, dim3((unsigned)(p.n_seq * p.HKV), kHeadDim / kMergeDims), 16 * p.G * p.merge_ways, 0, st,
+  return launch_after(merge_kernel, dim3((unsigned)(p.n_seq * p.HKV), kHeadDim / kMergeDims),
+                      kMergeDims / 4 * p.G * p.merge_ways, 0, st,
                       p, t);
 }
 

@@ -11,10 +11,10 @@
 namespace pa {
 
 constexpr int kShSeqs = 512;                        // sequences per launch, their table in its parameters
-constexpr int kShGroups = kShSeqs * 8 / kUnitRows;  // row groups of one kv head at most (8 q heads a kv head)
+constexpr int kShGroups = kShSeqs * 8 / (2 * kRows);  // row groups of one kv head at most (8 q heads a kv head)
 
-// Blocks of the prefix that some row of a group of 256 query rows sees: the
-// sink run [0, sink) and the run [lo, prefix blocks).
+// Blocks of the prefix that some row of a group of query rows (128 for each CTA
+// that works on it) sees: the sink run [0, sink) and the run [lo, prefix blocks).
 struct ShGroup {
   int x0;    // tiles of the head's earlier groups
   int sink;
@@ -22,7 +22,7 @@ struct ShGroup {
   int n_blk; // sink + prefix blocks - lo
 };
 
-constexpr int kShPairs = 128;  // SM pairs of a launch at most
+constexpr int kShUnits = 256;  // units (a CTA or a pair of them) of the prefix pass at most
 
 constexpr int kShOwnListed = 1024;
 constexpr int kShOwnPerSm = 3;  // CTAs of the per-sequence pass on an SM at a time
@@ -32,10 +32,10 @@ struct SharedSeqs {
   int4 s[kShSeqs];
   ShGroup grp[kShGroups];
   // The prefix pass's tiles (fewer than 2^30), head-major and group-major, laid
-  // end to end: pair c computes tiles [cut[c], cut[c + 1]); group j (head-major)
-  // lies in pairs first_pair[j] .. last_pair[j].
-  int cut[kShPairs + 1];
-  uint8_t first_pair[8 * kShGroups], last_pair[8 * kShGroups];
+  // end to end: unit c computes tiles [cut[c], cut[c + 1]); group j (head-major)
+  // lies in units first_unit[j] .. last_unit[j].
+  int cut[kShUnits + 1];
+  uint8_t first_unit[8 * kShGroups], last_unit[8 * kShGroups];
   uint16_t own_seq[kShOwnListed];  // sequence of the per-sequence pass's first CTAs (a search finds the others')
 };
 
@@ -53,17 +53,18 @@ struct SharedParams {
   int prefix_blk;          // blocks of the shared prefix; their pages are block_table row 0's
   int first_blk;           // the per-sequence pass starts at this block: prefix_blk, or 0 without a prefix pass
   int n_grp;               // row groups per kv head (0: no prefix pass)
-  int tiles_head;          // 128-key tiles of all groups of one kv head
-  int n_pairs;             // SM pairs of the prefix pass
+  int n_cta;               // CTAs of a unit of the prefix pass, 1 or 2: groups of 128 n_cta rows, tiles of 64 n_cta keys
+  int tiles_head;          // tiles of all groups of one kv head
+  int n_units;             // units of the prefix pass
   int chunk;               // blocks per CTA of the per-sequence pass
   int chunks_head;         // its CTAs per kv head
-  int merge_ways;          // threads that share a row's partials in the merge, 1 to 8
+  int merge_ways;          // threads that share a row's partials in the merge, 1 to 16
   float sm_scale_log2;
   // Partials: per row the reference (log2 units) and sum of its softmax, and
   // its unnormalised output, 4 dims x rows side by side.  Prefix: the partial
-  // of pair c for group j (head-major) is number c + j; own keys: the CTA's number.
-  float4* pre_o;           // [c + j][64][256]
-  float2* pre_ml;          // [c + j][256]
+  // of unit c for group j (head-major) is number c + j; own keys: the CTA's number.
+  float4* pre_o;           // [c + j][64][128 n_cta]
+  float2* pre_ml;          // [c + j][128 n_cta]
   float4* own_o;           // [cta][64][8]
   float2* own_ml;          // [cta][8]
   int* err;
