@@ -58,8 +58,8 @@ class Batch:
             j = j[(j // 16 < self.S) | (j // 16 >= max(0, t // 16 + 1 - self.W))]
         return j
 
-    def reference(self, skip_pages=()):
-        """Per sequence (out, bound) float64 [hq, 256].  The bound, per output:
+    def reference(self, skip_pages=(), only=None):
+        """Per sequence (of `only`, if given) (out, bound) float64 [hq, 256].  The bound, per output:
           2^-8 |out|             bf16 rounding of the result
           2^-11 sum p |v|        P' rounded to fp16 (half a step), and where P' is subnormal (below 2^-14 of its
                                  largest) half its fixed step, 2^-25, times the largest V magnitude
@@ -67,7 +67,7 @@ class Batch:
                                  products and the exponent's (2^-21 of |score|), 2^-21 for 2^x itself: they move
                                  p_j by a factor 1 + e_j, the output by sum p e |v| + |out| sum p e"""
         pb, G, out = self.prefix // 16, self.hq // self.hkv, []
-        for i in range(len(self.suffix)):
+        for i in range(len(self.suffix)) if only is None else only:
             j = self.visible(i)
             row = np.where(j // 16 < pb, 0, i)
             page = self.block_table[row, j // 16]

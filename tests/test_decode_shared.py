@@ -45,10 +45,10 @@ def call(h, b, d, out=None, seqs=None, stream=None, **over):
     return out
 
 
-def check(b, out, skip_pages=()):
+def check(b, out, skip_pages=(), only=None):
     got = out.float().cpu().numpy().astype(np.float64)
-    ref, bound = b.reference(skip_pages)
-    err = np.abs(got[b.rows] - ref)
+    ref, bound = b.reference(skip_pages, only)
+    err = np.abs(got[b.rows if only is None else b.rows[list(only)]] - ref)
     assert np.all(err <= bound), float((err / bound).max())
     others = np.setdiff1d(np.arange(got.shape[0]), b.rows)
     assert np.isnan(got[others]).all(), "a row of no sequence was written"
@@ -237,6 +237,33 @@ def test_calls_back_to_back_of_changing_sizes():
             assert pa.pa_last_error(h) == 0
             import torch
             assert torch.equal(o.view(torch.int16), alone.view(torch.int16))
+
+
+@pytest.mark.parametrize("hq, n, prefix, short", ((8, 3, 6160, (1, 1)), (8, 3, 8176, (1, 2)), (8, 3, 13504, (1, 7)),
+                                                  (8, 101, 6288, (1, 2)), (64, 17, 6160, (1, 1)), (64, 17, 12000, (2, 5))))
+def test_units_that_begin_with_a_short_segment(hq, n, prefix, short):
+    """Units whose first group ends after a tile or two: the next one's queries, K and V come in while the first
+    one's are on their way (with 101 sequences of one row a head, 101 copies a group)."""
+    import torch
+
+    import windowed_prefill_attention_gb300 as pa
+    b = Batch(hq, 8, prefix, (1,) * n if n > 100 else tuple(1 + i for i in range(n)), 1, 0, 50).make()
+    runs, _ = pa.pa_decode_shared_plan(hq, 8, b.max_pages, 152, b.seqs, b.prefix, b.S, b.W, 1)
+    tile = 4 if n * hq // 8 <= 128 else 8
+    segs = {}
+    for r in runs.tolist():
+        segs.setdefault(r[0], []).append((r[7] - r[6] + tile - 1) // tile)
+    assert list(short) in segs.values()
+    first = None
+    for _ in range(20):
+        d = to_device(b)
+        with Handle(b) as h:
+            out = call(h, b, d)
+            assert pa.pa_last_error(h) == 0
+        if first is None:
+            first = out
+            check(b, out, only=range(0, n, max(1, n // 5)))
+        assert torch.equal(out.view(torch.int16), first.view(torch.int16))
 
 
 @pytest.mark.parametrize("case", ("long_prefix", "long_prefix_pair"))

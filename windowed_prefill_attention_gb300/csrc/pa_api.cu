@@ -1639,19 +1639,20 @@ int decode_shared_check(int HQ, int HKV, int max_pages, int n_seq, const pa_seq*
 // runs (about 12000 cycles against 3000 to 4000 a pair's tile on GB300).  The
 // per-sequence pass: chunks of equal block counts, four to 128 blocks each.
 constexpr int kShSegCost = 4, kShOwnWaves = 2;
-// Microseconds on GB300, fitted to 15 batches at 11 numbers of pairs each: a
-// pair's set-up, queries and epilogue, its first ten tiles, the others; the SM
-// time of an own block, of a prefix block that a sequence reads again (from L2)
-// and of an own CTA, what the per-sequence pass takes to get going, what it adds
-// when it ends after the prefix pass, and how full it keeps its SMs when not even
-// a CTA for every sequence fits them at once.
+// Microseconds on GB300, fitted to 27 batches at 5 to 14 numbers of units each: a
+// unit's set-up, queries and epilogue, its first ten tiles, the others, and what
+// the per-sequence pass adds when it ends after the prefix pass; a tile's factor
+// where windows mask keys; the SM time of an own block, of a prefix block that a
+// sequence reads again (from L2) and of an own CTA, what the per-sequence pass
+// takes to get going, and how full it keeps its SMs when not even a CTA for every
+// sequence fits them at once.
 struct ShCost {
-  double unit, tile, late;
-  int early;
+  double unit, tile, late, tail;
 };
-constexpr ShCost kShCost[2] = {{9.5, 1.5, 1.45, 10}, {11.0, 2.1, 1.65, 10}};
+constexpr ShCost kShCost[2] = {{11.5, 1.4, 1.45, 2.0}, {11.0, 2.1, 1.65, 4.0}};  // units of one CTA, of two
+constexpr double kShMaskedTile = 1.25;
 constexpr double kShOwnBlockUs = 0.215, kShAgainBlockUs = 0.165, kShOwnCtaUs = 0.25;
-constexpr double kShOwnStartUs = 4.5, kShOwnTailUs = 4.0, kShOwnFull = 0.85;
+constexpr double kShOwnStartUs = 4.5, kShOwnFull = 0.85;
 // Packs the groups (nt[j] tiles each, laid end to end) into runs of at most
 // `budget` cost; false if they take more than max_units.
 bool shared_pack(const int* nt, int n_groups, int budget, int max_units, int* cut, int& n_units) {
@@ -1747,14 +1748,15 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
       const int use = std::min(max_units - left, T), free_sm = n_sm - p.n_cta * use;
       // a unit's cost when all are equal: its tiles, and its share of the groups' changes
       const int budget = (T + kShSegCost * std::max(0, J - use) + use - 1) / use + (J > 1 && J < use && use % J ? 1 : 0);
-      const double prefix_us = cost.unit + cost.tile * std::min(budget, cost.early) + cost.late * std::max(0, budget - cost.early);
+      const double prefix_us =
+          cost.unit + (cost.tile * std::min(budget, 10) + cost.late * std::max(0, budget - 10)) * (W > 0 ? kShMaskedTile : 1.0);
       const double slots = kShOwnPerSm * free_sm, ctas = std::max(least_ctas, std::min(own_blk / 4, kShOwnWaves * slots));
       const double own_us = (kShOwnBlockUs * own_blk + kShOwnCtaUs * ctas) / (least_ctas > slots ? kShOwnFull : 1.0);
       // SM time before the prefix pass ends: that of the SMs left out; if none is, of the units with a tile less
       const double idle = free_sm > 1 ? free_sm * std::max(0.0, prefix_us - kShOwnStartUs)
                                       : p.n_cta * cost.late * std::max(0, budget * use - T);
       const double rest = std::max(0.0, own_us - idle);
-      const double end = prefix_us + (rest > 0.0 ? rest / n_sm + kShOwnTailUs : 0.0);
+      const double end = prefix_us + (rest > 0.0 ? rest / n_sm + cost.tail : 0.0);
       if (end < best) {
         best = end;
         units = use;

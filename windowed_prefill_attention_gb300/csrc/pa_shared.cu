@@ -387,6 +387,10 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
       for (int n = 0; n < 8; ++n) widen16(r[n], at0 + st * kStageBytes + step * n * 128, row0 + step * n, u);
       fence_proxy_async_shared();
       __syncwarp();
+      // K warps take no part in the first segment's staging; they see that its
+      // rows have landed all the same, before their first tile leads to the next
+      // segment's: a parity wait there would take this phase's for it.
+      if (n_tile == 0 && !kv && !c.wait(B_RAWF, 0)) return;
       if (lane == 0) mbar_arrive(c.bar((kv ? (c.rank == 0 ? B_VF : B_VL) : (c.rank == 0 ? B_KF : B_KL)) + st));
       if (t + 1 < nt) load((t + 1) & (kWin - 1));
     }
