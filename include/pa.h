@@ -331,7 +331,7 @@ int pa_decode_plan(int n_kv_heads, int slots, int n_seq, const pa_seq* seqs, int
  *   others        as pa_decode; sequences must not share a row of q / out (PA_EINVAL)
  * A prefix page outside the pool is skipped for all sequences, one of a
  * sequence's own pages for that sequence (PA_EBADPAGE through pa_last_error).
- * Two or three kernel launches per 512 sequences, asynchronous on `stream`.  Calls on
+ * One to three kernel launches per 512 sequences, asynchronous on `stream`.  Calls on
  * one handle share its work buffers: issue them, and replay graphs captured
  * from them, one after another.  The buffers grow by allocation; a call on a
  * capturing stream that would have to grow them returns PA_ENOMEM (make a call

@@ -79,6 +79,7 @@ CASES = {
     "no_prefix": Batch(8, 2, 0, (77, 1, 2500, 16), 1, 0, 18),
     "long_own": Batch(8, 2, 256, (9000, 1, 3000), 1, 0, 19),
     "over_512": Batch(2, 1, 320, tuple(1 + (13 * i) % 40 for i in range(1030)), 1, 0, 20),
+    "one_chunk_a_row": Batch(8, 2, 16, tuple(1 + i % 40 for i in range(200)), 1, 0, 27),
     "cold_softmax": Batch(8, 1, 1024, (9, 90, 3), 1, 0, 21, outliers=0.0, sm_scale=0.0),
     "steep_softmax": Batch(8, 1, 1024, (9, 90, 3), 1, 0, 22, outliers=0.05, sm_scale=2.0),
     "steep_softmax_pair": Batch(8, 1, 2560, tuple(1 + i for i in range(40)), 1, 0, 26, outliers=0.05, sm_scale=2.0),

@@ -947,6 +947,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
+// Dims 4 dq .. + 3 of a row's output: its unnormalised sum over the softmax's.
+__device__ __forceinline__ void store_row(const SharedParams& p, int row, int g, int r, int dq, const float4 acc, float l) {
+  const float il = l > 0.f ? 1.f / l : 0.f;
+  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * il, acc.y * il), b = __floats2bfloat162_rn(acc.z * il, acc.w * il);
+  *reinterpret_cast<uint2*>(p.out + ((size_t)row * p.HQ + (size_t)g * p.G + r) * kHeadDim + 4 * dq) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
 __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const __grid_constant__ SharedParams p,
                                                              const __grid_constant__ SharedSeqs tab,
                                                              const __grid_constant__ DecodeMaps maps) {
@@ -1185,6 +1193,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const 
     f[w] = wm[w][r] == -INFINITY ? 0.f : ex2f(wm[w][r] - mx);
     ls += f[w] * wl[w][r];
   }
+  float4 part_o[4];
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
     const int dq = (threadIdx.x >> 3) + 16 * n;
@@ -1197,8 +1206,17 @@ __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const 
       acc.z = fmaf(f[w], v.z, acc.z);
       acc.w = fmaf(f[w], v.w, acc.w);
     }
-    p.own_o[((size_t)blockIdx.x * 64 + dq) * 8 + r] = acc;
+    part_o[n] = acc;
   }
+  if (p.merge_ways == 0) {  // no prefix pass, and a row's keys are one chunk: its output
+    if (r < p.G) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) store_row(p, sq.x, g, r, (threadIdx.x >> 3) + 16 * n, part_o[n], ls);
+    }
+    return;
+  }
+#pragma unroll
+  for (int n = 0; n < 4; ++n) p.own_o[((size_t)blockIdx.x * 64 + (threadIdx.x >> 3) + 16 * n) * 8 + r] = part_o[n];
   if (threadIdx.x < 8) p.own_ml[(size_t)blockIdx.x * 8 + r] = make_float2(mx, ls);
   // This grid's end has to mean that the prefix pass has ended too.  One CTA
   // waits for it, the last: the others leave their places to those still to come.
@@ -1284,10 +1302,7 @@ __global__ void __launch_bounds__(8 * kMergeDims / 4 * kMergeMostWays) merge_ker
   __syncthreads();
   if (way > 0) return;
   for (int w = 0; w < p.merge_ways - 1; ++w) add(ml_sh[w][slot], acc_sh[w][slot]);
-  const float il = l > 0.f ? 1.f / l : 0.f;
-  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * il, acc.y * il), b = __floats2bfloat162_rn(acc.z * il, acc.w * il);
-  *reinterpret_cast<uint2*>(p.out + ((size_t)sq.x * p.HQ + (size_t)g * p.G + r) * kHeadDim + 4 * dq) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  store_row(p, sq.x, g, r, dq, acc, l);
 }
 
 template <typename... Params>
@@ -1322,6 +1337,7 @@ cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, con
     own_kernel<<<own_grid, kOwnWarps * 32, kOwnSmem, st>>>(p, t, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
+  if (p.merge_ways == 0) return cudaSuccess;
   return launch_after(merge_kernel, dim3((unsigned)(p.n_seq * p.HKV), kHeadDim / kMergeDims),
                       kMergeDims / 4 * p.G * p.merge_ways, 0, st,
                       p, t);

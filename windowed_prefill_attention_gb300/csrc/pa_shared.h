@@ -58,7 +58,7 @@ struct SharedParams {
   int n_units;             // units of the prefix pass
   int chunk;               // blocks per CTA of the per-sequence pass
   int chunks_head;         // its CTAs per kv head
-  int merge_ways;          // threads that share a row's partials in the merge, 1 to 16
+  int merge_ways;          // threads that share a row's partials in the merge, 1 to 16; 0: no merge, every row is one CTA's
   float sm_scale_log2;
   // Partials: per row the reference (log2 units) and sum of its softmax, and
   // its unnormalised output, 4 dims x rows side by side.  Prefix: the partial
