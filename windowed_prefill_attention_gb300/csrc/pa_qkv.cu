@@ -368,14 +368,24 @@ cudaError_t launch(const QkvParams& p, const QkvSeqs<kCap>& tab, int n_sm, cudaS
 
 }  // namespace
 
+// How many of a token's rows a warp takes at a time: the number whose last wave
+// of items ends first.  An item costs its set-up (the token's page, its gains,
+// sines and cosines) and its rows, four, two or one at a time; in units of a
+// twentieth of the set-up, from batches of 300 to 32768 tokens (us, all sizes
+// from one row to all tried).  300 tokens of 12 rows: 3.7 with four rows (5.2
+// with all, 4.0 with one); 2000: 6.4 with all (7.1 with four); 9776 of 24: 42.8
+// with all (64.2 with four, 51.4 with 16).
 int qkv_rows_per_part(long long n_tok, int rows, int n_sm) {
-  const long long warps = (long long)n_sm * kQkvPerSm * kQkvWarps, total = n_tok * rows;
-  // few rows: as many warps as there are rows, up to a full GPU; more: whole
-  // batches of four rows, about eight items a warp to even out the end (with
-  // four, 9776 tokens of 24 rows took 65 us instead of 57)
-  long long per = (total + warps - 1) / warps;
-  if (per > 4) per = (total + 32 * warps - 1) / (32 * warps) * 4;
-  return (int)(per < rows ? per : rows);
+  const long long warps = (long long)n_sm * kQkvPerSm * kQkvWarps;
+  double best = 0.0;
+  int per = 0;
+  for (int r = 1;; r = r < 4 ? 2 * r : r + 4) {
+    r = r < rows ? r : rows;
+    const long long items = n_tok * ((rows + r - 1) / r), waves = (items + warps - 1) / warps;
+    const double cost = (double)waves * (20 + 6 * (r / 4) + (r % 4 >= 2 ? 5 : 0) + (r % 2 ? 4 : 0)) + 6.0 * items / warps;
+    if (per == 0 || cost < best) best = cost, per = r;
+    if (r == rows) return per;
+  }
 }
 
 cudaError_t launch_qk_norm_rope(const QkvParams& p, int n_sm, cudaStream_t st) {
