@@ -328,6 +328,7 @@ int pa_decode_plan(int n_kv_heads, int slots, int n_seq, const pa_seq* seqs, int
  *   block_table   row s holds sequence s's pages; the prefix's pages are those
  *                 of row 0, and the other rows' entries for it are not read
  *   n_rows        rows of q and out; a sequence's row outside them is PA_EINVAL
+ *   out           q itself (in place), or apart from it (else PA_EINVAL)
  *   others        as pa_decode; sequences must not share a row of q / out (PA_EINVAL)
  * A prefix page outside the pool is skipped for all sequences, one of a
  * sequence's own pages for that sequence (PA_EBADPAGE through pa_last_error).

@@ -80,6 +80,7 @@ CASES = {
     "long_own": Batch(8, 2, 256, (9000, 1, 3000), 1, 0, 19),
     "over_512": Batch(2, 1, 320, tuple(1 + (13 * i) % 40 for i in range(1030)), 1, 0, 20),
     "one_chunk_a_row": Batch(8, 2, 16, tuple(1 + i % 40 for i in range(200)), 1, 0, 27),
+    "many_ctas": Batch(8, 8, 16, tuple(1 + i % 50 for i in range(200)), 1, 0, 28),
     "cold_softmax": Batch(8, 1, 1024, (9, 90, 3), 1, 0, 21, outliers=0.0, sm_scale=0.0),
     "steep_softmax": Batch(8, 1, 1024, (9, 90, 3), 1, 0, 22, outliers=0.05, sm_scale=2.0),
     "steep_softmax_pair": Batch(8, 1, 2560, tuple(1 + i for i in range(40)), 1, 0, 26, outliers=0.05, sm_scale=2.0),
@@ -222,6 +223,51 @@ def test_on_a_side_stream_and_shapes_are_checked():
                     dict(bt=d["bt"][:5]), dict(vs=d["vs"][..., :1].contiguous()), dict(q=d["q"][:3])):
             with pytest.raises(ValueError):
                 call(h, b, d, out=out, **bad)
+
+
+@pytest.mark.parametrize("prefix_pass", (1, 0))
+def test_in_place_and_overlapping_outputs(prefix_pass):
+    import torch
+
+    import windowed_prefill_attention_gb300 as pa
+    b = CASES["two_ctas"].make()
+    d = to_device(b)
+    rows = torch.from_numpy(b.rows).cuda()
+    with Handle(b, prefix_pass) as h:
+        want = call(h, b, d)[rows]
+        q = d["q"].clone()
+        call(h, b, d, q=q, out=q)
+        assert torch.equal(q[rows].view(torch.int16), want.view(torch.int16))
+        both = torch.empty(2 * d["q"].shape[0] - 1, *d["q"].shape[1:], dtype=torch.bfloat16, device="cuda")
+        n = d["q"].shape[0]
+        with pytest.raises(pa.PAError) as e:
+            call(h, b, d, q=both[:n], out=both[n - 1:])
+        assert e.value.code == pa.PA_EINVAL and pa.pa_last_error(h) == 0
+
+
+def test_two_handles_on_two_streams_at_once():
+    """Batches of all forms, each handle's calls on its own stream, beside one another."""
+    import torch
+
+    import windowed_prefill_attention_gb300 as pa
+    work = []
+    for case, prefix_pass in (("long_prefix", 1), ("many_rows", 1), ("gqa4_windowed", 0), ("long_own", 1)):
+        b = CASES[case].make()
+        d = to_device(b)
+        h = pa.pa_create(b.hq, b.hkv, b.n_pool, b.max_pages)
+        pa.pa_debug_decode_shared_pass(h, prefix_pass)
+        work.append((h, b, d, call(h, b, d), torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+    for _ in range(40):
+        for h, b, d, _, stream, outs in work:
+            outs.append(torch.empty_like(d["q"]))
+            call(h, b, d, out=outs[-1], stream=stream)
+    torch.cuda.synchronize()
+    for h, b, _, want, _, outs in work:
+        assert pa.pa_last_error(h) == 0
+        pa.pa_destroy(h)
+        rows = torch.from_numpy(b.rows).cuda()
+        assert all(torch.equal(o[rows].view(torch.int16), want[rows].view(torch.int16)) for o in outs)
 
 
 def test_calls_back_to_back_of_changing_sizes():

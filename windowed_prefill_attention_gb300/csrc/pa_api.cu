@@ -1834,6 +1834,8 @@ int pa_decode_shared(pa_handle h, int n_seq, const pa_seq* seqs, int n_prefix, i
   if ((rc = decode_shared_check(h->HQ, h->HKV, h->max_pages, n_seq, seqs, n_prefix, n_sink_blk, sm_scale))) return rc;
   for (int s = 0; s < n_seq; ++s)
     if (seqs[s].q_off >= n_rows) return PA_EINVAL;
+  const size_t row_bytes = (size_t)h->HQ * kHeadDim * sizeof(__nv_bfloat16);
+  if (out != q && span_of(out, n_rows * row_bytes).meets(span_of(q, n_rows * row_bytes))) return PA_EINVAL;
   OnDevice dev(h->device);
   if (!dev.ok) return PA_ECUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

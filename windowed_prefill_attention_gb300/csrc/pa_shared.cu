@@ -4,20 +4,21 @@
 // Softmax over the visible keys splits over any partition of them: with
 // (m, l, O) the reference, sum and unnormalised output of a part,
 //   m = max m_i,  l = sum 2^(m_i - m) l_i,  O = sum 2^(m_i - m) O_i.
-// Three kernels:
-//   prefix_kernel  the prefix's keys against the queries of ALL sequences: per
-//                  kv head a matrix of n_seq x G rows, so its K and V codes are
-//                  read once and the products run on the tensor cores
-//                  (tcgen05) instead of once per sequence
-//   own_kernel     each sequence's own keys, as pa_decode splits them
-//   merge_kernel   the partials of both, and the division
+// Up to three launches:
+//   prefix_*_kernel  the prefix's keys against the queries of ALL sequences: per
+//                    kv head a matrix of n_seq x G rows, so its K and V codes
+//                    are read once and the products run on the tensor cores
+//                    (tcgen05) instead of once per sequence
+//   own_kernel       each sequence's own keys (with few sequences or a short
+//                    prefix, all its keys), split into chunks
+//   merge_kernel     the partials of both, and the division
 //
-// prefix_kernel.  Groups of 256 query rows x tiles of 128 keys.  The int8
-// codes are widened to fp16 (exact) on their way into shared memory, K and V
-// alike as [key][64 dims] rows of 128 bytes: a K-major B operand for S = Q K^T
-// and an MN-major one for O = P V, so V needs no transpose.  Scores, softmax
-// and P' are those of the decode kernel: the bf16 query enters as fp16
-// through a power of two per row, P' = p * v_scale * 2^-e in fp16, fp32 sums.
+// The prefix pass.  The int8 codes are widened to fp16 (exact) on their way into
+// shared memory, K and V alike as [key][64 dims] rows of 128 bytes: a K-major B
+// operand for S = Q K^T and an MN-major one for O = P V, so V needs no transpose.
+// Scores, softmax and P' are those of the decode kernel: the bf16 query enters as
+// fp16 through a power of two per row, P' = p * v_scale * 2^-e in fp16 (11 bits
+// against the 8 of the output), fp32 sums.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -114,13 +115,28 @@ __device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
 // ====================================================================
 // The prefix
 // ====================================================================
-// A pair of SMs (cluster of two CTAs) computes groups of 256 query rows, 128 in
-// each CTA's TMEM, against tiles of 128 keys; one thread of the even CTA issues
-// every product of both (cta_group::2).  The B operands are split: each CTA
-// holds K of 64 of a tile's keys and V of 128 of the 256 dims, so it reads and
-// widens half of every tile's codes, which (with one CTA per tile: 64 KB of
-// codes read, 128 KB of operands written and 192 KB of operands read per tile
-// and SM) would otherwise bound the kernel.
+// kN = 2, more than 128 query rows a kv head: a pair of SMs (cluster of two CTAs)
+// computes groups of 256 rows, 128 in each CTA's TMEM, against tiles of 128 keys;
+// one thread of the even CTA issues every product of both (cta_group::2).  The B
+// operands are split: each CTA holds K of 64 of a tile's keys and V of 128 of the
+// 256 dims, so it reads and widens half of every tile's codes, which (with one CTA
+// per tile: 64 KB of codes read, 128 KB of operands written and 192 KB of operands
+// read per tile and SM) would otherwise bound the kernel.
+// kN = 1, up to 128 rows: a pair's second CTA would have none.  Each CTA takes
+// tiles of 64 keys by itself, with the same stages.  (9 sequences of 8 rows on
+// 131072 keys: 35 us, on pairs 40.)
+//
+// What bounds it.  64 sequences, 16 q and 2 kv heads, 32768 keys: 51 us, 18 tiles
+// a pair of ~3500 cycles each, between 11000 of set-up and 5500 of storing partials.
+// The tensor pipe runs 2048 of a tile's cycles.  The rest is the chain from scores
+// to products: softmax (~2000), an arrival from the other CTA (300 to 1100), the
+// issue of the products (70 to 90 cycles each), and in most tiles some warp that
+// moves a reference and rescales O (~1500; without outlier keys, 50.5 us instead
+// of 53.4 at the time).  A CTA alone: ~2750 cycles a 64-key tile, issue and rescale.
+// Tried and not better: two sets of softmax warps in turn, 16 of them on half of
+// the keys each, warps of their own for the rescale (all: more warps, each
+// slower), and a thread each for Q K^T and P V (what runs in order on one thread
+// then waits for the other's commit).
 constexpr int kSoftWarps = 8;                       // warps 0-7: softmax; TMEM quadrant w % 4, 16 rows w / 4 of it
 constexpr int kConvWarps = 8;                       // warps 8-15: codes -> fp16 operands (K: four, V: four), the queries
 constexpr int kIssueWarp = kSoftWarps + kConvWarps; // warp 16: TMEM; even CTA: the products, odd CTA: forwards K
@@ -924,6 +940,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 // scores are done: one to two blocks a warp are always on their way.  Which dims
 // a thread's operands hold is free as long as Q and O agree: chosen so that its
 // 16-byte reads of the 128-byte swizzled rows have no bank conflicts.
+// Bound by memory where there is enough of it: 100 sequences of 1500 keys, 8 kv
+// heads (626 MB) in 115 us, 5.4 TB/s; short passes by the latency of a CTA's start
+// (~4.5 us) and of a block in a warp (~2 us: load, products, softmax, products).
+// Straight from global memory into registers, half a block ahead, spilled at 168
+// registers and took 41 us for 48 windowed sequences, with TMA 38.8.
 constexpr int kOwnWarps = 4;
 constexpr int kOwnStage = 8192;                              // K and V of a block, each two halves of [16][128]
 constexpr int kOwnRing = 2 * kOwnStage;                      // a warp's; at the end its partial output [8][kOwnPitch]
@@ -1226,11 +1247,13 @@ __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const 
 // ====================================================================
 // Merge
 // ====================================================================
-// CTA = (sequence, kv head, 64 of the dims); thread (row i % G, dims 4 (i / G %
-// 16), every merge_ways-th partial from i / (16 G) on), then the ways' parts
+// CTA = (sequence, kv head, 32 of the dims); thread (row i % G, dims 4 (i / G %
+// 8), every merge_ways-th partial from i / (8 G) on), then the ways' parts
 // through shared memory in a fixed order.  Bound by the latency of the partials'
 // loads: the ways (as many as give a thread about four partials) and four loads
-// a thread keep them in flight together.
+// a thread keep them in flight together.  (64 dims and 8 ways at most: 53 us
+// instead of 51 for 64 sequences on 32768 keys, 37.5 instead of 35.3 for 9 on
+// 131072, whose rows have 150 partials.)
 constexpr int kMergeMostWays = 16;
 constexpr int kMergeDims = 32;
 
