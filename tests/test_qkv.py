@@ -122,6 +122,28 @@ def test_norm_rope_one_kind_in_place_and_another_stream():
         assert torch.equal(qo, q3) and torch.equal(ko, k3)
 
 
+def test_norm_rope_in_place_over_many_items():
+    """More tokens than warps, so that a warp's next rows are on their way while it writes others: in place gives
+    the bits of the call into other rows, and each token's those of a call of its own."""
+    import torch
+
+    import windowed_prefill_attention_gb300 as pa
+    g = torch.Generator("cuda").manual_seed(5)
+    n, hq, hkv = 9001, 10, 5
+    q, k = (torch.randn(n, h, 256, device="cuda", generator=g).bfloat16() for h in (hq, hkv))
+    rope = pa.pa_rope_init(ut.frequencies(96), pa.PA_ROPE_ADJACENT)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    qo, ko = empty_rows(n, hq), empty_rows(n, hkv)
+    with Handle(hq, hkv) as h:
+        pa.pa_qk_norm_rope(h, q, k, None, None, 1e-6, rope, pos, qo, ko)
+        for i in (0, 4000, n - 1):
+            q1, k1 = empty_rows(1, hq), empty_rows(1, hkv)
+            pa.pa_qk_norm_rope(h, q[i:i + 1], k[i:i + 1], None, None, 1e-6, rope, pos[i:i + 1], q1, k1)
+            assert torch.equal(q1[0], qo[i]) and torch.equal(k1[0], ko[i])
+        pa.pa_qk_norm_rope(h, q, k, None, None, 1e-6, rope, pos, q, k)
+        assert torch.equal(q, qo) and torch.equal(k, ko)
+
+
 def test_norm_rope_broadcast_rows_zero_rows_and_no_tokens():
     """Rows at stride 0 (one row for all tokens and heads), rows of zeros with eps 0, an empty call."""
     import torch

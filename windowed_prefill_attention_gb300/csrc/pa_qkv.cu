@@ -28,8 +28,12 @@
 namespace pa {
 namespace {
 
-constexpr int kQkvWarps = 8;
-constexpr int kQkvPerSm = 3;  // CTAs: 24 warps with four rows (2 KB) each in flight cover the loads' latency
+// 20 warps an SM at 96 registers, each with the next four rows (2 KB) on their way
+// beside the four in work.  32768 tokens of 18 rows: 104 us, 5.8 TB/s read and
+// written; 16 warps 106, 24 (which spill) 114; without the copies ahead 110; three
+// batches ahead 109.
+constexpr int kQkvWarps = 10;
+constexpr int kQkvPerSm = 2;  // CTAs
 constexpr int kMaxPairs = kHeadDim / 2;
 constexpr unsigned kAll = 0xffffffffu;
 enum : int { TURN_NONE, TURN_HALVES, TURN_ADJACENT };
@@ -196,14 +200,53 @@ __device__ __forceinline__ void store_codes(Vals (&x)[N], int lane, int8_t* code
   }
 }
 
-// N rows: loaded together, normed and turned (kNorm), stored as bf16 (kCodes
+// A warp's rows on their way in: batches of up to four rows of one kind, copied
+// asynchronously into two slots of its own, a batch ahead of the one in work, from
+// item to item.  A lane reads only bytes that it copied itself.
+struct Feed {
+  uint32_t at;    // the lane's 16 bytes of slot 0's first row
+  int n_fetched;  // batches so far
+  int row, r, r1;  // the token's row; its rows r .. r1 are still to come
+  int next_row, next_r0, next_r1;  // then those of the next item; row -1: none
+
+  __device__ __forceinline__ void fetch(const QkvParams& p, int lane) {
+    if (r >= r1) {
+      r = next_r0, r1 = next_r1, row = next_row;
+      next_row = -1;
+      if (row < 0) r = r1 = 0;
+    }
+    if (r < r1) {
+      const int nk = p.n_q + p.n_k;
+      const RowsIn& in = r < p.n_q ? p.q : (r < nk ? p.k : p.v);
+      const int first = r < p.n_q ? 0 : (r < nk ? p.n_q : nk), end = r < p.n_q ? p.n_q : (r < nk ? nk : r1);
+      const int n = min(min(end, r1) - r, 4);
+      const __nv_bfloat16* src = in.p + (size_t)row * in.ts + (size_t)(r - first) * in.hs + 8 * lane;
+      const uint32_t dst = at + (n_fetched & 1) * (4 * 512);
+      for (int i = 0; i < n; ++i, src += in.hs)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512 * i), "l"(src) : "memory");
+      r += n;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ++n_fetched;
+  }
+  // The slot of the batch before the last one fetched, which has landed.
+  __device__ __forceinline__ uint32_t slot() const {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    return at + (n_fetched & 1) * (4 * 512);
+  }
+};
+
+// N rows from their slot, normed and turned (kNorm), stored as bf16 (kCodes
 // false; dst: the lane's 16 bytes of the first row) or as codes.
 template <int N, int kTurn, bool kNorm, bool kCodes>
-__device__ __forceinline__ void do_rows(const uint4* src, size_t step, const Turn& t, int from, float eps, int lane,
+__device__ __forceinline__ void do_rows(uint32_t src, const Turn& t, int from, float eps, int lane,
                                         uint4* dst, int8_t* codes, float* scales, bool store) {
   uint4 raw[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) raw[i] = src[i * step];
+  for (int i = 0; i < N; ++i)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(raw[i].x), "=r"(raw[i].y), "=r"(raw[i].z), "=r"(raw[i].w)
+                 : "r"(src + 512 * i));
   Vals y[N];
   if (kNorm) {
     float ss[N];
@@ -241,41 +284,41 @@ __device__ __forceinline__ void do_rows(const uint4* src, size_t step, const Tur
   }
 }
 
-// Heads [a, b) of one kind of row of a token.
+// `n` heads from head `a` of one kind of row of a token, the next batches of the feed.
 template <int kTurn, bool kNorm, bool kCodes>
-__device__ __forceinline__ void do_heads(const RowsIn& in, size_t row, int a, int b, const Turn& t, int from, float eps,
+__device__ __forceinline__ void do_heads(const QkvParams& p, Feed& feed, int a, int n, const Turn& t, int from, float eps,
                                          int lane, __nv_bfloat16* out, int8_t* codes, float* scales, bool store) {
-  const size_t step = (size_t)in.hs / 8;
-  const uint4* src = reinterpret_cast<const uint4*>(in.p + row * in.ts + (size_t)a * in.hs) + lane;
   uint4* dst = reinterpret_cast<uint4*>(out + (size_t)a * kHeadDim) + lane;
   if (kCodes) codes += a * kHeadDim, scales += a;
-  int h = a;
 #pragma unroll 1
-  for (; h + 4 <= b; h += 4) {
-    do_rows<4, kTurn, kNorm, kCodes>(src, step, t, from, eps, lane, dst, codes, scales, store);
-    src += 4 * step;
-    dst += 4 * (kHeadDim / 8);
-    if (kCodes) codes += 4 * kHeadDim, scales += 4;
+  for (; n > 0; n -= 4) {
+    feed.fetch(p, lane);
+    uint32_t src = feed.slot();
+    if (n >= 4) {
+      do_rows<4, kTurn, kNorm, kCodes>(src, t, from, eps, lane, dst, codes, scales, store);
+      dst += 4 * (kHeadDim / 8);
+      if (kCodes) codes += 4 * kHeadDim, scales += 4;
+    } else {
+      if (n >= 2) {
+        do_rows<2, kTurn, kNorm, kCodes>(src, t, from, eps, lane, dst, codes, scales, store);
+        src += 2 * 512;
+        dst += 2 * (kHeadDim / 8);
+        if (kCodes) codes += 2 * kHeadDim, scales += 2;
+      }
+      if (n & 1) do_rows<1, kTurn, kNorm, kCodes>(src, t, from, eps, lane, dst, codes, scales, store);
+    }
   }
-  if (h + 2 <= b) {
-    do_rows<2, kTurn, kNorm, kCodes>(src, step, t, from, eps, lane, dst, codes, scales, store);
-    h += 2;
-    src += 2 * step;
-    dst += 2 * (kHeadDim / 8);
-    if (kCodes) codes += 2 * kHeadDim, scales += 2;
-  }
-  if (h < b) do_rows<1, kTurn, kNorm, kCodes>(src, step, t, from, eps, lane, dst, codes, scales, store);
 }
 
 // A warp takes items (token, part of its rows: queries, keys, values in turn)
-// with a grid stride, rows four at a time, all their loads before the first is
-// used.
+// with a grid stride, rows four at a time.
 template <bool kAppend, int kCap, int kTurn>
 __global__ void __launch_bounds__(kQkvWarps * 32, kQkvPerSm) qkv_kernel(const __grid_constant__ QkvParams p,
                                                                         const __grid_constant__ QkvSeqs<kCap> tab) {
   __shared__ uint64_t turn[kMaxPairs];
   __shared__ int axis[kMaxPairs];
   __shared__ float2 cs_all[kQkvWarps][kMaxPairs];
+  __shared__ __align__(16) uint4 ring[kQkvWarps][2 * 4 * kHeadDim / 8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pairs = kTurn == TURN_NONE ? 0 : p.rope.rot_dim / 2;
   if (kTurn != TURN_NONE) {
@@ -289,16 +332,20 @@ __global__ void __launch_bounds__(kQkvWarps * 32, kQkvPerSm) qkv_kernel(const __
   const int hl = p.rope.rot_dim / 16;  // lanes of half the rotated dims
   const int from = lane < hl ? lane + hl : (lane < 2 * hl ? lane - hl : lane);
   const int n_rows = p.n_q + p.n_k + p.n_v;
-  const long long n_items = (long long)p.n_tok * p.parts;
-  for (long long item = (long long)blockIdx.x * kQkvWarps + warp; item < n_items;
-       item += (long long)gridDim.x * kQkvWarps) {
+  const long long n_items = (long long)p.n_tok * p.parts, stride = (long long)gridDim.x * kQkvWarps;
+  struct Item {
+    int row, tok, seq, r0, r1;
+  };
+  auto item_at = [&](long long item) {
+    Item it;
     const int i = p.parts == 1 ? (int)item : (int)(item / p.parts);
-    const int r0 = p.parts == 1 ? 0 : (int)(item - (long long)i * p.parts) * p.rows_per_part;
-    const int r1 = min(n_rows, r0 + p.rows_per_part);
-    int row = i, tok = i, seq = 0;
+    it.r0 = p.parts == 1 ? 0 : (int)(item - (long long)i * p.parts) * p.rows_per_part;
+    it.r1 = min(n_rows, it.r0 + p.rows_per_part);
+    it.row = it.tok = i;
+    it.seq = 0;
     if (kAppend) {  // the launch's i-th token: its sequence, row and position
       if (p.same_len > 0) {
-        seq = i / p.same_len;
+        it.seq = i / p.same_len;
       } else {
         int lo = 0, hi = p.n_seq - 1;
         while (lo < hi) {
@@ -306,12 +353,25 @@ __global__ void __launch_bounds__(kQkvWarps * 32, kQkvPerSm) qkv_kernel(const __
           if (tab.s[mid].z <= i) lo = mid;
           else hi = mid - 1;
         }
-        seq = lo;
+        it.seq = lo;
       }
-      const int4 s = tab.s[seq];
-      row = s.x + (i - s.z);
-      tok = s.y + (i - s.z);
+      const int4 s = tab.s[it.seq];
+      it.row = s.x + (i - s.z);
+      it.tok = s.y + (i - s.z);
     }
+    return it;
+  };
+  long long item = (long long)blockIdx.x * kQkvWarps + warp;
+  if (item >= n_items) return;
+  Item now = item_at(item), then{};
+  Feed feed{smem_u32(ring[warp]) + 16 * lane, 0, now.row, now.r0, now.r1, -1, 0, 0};
+  feed.fetch(p, lane);
+  for (; item < n_items; item += stride, now = then) {
+    if (item + stride < n_items) {
+      then = item_at(item + stride);
+      feed.next_row = then.row, feed.next_r0 = then.r0, feed.next_r1 = then.r1;
+    }
+    const int row = now.row, tok = now.tok, seq = now.seq, r0 = now.r0, r1 = now.r1;
     int phys = -1;
     if (kAppend && r1 > p.n_q) {
       phys = __ldg(p.block_table + (size_t)(p.bt_row0 + seq) * p.bt_stride + tok / kPage);
@@ -336,20 +396,20 @@ __global__ void __launch_bounds__(kQkvWarps * 32, kQkvPerSm) qkv_kernel(const __
     Turn t;
     if (r0 < p.n_q) {
       make_turn<kTurn>(p, p.qw, cs, lane, from, t);
-      do_heads<kTurn, true, false>(p.q, row, r0, min(r1, p.n_q), t, from, p.eps, lane,
+      do_heads<kTurn, true, false>(p, feed, r0, min(r1, p.n_q) - r0, t, from, p.eps, lane,
                                    p.q_out + (size_t)row * p.n_q * kHeadDim, nullptr, nullptr, true);
     }
     const size_t slot = kAppend ? ((size_t)max(phys, 0) * kPage + tok % kPage) * p.HKV : 0;
     const int ka = max(r0 - p.n_q, 0), kb = min(r1 - p.n_q, p.n_k);
     if (ka < kb) {
       make_turn<kTurn>(p, p.kw, cs, lane, from, t);
-      do_heads<kTurn, true, kAppend>(p.k, row, ka, kb, t, from, p.eps, lane, p.k_out + (size_t)row * p.n_k * kHeadDim,
+      do_heads<kTurn, true, kAppend>(p, feed, ka, kb - ka, t, from, p.eps, lane, p.k_out + (size_t)row * p.n_k * kHeadDim,
                                      p.k_pool + slot * kHeadDim, p.k_scale + slot, phys >= 0);
     }
     if (kAppend) {
       const int va = max(r0 - p.n_q - p.n_k, 0), vb = r1 - p.n_q - p.n_k;
       if (va < vb)
-        do_heads<TURN_NONE, false, true>(p.v, row, va, vb, t, from, 0.f, lane, p.k_out, p.v_pool + slot * kHeadDim,
+        do_heads<TURN_NONE, false, true>(p, feed, va, vb - va, t, from, 0.f, lane, p.k_out, p.v_pool + slot * kHeadDim,
                                          p.v_scale + slot, phys >= 0);
     }
   }
@@ -372,9 +432,9 @@ cudaError_t launch(const QkvParams& p, const QkvSeqs<kCap>& tab, int n_sm, cudaS
 // of items ends first.  An item costs its set-up (the token's page, its gains,
 // sines and cosines) and its rows, four, two or one at a time; in units of a
 // twentieth of the set-up, from batches of 300 to 32768 tokens (us, all sizes
-// from one row to all tried).  300 tokens of 12 rows: 3.7 with four rows (5.2
-// with all, 4.0 with one); 2000: 6.4 with all (7.1 with four); 9776 of 24: 42.8
-// with all (64.2 with four, 51.4 with 16).
+// from one row to all tried).  300 tokens of 12 rows: 3.8 with four rows (5.4
+// with all, 5.2 with one); 3000: 8.3 with all (10.5 with four); 9776 of 24: 41.6
+// with all (57.3 with four, 58.0 with 16).
 int qkv_rows_per_part(long long n_tok, int rows, int n_sm) {
   const long long warps = (long long)n_sm * kQkvPerSm * kQkvWarps;
   double best = 0.0;
