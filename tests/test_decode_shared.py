@@ -286,21 +286,30 @@ def test_calls_back_to_back_of_changing_sizes():
             assert torch.equal(o.view(torch.int16), alone.view(torch.int16))
 
 
-@pytest.mark.parametrize("hq, n, prefix, short", ((8, 3, 6160, (1, 1)), (8, 3, 8176, (1, 2)), (8, 3, 13504, (1, 7)),
-                                                  (8, 101, 6288, (1, 2)), (64, 17, 6160, (1, 1)), (64, 17, 12000, (2, 5))))
-def test_units_that_begin_with_a_short_segment(hq, n, prefix, short):
+def short_first_segment(hq, n, from_prefix):
+    """The first prefix from this one on whose split has a unit with two groups or more, the first of them short."""
+    import windowed_prefill_attention_gb300 as pa
+    for prefix in range(from_prefix, from_prefix + 8192, 64):
+        b = Batch(hq, 8, prefix, (1,) * n if n > 100 else tuple(1 + i for i in range(n)), 1, 0, 50)
+        seqs = [(i, prefix + s - 1, 1, prefix + s) for i, s in enumerate(b.suffix)]
+        runs, _ = pa.pa_decode_shared_plan(hq, 8, 4096, 152, seqs, prefix, b.S, b.W, 1)
+        segs = {}  # tiles of eight blocks
+        for r in runs.tolist():
+            segs.setdefault(r[0], []).append((r[7] - r[6] + 7) // 8)
+        if any(len(s) > 1 and s[0] <= 2 for s in segs.values()):
+            return b.make()
+    raise AssertionError("no such split")
+
+
+@pytest.mark.parametrize("hq, n, from_prefix", ((8, 3, 8192), (8, 3, 14384), (8, 3, 19712), (8, 101, 9216), (64, 17, 6144),
+                                                (64, 17, 9600)))
+def test_units_that_begin_with_a_short_segment(hq, n, from_prefix):
     """Units whose first group ends after a tile or two: the next one's queries, K and V come in while the first
     one's are on their way (with 101 sequences of one row a head, 101 copies a group)."""
     import torch
 
     import windowed_prefill_attention_gb300 as pa
-    b = Batch(hq, 8, prefix, (1,) * n if n > 100 else tuple(1 + i for i in range(n)), 1, 0, 50).make()
-    runs, _ = pa.pa_decode_shared_plan(hq, 8, b.max_pages, 152, b.seqs, b.prefix, b.S, b.W, 1)
-    tile = 4 if n * hq // 8 <= 128 else 8
-    segs = {}
-    for r in runs.tolist():
-        segs.setdefault(r[0], []).append((r[7] - r[6] + tile - 1) // tile)
-    assert list(short) in segs.values()
+    b = short_first_segment(hq, n, from_prefix)
     first = None
     for _ in range(20):
         d = to_device(b)

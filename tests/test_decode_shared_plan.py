@@ -51,7 +51,7 @@ def test_every_visible_block_is_computed_once(pa, case, prefix_pass):
     assert prefix_pass or not len(pre)
     n, pb = min(512, len(suffix)), prefix // 16
     n_cta = 1 if n * (hq // hkv) <= 128 else 2  # CTAs of a unit of the prefix pass
-    tile, rows = 4 * n_cta, 128 * n_cta         # blocks of a tile; rows of a group
+    tile, rows = 8, 128 * n_cta                 # blocks of a tile; rows of a group
     done = {}  # (sequence, head) -> blocks of its own passes
     for s, g, base, sink, lo, first, last in own.tolist():
         assert 0 < last - first <= 128

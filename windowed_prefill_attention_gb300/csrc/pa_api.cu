@@ -1630,9 +1630,9 @@ int decode_shared_check(int HQ, int HKV, int max_pages, int n_seq, const pa_seq*
 }
 
 // One launch (sequences [s0, s0 + n)) of the shared-prefix decode: its table and split.
-// The prefix pass: up to 128 rows of a kv head (n sequences x G) are one CTA's, in
-// 64-key tiles; more are worked on by pairs of CTAs, in groups of 256 and 128-key
-// tiles.  Per group the blocks some row sees; all tiles, group after group, cut
+// The prefix pass: up to 128 rows of a kv head (n sequences x G) are one CTA's; more
+// are worked on by pairs of CTAs, in groups of 256.  Per group the blocks some row
+// sees, in 128-key tiles; all tiles, group after group, cut
 // into runs of equal cost, one for each unit (a CTA or a pair, one CTA an SM).  A
 // run costs its tiles plus kShSegCost for every group after its first: the next
 // group's queries are staged and the last one's output stored while no product
@@ -1649,7 +1649,7 @@ constexpr int kShSegCost = 4, kShOwnWaves = 2;
 struct ShCost {
   double unit, tile, late, tail;
 };
-constexpr ShCost kShCost[2] = {{11.5, 1.4, 1.45, 2.0}, {11.0, 2.1, 1.65, 4.0}};  // units of one CTA, of two
+constexpr ShCost kShCost[2] = {{11.5, 2.5, 2.65, 2.0}, {11.0, 2.1, 1.65, 4.0}};  // units of one CTA, of two
 constexpr double kShMaskedTile = 1.25;
 constexpr double kShOwnBlockUs = 0.215, kShAgainBlockUs = 0.165, kShOwnCtaUs = 0.25;
 constexpr double kShOwnStartUs = 4.5, kShOwnFull = 0.85;
@@ -1692,7 +1692,7 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
   p.W = W;
   p.prefix_blk = Pb;
   p.n_cta = n * G <= kRows ? 1 : 2;
-  const int unit_rows = kRows * p.n_cta, tile_blk = kTileBlocks / 2 * p.n_cta;
+  const int unit_rows = kRows * p.n_cta;
   p.n_grp = n < 2 || Pb == 0 ? 0 : (n * G + unit_rows - 1) / unit_rows;
   p.first_blk = p.n_grp > 0 ? Pb : 0;
   p.tiles_head = 0;
@@ -1705,7 +1705,7 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
     g.lo = lo;
     g.sink = W > 0 ? std::min(S, lo) : 0;
     g.n_blk = g.sink + Pb - lo;
-    p.tiles_head += (g.n_blk + tile_blk - 1) / tile_blk;
+    p.tiles_head += (g.n_blk + kTileBlocks - 1) / kTileBlocks;
   }
   // at most 16 groups of 2^23 tiles: no overflow before the test
   if ((long long)HKV * p.tiles_head >= (1ll << 30)) return PA_EINVAL;
@@ -1741,7 +1741,7 @@ int decode_shared_plan(int HQ, int HKV, int n_sm, const pa_seq* seqs, int s0, in
   p.merge_ways = 0;
   int nt[8 * kShGroups], units = max_units;
   if (T > 0) {
-    for (int j = 0; j < J; ++j) nt[j] = (t.grp[j % p.n_grp].n_blk + tile_blk - 1) / tile_blk;
+    for (int j = 0; j < J; ++j) nt[j] = (t.grp[j % p.n_grp].n_blk + kTileBlocks - 1) / kTileBlocks;
     double best = 1e30;
     const double own_blk = (double)own * HKV, least_ctas = (double)n * HKV;
     for (int left = 0; left < max_units; left += 8 / p.n_cta) {
@@ -1899,12 +1899,12 @@ int pa_decode_shared_plan(int n_q_heads, int n_kv_heads, int max_pages_per_seq, 
   if ((rc = decode_shared_plan(n_q_heads, n_kv_heads, n_sm, seqs, 0, std::min(n_seq, kShSeqs), n_prefix, n_sink_blk,
                                n_win_blk, prefix_pass, p, t)))
     return rc;
-  const int per = kRows * p.n_cta / p.G, tile_blk = kTileBlocks / 2 * p.n_cta;
+  const int per = kRows * p.n_cta / p.G;
   int np = 0;
   for (int g = 0; g < p.HKV; ++g)
     for (int j = 0; j < p.n_grp; ++j) {
       const ShGroup& gr = t.grp[j];
-      const int nt = (gr.n_blk + tile_blk - 1) / tile_blk;
+      const int nt = (gr.n_blk + kTileBlocks - 1) / kTileBlocks;
       const int a = g * p.tiles_head + gr.x0;
       for (int t0 = 0; t0 < nt;) {
         const int c = (int)(std::upper_bound(t.cut, t.cut + p.n_units, a + t0) - t.cut) - 1;
@@ -1918,8 +1918,8 @@ int pa_decode_shared_plan(int n_q_heads, int n_kv_heads, int max_pages_per_seq, 
           o[3] = std::min(p.n_seq, (j + 1) * per) - o[2];
           o[4] = gr.sink;
           o[5] = gr.lo;
-          o[6] = t0 * tile_blk;
-          o[7] = std::min(gr.n_blk, t1 * tile_blk);
+          o[6] = t0 * kTileBlocks;
+          o[7] = std::min(gr.n_blk, t1 * kTileBlocks);
         }
         ++np;
         t0 = t1;

@@ -123,8 +123,10 @@ __device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
 // per tile: 64 KB of codes read, 128 KB of operands written and 192 KB of operands
 // read per tile and SM) would otherwise bound the kernel.
 // kN = 1, up to 128 rows: a pair's second CTA would have none.  Each CTA takes
-// tiles of 64 keys by itself, with the same stages.  (9 sequences of 8 rows on
-// 131072 keys: 35 us, on pairs 40.)
+// whole tiles by itself: K in two parts of 128 dims and V in two of 64 keys, one
+// stage for each, so that a part is widened while the other one's products run.
+// (9 sequences of 8 rows on 131072 keys: 33 us, with 64-key tiles in double stages
+// 35, on pairs 40; 12 on 16384: 21, 20, 22.)
 //
 // What bounds it.  64 sequences, 16 q and 2 kv heads, 32768 keys: 51 us, 18 tiles
 // a pair of ~3500 cycles each, between 11000 of set-up and 5500 of storing partials.
@@ -132,11 +134,12 @@ __device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
 // to products: softmax (~2000), an arrival from the other CTA (300 to 1100), the
 // issue of the products (70 to 90 cycles each), and in most tiles some warp that
 // moves a reference and rescales O (~1500; without outlier keys, 50.5 us instead
-// of 53.4 at the time).  A CTA alone: ~2750 cycles a 64-key tile, issue and rescale.
+// of 53.4 at the time).  A CTA alone: ~5000 cycles a tile, all of whose codes it
+// widens itself, beside the same softmax.
 // Tried and not better: two sets of softmax warps in turn, 16 of them on half of
 // the keys each, warps of their own for the rescale (all: more warps, each
-// slower), and a thread each for Q K^T and P V (what runs in order on one thread
-// then waits for the other's commit).
+// slower), a thread each for Q K^T and P V (what runs in order on one thread then
+// waits for the other's commit), and prefetches of later tiles' codes into L2.
 constexpr int kSoftWarps = 8;                       // warps 0-7: softmax; TMEM quadrant w % 4, 16 rows w / 4 of it
 constexpr int kConvWarps = 8;                       // warps 8-15: codes -> fp16 operands (K: four, V: four), the queries
 constexpr int kIssueWarp = kSoftWarps + kConvWarps; // warp 16: TMEM; even CTA: the products, odd CTA: forwards K
@@ -155,8 +158,8 @@ static_assert(kSoftRegs >= 96 && kConvRegs <= 96 && kMiscRegs <= 96, "an increas
 // converters' loads in flight live.
 constexpr int kStageBytes = 32768;
 constexpr int kSmQ = 0;                             // 4 regions [128 rows][64 dims]
-constexpr int kSmK = 65536;                         // 2 stages x 4 regions [64 keys][64 dims]
-constexpr int kSmV = kSmK + 2 * kStageBytes;        // 2 stages x 2 regions [128 keys][64 dims]
+constexpr int kSmK = 65536;                         // a pair: 2 stages x 4 regions [64 keys][64 dims]; one CTA: 4 regions [128][64]
+constexpr int kSmV = kSmK + 2 * kStageBytes;        // a pair: 2 stages x 2 regions [128 keys][64 dims]; one CTA: 2 x 4 regions [64][64]
 constexpr int kSmScale = kSmV + 2 * kStageBytes;    // [2] x {K scales 128, V scales 128, valid blocks, exponent}
 constexpr int kScaleSlot = 2 * 512 + 16;
 constexpr int kSmRow = kSmScale + 2 * kScaleSlot;   // [2][128] int8 exponents of the rows' factors, by segment parity
@@ -166,10 +169,12 @@ constexpr int kSmBar = kSmRow + 2 * kRows;
 // a commit arrives in both CTAs.  A parity wait tells a phase only from the one
 // before it; every wait below comes when the phase before is known to be over.
 enum : int {
-  B_KF = 0,    // [2] even: a tile's K is written (four warps, and the odd CTA's forward)
+  B_KF = 0,    // [2] even: a tile's K is written (four warps, and the odd CTA's forward); one CTA: [2] its halves
   B_VF = 2,    // [2] even: its V
   B_KL = 4,    // [2] odd: its own half of K, V (four warps), to be forwarded
   B_VL = 6,    // [2]
+  B_KE = B_KL, // [2] one CTA alone: Q K^T of half of a tile's dims is done; its K is free
+  B_VE = B_VL, // [2] one CTA alone: P V of half of a tile's keys is done; its V is free
   B_SF = 8,    // [2] both: scores of a tile in TMEM; its K stage is free
   B_PF = 10,   // [2] even: P' of a tile in TMEM (every softmax warp of both)
   B_OD = 12,   // [2] both: P V of a tile is done; its V stage is free
@@ -193,7 +198,7 @@ constexpr uint32_t kTmemO = 0, kTmemS = 256;        // O [0, 256), S of even / o
 
 // The B operand of O = P V: V as [key][64 dims] rows of 128 bytes with the
 // 128-byte swizzle, dims (N) contiguous: 8-key atoms of 1024 bytes along K,
-// regions of a tile's keys x 128 bytes along N.
+// regions of the stage's keys (a tile's, or half of one CTA's) x 128 bytes along N.
 template <int kN>
 __device__ __forceinline__ uint64_t sdesc_v(uint32_t saddr) {
   uint64_t d = 0;
@@ -205,7 +210,7 @@ __device__ __forceinline__ uint64_t sdesc_v(uint32_t saddr) {
   return d;
 }
 template <int kN>
-constexpr uint32_t kIdescQK = idesc_f16(kN * 128, kN * 64, false, false);
+constexpr uint32_t kIdescQK = idesc_f16(kN * 128, kTileKeys, false, false);
 template <int kN>
 constexpr uint32_t kIdescPV = idesc_f16(kN * 128, 256, false, false) | (1u << 16);  // B is N-major
 
@@ -226,7 +231,7 @@ __device__ __forceinline__ Segment segment_at(const SharedParams& p, const Share
   s.j = s.g * p.n_grp + s.rg;
   s.grp = tab.grp[s.rg];
   s.t0 = xh - s.grp.x0;
-  s.t1 = min((s.grp.n_blk + kN * 4 - 1) / (kN * 4), s.t0 + (x_end - x));
+  s.t1 = min((s.grp.n_blk + kTileBlocks - 1) / kTileBlocks, s.t0 + (x_end - x));
   s.row0 = s.rg * (kN * kRows) + rank * kRows;
   s.rows = max(0, min(kRows, p.n_seq * p.G - s.row0));
   return s;
@@ -340,42 +345,47 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kSoftWarps;
   const bool kv = warp >= kConvWarps / 2;  // V
   const int w = warp & 3;
-  uint32_t n_tile = 0, n_seg = 0;
+  uint32_t n_step = 0, n_seg = 0;  // steps: a pair's tiles, one CTA's parts of tiles
   const size_t tok = (size_t)p.HKV * kHeadDim;  // bytes from a token to the next
-  // Warp w the 16 keys 64 rank + 16 w on, all dims; a load takes two keys.  V of a
-  // pair: keys 32 w on, dims 128 rank on; a load takes four keys.  Lane bit 2
-  // (and 4) the key, the others the 16 bytes.
-  const bool wide = kN == 2 && kv;
+  // What a warp widens at a time lies in one of two places of 32 KB:
+  //   a pair's K: keys 64 rank + 16 w on, all dims; one CTA's V: 64 of the tile's
+  //   keys (part h), of them 16 w on, all dims.  A load takes two keys.
+  //   wide: a pair's V: keys 32 w on, dims 128 rank on; one CTA's K: keys 32 w on,
+  //   dims 128 h on.  A load takes four keys.
+  // Lane bit 2 (and 4) the key, the others the 16 bytes.
+  const bool wide = kv == (kN == 2);
   const int u = wide ? (lane & 3) | (lane >> 1 & 4) : (lane & 3) | (lane >> 3) << 2;
   const int sub = wide ? (lane >> 2 & 1) | (lane >> 4) << 1 : lane >> 2 & 1;
   const int step = wide ? 4 : 2;                                // keys per load
-  const int row0 = (wide ? 32 : 16) * w + sub;                  // the stage's row of the lane's first load
+  const int row0 = (wide ? 32 : 16) * w + sub;                  // the place's row of the lane's first load
   const uint32_t at0 = c.sb + (kv ? kSmV : kSmK) + (u >> 2) * (wide ? 16384 : 8192) + row0 * 128;
   const int blk0 = wide ? 2 * w : 4 * c.rank + w;               // first block of the tile it loads
   const size_t step_b = step * tok, half_b = wide ? 0 : 8 * tok;  // from a load to the next; from load 0 to load 4
   const int blk4 = wide ? blk0 + 1 : blk0;                      // block of load 4
   const int8_t* base = (kv ? p.v_pool + (wide ? 128 * c.rank : 0) : p.k_pool) + 16 * u + (size_t)sub * tok;
-  constexpr int kBlk = 4 * kN, kWin = 32 / kBlk;                // a tile's blocks; tiles of a window of pages
+  constexpr int kParts = 2 / kN;
   for (int x = c.x0; x < c.x1; ++n_seg) {
     const Segment s = segment_at<kN>(p, tab, c.rank, x, c.x1);
     const int8_t* src = base + (size_t)s.g * kHeadDim;
     // pages of the segment's blocks, 32 at a time, one per lane
-    const int b0 = s.t0 * kBlk;
+    const int b0 = s.t0 * kTileBlocks;
     int pg = group_page(p, s.grp, b0 + lane), pg_next = group_page(p, s.grp, b0 + 32 + lane);
     uint4 r[8];
     // a block past the list or of a bad page loads page 0's codes: whatever finite values they widen to,
     // the softmax gives those keys no weight
-    auto load = [&](int tw) {
-      const int pa = max(0, __shfl_sync(kAllLanes, pg, tw * kBlk + blk0));
-      const int pb = max(0, __shfl_sync(kAllLanes, pg, tw * kBlk + blk4));
-      const int8_t* a = src + (size_t)pa * (kPage * tok);
-      const int8_t* b = src + (size_t)pb * (kPage * tok) + half_b;
+    auto load = [&](int t4, int h) {
+      const int more = kN == 1 && kv ? 4 * h : 0;  // blocks
+      const int pa = max(0, __shfl_sync(kAllLanes, pg, t4 * kTileBlocks + blk0 + more));
+      const int pb = max(0, __shfl_sync(kAllLanes, pg, t4 * kTileBlocks + blk4 + more));
+      const int8_t* part = src + (kN == 1 && !kv ? 128 * h : 0);
+      const int8_t* a = part + (size_t)pa * (kPage * tok);
+      const int8_t* b = part + (size_t)pb * (kPage * tok) + half_b;
 #pragma unroll
       for (int n = 0; n < 4; ++n, a += step_b) r[n] = ldg_stream(a);
 #pragma unroll
       for (int n = 4; n < 8; ++n, b += step_b) r[n] = ldg_stream(b);
     };
-    load(0);
+    load(0, 0);
     if (n_seg > 0 || kv) {
       if (!c.wait(B_RAWF, n_seg)) return;
       const int first = n_seg > 0 ? 16 * warp : kSoftWarps * kHelpRows + 8 * w;
@@ -390,15 +400,16 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
     // every warp has read its raw rows: the stages that held them may be written
     if ((n_seg > 0 || kv) && !c.wait(B_RAW, n_seg)) return;
 
-    const int nt = s.t1 - s.t0;
-    for (int t = 0; t < nt; ++t, ++n_tile) {
-      if (((t + 1) & (kWin - 1)) == 0) {  // the next tile's pages are in the next window
+    const int steps = (s.t1 - s.t0) * kParts;
+    for (int i = 0; i < steps; ++i, ++n_step) {
+      const int t_next = (i + 1) / kParts, h_next = (i + 1) % kParts;  // what is loaded next
+      if (h_next == 0 && (t_next & 3) == 0) {  // its pages are in the next window
         pg = pg_next;
-        pg_next = group_page(p, s.grp, b0 + kBlk * (t + 1) + 32 + lane);
+        pg_next = group_page(p, s.grp, b0 + 8 * t_next + 32 + lane);
       }
-      // the stage's products of two tiles before are done
-      const int st = n_tile & 1;
-      if (n_tile > 1 && !c.wait((kv ? B_OD : B_SF) + st, (n_tile >> 1) - 1)) return;
+      // the products that read what was in this place are done
+      const uint32_t st = n_step & 1;
+      if (n_step > 1 && !c.wait((kv ? (kN == 2 ? B_OD : B_VE) : (kN == 2 ? B_SF : B_KE)) + st, (n_step >> 1) - 1)) return;
 #pragma unroll
       for (int n = 0; n < 8; ++n) widen16(r[n], at0 + st * kStageBytes + step * n * 128, row0 + step * n, u);
       fence_proxy_async_shared();
@@ -406,11 +417,11 @@ __device__ __forceinline__ void role_convert(const SharedParams& p, const Shared
       // K warps take no part in the first segment's staging; they see that its
       // rows have landed all the same, before their first tile leads to the next
       // segment's: a parity wait there would take this phase's for it.
-      if (n_tile == 0 && !kv && !c.wait(B_RAWF, 0)) return;
+      if (n_step == 0 && !kv && !c.wait(B_RAWF, 0)) return;
       if (lane == 0) mbar_arrive(c.bar((kv ? (c.rank == 0 ? B_VF : B_VL) : (c.rank == 0 ? B_KF : B_KL)) + st));
-      if (t + 1 < nt) load((t + 1) & (kWin - 1));
+      if (i + 1 < steps) load(t_next & 3, h_next);
     }
-    x += nt;
+    x += s.t1 - s.t0;
   }
 }
 
@@ -467,15 +478,14 @@ __device__ __forceinline__ void role_scales(const SharedParams& p, const SharedS
   for (int x = c.x0; x < c.x1;) {
     const Segment s = segment_at<kN>(p, tab, c.rank, x, c.x1);
     int ev = -100;
-    // lane: keys 4 lane .. + 3 of a tile, in block lane / 4 (one CTA alone: half the lanes)
-    const bool mine = lane < 16 * kN;
+    // lane: keys 4 lane .. + 3 of a tile, in block lane / 4
     float ks[4], vs[4];
     bool valid = false;
     auto load = [&](int t) {
-      const int b = t * (4 * kN) + (lane >> 2);
-      const int page = mine ? group_page(p, s.grp, b) : -1;
+      const int b = t * kTileBlocks + (lane >> 2);
+      const int page = group_page(p, s.grp, b);
       valid = page >= 0;
-      if (!valid && mine && b < s.grp.n_blk && (lane & 3) == 0) atomicCAS(p.err, 0, DEV_ERR_BAD_PAGE);
+      if (!valid && b < s.grp.n_blk && (lane & 3) == 0) atomicCAS(p.err, 0, DEV_ERR_BAD_PAGE);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const size_t at = ((size_t)(valid ? page : 0) * kPage + 4 * (lane & 3) + e) * p.HKV + s.g;
@@ -500,7 +510,7 @@ __device__ __forceinline__ void role_scales(const SharedParams& p, const SharedS
       if (lane == 0) {
         uint32_t m8 = 0;
 #pragma unroll
-        for (int e = 0; e < 4 * kN; ++e) m8 |= ((ok >> (4 * e)) & 1u) << e;
+        for (int e = 0; e < kTileBlocks; ++e) m8 |= ((ok >> (4 * e)) & 1u) << e;
         sts128(at + 1024, m8, (uint32_t)ev, 0, 0);
       }
       __syncwarp();
@@ -511,28 +521,31 @@ __device__ __forceinline__ void role_scales(const SharedParams& p, const SharedS
   }
 }
 
-// ---- the products, one thread of the even CTA.  A tile's instructions go out
+// ---- the products, one thread (of a pair's even CTA).  A tile's instructions go out
 // of one asm block with the operands' offsets added inside it: instructions
 // between them, a branch above all, leave the tensor pipe waiting.
 // S = Q K^T: four regions of 64 dims, four k-steps of 32 bytes each.
 #define PA_SH_QK(G, qo, ko)                                \
   "add.s64 a, %1, " qo ";\n\tadd.s64 b, %2, " ko ";\n\t" \
   "tcgen05.mma.cta_group::" G ".kind::f16 [%0], a, b, %3, pt;\n\t"
-#define PA_SH_QK4(G, r)                                                                                           \
-  PA_SH_QK(G, r " * 1024", r " * 512") PA_SH_QK(G, r " * 1024 + 2", r " * 512 + 2") PA_SH_QK(G, r " * 1024 + 4", r " * 512 + 4") \
-      PA_SH_QK(G, r " * 1024 + 6", r " * 512 + 6")
-#define PA_SH_QK_TILE(G)                                                                                          \
-  "{\n\t.reg .pred pf, pt;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 pf, %4, %4;\n\tsetp.eq.b32 pt, %4, %4;\n\t"          \
-  "tcgen05.mma.cta_group::" G ".kind::f16 [%0], %1, %2, %3, pf;\n\t"                                              \
-  PA_SH_QK(G, "2", "2") PA_SH_QK(G, "4", "4") PA_SH_QK(G, "6", "6") PA_SH_QK4(G, "1") PA_SH_QK4(G, "2") PA_SH_QK4(G, "3") "}"
-template <int kN>
-__device__ __forceinline__ void mma_qk_tile(uint32_t d, uint64_t qd, uint64_t kd) {
-  if constexpr (kN == 2)
-    asm volatile(PA_SH_QK_TILE("2") ::"r"(d), "l"(qd), "l"(kd), "r"(kIdescQK<2>), "r"(0u) : "memory");
-  else
-    asm volatile(PA_SH_QK_TILE("1") ::"r"(d), "l"(qd), "l"(kd), "r"(kIdescQK<1>), "r"(0u) : "memory");
+#define PA_SH_QK4(G, r, K)                                                                            \
+  PA_SH_QK(G, r " * 1024", r " * " K) PA_SH_QK(G, r " * 1024 + 2", r " * " K " + 2")                  \
+      PA_SH_QK(G, r " * 1024 + 4", r " * " K " + 4") PA_SH_QK(G, r " * 1024 + 6", r " * " K " + 6")
+#define PA_SH_QK_FIRST(G)                                                                             \
+  "{\n\t.reg .pred p0, pt;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 pt, %4, %4;\n\t" \
+  "tcgen05.mma.cta_group::" G ".kind::f16 [%0], %1, %2, %3, p0;\n\t"                                  \
+  PA_SH_QK(G, "2", "2") PA_SH_QK(G, "4", "4") PA_SH_QK(G, "6", "6")
+// A pair: the whole tile, each CTA with its 64 keys of K.
+__device__ __forceinline__ void mma_qk_pair(uint32_t d, uint64_t qd, uint64_t kd) {
+  asm volatile(PA_SH_QK_FIRST("2") PA_SH_QK4("2", "1", "512") PA_SH_QK4("2", "2", "512") PA_SH_QK4("2", "3", "512") "}" ::"r"(d),
+               "l"(qd), "l"(kd), "r"(kIdescQK<2>), "r"(0u) : "memory");
 }
-// O (+)= P V: k-steps of 16 keys, 8 TMEM columns of P' and 2048 bytes of V each.
+// One CTA: half of the dims of 128 keys.
+__device__ __forceinline__ void mma_qk_half(uint32_t d, uint64_t qd, uint64_t kd, uint32_t acc0) {
+  asm volatile(PA_SH_QK_FIRST("1") PA_SH_QK4("1", "1", "1024") "}" ::"r"(d), "l"(qd), "l"(kd), "r"(kIdescQK<1>), "r"(acc0)
+               : "memory");
+}
+// O (+)= P V over a stage's keys: k-steps of 16 keys, 8 TMEM columns of P' and 2048 bytes of V each.
 #define PA_SH_PV(G, po, vo)                                \
   "add.u32 a, %1, " po ";\n\tadd.s64 b, %2, " vo ";\n\t" \
   "tcgen05.mma.cta_group::" G ".kind::f16 [%0], [a], b, %3, pt;\n\t"
@@ -571,17 +584,41 @@ __device__ __forceinline__ void role_issue(const SharedParams& p, const SharedSe
     return kN == 2 ? mbar_wait_cluster(c.bar(i), parity & 1u, c.wc, 80 + i) : mbar_wait(c.bar(i), parity & 1u, c.wc, 80 + i);
   };
   auto wait = [&](int i, uint32_t parity) { return mbar_wait(c.bar(i), parity & 1u, c.wc, 80 + i); };
-  auto qk = [&](uint32_t n) {  // n: the tile's number in the pair's order
-    if (!wait_pair(B_KF + (n & 1), n >> 1)) return false;
-    tc_fence_after();
-    mma_qk_tile<kN>(c.tm + kTmemS + 128 * (n & 1), qd, (n & 1) ? kd1 : kd0);
+  auto qk = [&](uint32_t n) {  // n: the tile's number in the unit's order
+    const uint32_t d = c.tm + kTmemS + 128 * (n & 1);
+    if (kN == 2) {
+      if (!wait_pair(B_KF + (n & 1), n >> 1)) return false;
+      tc_fence_after();
+      mma_qk_pair(d, qd, (n & 1) ? kd1 : kd0);
+    } else {
+      if (!wait(B_KF, n)) return false;
+      tc_fence_after();
+      mma_qk_half(d, qd, kd0, 0);
+      commit<kN>(c.bar(B_KE));
+      if (!wait(B_KF + 1, n)) return false;
+      tc_fence_after();
+      mma_qk_half(d, qd + 2048, kd1, 1);
+      commit<kN>(c.bar(B_KE + 1));
+    }
     commit<kN>(c.bar(B_SF + (n & 1)));
     return true;
   };
   auto pv = [&](uint32_t n, uint32_t acc) {
-    if (!wait_pair(B_VF + (n & 1), n >> 1) || !wait(B_PF + (n & 1), n >> 1)) return false;
-    tc_fence_after();
-    mma_pv_tile<kN>(c.tm + kTmemO, c.tm + kTmemS + 128 * (n & 1), (n & 1) ? vd1 : vd0, acc);
+    const uint32_t ptm = c.tm + kTmemS + 128 * (n & 1);
+    if (kN == 2) {
+      if (!wait_pair(B_VF + (n & 1), n >> 1) || !wait(B_PF + (n & 1), n >> 1)) return false;
+      tc_fence_after();
+      mma_pv_tile<kN>(c.tm + kTmemO, ptm, (n & 1) ? vd1 : vd0, acc);
+    } else {
+      if (!wait(B_PF + (n & 1), n >> 1) || !wait(B_VF, n)) return false;
+      tc_fence_after();
+      mma_pv_tile<kN>(c.tm + kTmemO, ptm, vd0, acc);
+      commit<kN>(c.bar(B_VE));
+      if (!wait(B_VF + 1, n)) return false;
+      tc_fence_after();
+      mma_pv_tile<kN>(c.tm + kTmemO, ptm + 32, vd1, 1);
+      commit<kN>(c.bar(B_VE + 1));
+    }
     commit<kN>(c.bar(B_OD + (n & 1)));
     return true;
   };
@@ -616,12 +653,12 @@ struct SliceRows {
 };
 
 // z = score * k_scale, and the rows' maxima.
-template <bool kMasked, int kN>
-__device__ __forceinline__ void scale_and_max(uint32_t (&s)[32 * kN], uint32_t ks_at, uint32_t seen0, uint32_t seen1,
+template <bool kMasked>
+__device__ __forceinline__ void scale_and_max(uint32_t (&s)[64], uint32_t ks_at, uint32_t seen0, uint32_t seen1,
                                               float& z0, float& z1) {
   float za = -INFINITY, zb = -INFINITY;
 #pragma unroll
-  for (int k = 0; k < 8 * kN; ++k) {
+  for (int k = 0; k < 16; ++k) {
     float2 ks;
     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks.x), "=f"(ks.y) : "r"(ks_at + 32 * k));
     float2 a = mul2(make_float2(__uint_as_float(s[4 * k]), __uint_as_float(s[4 * k + 1])), ks);
@@ -642,19 +679,17 @@ __device__ __forceinline__ void scale_and_max(uint32_t (&s)[32 * kN], uint32_t k
 }
 
 // One tile of the warp's rows: P' over its scores.  `first`: no O to rescale yet.
-template <int kN>
 __device__ __forceinline__ bool softmax_tile(const SharedParams& p, const PreCtx& c, const ShGroup& grp, int blk0,
                                              uint32_t stm, uint32_t otm, uint32_t sc, uint32_t valid, float fe,
                                              bool first, uint32_t n_before, SliceRows& r) {
   const int lane = threadIdx.x & 31;
   const uint32_t ks_at = sc + 8 * (lane & 3);
-  uint32_t s[32 * kN];
-  if constexpr (kN == 2) tmem_ld_16x256b_x16(stm, s);
-  else tmem_ld_16x256b_x8(stm, s);
+  uint32_t s[64];
+  tmem_ld_16x256b_x16(stm, s);
   uint32_t seen[2] = {valid, valid};  // blocks of the tile that the rows see
   if (p.W > 0) {
 #pragma unroll
-    for (int e = 0; e < 4 * kN; ++e) {
+    for (int e = 0; e < kTileBlocks; ++e) {
       const int lb = group_block(grp, blk0 + e);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -663,8 +698,8 @@ __device__ __forceinline__ bool softmax_tile(const SharedParams& p, const PreCtx
   }
   tmem_wait_ld(s);
   float z[2];
-  if (__all_sync(kAllLanes, (seen[0] & seen[1]) == (1u << (4 * kN)) - 1u)) scale_and_max<false, kN>(s, ks_at, 0, 0, z[0], z[1]);
-  else scale_and_max<true, kN>(s, ks_at, seen[0], seen[1], z[0], z[1]);
+  if (__all_sync(kAllLanes, (seen[0] & seen[1]) == 0xffu)) scale_and_max<false>(s, ks_at, 0, 0, z[0], z[1]);
+  else scale_and_max<true>(s, ks_at, seen[0], seen[1], z[0], z[1]);
   // The rows' references.  Mostly no row passes its own by enough to move it,
   // which each thread sees from its own keys; only else are the rows' maxima
   // put together.
@@ -695,7 +730,7 @@ __device__ __forceinline__ bool softmax_tile(const SharedParams& p, const PreCtx
   const float n0 = r.m[0] == -INFINITY ? 0.f : -r.m[0], n1 = r.m[1] == -INFINITY ? 0.f : -r.m[1];
   const float c0 = fmaxf(r.c[0], 1e-30f), c1 = fmaxf(r.c[1], 1e-30f);
 #pragma unroll
-  for (int h = 0; h < kN; ++h) {  // 64 keys
+  for (int h = 0; h < 2; ++h) {  // 64 keys
     uint32_t ph[16];
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
@@ -775,7 +810,7 @@ __device__ __forceinline__ void role_softmax(const SharedParams& p, const Shared
       const int ev_t = (int)__float_as_uint(meta.y);
       const float fe = ev_t > ev ? pow2i(max(-126, ev - ev_t)) : 1.f;
       ev = ev_t;
-      if (!softmax_tile<kN>(p, c, s.grp, (s.t0 + t) * (4 * kN), stm, c.tm + kTmemO + lanes, sc, __float_as_uint(meta.x), fe,
+      if (!softmax_tile(p, c, s.grp, (s.t0 + t) * kTileBlocks, stm, c.tm + kTmemO + lanes, sc, __float_as_uint(meta.x), fe,
                         t == 0, n_tile - 1, r))
         return;
       tmem_wait_st();
@@ -843,7 +878,7 @@ __device__ __forceinline__ void prefix_pass(const SharedParams& p, const SharedS
     const int i = threadIdx.x;
     int n = 1;
     if (i < B_KL) n = kConvWarps / 2 + kN - 1;
-    if (i >= B_KL && i < B_SF) n = kConvWarps / 2;
+    if (i >= B_KL && i < B_SF) n = kN == 2 ? kConvWarps / 2 : 1;
     if (i == B_QF) n = kConvWarps + kN - 1;
     if (i == B_QL || i == B_RAW) n = kConvWarps;
     if ((i >= B_SCE && i < B_QF) || i == B_HELP) n = kSoftWarps;

@@ -53,8 +53,8 @@ struct SharedParams {
   int prefix_blk;          // blocks of the shared prefix; their pages are block_table row 0's
   int first_blk;           // the per-sequence pass starts at this block: prefix_blk, or 0 without a prefix pass
   int n_grp;               // row groups per kv head (0: no prefix pass)
-  int n_cta;               // CTAs of a unit of the prefix pass, 1 or 2: groups of 128 n_cta rows, tiles of 64 n_cta keys
-  int tiles_head;          // tiles of all groups of one kv head
+  int n_cta;               // CTAs of a unit of the prefix pass, 1 or 2: groups of 128 n_cta rows
+  int tiles_head;          // 128-key tiles of all groups of one kv head
   int n_units;             // units of the prefix pass
   int chunk;               // blocks per CTA of the per-sequence pass
   int chunks_head;         // its CTAs per kv head
