@@ -158,8 +158,10 @@ int pa_prefill_host(pa_handle h, int n_seq, const pa_seq* seqs, const void* q, c
  * for a NULL handle, PA_ECUDA if a stream reports an error.  Does not wait. */
 int pa_debug_copy_streams_idle(pa_handle h);
 
-/* Synchronise `stream`, then report and clear the first device-side error
- * recorded since the last call (PA_ETIMEOUT, PA_EBADPAGE) or PA_ECUDA. */
+/* Synchronise `stream`, then report and clear the device-side error recorded
+ * since the last call: PA_ETIMEOUT or PA_ECUDA (any result since then may be
+ * lost) before PA_EBADPAGE (only what the bad entry concerns is left out, in that
+ * call and no other). */
 int pa_last_error(pa_handle h, void* stream);
 
 /* Launch times recorded since the last reset (needs record_timing): sums of

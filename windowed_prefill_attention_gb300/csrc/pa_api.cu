@@ -218,7 +218,7 @@ struct pa_ctx {
   int seqs_cap = 0;
   Unit* d_units = nullptr;
   int units_cap = 0;
-  int* d_err = nullptr;
+  int* d_err = nullptr;  // kErrWords
   unsigned int* d_qflags = nullptr;  // host path: chunk c's q rows are in when d_qflags[c] == q_epoch
   int qflags_cap = 0;
   unsigned int q_epoch = 0;
@@ -654,8 +654,8 @@ int pa_create(pa_handle* out, int n_q_heads, int n_kv_heads, int head_dim, int p
   h->opt = o;
   h->device = dev;
   h->n_sm = prop.multiProcessorCount;
-  if (cudaMalloc(&h->d_err, sizeof(int)) != cudaSuccess ||
-      cudaMemset(h->d_err, 0, sizeof(int)) != cudaSuccess ||
+  if (cudaMalloc(&h->d_err, kErrWords * sizeof(int)) != cudaSuccess ||
+      cudaMemset(h->d_err, 0, kErrWords * sizeof(int)) != cudaSuccess ||
       cudaEventCreateWithFlags(&h->upload_done, cudaEventDisableTiming) != cudaSuccess) {
     pa_destroy(h);
     return PA_ECUDA;
@@ -947,12 +947,12 @@ int pa_debug_copy_streams_idle(pa_handle h) {
 int pa_last_error(pa_handle h, void* stream) {
   if (!h) return PA_EINVAL;
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return PA_ECUDA;
-  int e = 0;
-  if (cudaMemcpy(&e, h->d_err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return PA_ECUDA;
-  if (e != 0 && cudaMemset(h->d_err, 0, sizeof(int)) != cudaSuccess) return PA_ECUDA;
-  if (e & DEV_ERR_TIMEOUT) return PA_ETIMEOUT;
-  if (e & DEV_ERR_BAD_PAGE) return PA_EBADPAGE;
-  if (e != 0) return PA_ECUDA;
+  int e[kErrWords] = {};
+  if (cudaMemcpy(e, h->d_err, sizeof e, cudaMemcpyDeviceToHost) != cudaSuccess) return PA_ECUDA;
+  if ((e[0] | e[1]) != 0 && cudaMemset(h->d_err, 0, sizeof e) != cudaSuccess) return PA_ECUDA;
+  if (e[0] & DEV_ERR_TIMEOUT) return PA_ETIMEOUT;
+  if (e[0] != 0) return PA_ECUDA;
+  if (e[1] != 0) return PA_EBADPAGE;
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ECUDA;
 }
 

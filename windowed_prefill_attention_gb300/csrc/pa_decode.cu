@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kDecWarps * 32) decode_kernel(const __grid_con
       const int b = x0 + warp + kDecWarps * it - pp.start;
       const int phys = __shfl_sync(0xffffffffu, my_page, it);
       if (phys < 0 || phys >= p.n_pool) {
-        if (lane == 0) atomicCAS(p.err, 0, DEV_ERR_BAD_PAGE);
+        if (lane == 0) record_bad_page(p.err);
       } else {
         const uint32_t kb = slot0 + (uint32_t)(st * kBlockBytes), vb = kb + 2 * kHalfBytes;
         // S^T = K Q^T: keys gq, gq+8 x rows 2tq, 2tq+1.  Dims group j (64 dims,

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kernel(const WidenParams 
   const int row0 = blk * kPage;
   const int phys = p.block_table[(size_t)sg.bt_row * p.bt_stride + kb];
   const bool bad = phys < 0 || phys >= p.n_pool;
-  if (bad && tid == 0) atomicCAS(p.err, 0, DEV_ERR_BAD_PAGE);
+  if (bad && tid == 0) record_bad_page(p.err);
   const int n_valid = bad ? 0 : imax(0, imin(kPage, sg.n_ctx - kb * kPage));
   const size_t page_base = (size_t)(bad ? 0 : phys) * kPage * HKV * kHeadDim;
 
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv_append_kernel(const K
     rv[g] = reinterpret_cast<const uint4*>(p.v_new + (row0 + g) * kHeadDim)[lane];
   }
   if (phys < 0 || phys >= p.n_pool) {  // never dereferenced
-    if (lane == 0) atomicCAS(p.err, 0, DEV_ERR_BAD_PAGE);
+    if (lane == 0) record_bad_page(p.err);
     return;
   }
   const size_t slot0 = ((size_t)phys * kPage + tok % kPage) * HKV;

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kPlanThreads) noalloc_plan_kernel(SeqGeom sg, 
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *seq_out = sg;
-    *err = 0;
+    for (int i = 0; i < kErrWords; ++i) err[i] = 0;
   }
   if (blockIdx.x == 0 && threadIdx.x < HKV) vsmax[threadIdx.x] = 0u;
 }
@@ -287,12 +287,12 @@ extern "C" int pa_prefill_noalloc(int n_q_heads, int n_kv_heads, int n_pool_page
 
   // synchronous: report this call's device-side status, read on `stream`
   // behind the kernels (no other stream is waited for)
-  int e = 0;
-  if (cudaMemcpyAsync(&e, err, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess) return PA_ECUDA;
+  int e[kErrWords] = {};
+  if (cudaMemcpyAsync(e, err, sizeof e, cudaMemcpyDeviceToHost, st) != cudaSuccess) return PA_ECUDA;
   if (cudaStreamSynchronize(st) != cudaSuccess) return PA_ECUDA;
-  if (e & DEV_ERR_TIMEOUT) return PA_ETIMEOUT;
-  if (e & DEV_ERR_BAD_PAGE) return PA_EBADPAGE;
-  return e ? PA_ECUDA : PA_OK;
+  if (e[0] & DEV_ERR_TIMEOUT) return PA_ETIMEOUT;
+  if (e[0] != 0) return PA_ECUDA;
+  return e[1] != 0 ? PA_EBADPAGE : PA_OK;
 }
 
 // Debug export (tests): the work list the last call on the current device

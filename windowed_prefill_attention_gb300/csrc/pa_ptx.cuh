@@ -10,12 +10,18 @@
 
 namespace pa {
 
-// Device error codes written into the caller-visible error word.  The low
-// byte carries the site that gave up, so a timeout names the wait that ran out.
+// Device error codes written into the caller-visible error words.  The first word
+// holds what ends a launch, whose waits give up when it is set (the low byte of a
+// timeout carries the site that gave up, so it names the wait that ran out); the
+// second a bad page entry, which only leaves work out: that launch and those after
+// it go on, and their waits do not look at it.
 enum : int {
   DEV_ERR_TIMEOUT = 0x100,
   DEV_ERR_BAD_PAGE = 0x200,
 };
+constexpr int kErrWords = 2;
+
+__device__ __forceinline__ void record_bad_page(int* err) { atomicCAS(err + 1, 0, DEV_ERR_BAD_PAGE); }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -125,7 +131,7 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
 
 // Where a bounded wait reports, and how long it may spin.
 struct WaitCtl {
-  int* err;           // device error word (0 = fine); first error wins
+  int* err;           // device error words; the first: 0 = fine, first error wins
   uint64_t limit_ns;  // give up after this long
 };
 

@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kQkvWarps * 32, kQkvPerSm) qkv_kernel(const __
     if (kAppend && r1 > p.n_q) {
       phys = __ldg(p.block_table + (size_t)(p.bt_row0 + seq) * p.bt_stride + tok / kPage);
       if (phys < 0 || phys >= p.n_pool) {  // never dereferenced
-        if (lane == 0) atomicCAS(p.err, 0, DEV_ERR_BAD_PAGE);
+        if (lane == 0) record_bad_page(p.err);
         phys = -1;
       }
     }

@@ -485,7 +485,7 @@ __device__ __forceinline__ void role_scales(const SharedParams& p, const SharedS
       const int b = t * kTileBlocks + (lane >> 2);
       const int page = group_page(p, s.grp, b);
       valid = page >= 0;
-      if (!valid && b < s.grp.n_blk && (lane & 3) == 0) atomicCAS(p.err, 0, DEV_ERR_BAD_PAGE);
+      if (!valid && b < s.grp.n_blk && (lane & 3) == 0) record_bad_page(p.err);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const size_t at = ((size_t)(valid ? page : 0) * kPage + 4 * (lane & 3) + e) * p.HKV + s.g;
@@ -1049,7 +1049,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, kShOwnPerSm) own_kernel(const 
     page = __ldg(p.block_table + (lb < p.prefix_blk ? 0 : (size_t)(p.bt_row0 + lo) * p.bt_stride) + lb);
     if (page < 0 || page >= p.n_pool) {
       page = -1;
-      atomicCAS(p.err, 0, DEV_ERR_BAD_PAGE);
+      record_bad_page(p.err);
     }
   }
   const int n_it = b1 > b0 + warp ? (b1 - b0 - warp + kOwnWarps - 1) / kOwnWarps : 0;
