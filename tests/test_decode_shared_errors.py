@@ -1,5 +1,5 @@
-"""GPU: what a bad page entry and an error that was not read do to a shared-prefix
-decode whose units work on one group for a millisecond and more."""
+"""GPU: what a bad page entry, an error that was not read, and a short wait limit do
+to a shared-prefix decode whose units work on one group for a millisecond and more."""
 import numpy as np
 import pytest
 
@@ -104,3 +104,15 @@ def test_long_segments_bad_pages_and_unread_errors(long):
     assert torch.equal(bits(got)[others], bits(want)[others])
     assert torch.isfinite(got).all()
     assert torch.equal(bits(after), bits(want))
+
+
+def test_long_segments_outlast_a_short_wait_limit(long):
+    """The limit bounds a wait for one step of the work, not for a whole group's (1.7 ms here)."""
+    import torch
+    with handle(long) as h:
+        want = long.call(h)
+        assert long.pa.pa_last_error(h) == 0
+    with handle(long, wait_timeout_ms=1) as h:
+        got = long.call(h)
+        assert long.pa.pa_last_error(h) == 0
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))

@@ -160,7 +160,7 @@ constexpr int kStageBytes = 32768;
 constexpr int kSmQ = 0;                             // 4 regions [128 rows][64 dims]
 constexpr int kSmK = 65536;                         // a pair: 2 stages x 4 regions [64 keys][64 dims]; one CTA: 4 regions [128][64]
 constexpr int kSmV = kSmK + 2 * kStageBytes;        // a pair: 2 stages x 2 regions [128 keys][64 dims]; one CTA: 2 x 4 regions [64][64]
-constexpr int kSmScale = kSmV + 2 * kStageBytes;    // [2] x {K scales 128, V scales 128, valid blocks, exponent}
+constexpr int kSmScale = kSmV + 2 * kStageBytes;    // [2] x {K scales 128, V scales 128, valid blocks, exponent, tile}
 constexpr int kScaleSlot = 2 * 512 + 16;
 constexpr int kSmRow = kSmScale + 2 * kScaleSlot;   // [2][128] int8 exponents of the rows' factors, by segment parity
 constexpr int kSmBar = kSmRow + 2 * kRows;
@@ -255,6 +255,32 @@ struct PreCtx {
   // One outcome for the warp.
   __device__ bool wait(int i, uint32_t parity) const {
     return __all_sync(kAllLanes, mbar_wait(bar(i), parity & 1u, wc, 80 + i));
+  }
+  // As wait, for a phase that takes as many tiles as a segment has (131072 keys:
+  // 1024 tiles, 1.7 ms): the limit starts again whenever the scale warp, at most
+  // two tiles ahead of the softmax, has written another pair of tiles' scales.
+  __device__ bool wait_while_tiles_go_on(int i, uint32_t parity) const {
+    auto tile = [&] {
+      uint32_t n;
+      asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(n) : "r"(sb + kSmScale + 1024 + 8));
+      return n;
+    };
+    uint32_t seen = tile();
+    uint64_t t0 = globaltimer_ns();
+    bool ok = false;
+    for (uint32_t k = 1; !(ok = mbar_try_wait_sleep(bar(i), parity & 1u, 20000u)); ++k) {
+      if (k & 31u) continue;
+      if (*reinterpret_cast<volatile int*>(wc.err) != 0) break;
+      const uint32_t now = tile();
+      if (now != seen) {
+        seen = now;
+        t0 = globaltimer_ns();
+      } else if (globaltimer_ns() - t0 > wc.limit_ns) {
+        atomicCAS(wc.err, 0, DEV_ERR_TIMEOUT | ((80 + i) & 0xff));
+        break;
+      }
+    }
+    return __all_sync(kAllLanes, ok);
   }
   // An arrival on the even CTA's barrier that hands over tensor memory (the
   // caller has waited for its tcgen05 accesses and fenced them).
@@ -455,7 +481,7 @@ __device__ __forceinline__ void role_queries(const SharedParams& p, const Shared
   for (int x = c.x0; x < c.x1; ++n_seg) {
     const Segment s = segment_at<kN>(p, tab, c.rank, x, c.x1);
     if (n_seg > 0) {
-      if (!c.wait(B_QE, n_seg - 1)) break;
+      if (!c.wait_while_tiles_go_on(B_QE, n_seg - 1)) break;
       copy_queries(p, tab, c, s, c.sb + kSmK);
       ++copied;
     }
@@ -511,7 +537,7 @@ __device__ __forceinline__ void role_scales(const SharedParams& p, const SharedS
         uint32_t m8 = 0;
 #pragma unroll
         for (int e = 0; e < kTileBlocks; ++e) m8 |= ((ok >> (4 * e)) & 1u) << e;
-        sts128(at + 1024, m8, (uint32_t)ev, 0, 0);
+        sts128(at + 1024, m8, (uint32_t)ev, n_tile, 0);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(c.bar(B_SCF + b));
