@@ -192,10 +192,15 @@ def pa_default_options() -> pa_options:
 _geometry = {}
 
 
+def _address(h):
+    """Address of a handle: a c_void_p (as pa_create gives it) or a plain integer; None for no handle."""
+    return getattr(h, "value", h)
+
+
 def _geometry_of(h):
     try:
-        return _geometry[h.value]
-    except (AttributeError, KeyError):
+        return _geometry[_address(h)]
+    except (KeyError, TypeError):
         raise ValueError("not a live handle") from None
 
 
@@ -212,7 +217,7 @@ def pa_create(n_q_heads, n_kv_heads, n_pool_pages, max_pages_per_seq, head_dim=2
 
 
 def pa_destroy(h) -> None:
-    _geometry.pop(h.value, None)
+    _geometry.pop(_address(h), None)
     _lib.pa_destroy(h)
 
 
