@@ -27,23 +27,25 @@ def append_rows(k, kw, offset, eps, rope=None):
     return kp.view(-1, hkv, 256)[:n].cpu().numpy(), ks.view(-1, hkv)[:n].cpu().numpy()
 
 
-def test_codes_of_a_scale_whose_significand_is_all_ones():
-    """Rows whose values are exact in fp32 (r = 2^-30 by eps = 2^60, gains offset + w): the largest, 127 - 2^-17, has
-    the scale 1 - 2^-24, and a value of 1/2 is then a little more than half a step: code 1, both signs."""
+@pytest.mark.parametrize("half", (45, 46, 50, 60))
+def test_codes_of_a_scale_whose_significand_is_all_ones(half):
+    """Rows whose values are exact in fp32: the gains offset + w are, and r = 2^-half, since eps = 2^(2 half) swallows a
+    mean square under 2^46 (squares of at most (60 2^17)^2 < 2^46).  The largest, 127 - 2^-17 (times r), has the scale
+    1 - 2^-24, and a value of 1/2 is then a little more than half a step: code 1, both signs."""
     offset = -2.0 ** -17
     w = np.zeros(256, np.float32)
     w[0], w[1:9] = 127.0, 2.0 ** -16
     x = np.zeros((7, 3, 256), np.float32)
     x[..., 0] = 1.0
-    # multiples n of 2^16 2^-17: n a half and a bit of steps, or whole steps; and of one gain or the other's sign
+    # halves of a step and a little more, and whole steps, of either sign; then values of the other gain
     x[..., 1:9] = 2.0 ** 16 * np.array([1, -1, 3, -3, 2, 5, -127, 253], np.float32)
     x[..., 9:30] = np.random.default_rng(2).integers(-60, 61, (7, 3, 21)) * 2.0 ** 17
     x = ut.bf16_values(ut.bf16_bits(x)).astype(np.float32)
-    y = (x * (np.float32(offset) + w)) * np.float32(2.0 ** -30)
+    y = (x * (np.float32(offset) + w)) * np.float32(2.0 ** -half)
     y = y.astype(np.float32)
-    codes, scale = append_rows(ut.bf16_bits(x), ut.bf16_bits(w), offset, 2.0 ** 60)
+    codes, scale = append_rows(ut.bf16_bits(x), ut.bf16_bits(w), offset, 2.0 ** (2 * half))
     want_scale = (np.abs(y).max(-1) / np.float32(127)).astype(np.float32)
-    assert np.all(want_scale == np.float32((1 - 2.0 ** -24) * 2.0 ** -30))
+    assert np.all(want_scale == np.float32((1 - 2.0 ** -24) * 2.0 ** -half))
     want = np.rint((y / want_scale[..., None]).astype(np.float32))
     assert np.all(want[..., 1] == 1) and np.all(want[..., 2] == -1)
     assert np.array_equal(scale, want_scale)

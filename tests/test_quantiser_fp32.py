@@ -5,8 +5,8 @@ quotients, without a division.
 * Scale: q0 = RN(a r), r = RN(1/127), q1 = RN(q0 + (a - 127 q0) r) is RN(a / 127)
   for every binary32 significand of a, and where the result is subnormal.
 * Codes: r0 approximates 1/b within a unit in its last place (what the hardware
-  reciprocal is documented to give), r = RN(r0 + r0 RN(1 - r0 b)), its last bit
-  set where b's significand is all ones; q0 = RN(a r), q1 = RN(q0 + (a - q0 b) r).
+  reciprocal is documented to give), r = RN(r0 + r0 RN(1 - r0 b)), q0 = RN(a r),
+  q1 = RN(q0 + (a - q0 b) r).
   r is within (1/2 + 2^-22) units of 1/b, so |1 - b r| < 1.01 2^-25 b (b in
   [1, 2)) and |a/b - q0| < 1.5 units of q0, and q0 + (a - q0 b) r is off by
   (a/b - q0)(1 - b r), under 2^-23 units.  q1 and RN(a / b) therefore differ only
@@ -14,7 +14,9 @@ quotients, without a division.
   different codes only where one of the two is a tie n + 1/2.  The quotients next
   to those middles are a/b = mid + k / (2^j b), k a small integer: with mid =
   M / 2^s the pairs solve A 2^t - M b = k, so b is -k / M modulo 2^t.  All of them
-  with |k| <= 6 (the bound above leaves |k| <= 2) are run through the steps."""
+  with |k| <= 6 (the bound above leaves |k| <= 2) are run through the steps.  One
+  of them hangs on the approximation: 2^23 / (2^24 - 1), which test_qkv_rows.py
+  holds on the GPU."""
 import math
 from fractions import Fraction
 
@@ -54,12 +56,6 @@ def reciprocals(b):
     return out
 
 
-def set_last_bit(r):
-    m = r * 2 ** 47  # r in [2^-24, 2^-23): 24 bits
-    assert m.denominator == 1 and 1 << 23 <= m < 1 << 24
-    return Fraction(m.numerator | 1, 2 ** 47)
-
-
 def quotient(a, b, r):
     q0 = _rn32(a * r)
     rem = a - q0 * b
@@ -92,23 +88,16 @@ def near_pairs(n, k_most=6):
 
 
 def test_codes_are_those_of_the_rounded_quotient():
-    n_pairs, fixed = 0, []
+    n_pairs, hang = 0, set()
     for n in range(128):
         for a, b in near_pairs(n):
             want = _rn32(a / b)
-            ones = b == (1 << 24) - 1
             for r in reciprocals(b):
                 n_pairs += 1
-                if ones and round(quotient(a, b, r)) != round(want):
-                    fixed.append((a, b))
-                assert quotient(a, b, set_last_bit(r) if ones else r) == want, (n, a, b)
+                if quotient(a, b, r) != want:
+                    hang.add((a, b, r < Fraction(1, b)))
     assert n_pairs > 1000
-    # the pair that needs the last bit: 2^23 over all ones, just above 1/2 + 2^-25, is 1, not 0
-    assert fixed == [(Fraction(1 << 23), (1 << 24) - 1)]
-
-
-def test_reciprocal_of_all_ones_is_made_the_rounded_one():
-    """1 / (2^24 - 1) = 2^-24 (1 + 2^-24 + ...) lies just above a middle, and the step ends on either side of it."""
+    # just above 1/2 + 2^-25: 1, but 0 with the reciprocal's lower neighbour, on which the step ends from itself
+    assert hang == {(Fraction(1 << 23), (1 << 24) - 1, True)}
     ones = (1 << 24) - 1
-    assert len(reciprocals(ones)) == 2
-    assert {set_last_bit(r) for r in reciprocals(ones)} == {_rn32(Fraction(1, ones))}
+    assert reciprocals(ones) == {Fraction(1, 1 << 24), _rn32(Fraction(1, ones))}

@@ -152,10 +152,16 @@ __device__ __forceinline__ void make_turn(const QkvParams& p, const __nv_bfloat1
 // N rows into the pool: scale = absmax / 127, codes rint(x / scale) half to
 // even, decided on the IEEE quotients as kv_append_kernel decides them.  Both
 // divisions by Markstein's correction of an approximate quotient: with r near
-// 1/b, q0 = RN(a r), the remainder a - q0 b is exact in one FMA and RN(q0 +
-// remainder r) is RN(a / b).  For the scale r = RN(1/127); for the codes r is the
-// hardware reciprocal after one Newton step (checked for every bf16 absmax and
-// value, with a reciprocal up to an ulp off).  Adding 1.5 * 2^23 rounds a quotient
+// 1/b, q0 = RN(a r), the remainder a - q0 b is exact in one FMA and q1 = RN(q0 +
+// remainder r).  For the scale r = RN(1/127), and q1 = RN(a / 127) for every fp32
+// a.  For the codes r is the hardware reciprocal after one Newton step, within
+// half a place of 1/b and a little more.  q1 is then off by under 2^-23 of its last
+// place before its rounding, and the pairs (a, b) whose quotient comes that near to
+// the border of a tie's neighbourhood are few enough to be listed: all round to the
+// code that RN(a / b) rounds to, whatever approximation within an ulp the step began
+// with, but one: where b's significand is all ones and the step ends below 1/b,
+// a = 2^k would get 0 and not 1.  GB300's reciprocal leads the step above it (both
+// are held by tests).  Adding 1.5 * 2^23 rounds a quotient
 // to an integer, half to even, and leaves the code in the sum's low byte.  A row
 // whose remainders could be subnormal is raised by 2^64 first, its scale too.
 template <int N>
