@@ -246,7 +246,8 @@ int pa_rope_init(pa_rope* rope, int rot_dim, int pairing, int n_axes, const doub
  *   q_weight,
  *   k_weight        device bf16 [256], 16-byte aligned, or NULL: gain 1
  *                   (weight_offset is then not used)
- *   eps             >= 0; a row of zeros with eps 0 gives zeros
+ *   eps             >= 0; a row of zeros with eps 0 gives zeros, any other row its
+ *                   root mean square of 1, down to the smallest subnormals
  *   rope            host struct, or NULL: norm only
  *   positions       device int32 [n_axes][pos_stride], entry t of each axis for
  *                   token t; any int32; NULL only without a rotation

@@ -242,10 +242,28 @@ struct Feed {
   }
 };
 
+// A row whose mean square (with eps) is below this is raised by 2^76, exactly, and
+// eps by its square: the squares of values under 2^-63 leave fp32's normal range.
+// Above it what they lose is nothing to the sum; raised, the sum of squares is under
+// 2^120 and the smallest nonzero square 2^-114.
+constexpr float kTinyMeanSquare = 9.094947017729282e-13f;  // 2^-40
+constexpr float kRaise = 75557863725914323419136.f;        // 2^76
+
+__device__ __forceinline__ void raise_row(uint32_t at) {
+  uint4 w;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at));
+  Vals x = unpack8(w);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x.v[j] = mul2(x.v[j], make_float2(kRaise, kRaise));
+  w = pack8(x);
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+}
+
 // N rows from their slot, normed and turned (kNorm), stored as bf16 (kCodes
-// false; dst: the lane's 16 bytes of the first row) or as codes.
+// false; dst: the lane's 16 bytes of the first row) or as codes.  Rows of which
+// one's mean square is below `least_ok` are left alone (false).
 template <int N, int kTurn, bool kNorm, bool kCodes>
-__device__ __forceinline__ void do_rows(uint32_t src, const Turn& t, int from, float eps, int lane,
+__device__ __forceinline__ bool do_rows(uint32_t src, const Turn& t, int from, float eps, float least_ok, int lane,
                                         uint4* dst, int8_t* codes, float* scales, bool store) {
   uint4 raw[N];
 #pragma unroll
@@ -265,10 +283,16 @@ __device__ __forceinline__ void do_rows(uint32_t src, const Turn& t, int from, f
       ss[i] = s.x + s.y;
     }
     warp_reduce<N, false>(ss, lane);
+    float least = INFINITY;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float ms = fmaf(ss[i], 1.f / kHeadDim, eps);
-      const float r = ms > 0.f ? rsqrtf(ms) : 0.f;  // an all-zero row with eps 0 stays zero
+      ss[i] = fmaf(ss[i], 1.f / kHeadDim, eps);
+      least = fminf(least, ss[i]);
+    }
+    if (least < least_ok) return false;  // the same in all lanes
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float r = ss[i] > 0.f ? rsqrtf(ss[i]) : 0.f;  // an all-zero row with eps 0 stays zero
       Vals xp;
       if (kTurn != TURN_NONE) xp = partners<kTurn>(raw[i], y[i], from);
 #pragma unroll
@@ -288,7 +312,13 @@ __device__ __forceinline__ void do_rows(uint32_t src, const Turn& t, int from, f
 #pragma unroll
     for (int i = 0; i < N; ++i) dst[i * (kHeadDim / 8)] = pack8(y[i]);
   }
+  return true;
 }
+
+template <int N>
+struct Rows {
+  static constexpr int value = N;
+};
 
 // `n` heads from head `a` of one kind of row of a token, the next batches of the feed.
 template <int kTurn, bool kNorm, bool kCodes>
@@ -299,20 +329,34 @@ __device__ __forceinline__ void do_heads(const QkvParams& p, Feed& feed, int a, 
 #pragma unroll 1
   for (; n > 0; n -= 4) {
     feed.fetch(p, lane);
-    uint32_t src = feed.slot();
+    const uint32_t src = feed.slot();
+    // rows i .. of the batch
+    const auto do_some = [&](auto rows, int i, float e, float least_ok) {
+      return do_rows<decltype(rows)::value, kTurn, kNorm, kCodes>(
+          src + 512 * i, t, from, e, least_ok, lane, dst + i * (kHeadDim / 8), codes + (kCodes ? i * kHeadDim : 0),
+          scales + (kCodes ? i : 0), store);
+    };
+    bool done = true;
     if (n >= 4) {
-      do_rows<4, kTurn, kNorm, kCodes>(src, t, from, eps, lane, dst, codes, scales, store);
-      dst += 4 * (kHeadDim / 8);
-      if (kCodes) codes += 4 * kHeadDim, scales += 4;
+      done = do_some(Rows<4>{}, 0, eps, kTinyMeanSquare);
     } else {
-      if (n >= 2) {
-        do_rows<2, kTurn, kNorm, kCodes>(src, t, from, eps, lane, dst, codes, scales, store);
-        src += 2 * 512;
-        dst += 2 * (kHeadDim / 8);
-        if (kCodes) codes += 2 * kHeadDim, scales += 2;
-      }
-      if (n & 1) do_rows<1, kTurn, kNorm, kCodes>(src, t, from, eps, lane, dst, codes, scales, store);
+      if (n >= 2) done = do_some(Rows<2>{}, 0, eps, kTinyMeanSquare);
+      if (n & 1) done &= do_some(Rows<1>{}, n & 2, eps, kTinyMeanSquare);
     }
+    if (__builtin_expect(!done, 0)) {
+#pragma unroll 1
+      for (int i = 0; i < min(n, 4); ++i) {
+        float e = eps, least_ok = kTinyMeanSquare;
+#pragma unroll 1
+        while (!do_some(Rows<1>{}, i, e, least_ok)) {
+          raise_row(src + 512 * i);
+          e = e * kRaise * kRaise;
+          least_ok = -1.f;
+        }
+      }
+    }
+    dst += 4 * (kHeadDim / 8);
+    if (kCodes) codes += 4 * kHeadDim, scales += 4;
   }
 }
 
