@@ -252,8 +252,9 @@ int pa_rope_init(pa_rope* rope, int rot_dim, int pairing, int n_axes, const doub
  *   positions       device int32 [n_axes][pos_stride], entry t of each axis for
  *                   token t; any int32; NULL only without a rotation
  * q_out may be q.data, and k_out k.data, where those rows are contiguous (in
- * place); any other overlap of an output with an input or the other output
- * is PA_EINVAL, as are bad strides, alignment or ranges.  Inputs must be
+ * place); any other overlap of an output with an input (rows, weights,
+ * positions) or the other output is PA_EINVAL, as are bad strides, alignment or
+ * ranges.  Inputs must be
  * finite with |x| < 2^56.  n_tok 0 does nothing.  Asynchronous on `stream`. */
 int pa_qk_norm_rope(pa_handle h, int n_tok, const pa_rows* q, const pa_rows* k, const void* q_weight,
                     const void* k_weight, float weight_offset, float eps, const pa_rope* rope,
@@ -275,7 +276,9 @@ int pa_qk_norm_rope(pa_handle h, int n_tok, const pa_rows* q, const pa_rows* k, 
  * Sequences must not share rows (PA_EINVAL) nor the pages they write (the
  * slot's contents are then undefined).  A page entry outside the pool is never
  * dereferenced: the token's K and V are skipped and pa_last_error reports
- * PA_EBADPAGE.  Other errors and requirements as pa_qk_norm_rope and
+ * PA_EBADPAGE.  q_out, the pools and the scales must not overlap each other, the
+ * block table's rows or any other input but the query rows in place (PA_EINVAL).
+ * Other errors and requirements as pa_qk_norm_rope and
  * pa_kv_append; n_seq 0 does nothing.  Asynchronous on `stream`. */
 int pa_qkv_append(pa_handle h, int n_seq, const pa_seq* seqs, const pa_rows* q, const pa_rows* k, const pa_rows* v,
                   const void* q_weight, const void* k_weight, float weight_offset, float eps, const pa_rope* rope,
@@ -442,7 +445,8 @@ int pa_debug_qcodes(const void* q_rows, int n_rows, int8_t* codes, float* scales
 
 /* Debug (tests), host-only, no GPU needed: what pa_qk_norm_rope and
  * pa_qkv_append say of their arguments (PA_OK or PA_EINVAL) on a handle of
- * these shapes; no pointer but those to host structs is read. */
+ * these shapes; the form with n_pool_pages also of overlaps with the pools, whose
+ * size the other does not know; no pointer but those to host structs is read. */
 int pa_debug_qk_norm_rope_check(int n_q_heads, int n_kv_heads, int n_tok, const pa_rows* q, const pa_rows* k,
                                 const void* q_weight, const void* k_weight, float weight_offset, float eps,
                                 const pa_rope* rope, const int32_t* positions, long long pos_stride, void* q_out,
@@ -452,6 +456,12 @@ int pa_debug_qkv_append_check(int n_q_heads, int n_kv_heads, int max_pages_per_s
                               const void* k_weight, float weight_offset, float eps, const pa_rope* rope,
                               const int32_t* positions, long long pos_stride, const int32_t* block_table,
                               int8_t* k_pool, int8_t* v_pool, float* k_scale, float* v_scale, void* q_out);
+int pa_debug_qkv_append_pool_check(int n_q_heads, int n_kv_heads, int n_pool_pages, int max_pages_per_seq, int n_seq,
+                                   const pa_seq* seqs, const pa_rows* q, const pa_rows* k, const pa_rows* v,
+                                   const void* q_weight, const void* k_weight, float weight_offset, float eps,
+                                   const pa_rope* rope, const int32_t* positions, long long pos_stride,
+                                   const int32_t* block_table, int8_t* k_pool, int8_t* v_pool, float* k_scale,
+                                   float* v_scale, void* q_out);
 
 /* Allocation-free variant of pa_prefill (one sequence, default
  * containers).  The pages have no counterpart of this entry point: it exists

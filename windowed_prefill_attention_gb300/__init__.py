@@ -37,6 +37,7 @@ EXPORTED = ("pa_default_options", "pa_create", "pa_destroy", "pa_prefill", "pa_p
             "pa_debug_gather",
             "pa_debug_maskset", "pa_debug_qcodes", "pa_debug_copy_streams_idle", "pa_prefill_noalloc",
             "pa_debug_noalloc_units", "pa_debug_qk_norm_rope_check", "pa_debug_qkv_append_check",
+            "pa_debug_qkv_append_pool_check",
             "pa_debug_decode_shared_pass")
 
 
@@ -78,6 +79,7 @@ _lib.pa_qkv_append.argtypes = ([_vp, _i, _vp] + [C.POINTER(pa_rows)] * 3
                                + [_vp, _vp, _f, _f, C.POINTER(pa_rope), _vp, _ll] + [_vp] * 7)
 _lib.pa_debug_qk_norm_rope_check.argtypes = [_i, _i] + _lib.pa_qk_norm_rope.argtypes[1:-1]
 _lib.pa_debug_qkv_append_check.argtypes = [_i, _i, _i] + _lib.pa_qkv_append.argtypes[1:-1]
+_lib.pa_debug_qkv_append_pool_check.argtypes = [_i, _i, _i, _i] + _lib.pa_qkv_append.argtypes[1:-1]
 _lib.pa_decode.argtypes = _lib.pa_prefill_batch.argtypes
 _lib.pa_decode_shared.argtypes = [_vp, _i, _vp, _i, _i] + [_vp] * 6 + [_i, _i, _f, _vp, _vp]
 _lib.pa_decode_shared_plan.argtypes = ([_i] * 5 + [C.POINTER(pa_seq)] + [_i] * 4

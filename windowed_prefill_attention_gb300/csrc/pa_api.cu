@@ -1153,6 +1153,8 @@ bool rope_ok(const pa_rope* r) {
 // indexes, gains, eps, rotation, positions, the query's output.
 struct QkvSpans {
   Span q, k, q_out;
+  Span qw, kw, pos;  // empty where the kernel reads none
+  bool read_beside_rows(const Span& out) const { return out.meets(qw) || out.meets(kw) || out.meets(pos); }
 };
 struct Heads {
   int HQ, HKV;
@@ -1185,10 +1187,15 @@ int qkv_common(const Heads& h, long long tokens, const pa_rows* q, const pa_rows
     p.rope = *rope;
   }
   if (p.rope.rot_dim > 0 && pos) {
-    if (!aligned(pos, 4) || pos_stride < 0 || (p.rope.n_axes > 1 && pos_stride < tokens)) return PA_EINVAL;
+    if (!aligned(pos, 4) || pos_stride < 0 || (p.rope.n_axes > 1 && (pos_stride < tokens || pos_stride > 1ll << 46)))
+      return PA_EINVAL;
     p.pos = pos;
     p.pos_stride = pos_stride;
+    sp.pos = span_of(pos, (size_t)((p.rope.n_axes - 1) * pos_stride + tokens) * sizeof(int32_t));
   }
+  if (q && qw) sp.qw = span_of(qw, kHeadDim * 2);
+  if (k && kw) sp.kw = span_of(kw, kHeadDim * 2);
+  if (q && sp.read_beside_rows(sp.q_out)) return PA_EINVAL;
   p.q_out = static_cast<__nv_bfloat16*>(q_out);
   return PA_OK;
 }
@@ -1219,7 +1226,7 @@ int qk_norm_rope_args(const Heads& h, int n_tok, const pa_rows* q, const pa_rows
     if (!aligned(k_out, 16)) return PA_EINVAL;
     const Span ko = span_of(k_out, (size_t)n_tok * h.HKV * kHeadDim * 2);
     if (!out_ok(ko, sp.k, p.k, h.HKV, n_tok)) return PA_EINVAL;
-    if (q && (ko.meets(sp.q) || ko.meets(sp.q_out))) return PA_EINVAL;
+    if ((q && (ko.meets(sp.q) || ko.meets(sp.q_out))) || sp.read_beside_rows(ko)) return PA_EINVAL;
     p.k_out = static_cast<__nv_bfloat16*>(k_out);
   }
   p.n_tok = n_tok;
@@ -1227,7 +1234,8 @@ int qk_norm_rope_args(const Heads& h, int n_tok, const pa_rows* q, const pa_rows
 }
 
 // Arguments of pa_qkv_append (n_seq >= 1) -> the kernel's parameters, but for each launch's sequences.
-int qkv_append_args(const Heads& h, int max_pages, int n_seq, const pa_seq* seqs, const pa_rows* q, const pa_rows* k,
+// n_pool 0: the pools' sizes are not known, and overlaps with them not looked for.
+int qkv_append_args(const Heads& h, int n_pool, int max_pages, int n_seq, const pa_seq* seqs, const pa_rows* q, const pa_rows* k,
                     const pa_rows* v, const void* qw, const void* kw, float w_off, float eps, const pa_rope* rope,
                     const int32_t* pos, long long pos_stride, const int32_t* bt, int8_t* kp, int8_t* vp, float* ksc,
                     float* vsc, void* q_out, QkvParams& p) {
@@ -1248,6 +1256,20 @@ int qkv_append_args(const Heads& h, int max_pages, int n_seq, const pa_seq* seqs
   if (rc) return rc;
   Span vs;
   if (!rows_ok(v, tokens, h.HKV, p.v, vs) || (q && sp.q_out.meets(vs))) return PA_EINVAL;
+  const Span table = span_of(bt, (size_t)n_seq * max_pages * sizeof(int32_t));
+  if (q && sp.q_out.meets(table)) return PA_EINVAL;
+  if (n_pool > 0) {
+    const size_t slots = (size_t)n_pool * kPage * h.HKV;
+    const Span pool[4] = {span_of(kp, slots * kHeadDim), span_of(vp, slots * kHeadDim), span_of(ksc, slots * sizeof(float)),
+                          span_of(vsc, slots * sizeof(float))};
+    for (int i = 0; i < 4; ++i) {
+      const Span& w = pool[i];
+      if (w.meets(sp.q) || w.meets(sp.k) || w.meets(vs) || w.meets(table) || sp.read_beside_rows(w)) return PA_EINVAL;
+      if (w.meets(sp.q_out)) return PA_EINVAL;
+      for (int j = 0; j < i; ++j)
+        if (w.meets(pool[j])) return PA_EINVAL;
+    }
+  }
   p.n_v = h.HKV;
   p.block_table = bt;
   p.bt_stride = max_pages;
@@ -1318,7 +1340,7 @@ int pa_qkv_append(pa_handle h, int n_seq, const pa_seq* seqs, const pa_rows* q, 
   if (!h || n_seq < 0) return PA_EINVAL;
   if (n_seq == 0) return PA_OK;
   QkvParams p{};
-  const int rc = qkv_append_args(Heads{h->HQ, h->HKV}, h->max_pages, n_seq, seqs, q, k, v, q_weight, k_weight,
+  const int rc = qkv_append_args(Heads{h->HQ, h->HKV}, h->n_pool, h->max_pages, n_seq, seqs, q, k, v, q_weight, k_weight,
                                  weight_offset, eps, rope, positions, pos_stride, block_table, k_pool, v_pool,
                                  k_scale, v_scale, q_out, p);
   if (rc) return rc;
@@ -1356,17 +1378,28 @@ int pa_debug_qk_norm_rope_check(int n_q_heads, int n_kv_heads, int n_tok, const 
                            positions, pos_stride, q_out, k_out, p);
 }
 
+int pa_debug_qkv_append_pool_check(int n_q_heads, int n_kv_heads, int n_pool_pages, int max_pages_per_seq, int n_seq,
+                                   const pa_seq* seqs, const pa_rows* q, const pa_rows* k, const pa_rows* v,
+                                   const void* q_weight, const void* k_weight, float weight_offset, float eps,
+                                   const pa_rope* rope, const int32_t* positions, long long pos_stride,
+                                   const int32_t* block_table, int8_t* k_pool, int8_t* v_pool, float* k_scale,
+                                   float* v_scale, void* q_out) {
+  if (!heads_ok(n_q_heads, n_kv_heads) || n_seq < 0 || n_pool_pages < 0) return PA_EINVAL;
+  if (n_seq == 0) return PA_OK;
+  QkvParams p{};
+  return qkv_append_args(Heads{n_q_heads, n_kv_heads}, n_pool_pages, max_pages_per_seq, n_seq, seqs, q, k, v, q_weight,
+                         k_weight, weight_offset, eps, rope, positions, pos_stride, block_table, k_pool, v_pool, k_scale,
+                         v_scale, q_out, p);
+}
+
 int pa_debug_qkv_append_check(int n_q_heads, int n_kv_heads, int max_pages_per_seq, int n_seq, const pa_seq* seqs,
                               const pa_rows* q, const pa_rows* k, const pa_rows* v, const void* q_weight,
                               const void* k_weight, float weight_offset, float eps, const pa_rope* rope,
                               const int32_t* positions, long long pos_stride, const int32_t* block_table,
                               int8_t* k_pool, int8_t* v_pool, float* k_scale, float* v_scale, void* q_out) {
-  if (!heads_ok(n_q_heads, n_kv_heads) || n_seq < 0) return PA_EINVAL;
-  if (n_seq == 0) return PA_OK;
-  QkvParams p{};
-  return qkv_append_args(Heads{n_q_heads, n_kv_heads}, max_pages_per_seq, n_seq, seqs, q, k, v, q_weight, k_weight,
-                         weight_offset, eps, rope, positions, pos_stride, block_table, k_pool, v_pool, k_scale,
-                         v_scale, q_out, p);
+  return pa_debug_qkv_append_pool_check(n_q_heads, n_kv_heads, 0, max_pages_per_seq, n_seq, seqs, q, k, v, q_weight,
+                                        k_weight, weight_offset, eps, rope, positions, pos_stride, block_table, k_pool,
+                                        v_pool, k_scale, v_scale, q_out);
 }
 
 namespace {
