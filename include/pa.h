@@ -203,8 +203,8 @@ int pa_kv_append(pa_handle h, const void* k_new, const void* v_new, int n_new, i
  * by the angle a = position[axis[i]] * inv_freq[i],
  *   (y1, y2) -> (y1 cos a - y2 sin a, y2 cos a + y1 sin a).
  * All in fp32, rounded to bf16 once at the end; the angle is reduced to a
- * fraction of a turn in 64-bit integers, so it is as exact at position 2^31 as
- * at 0.  Several axes: positions of time, height and width for images and
+ * fraction of a turn in 64-bit integers, off by 2^-65 of a turn a position (at
+ * position 2^31, 7e-10 rad), whatever the frequency.  Several axes: positions of time, height and width for images and
  * video, each pair following the axis its table names. */
 #define PA_ROPE_HALF 0
 #define PA_ROPE_ADJACENT 1
@@ -234,7 +234,7 @@ typedef struct {
 /* Host-only.  rot_dim: a multiple of 16 in [0, 256].  inv_freq (host, rot_dim/2
  * entries): radians per position.  pair_axis (host, rot_dim/2 entries; NULL:
  * all 0): the axis of each pair, in [0, n_axes).  PA_EINVAL for anything else,
- * or a frequency that is not finite. */
+ * or a frequency that is not below 2^64 in magnitude. */
 int pa_rope_init(pa_rope* rope, int rot_dim, int pairing, int n_axes, const double* inv_freq,
                  const int32_t* pair_axis);
 

@@ -1294,6 +1294,35 @@ bool heads_ok(int HQ, int HKV) {  // pa_create's requirements
 }
 }  // namespace
 
+namespace {
+// inv_freq / (2 pi) modulo 1, times 2^64, to the nearest integer (|inv_freq| < 2^64):
+// the double's 53 bits times 1 / (2 pi) to 256 bits, from which 2^64 takes 117 at most.
+uint64_t turn_of(double inv_freq) {
+  static constexpr uint64_t kInv2Pi[4] = {0x28be60db9391054aull, 0x7f09d5f47d4d3770ull, 0x36d8a5664f10e410ull,
+                                          0x7f9458eaf7aef158ull};  // 2^-64, 2^-128, ...
+  int e = 0;
+  const uint64_t m = (uint64_t)std::ldexp(std::frexp(std::fabs(inv_freq), &e), 53);
+  e -= 53;  // |inv_freq| = m 2^e
+  uint64_t p[6] = {};  // m times the 256-bit integer, lowest word first
+  unsigned __int128 carry = 0;
+  for (int i = 0; i < 4; ++i) {
+    carry += (unsigned __int128)m * kInv2Pi[3 - i];
+    p[i] = (uint64_t)carry;
+    carry >>= 64;
+  }
+  p[4] = (uint64_t)carry;
+  // the turns are p 2^(e - 256): their fraction's first 64 bits, and the next one to round by
+  const int s = 192 - e;  // at least 181
+  auto bits64 = [&](int at) -> uint64_t {
+    const int w = at >> 6, b = at & 63;
+    if (w > 4) return 0;
+    return p[w] >> b | (b ? p[w + 1] << (64 - b) : 0);
+  };
+  const uint64_t turn = bits64(s) + (bits64(s - 1) & 1);
+  return inv_freq < 0.0 ? 0 - turn : turn;
+}
+}  // namespace
+
 int pa_rope_init(pa_rope* rope, int rot_dim, int pairing, int n_axes, const double* inv_freq,
                  const int32_t* pair_axis) {
   if (!rope || rot_dim < 0 || rot_dim > kHeadDim || rot_dim % 16 || n_axes < 1 || n_axes > PA_ROPE_MAX_AXES ||
@@ -1306,12 +1335,9 @@ int pa_rope_init(pa_rope* rope, int rot_dim, int pairing, int n_axes, const doub
   r.n_axes = n_axes;
   for (int i = 0; i < rot_dim / 2; ++i) {
     const int a = pair_axis ? pair_axis[i] : 0;
-    if (a < 0 || a >= n_axes || !std::isfinite(inv_freq[i])) return PA_EINVAL;
+    if (a < 0 || a >= n_axes || !(std::fabs(inv_freq[i]) < 18446744073709551616.0)) return PA_EINVAL;  // 2^64; NaN
     r.axis[i] = (uint8_t)a;
-    // whole turns drop out; the fraction of one, times 2^64 (exact: a power of two)
-    const double turns = inv_freq[i] / 6.283185307179586476925286766559;
-    const double frac = turns - std::floor(turns);
-    r.turn[i] = frac < 1.0 ? (uint64_t)std::ldexp(frac, 64) : 0u;
+    r.turn[i] = turn_of(inv_freq[i]);
   }
   *rope = r;
   return PA_OK;

@@ -11,9 +11,10 @@
 //
 // The angle: a position times a frequency in fp32 would be off by 2^-24 of
 // the angle (0.01 rad at 10^5 rad).  The frequency is held in turns as a
-// 64-bit binary fraction F instead; position * F mod 2^64 is the exact
-// fraction of a turn, in one integer product, and the sine and cosine are
-// taken of that fraction (|x| <= 1 half turn, error 2^-25 of one).
+// 64-bit binary fraction F instead, rounded to the nearest from the double;
+// position * F mod 2^64 is the fraction of a turn, in one integer product, off
+// by 2^-65 a position (2^-34 of a turn at position 2^31), and the sine and cosine
+// are taken of that fraction (|x| <= 1 half turn, error 2^-25 of one).
 //
 // Bound by memory: 512 bytes read and 512 written per query row (K and V rows
 // of the append: 512 read, 260 written).
