@@ -99,6 +99,10 @@ void pa_default_options(pa_options* opt);
 int pa_create(pa_handle* h, int n_q_heads, int n_kv_heads, int head_dim, int page_size, int n_pool_pages,
               int max_pages_per_seq, const pa_options* opt);
 
+/* Index of the CUDA device that the handle is bound to; -1 for NULL.  Every
+ * pointer a call takes for device memory, and its stream, are that device's. */
+int pa_device(pa_handle h);
+
 /* Release the handle and its workspace (synchronises the device). */
 void pa_destroy(pa_handle h);
 

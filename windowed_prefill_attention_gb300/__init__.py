@@ -30,7 +30,7 @@ PA_Q_BF16, PA_Q_INT8 = 0, 1
 PA_P_F16, PA_P_U8 = 0, 1
 PA_ROPE_HALF, PA_ROPE_ADJACENT, PA_ROPE_MAX_AXES = 0, 1, 4
 
-EXPORTED = ("pa_default_options", "pa_create", "pa_destroy", "pa_prefill", "pa_prefill_batch",
+EXPORTED = ("pa_default_options", "pa_create", "pa_device", "pa_destroy", "pa_prefill", "pa_prefill_batch",
             "pa_prefill_batch_gated", "pa_prefill_host", "pa_kv_append", "pa_rope_init", "pa_qk_norm_rope",
             "pa_qkv_append", "pa_decode", "pa_decode_shared", "pa_decode_shared_plan",
             "pa_last_error", "pa_timing", "pa_strerror", "pa_plan", "pa_plan_pairs", "pa_host_chunks", "pa_decode_plan",
@@ -85,6 +85,7 @@ _lib.pa_decode_shared.argtypes = [_vp, _i, _vp, _i, _i] + [_vp] * 6 + [_i, _i, _
 _lib.pa_decode_shared_plan.argtypes = ([_i] * 5 + [C.POINTER(pa_seq)] + [_i] * 4
                                        + [_vp, _i, C.POINTER(_i), _vp, _i, C.POINTER(_i)])
 _lib.pa_debug_decode_shared_pass.argtypes = [_vp, _i]
+_lib.pa_device.argtypes = [_vp]
 _lib.pa_last_error.argtypes = [_vp, _vp]
 _lib.pa_timing.argtypes = [_vp, _i, C.POINTER(C.c_double), C.POINTER(C.c_double), C.POINTER(_i)]
 _lib.pa_strerror.argtypes = [_i]
@@ -190,7 +191,7 @@ def pa_default_options() -> pa_options:
     return o
 
 
-# (q heads, kv heads, pool pages, pages per sequence) of the live handles, for the calls that check their tensors
+# (q heads, kv heads, pool pages, pages per sequence, device) of the live handles, for the calls that check their tensors
 _geometry = {}
 
 
@@ -214,8 +215,13 @@ def pa_create(n_q_heads, n_kv_heads, n_pool_pages, max_pages_per_seq, head_dim=2
     h = C.c_void_p()
     _check(_lib.pa_create(C.byref(h), n_q_heads, n_kv_heads, head_dim, page_size, n_pool_pages, max_pages_per_seq,
                           C.byref(o)), "pa_create")
-    _geometry[h.value] = (n_q_heads, n_kv_heads, n_pool_pages, max_pages_per_seq)
+    _geometry[h.value] = (n_q_heads, n_kv_heads, n_pool_pages, max_pages_per_seq, pa_device(h))
     return h
+
+
+def pa_device(h) -> int:
+    """Index of the CUDA device the handle is bound to (-1: no handle)."""
+    return _lib.pa_device(h)
 
 
 def pa_destroy(h) -> None:
@@ -266,16 +272,17 @@ def pa_decode(h, seqs, q, k_pool, v_pool, k_scale, v_scale, block_table, n_sink_
 def pa_decode_shared(h, seqs, n_prefix, q, k_pool, v_pool, k_scale, v_scale, block_table, n_sink_blk, n_win_blk,
                      sm_scale, out, stream=None) -> None:
     """pa_decode for sequences that share their first n_prefix tokens (the pages of block_table row 0).  seqs as
-    pa_qkv_append takes them; stream None: the current one of q's device."""
+    pa_qkv_append takes them; stream None: the current one of the handle's device."""
     geometry = _geometry_of(h)
+    device = geometry[4]
     bf16, _, _, _, raw_stream = _torch()
     s, n_seq = _seq_array(seqs)
     rows = (q.shape[0], geometry[0], 256)
     bt, kp, vp, ks, vs = _pool_args(geometry, n_seq, block_table, k_pool, v_pool, k_scale, v_scale)
     _check(_lib.pa_decode_shared(
-        h, n_seq, s.ctypes.data, n_prefix, rows[0], _array(q, bf16, rows, "q"), kp, vp, ks, vs, bt, n_sink_blk,
-        n_win_blk, sm_scale, _array(out, bf16, rows, "out"),
-        raw_stream(q.get_device()) if stream is None else stream.cuda_stream), "pa_decode_shared")
+        h, n_seq, s.ctypes.data, n_prefix, rows[0], _array(q, bf16, rows, "q", device), kp, vp, ks, vs, bt, n_sink_blk,
+        n_win_blk, sm_scale, _array(out, bf16, rows, "out", device),
+        raw_stream(device) if stream is None else stream.cuda_stream), "pa_decode_shared")
 
 
 def pa_kv_append(h, k_new, v_new, tok_start, block_table_row, k_pool, v_pool, k_scale, v_scale,
@@ -304,48 +311,52 @@ def pa_rope_init(inv_freq, pairing=PA_ROPE_HALF, pair_axis=None) -> pa_rope:
     return r
 
 
-def _wrong(t, dtype, shape, name, what="contiguous"):
+def _wrong(t, dtype, shape, name, device, what="contiguous"):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         return TypeError("%s must be a CUDA tensor" % name)
     if t.dtype != dtype:
         return TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.get_device() != device:
+        return ValueError("%s must be on the handle's device %d, got %d" % (name, device, t.get_device()))
     return ValueError("%s must be %s and %s, got %s with strides %s" % (name, what, tuple(shape), tuple(t.shape), t.stride()))
 
 
-def _array(t, dtype, shape, name):
-    """Address of a contiguous CUDA tensor of this type and shape."""
+def _array(t, dtype, shape, name, device):
+    """Address of a contiguous CUDA tensor of this type and shape on this device."""
     try:
-        if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+        if t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
-    raise _wrong(t, dtype, shape, name)
+    raise _wrong(t, dtype, shape, name, device)
 
 
-def _rows(t, bf16, shape, name):
+def _rows(t, bf16, shape, name, device):
     """bf16 rows [token, head, 256] at any strides (the 256 values of a row contiguous)."""
     try:
-        if t.dtype is bf16 and t.is_cuda and t.shape == shape:
+        if t.dtype is bf16 and t.get_device() == device and t.shape == shape:
             ts, hs, one = t.stride()
             if one == 1:
                 return pa_rows(t.data_ptr(), shape[0], ts, hs)
     except AttributeError:
         pass
-    raise _wrong(t, bf16, shape, name, "with contiguous rows")
+    raise _wrong(t, bf16, shape, name, device, "with contiguous rows")
 
 
-def _gain(w, bf16, name):
-    return None if w is None else _array(w, bf16, (256,), name)
+def _gain(w, bf16, name, device):
+    return None if w is None else _array(w, bf16, (256,), name, device)
 
 
-def _positions(positions, rope, tokens, int32):
+def _positions(positions, rope, tokens, int32, device):
     """int32 [tokens] or [axes, tokens] -> address and row stride."""
     if positions is None:
         return None, 0
     shape, stride = positions.shape, positions.stride()
     if positions.dtype is not int32 or not positions.is_cuda:
         raise TypeError("positions must be a CUDA int32 tensor")
+    if positions.get_device() != device:
+        raise ValueError("positions must be on the handle's device %d, got %d" % (device, positions.get_device()))
     n_axes = shape[0] if len(shape) == 2 else 1
     if len(shape) not in (1, 2) or shape[-1] < tokens or (stride[-1] != 1 and shape[-1] > 1):
         raise ValueError("positions must be [tokens] or [axes, tokens], contiguous along the tokens")
@@ -357,34 +368,35 @@ def _positions(positions, rope, tokens, int32):
 def _pool_args(geometry, n_seq, block_table, k_pool, v_pool, k_scale, v_scale):
     """Addresses of the block table, pools and scales, of the handle's shapes."""
     _, f32, int8, int32, _ = _torch()
-    _, hkv, n_pool, max_pages = geometry
+    _, hkv, n_pool, max_pages, device = geometry
     if block_table.shape[0] < n_seq:
         raise ValueError("block_table must have a row for each sequence")
     rows, scales = (n_pool, 16, hkv, 256), (n_pool, 16, hkv)
-    return (_array(block_table, int32, (block_table.shape[0], max_pages), "block_table"),
-            _array(k_pool, int8, rows, "k_pool"), _array(v_pool, int8, rows, "v_pool"),
-            _array(k_scale, f32, scales, "k_scale"), _array(v_scale, f32, scales, "v_scale"))
+    return (_array(block_table, int32, (block_table.shape[0], max_pages), "block_table", device),
+            _array(k_pool, int8, rows, "k_pool", device), _array(v_pool, int8, rows, "v_pool", device),
+            _array(k_scale, f32, scales, "k_scale", device), _array(v_scale, f32, scales, "v_scale", device))
 
 
 def pa_qk_norm_rope(h, q, k, q_weight, k_weight, eps, rope, positions, q_out, k_out, weight_offset=0.0,
                     stream=None) -> None:
     """Norm and rotate query rows q [tokens, HQ, 256] into q_out and key rows k [tokens, HKV, 256] into k_out
     (contiguous; q or k None leaves that kind out).  rope: a pa_rope, or None for the norm alone; positions
-    int32 [tokens] or [axes, tokens].  stream None: the current one of the rows' device."""
+    int32 [tokens] or [axes, tokens].  stream None: the current one of the handle's device."""
     some = k if q is None else q
     if some is None:
         raise ValueError("q or k is needed")
-    hq, hkv, _, _ = _geometry_of(h)
+    hq, hkv, _, _, device = _geometry_of(h)
     bf16, _, _, int32, raw_stream = _torch()
     n = some.shape[0]
     qs, ks = (n, hq, 256), (n, hkv, 256)
-    pos, pos_stride = _positions(positions, rope, n, int32)
+    pos, pos_stride = _positions(positions, rope, n, int32, device)
     _check(_lib.pa_qk_norm_rope(
-        h, n, None if q is None else _rows(q, bf16, qs, "q"), None if k is None else _rows(k, bf16, ks, "k"),
-        _gain(q_weight, bf16, "q_weight"), _gain(k_weight, bf16, "k_weight"), weight_offset, eps, rope, pos,
-        pos_stride, None if q is None else _array(q_out, bf16, qs, "q_out"),
-        None if k is None else _array(k_out, bf16, ks, "k_out"),
-        raw_stream(some.get_device()) if stream is None else stream.cuda_stream), "pa_qk_norm_rope")
+        h, n, None if q is None else _rows(q, bf16, qs, "q", device),
+        None if k is None else _rows(k, bf16, ks, "k", device), _gain(q_weight, bf16, "q_weight", device),
+        _gain(k_weight, bf16, "k_weight", device), weight_offset, eps, rope, pos, pos_stride,
+        None if q is None else _array(q_out, bf16, qs, "q_out", device),
+        None if k is None else _array(k_out, bf16, ks, "k_out", device),
+        raw_stream(device) if stream is None else stream.cuda_stream), "pa_qk_norm_rope")
 
 
 def pa_qkv_append(h, seqs, q, k, v, q_weight, k_weight, eps, rope, positions, block_table, k_pool, v_pool, k_scale,
@@ -392,20 +404,20 @@ def pa_qkv_append(h, seqs, q, k, v, q_weight, k_weight, eps, rope, positions, bl
     """The new tokens of a batch of sequences (seqs: (q_off, q_start, n_q, n_ctx) each, an int32 array is taken as it
     is; rows q_off .. q_off + n_q of q, k, v): queries normed and rotated into q_out, keys normed, rotated and
     quantised, values quantised into the pool.  positions None: the tokens' own; q None (with q_out None): keys and
-    values only."""
+    values only.  stream None: the current one of the handle's device."""
     geometry = _geometry_of(h)
-    hq, hkv, _, _ = geometry
+    hq, hkv, _, _, device = geometry
     bf16, _, _, int32, raw_stream = _torch()
     s, n_seq = _seq_array(seqs)
     n = k.shape[0]
-    pos, pos_stride = _positions(positions, rope, n, int32)
+    pos, pos_stride = _positions(positions, rope, n, int32, device)
     _check(_lib.pa_qkv_append(
-        h, n_seq, s.ctypes.data, None if q is None else _rows(q, bf16, (n, hq, 256), "q"),
-        _rows(k, bf16, (n, hkv, 256), "k"), _rows(v, bf16, (n, hkv, 256), "v"),
-        _gain(q_weight, bf16, "q_weight"), _gain(k_weight, bf16, "k_weight"), weight_offset, eps, rope, pos,
-        pos_stride, *_pool_args(geometry, n_seq, block_table, k_pool, v_pool, k_scale, v_scale),
-        None if q is None else _array(q_out, bf16, (n, hq, 256), "q_out"),
-        raw_stream(k.get_device()) if stream is None else stream.cuda_stream), "pa_qkv_append")
+        h, n_seq, s.ctypes.data, None if q is None else _rows(q, bf16, (n, hq, 256), "q", device),
+        _rows(k, bf16, (n, hkv, 256), "k", device), _rows(v, bf16, (n, hkv, 256), "v", device),
+        _gain(q_weight, bf16, "q_weight", device), _gain(k_weight, bf16, "k_weight", device), weight_offset, eps, rope,
+        pos, pos_stride, *_pool_args(geometry, n_seq, block_table, k_pool, v_pool, k_scale, v_scale),
+        None if q is None else _array(q_out, bf16, (n, hq, 256), "q_out", device),
+        raw_stream(device) if stream is None else stream.cuda_stream), "pa_qkv_append")
 
 
 def pa_prefill_host(h, seqs, q, k_pool, v_pool, k_scale, v_scale, block_table, n_sink_blk, n_win_blk, sm_scale,

@@ -664,6 +664,8 @@ int pa_create(pa_handle* out, int n_q_heads, int n_kv_heads, int head_dim, int p
   return PA_OK;
 }
 
+int pa_device(pa_handle h) { return h ? h->device : -1; }
+
 void pa_destroy(pa_handle h) {
   if (!h) return;
   cudaDeviceSynchronize();
