@@ -334,7 +334,8 @@ int pa_decode_plan(int n_kv_heads, int slots, int n_seq, const pa_seq* seqs, int
  * each sequence's own keys are computed as pa_decode does, and the parts are
  * merged.  Where few sequences or a short prefix make that the slower way, by
  * sizes alone, each sequence reads the prefix too.  The result is pa_decode's on the same keys, but for the order of
- * sums and the roundings of P' to fp16.
+ * sums and the roundings of P' to fp16 (as in pa_decode, the handle's q_mode and
+ * p_mode have no say).
  *   block_table   row s holds sequence s's pages; the prefix's pages are those
  *                 of row 0, and the other rows' entries for it are not read
  *   n_rows        rows of q and out; a sequence's row outside them is PA_EINVAL

@@ -42,7 +42,9 @@ struct QkvParams {
 // Sequences of one append launch, carried in its parameters: {first row, first
 // position, tokens of the launch's earlier sequences, 0}.
 constexpr int kQkvSeqs = 512;
-constexpr int kQkvFewSeqs = 16;  // a smaller table for the common small batches (fewer parameter bytes to launch)
+// A smaller table for the common small batches, 256 bytes of parameters and not 8 KB: one call, waited for, of one to
+// 16 sequences takes 27.6 us, with the large one 28.5; among others, and on the device, both take the same.
+constexpr int kQkvFewSeqs = 16;
 template <int N>
 struct QkvSeqs {
   int4 s[N];

@@ -148,7 +148,8 @@ constexpr int kScaleWarp = kIssueWarp + 1;          // warp 17: the tiles' scale
 constexpr int kQueryWarp = kIssueWarp + 3;          // warp 19: copies the queries in; odd CTA: forwards them
 constexpr int kPreThreads = 32 * (kQueryWarp + 1);
 // Registers a thread, of the 96 each is launched with (65536 / 640): in units
-// of a warp's, 8 x 112 + 8 x 96 + 4 x 64 = 20 x 96.
+// of a warp's, 8 x 112 + 8 x 96 + 4 x 64 = 20 x 96.  (A thread spills 24 bytes in the
+// single CTAs' kernel, 32 in the pairs'.)
 constexpr int kSoftRegs = 112, kConvRegs = 96, kMiscRegs = 64;
 static_assert(8 * kSoftRegs + 8 * kConvRegs + 4 * kMiscRegs <= 20 * 96, "register split: above it the increase waits forever");
 static_assert(kSoftRegs >= 96 && kConvRegs <= 96 && kMiscRegs <= 96, "an increase and two decreases from the launch's 96");
