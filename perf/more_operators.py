@@ -92,7 +92,7 @@ def draw(rng):
         elif op == "prefill":
             if hq == hkv and rng.random() < 0.5:
                 c["hkv"], hq = 2, 32
-            elif hkv == 5:
+            if hkv == 5:
                 hq = 10
             c.update(seqs=_log_int(rng, 1, 8), hq=hq, sink=rng.choice((0, 1, 4)), win=rng.choice((0, 0, 64, 256)))
             c["new_hi"] = _log_int(rng, 1, 4096)
