@@ -991,6 +991,18 @@ __device__ __forceinline__ void role_correction(const AttnParams& p, const AttnS
   }
 }
 
+__device__ __forceinline__ void take_units(const AttnParams& p, Ctx& c) {
+  if (p.pair_off) {  // the host's assignment (longest units first, to the least-loaded pair)
+    c.u0 = p.pair_off[c.pair];
+    c.u1 = p.pair_off[c.pair + 1];
+    c.ustep = 1;
+  } else {
+    c.u0 = c.pair;
+    c.u1 = p.n_units;
+    c.ustep = c.n_pairs;
+  }
+}
+
 template <bool kSplit>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnMaps m,
@@ -1005,15 +1017,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   c.rank = cluster_rank();
   c.pair = (int)(blockIdx.x >> 1);
   c.n_pairs = (int)(gridDim.x >> 1);
-  if (p.pair_off) {  // the host's assignment (longest units first, to the least-loaded pair)
-    c.u0 = p.pair_off[c.pair];
-    c.u1 = p.pair_off[c.pair + 1];
-    c.ustep = 1;
-  } else {
-    c.u0 = c.pair;
-    c.u1 = p.n_units;
-    c.ustep = c.n_pairs;
-  }
+  if (!p.early) take_units(p, c);
   c.wc = WaitCtl{p.err, p.wait_ns};
   // a launch queued behind this one that reads nothing this one writes may
   // start on each pair this one leaves
@@ -1057,7 +1061,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync_all();  // both CTAs' barriers exist before either may arrive on the other's
   tc_fence_after();
   c.tb = *tmem_slot;
-  if (p.early) wait_for_previous();
+  if (p.early) {
+    wait_for_previous();
+    take_units(p, c);  // not before: the plan may be on its way up
+  }
 
   const int lane = threadIdx.x & 31;
   if (warp < 4) {
