@@ -387,8 +387,8 @@ int pa_debug_decode_shared_pass(pa_handle h, int prefix_pass);
  *   [4352, 4608)  V block scales
  *   [4608, 4672)  K row scales, fp32 [16 tokens]; [4672, 4736) V row scales
  * A value is code (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) x block scale (e4m3)
- * x row scale.  Row scales are finite and not negative, block scales not negative;
- * what slots without a token hold does not matter. */
+ * x row scale.  Row scales are at most 2^117, as pa_kv4_append gives them, and not negative,
+ * block scales not negative; what slots without a token hold does not matter. */
 #define PA_KV4_TILE_BYTES 4736
 
 /* Append to the 4-bit pool: the new tokens of a batch of sequences, K and V rows of
@@ -418,8 +418,8 @@ int pa_kv4_gather(pa_handle h, int n_seq, const pa_seq* seqs, const int32_t* blo
 /* pa_decode on the 4-bit pool: one new token per sequence, the same mask and the same
  * requirements (n_q_heads / n_kv_heads <= 8, fewer than 2^30 visible blocks x kv heads
  * per 512 sequences).  K and V enter the products exactly, the query as bf16 (but for
- * values under 2^-20 of its row's largest), the weights P' in fp16, sums in fp32; the
- * handle's q_mode and p_mode have no say.
+ * values under 2^-20 of its row's largest), a weight times V's row scale in fp16 (normal down to
+ * 2^-20 of the row's largest such product), sums in fp32; the handle's q_mode and p_mode have no say.
  *   n_rows  rows of q and out; a sequence's row outside them is PA_EINVAL, and so are
  *           two sequences with one row
  *   out     q itself (in place), or apart from it; apart from the pool and the table

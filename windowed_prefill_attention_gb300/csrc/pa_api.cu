@@ -2394,7 +2394,7 @@ int kv4_decode(pa_handle h, int n_seq, const pa_seq* seqs, const void* q, const 
   p.G = h->G;
   p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
   p.part = static_cast<float*>(h->k4_part.p);
-  p.ml = reinterpret_cast<float2*>(static_cast<char*>(h->k4_part.p) + o_bytes);
+  p.nw = reinterpret_cast<float2*>(static_cast<char*>(h->k4_part.p) + o_bytes);
   p.err = h->d_err;
   p.wait_ns = (unsigned long long)h->opt.wait_timeout_ms * 1000000ull;
   for (int s0 = 0; s0 < n_seq; s0 += kKv4Seqs) {

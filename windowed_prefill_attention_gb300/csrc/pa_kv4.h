@@ -60,7 +60,7 @@ struct Kv4DecodeParams {
   int n_runs, most_runs;   // runs of the launch; of a pair, at most
   float sm_scale_log2;
   float* part;             // [n_runs][kKv4Part] float4
-  float2* ml;              // [n_runs][8]: reference and sum of each row
+  float2* nw;              // [n_runs][8]: of each row the reference of its O, the logarithm of its sum of weights
   int* err;
   unsigned long long wait_ns;
 };

@@ -18,14 +18,17 @@
 // transposed orientation, S^T = K Q^T and O^T = V^T P^T: keys and dims fill M, the
 // G <= 8 query rows N.  A code times its block scale is exact in fp16, so K and V
 // enter exactly; the query enters as fp16 through a power of two per row, exactly
-// but for values under 2^-20 of the row's largest; P' = p x (V's row scale),
-// normalised by a running power of two, is rounded to fp16: 2^-11 of each weight, far
-// under the rounding of the bf16 output, and at most 2^-30 of the largest where fp16's
-// normal range ends.
-// Scores, maxima, sums and O are fp32.  The reference that the softmax takes its
-// exponents from moves only when a score passes it by 2^8, and the normaliser of the
-// row scales when one passes it by 2^2, so the common block needs votes and no
-// reduction over the warp.
+// but for values under 2^-20 of the row's largest.
+// V's row scale s enters through the weights, and a row has two references: m follows its scores
+// y (log2), n its z = y + d, 2^d the power of two above s.  p = 2^(y - m) goes into the sum of
+// weights, P' = p s 2^(m - n) into the product: in fp16's range whatever the scales, and held
+// against the row's largest p s, not its largest s: a key of a huge V row and no weight costs
+// the others nothing.  P' is rounded to fp16: 2^-11 of each, far under the rounding of the
+// bf16 output, and at most 2^-31 of the largest where fp16's normal range ends.
+// Scores, references, sums and O are fp32.  A reference moves only when a y or z passes the largest one at its last
+// move by 2^8, so the common block needs a vote and no reduction over the warp.
+// What is joined is O in units of 2^n, with n and the logarithm of the weights' sum: a mean of values near
+// the top of fp32's range never passes through their sum, and a run of small values does not lose its weight.
 // Dims are permuted so that a thread's operands are whole words: thread (g, t) of
 // a warp reads dims [64 t, 64 t + 64) of keys g and g + 8 for K, dims [32 g, 32 g +
 // 32) of keys 2t, 2t + 1, 2t + 8, 2t + 9 for V (whose codes of a key pair are
@@ -47,18 +50,22 @@ namespace {
 
 // Two tiles a step, whose scores share one vote and whose products are independent
 // chains: 535 instructions a tile (605 one at a time) and as many registers as 8 warps an
-// SM leave.  5 contexts of 120 to 200 thousand tokens, 237 MB: 46.8 us (5.1 TB/s; the copies
-// alone take 40.6, the arithmetic alone about 44); one tile a step on 12 warps 48.4, on 8
-// warps 51.7, on 16 warps of 128 registers 52.6; three steps in the ring 47.6; queries in
-// shared memory 47.0.  64 windowed contexts, 157 MB: 36.6 us.
+// SM leave.  5 contexts of 120 to 200 thousand tokens, 237 MB: 46.9 us (5.0 TB/s; the copies
+// alone take 40.6), 64 windowed contexts, 157 MB: 35.9.  With the scales under a normaliser of the
+// largest one so far, which lost what lay far below it, 45.7 and 35.7, and then: one tile a
+// step on 12 warps 48.4, on 8 warps 51.7, on 16 warps of 128 registers 52.6; three steps in the ring
+// 47.6; queries in shared memory 47.0.
 constexpr int kWarps = 4;       // a CTA's, which share nothing until its runs are joined
 constexpr int kCtasPerSm = 2;
 constexpr int kStages = 2;      // steps, of two tiles each, of a warp in flight or in work
 constexpr int kStepBytes = 2 * kT4Bytes;
 constexpr int kSmBars = kWarps * kStages * kStepBytes;
 constexpr int kSmem = kSmBars + kWarps * kStages * 8 + 128;
-constexpr int kLift = 5;        // P' = p x row scale x 2^(kLift - ev): p <= 2^8, row scale <= 2^(ev + 2), P' <= 2^15
-constexpr float kMargin = 8.f;  // log2
+constexpr float kMargin = 8.f;  // log2: how far y and z may pass the largest ones at their references' last move
+constexpr float kLift = 7.f;    // m is that largest y, n that largest z - kLift: p <= 2^8, P' <= 2^15
+// Biased exponent that d is taken from: of row scales from 2^-100, the least that the append writes, on; for
+// less, and 0, d stays there (2^(m - n) is then at most 2^107)
+constexpr uint32_t kLeastExp = 27;
 constexpr int kMergeWarps = 32;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr unsigned kAll = 0xffffffffu;
@@ -82,6 +89,13 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+__device__ __forceinline__ float lg2f(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// A maximum as what exponents are taken from: where there is nothing (or NaN, which stays in the sums) not -inf.
+__device__ __forceinline__ float finite_ref(float m) { return m == -INFINITY ? 0.f : m; }
 __device__ __forceinline__ float lds_f32(uint32_t addr) { return __uint_as_float(lds32(addr)); }
 
 // Run i of n over a pair's blocks begins at this one: after whole steps of two blocks.
@@ -205,9 +219,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv4_decode_kernel(con
   uint4 q[8];
   float c[2];
   load_q(p, d, g, lane, q, c);
-  float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;  // references; the lane's share of the sums
-  float top_lo = -INFINITY, top_hi = -INFINITY, top_v = 0.f, vnorm = 0.f;  // what the references hold up to; 2^(kLift - ev)
-  int ev = -100;
+  float m_lo = -INFINITY, m_hi = -INFINITY, n_lo = -INFINITY, n_hi = -INFINITY;  // references
+  float top_m_lo = -INFINITY, top_m_hi = -INFINITY, top_n_lo = -INFINITY, top_n_hi = -INFINITY;  // what they hold up to
+  float r_lo = 0.f, r_hi = 0.f;                                                  // 2^(m - n)
+  float l_lo = 0.f, l_hi = 0.f;                                                  // the lane's share of the sums
   // the lane's offsets in a tile
   const int k_at0 = kv4_piece(gq, 2 * tq), k_at1 = kv4_piece(gq, 2 * tq + 1), kb_at = kT4Block + gq * 16 + 4 * tq;
   const int v_at0 = kT4V + kv4_piece(2 * tq, gq), v_at1 = kT4V + kv4_piece(2 * tq + 1, gq), vb_at = kT4Block + 256 + 32 * tq + 2 * gq;
@@ -272,16 +287,25 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv4_decode_kernel(con
           }
         }
       }
-      // scores in log2 units: y[e][row of 2][key of 2]
-      float y[2][4], vs[2][2];
+      float y[2][4], z[2][4], vs[2][2];  // [e][row of 2][key of 2]; of the keys V's row scales
       uint32_t vbs[2][4];  // V's block scales of keys 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint32_t at = kb + e * kT4Bytes;
         const float ks0 = lds_f32(at + row_at), ks1 = lds_f32(at + row_at + 32);
-        vs[e][0] = lds_f32(at + row_at + 64), vs[e][1] = lds_f32(at + row_at + 96);
-        y[e][0] = (sacc[e][0][0] + sacc[e][1][0]) * (ks0 * c[0]), y[e][1] = (sacc[e][0][1] + sacc[e][1][1]) * (ks0 * c[1]);
-        y[e][2] = (sacc[e][0][2] + sacc[e][1][2]) * (ks1 * c[0]), y[e][3] = (sacc[e][0][3] + sacc[e][1][3]) * (ks1 * c[1]);
+        float d[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t bits = lds32(at + row_at + 64 + 32 * r);  // not negative
+          vs[e][r] = __uint_as_float(bits);
+          d[r] = __uint_as_float(0x4b000000u | max(kLeastExp, bits >> 23)) - (8388608.f + 126.f);  // exponent - 126, exactly
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float x = sacc[e][0][k] + sacc[e][1][k], f = (k < 2 ? ks0 : ks1) * c[k & 1];
+          y[e][k] = x * f;
+          z[e][k] = fmaf(x, f, d[k >> 1]);
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) vbs[e][k] = lds16(at + vb_at + 16 * (k & 1) + 128 * (k >> 1));
       }
@@ -289,32 +313,28 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv4_decode_kernel(con
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int n_keys = !(e ? h1 : h0) ? 0 : (2 * it + e == last ? d.t % kPage + 1 : kPage);
-          if (gq >= n_keys) y[e][0] = y[e][1] = -INFINITY, vs[e][0] = 0.f;
-          if (gq + 8 >= n_keys) y[e][2] = y[e][3] = -INFINITY, vs[e][1] = 0.f;
+          if (gq >= n_keys) y[e][0] = y[e][1] = z[e][0] = z[e][1] = -INFINITY, vs[e][0] = 0.f;
+          if (gq + 8 >= n_keys) y[e][2] = y[e][3] = z[e][2] = z[e][3] = -INFINITY, vs[e][1] = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // e4m3 has a NaN (e2m1 has none)
             if (2 * tq + (k & 1) + 8 * (k >> 1) >= n_keys) vbs[e][k] = 0u;
         }
       }
-      float bm_lo = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2]));
-      float bm_hi = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
-      float bv = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
-      if (__any_sync(kAll, bm_lo > top_lo || bm_hi > top_hi || bv > top_v)) {
-        // new references: the maxima so far; a power of two over the row scales so far
+      float bm_lo = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2])), bm_hi = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
+      float bn_lo = fmaxf(fmaxf(z[0][0], z[0][2]), fmaxf(z[1][0], z[1][2])), bn_hi = fmaxf(fmaxf(z[0][1], z[0][3]), fmaxf(z[1][1], z[1][3]));
+      if (__any_sync(kAll, bm_lo > top_m_lo || bm_hi > top_m_hi || bn_lo > top_n_lo || bn_hi > top_n_hi)) {  // new references
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) {
           bm_lo = fmaxf(bm_lo, __shfl_xor_sync(kAll, bm_lo, sh));
           bm_hi = fmaxf(bm_hi, __shfl_xor_sync(kAll, bm_hi, sh));
-          bv = fmaxf(bv, __shfl_xor_sync(kAll, bv, sh));
+          bn_lo = fmaxf(bn_lo, __shfl_xor_sync(kAll, bn_lo, sh));
+          bn_hi = fmaxf(bn_hi, __shfl_xor_sync(kAll, bn_hi, sh));
         }
-        const float mn_lo = fmaxf(m_lo, bm_lo), mn_hi = fmaxf(m_hi, bm_hi);  // finite: key 0 of a block is visible
-        const int evn = max(ev, bv > 0.f ? min(100, (int)(__float_as_uint(bv) >> 23) - 126) : -100);
-        const float al_lo = ex2f(m_lo - mn_lo), al_hi = ex2f(m_hi - mn_hi);
-        // past 2^-126 the older terms are below fp32 resolution
-        const float vfix = evn - ev > 126 ? 0.f : __uint_as_float((uint32_t)(127 + ev - evn) << 23);
-        const float f_lo = al_lo * vfix, f_hi = al_hi * vfix;
-        l_lo *= al_lo;
-        l_hi *= al_hi;
+        const float mm_lo = fmaxf(m_lo, bm_lo), mm_hi = fmaxf(m_hi, bm_hi);  // finite: key 0 of a block is visible
+        const float nn_lo = fmaxf(n_lo, bn_lo - kLift), nn_hi = fmaxf(n_hi, bn_hi - kLift);
+        const float f_lo = ex2f(n_lo - nn_lo), f_hi = ex2f(n_hi - nn_hi);
+        l_lo *= ex2f(m_lo - mm_lo);
+        l_hi *= ex2f(m_hi - mm_hi);
 #pragma unroll
         for (int mt = 0; mt < 16; ++mt) {
           o[mt][0] *= f_lo;
@@ -322,13 +342,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv4_decode_kernel(con
           o[mt][2] *= f_lo;
           o[mt][3] *= f_hi;
         }
-        m_lo = mn_lo;
-        m_hi = mn_hi;
-        ev = evn;
-        top_lo = m_lo + kMargin;
-        top_hi = m_hi + kMargin;
-        top_v = __uint_as_float((uint32_t)(129 + ev) << 23);  // 2^(ev + 2)
-        vnorm = __uint_as_float((uint32_t)(127 + kLift - ev) << 23);
+        m_lo = mm_lo, m_hi = mm_hi, n_lo = nn_lo, n_hi = nn_hi;
+        top_m_lo = m_lo + kMargin, top_m_hi = m_hi + kMargin, top_n_lo = n_lo + (kLift + kMargin), top_n_hi = n_hi + (kLift + kMargin);
+        r_lo = ex2f(m_lo - n_lo), r_hi = ex2f(m_hi - n_hi);
       }
       uint32_t pb[2][2];
 #pragma unroll
@@ -336,9 +352,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv4_decode_kernel(con
         const float p0 = ex2f(y[e][0] - m_lo), p1 = ex2f(y[e][1] - m_hi), p2 = ex2f(y[e][2] - m_lo), p3 = ex2f(y[e][3] - m_hi);
         l_lo += p0 + p2;
         l_hi += p1 + p3;
-        const float n0 = vs[e][0] * vnorm, n1 = vs[e][1] * vnorm;
-        pb[e][0] = transpose8x8(pack_f16x2(p0 * n0, p1 * n0));
-        pb[e][1] = transpose8x8(pack_f16x2(p2 * n1, p3 * n1));
+        // p s first: what the factor 2^(m - n) alone would take out of fp32's range has no weight
+        pb[e][0] = transpose8x8(pack_f16x2(p0 * vs[e][0] * r_lo, p1 * vs[e][0] * r_hi));
+        pb[e][1] = transpose8x8(pack_f16x2(p2 * vs[e][1] * r_lo, p3 * vs[e][1] * r_hi));
       }
       // O^T += V^T P^T.  Row gq of m-tile mt is dim 32 gq + 2 mt, row gq + 8 dim 32 gq + 2 mt + 1.
 #pragma unroll
@@ -397,87 +413,87 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv4_decode_kernel(con
     __syncwarp();
   }
 
-    // 3. The run's result: O back to true V units.
-    const float back = __uint_as_float((uint32_t)(127 - kLift + ev) << 23);
+  // 3. The run's result.
 #pragma unroll
-    for (int sh = 4; sh < 32; sh <<= 1) {
-      l_lo += __shfl_xor_sync(kAll, l_lo, sh);
-      l_hi += __shfl_xor_sync(kAll, l_hi, sh);
-    }
-    if (n_runs == 1) {  // l is 0 where every page was outside the pool
-      const float f_lo = l_lo == 0.f ? 0.f : back / l_lo, f_hi = l_hi == 0.f ? 0.f : back / l_hi;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (2 * tq + e >= p.G) continue;
-        uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)d.q_row * p.HQ + (size_t)g * p.G + 2 * tq + e) * kHeadDim +
-                                              32 * gq);
-        const float f = e ? f_hi : f_lo;
-#pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-          const float4 a = o_element(o, 8 * e + k), b = o_element(o, 8 * e + k + 1);
-          const __nv_bfloat162 r[4] = {__floats2bfloat162_rn(a.x * f, a.y * f), __floats2bfloat162_rn(a.z * f, a.w * f),
-                                       __floats2bfloat162_rn(b.x * f, b.y * f), __floats2bfloat162_rn(b.z * f, b.w * f)};
-          const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
-          dst[k / 2] = make_uint4(u[0], u[1], u[2], u[3]);
-        }
-      }
-      return;
-    }
-    // The partial.  Where the CTA's runs are all of this pair they are joined first, through
-    // the rings: the first run's partial is then the CTA's.
-    const int r0 = tab.seq[s].z + g * n_runs, cta0 = blockIdx.x * kWarps;
-    const bool joined = cta0 >= r0 && cta0 + kWarps <= r0 + n_runs;
-    float4* part = reinterpret_cast<float4*>(p.part) + (size_t)(joined ? cta0 : run) * kKv4Part;
-    float2* ml = p.ml + (size_t)(joined ? cta0 : run) * 8;
-    if (!joined) {
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        if (2 * tq + (k >> 3) >= p.G) continue;
-        const float4 a = o_element(o, k);
-        part[k * 32 + lane] = make_float4(a.x * back, a.y * back, a.z * back, a.w * back);
-      }
-      if (gq == 0) {  // rows 2 tq and 2 tq + 1
-        ml[2 * tq] = make_float2(m_lo, l_lo);
-        ml[2 * tq + 1] = make_float2(m_hi, l_hi);
-      }
-      return;
-    }
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float4 a = o_element(o, k);
-      sts128(slot0 + (uint32_t)(k * 32 + lane) * 16, make_uint4(__float_as_uint(a.x * back), __float_as_uint(a.y * back),
-                                                               __float_as_uint(a.z * back), __float_as_uint(a.w * back)));
-    }
-    if (gq == 0) sts128(slot0 + kKv4Part * 16 + 16 * tq, make_uint4(__float_as_uint(m_lo), __float_as_uint(l_lo),
-                                                                  __float_as_uint(m_hi), __float_as_uint(l_hi)));
-    __syncthreads();  // all warps of the CTA come here: the choice is the CTA's
-    float f[2][kWarps];  // the warps' weights of rows 2 tq and 2 tq + 1
+  for (int sh = 4; sh < 32; sh <<= 1) {
+    l_lo += __shfl_xor_sync(kAll, l_lo, sh);
+    l_hi += __shfl_xor_sync(kAll, l_hi, sh);
+  }
+  if (n_runs == 1) {  // l is 0 where every page was outside the pool
+    const float f_lo = l_lo == 0.f ? 0.f : ex2f(n_lo - m_lo) / l_lo, f_hi = l_hi == 0.f ? 0.f : ex2f(n_hi - m_hi) / l_hi;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint32_t at = sbase + kKv4Part * 16 + 16 * tq + 8 * e;
-      float mw[kWarps], m = -INFINITY, l = 0.f;
+      if (2 * tq + e >= p.G) continue;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)d.q_row * p.HQ + (size_t)g * p.G + 2 * tq + e) * kHeadDim +
+                                            32 * gq);
+      const float f = e ? f_hi : f_lo;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        mw[w] = lds_f32(at + w * kStages * kStepBytes);
-        m = fmaxf(m, mw[w]);
+      for (int k = 0; k < 8; k += 2) {
+        const float4 a = o_element(o, 8 * e + k), b = o_element(o, 8 * e + k + 1);
+        const __nv_bfloat162 r[4] = {__floats2bfloat162_rn(a.x * f, a.y * f), __floats2bfloat162_rn(a.z * f, a.w * f),
+                                     __floats2bfloat162_rn(b.x * f, b.y * f), __floats2bfloat162_rn(b.z * f, b.w * f)};
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
+        dst[k / 2] = make_uint4(u[0], u[1], u[2], u[3]);
       }
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        f[e][w] = mw[w] == -INFINITY ? 0.f : ex2f(mw[w] - m);
-        l += f[e][w] * lds_f32(at + w * kStages * kStepBytes + 4);
-      }
-      if (warp == 0 && gq == 0) ml[2 * tq + e] = make_float2(m, l);
     }
-    for (int k = warp; k < 16; k += kWarps) {
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    return;
+  }
+  // The partial.  Where the CTA's runs are all of this pair they are joined first, through
+  // the rings: the first run's partial is then the CTA's.
+  const int r0 = tab.seq[s].z + g * n_runs, cta0 = blockIdx.x * kWarps;
+  const bool joined = cta0 >= r0 && cta0 + kWarps <= r0 + n_runs;
+  float4* part = reinterpret_cast<float4*>(p.part) + (size_t)(joined ? cta0 : run) * kKv4Part;
+  float2* nw = p.nw + (size_t)(joined ? cta0 : run) * 8;
+  const float w_lo = m_lo + lg2f(l_lo), w_hi = m_hi + lg2f(l_hi);  // -inf without a key
+  if (!joined) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 v = lds_f32x4(sbase + (uint32_t)(w * kStages * kStepBytes + (k * 32 + lane) * 16));
-        const float x = k >= 8 ? f[1][w] : f[0][w];
-        a = make_float4(a.x + x * v.x, a.y + x * v.y, a.z + x * v.z, a.w + x * v.w);
-      }
-      if (2 * tq + (k >> 3) < p.G) part[k * 32 + lane] = a;
+    for (int k = 0; k < 16; ++k) {
+      if (2 * tq + (k >> 3) >= p.G) continue;
+      part[k * 32 + lane] = o_element(o, k);
     }
+    if (gq == 0) {  // rows 2 tq and 2 tq + 1
+      nw[2 * tq] = make_float2(n_lo, w_lo);
+      nw[2 * tq + 1] = make_float2(n_hi, w_hi);
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float4 a = o_element(o, k);
+    sts128(slot0 + (uint32_t)(k * 32 + lane) * 16,
+           make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(a.z), __float_as_uint(a.w)));
+  }
+  if (gq == 0) sts128(slot0 + kKv4Part * 16 + 16 * tq, make_uint4(__float_as_uint(n_lo), __float_as_uint(w_lo),
+                                                                __float_as_uint(n_hi), __float_as_uint(w_hi)));
+  __syncthreads();  // all warps of the CTA come here: the choice is the CTA's
+  float f[2][kWarps];  // the warps' factors of rows 2 tq and 2 tq + 1
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const uint32_t at = sbase + kKv4Part * 16 + 16 * tq + 8 * e;
+    float n[kWarps], wt[kWarps], n_max = -INFINITY, w_max = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      n[w] = lds_f32(at + w * kStages * kStepBytes), wt[w] = lds_f32(at + w * kStages * kStepBytes + 4);
+      n_max = fmaxf(n_max, n[w]), w_max = fmaxf(w_max, wt[w]);
+    }
+    const float n_ref = finite_ref(n_max), w_ref = finite_ref(w_max);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      f[e][w] = ex2f(n[w] - n_ref);
+      l += ex2f(wt[w] - w_ref);
+    }
+    if (warp == 0 && gq == 0) nw[2 * tq + e] = make_float2(n_max, w_ref + lg2f(l));
+  }
+  for (int k = warp; k < 16; k += kWarps) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 v = lds_f32x4(sbase + (uint32_t)(w * kStages * kStepBytes + (k * 32 + lane) * 16));
+      const float x = k >= 8 ? f[1][w] : f[0][w];
+      a = make_float4(a.x + x * v.x, a.y + x * v.y, a.z + x * v.z, a.w + x * v.w);
+    }
+    if (2 * tq + (k >> 3) < p.G) part[k * 32 + lane] = a;
+  }
 }
 
 // The partials of a pair joined.  A warp takes one k (a float4 of every lane) of every
@@ -487,13 +503,13 @@ template <class Table>
 __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const __grid_constant__ Kv4DecodeParams p,
                                                                      const __grid_constant__ Table tab, int ways) {
   __shared__ float4 acc_sh[kMergeWarps][32];
-  __shared__ float2 ml_sh[kMergeWarps][32];
+  __shared__ float nwl_sh[3][kMergeWarps][32];
   const int s = blockIdx.x / p.HKV, g = blockIdx.x - s * p.HKV;
   const int n_runs = tab.seq[s].w;
   if (n_runs == 1) return;  // the run wrote the pair's output
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, way = warp % ways;
   const int k = blockIdx.y * ((blockDim.x >> 5) / ways) + warp / ways, row = 2 * (lane & 3) + (k >> 3);
-  float m = -INFINITY, l = 0.f;
+  float n = -INFINITY, w = -INFINITY, l = 0.f;  // acc in units of 2^n, the weights' sum l 2^w
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   wait_for_previous();
   dependents_may_start();  // not before: a decode behind this one would hold the registers that this one's CTAs need
@@ -504,50 +520,49 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_kernel(const __gri
     const auto part_id = [&](int i) { return (size_t)(first + i + (kWarps - 1) * min(max(i - lead, 0), full)); };
     constexpr int kAtOnce = 8;
     for (int r = way; r < n_parts; r += kAtOnce * ways) {
-      float2 ml[kAtOnce];
+      float2 nw[kAtOnce];
       float4 v[kAtOnce];
 #pragma unroll
       for (int e = 0; e < kAtOnce; ++e) {
         const bool have = r + e * ways < n_parts;
         const size_t id = part_id(have ? r + e * ways : r);
-        ml[e] = __ldcg(p.ml + id * 8 + row);
+        nw[e] = __ldcg(p.nw + id * 8 + row);
         v[e] = __ldcg(reinterpret_cast<const float4*>(p.part) + id * kKv4Part + k * 32 + lane);
-        if (!have) ml[e].x = -INFINITY;
+        if (!have) nw[e] = make_float2(-INFINITY, -INFINITY);
       }
-      float mn = m;
+      float n_max = n, w_max = w;
 #pragma unroll
-      for (int e = 0; e < kAtOnce; ++e) mn = fmaxf(mn, ml[e].x);
-      const float ref = mn == -INFINITY ? 0.f : mn;  // no page of these in the pool (or NaN, which stays in the sum)
-      const float al = ex2f(m - ref);
-      l *= al;
+      for (int e = 0; e < kAtOnce; ++e) n_max = fmaxf(n_max, nw[e].x), w_max = fmaxf(w_max, nw[e].y);
+      const float n_ref = finite_ref(n_max), w_ref = finite_ref(w_max);
+      const float al = ex2f(n - n_ref);
+      l *= ex2f(w - w_ref);
       acc = make_float4(acc.x * al, acc.y * al, acc.z * al, acc.w * al);
 #pragma unroll
       for (int e = 0; e < kAtOnce; ++e) {
-        const float w = ex2f(ml[e].x - ref);
-        l += w * ml[e].y;
-        acc = make_float4(acc.x + w * v[e].x, acc.y + w * v[e].y, acc.z + w * v[e].z, acc.w + w * v[e].w);
+        const float f = ex2f(nw[e].x - n_ref);
+        l += ex2f(nw[e].y - w_ref);
+        acc = make_float4(acc.x + f * v[e].x, acc.y + f * v[e].y, acc.z + f * v[e].z, acc.w + f * v[e].w);
       }
-      m = mn;
+      n = n_max, w = w_max;
     }
   }
   if (ways > 1) {
     acc_sh[warp][lane] = acc;
-    ml_sh[warp][lane] = make_float2(m, l);
+    nwl_sh[0][warp][lane] = n, nwl_sh[1][warp][lane] = w, nwl_sh[2][warp][lane] = l;
     __syncthreads();
     if (way > 0) return;
-    for (int w = 1; w < ways; ++w) m = fmaxf(m, ml_sh[warp + w][lane].x);
-    const float a0 = m == -INFINITY ? 0.f : ex2f(ml_sh[warp][lane].x - m);
-    l *= a0;  // (0 x NaN stays NaN)
-    acc = make_float4(acc.x * a0, acc.y * a0, acc.z * a0, acc.w * a0);
-    for (int w = 1; w < ways; ++w) {
-      const float al = m == -INFINITY ? 0.f : ex2f(ml_sh[warp + w][lane].x - m);
-      const float4 v = acc_sh[warp + w][lane];
-      l += al * ml_sh[warp + w][lane].y;
-      acc = make_float4(acc.x + al * v.x, acc.y + al * v.y, acc.z + al * v.z, acc.w + al * v.w);
+    for (int i = 1; i < ways; ++i) n = fmaxf(n, nwl_sh[0][warp + i][lane]), w = fmaxf(w, nwl_sh[1][warp + i][lane]);
+    const float n_ref = finite_ref(n), w_ref = finite_ref(w);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f), l = 0.f;
+    for (int i = 0; i < ways; ++i) {
+      const float f = ex2f(nwl_sh[0][warp + i][lane] - n_ref);
+      const float4 v = acc_sh[warp + i][lane];
+      l += ex2f(nwl_sh[1][warp + i][lane] - w_ref) * nwl_sh[2][warp + i][lane];
+      acc = make_float4(acc.x + f * v.x, acc.y + f * v.y, acc.z + f * v.z, acc.w + f * v.w);
     }
   }
   if (row >= p.G) return;
-  const float f = l == 0.f ? 0.f : 1.f / l;
+  const float f = l == 0.f ? 0.f : ex2f(n - w) / l;
   const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f), hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
   uint2 out;
   out.x = *reinterpret_cast<const uint32_t*>(&lo);
