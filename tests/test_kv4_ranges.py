@@ -106,3 +106,21 @@ def test_decode_beside_a_row_that_is_far_larger(n_ctx, ratio):
     pa.pa_kv4_decode(c.h, np.array([(0, n_ctx - 1, 1, n_ctx)], np.int32), dq, c.d_tiles, c.d_bt, 1, 0, sm, dq)
     assert pa.pa_last_error(c.h) == 0
     check_rows(host(dq), q, c, [(0, 0, n_ctx - 1)], 1, 0, sm, DECODE_STEP)
+
+
+@pytest.mark.parametrize("exponent", [-119, -122, -124, -126, -130])
+def test_decode_of_tiny_queries_on_great_keys(exponent):
+    """Queries down to bf16's subnormal values, keys of up to 2^122: scores of a few units all the same."""
+    import windowed_prefill_attention_gb300 as pa
+    rng = np.random.default_rng(12)
+    q = bf16_round(np.ldexp(rng.uniform(1, 2, (1, 4, D)) * rng.choice([-1, 1], (1, 4, D)), exponent).astype(np.float32))
+
+    def change(k, v, slots):
+        k[:] = np.ldexp(bf16_round(rng.standard_normal(k.shape).astype(np.float32)), 120)
+
+    c = cache_of(63, [200], 4, 2, change)
+    sm = float(np.ldexp(1.0, -exponent - 120 - 3))
+    dq = dev_bf16(q)
+    pa.pa_kv4_decode(c.h, np.array([(0, 199, 1, 200)], np.int32), dq, c.d_tiles, c.d_bt, 1, 0, sm, dq)
+    assert pa.pa_last_error(c.h) == 0
+    check_rows(host(dq), q, c, [(0, 0, 199)], 1, 0, sm, DECODE_STEP)

@@ -126,7 +126,7 @@ __device__ __forceinline__ void load_q(const Kv4DecodeParams& p, const DecSeq& d
   uint32_t am = max(am2 & 0xffffu, am2 >> 16);
   am = max(am, __shfl_xor_sync(kAll, am, 1));
   am = max(am, __shfl_xor_sync(kAll, am, 2));
-  const int k = am > 0u ? min(127, 133 - (int)(am >> 7)) : 0;
+  const int k = am > 0u ? min(126, 133 - (int)(am >> 7)) : 0;  // 2^-k stays a normal number
   const float mul = __uint_as_float((uint32_t)(127 + k) << 23);
   const float mine = row < p.G ? __uint_as_float((uint32_t)(127 - k) << 23) * p.sm_scale_log2 : 0.f;
 #pragma unroll
