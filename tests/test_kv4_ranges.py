@@ -26,12 +26,14 @@ def cache_of(seed, lengths, hq, hkv, change):
     return c
 
 
-def largest_share(q, c, s, t, S, W, sm):
-    """[HQ]: of a query token the largest weight x V row scale, over the sum of the weights."""
+def largest_share(q, c, s, t, S, W, sm, least):
+    """[HQ]: of a query token the largest weight x V row scale, over the sum of the weights; no scale counts less than
+    least(the sequence's largest)."""
     hq, hkv = q.shape[0], c.hkv
     n = len(c.k[s])
     scale = c.tiles[c.bt[s, np.arange(n) // PAGE], :, 4672:].copy().view(np.float32).reshape(n, hkv, PAGE)
     scale = scale[np.arange(n), :, np.arange(n) % PAGE].astype(np.float64)
+    scale = np.maximum(scale, least(scale.max()))
     j = np.arange(min(n, t + 1))
     if W > 0:
         j = j[(j // PAGE < S) | (j // PAGE >= max(0, t // PAGE + 1 - W))]
@@ -43,24 +45,28 @@ def largest_share(q, c, s, t, S, W, sm):
     return out
 
 
-def check_rows(got, q, c, rows, S, W, sm, half_step):
+def check_rows(got, q, c, rows, S, W, sm, half_step, least):
     """Against the 64-bit definition.  A weight x row scale is held in fp16 under a power of two of the row's own:
     2^-11 of it, or, where it leaves fp16's normal range, half_step of the row's largest; V's codes under their block
-    scales are at most 2688."""
+    scales are at most 2688.  For the choice of that power of two a scale counts as `least` at least, a row of zeros too."""
     worst = 0.0
     for row, s, t in rows:
         qq = q[row].astype(np.float64)
         ref, bound = attention(qq, c.k[s], c.v[s], t, S, W, sm, 0.0)
-        bound = bound + half_step * 2688 * (t + 1) * largest_share(qq, c, s, t, S, W, sm)[:, None]
+        bound = bound + half_step * 2688 * (t + 1) * largest_share(qq, c, s, t, S, W, sm, least)[:, None]
         assert np.isfinite(got[row]).all(), (row, s, t)
         worst = max(worst, float((np.abs(got[row] - ref) / bound).max()))
     assert worst <= 1.0, worst
 
 
 # decode: the largest product is at least 2^6 in its units (a reference up to 2^8 behind, a significand of 1/2 or more)
-DECODE_STEP = 2.0 ** (-25 - 6)
-# prefill: at least 2^-6 (the first reference lies 2^6 above the first tile's largest)
-PREFILL_STEP = 2.0 ** (-25 + 6)
+# with scales of 2^-100 and less at 2^-99.  A weight under 2^-126 of the largest, which fp32 does not hold, is 0: with any
+# scale a product of at most 2^-126 x the largest scale, half_step of 2^-95 of that scale.
+DECODE_STEP = 2.0 ** (-25 - 6), lambda most: max(2.0 ** -99, most * 2.0 ** -95)
+# prefill: at least 2^-13 (the first reference lies 2^6 above the first tile's largest, the normaliser 2^6 above the least
+# scale, a significand of 1/2 or more), scales of 2^-100 and less at 2^-99 again.  Weights are 0 under 2^-120 of the largest,
+# half_step of 2^-106 of the largest scale, or where a product is 2^-17 of the row's largest, under half_step of that.
+PREFILL_STEP = 2.0 ** (-25 + 13), lambda most: max(2.0 ** -99, most * 2.0 ** -106)
 
 
 @pytest.mark.parametrize("lengths", [[1, 40, 700], [5, 9000]])  # one run a pair and several; over many CTAs
@@ -83,7 +89,7 @@ def test_decode_of_values_at_the_top_of_the_range(lengths, exponent):
         dq = dev_bf16(q)
         pa.pa_kv4_decode(c.h, seqs, dq, c.d_tiles, c.d_bt, 1, 0, sm, dq)
         assert pa.pa_last_error(c.h) == 0
-        check_rows(host(dq), q, c, [(s, s, n - 1) for s, n in enumerate(lengths)], 1, 0, sm, DECODE_STEP)
+        check_rows(host(dq), q, c, [(s, s, n - 1) for s, n in enumerate(lengths)], 1, 0, sm, *DECODE_STEP)
 
 
 @pytest.mark.parametrize("n_ctx", [30, 700, 9000])
@@ -105,7 +111,7 @@ def test_decode_beside_a_row_that_is_far_larger(n_ctx, ratio):
     dq = dev_bf16(q)
     pa.pa_kv4_decode(c.h, np.array([(0, n_ctx - 1, 1, n_ctx)], np.int32), dq, c.d_tiles, c.d_bt, 1, 0, sm, dq)
     assert pa.pa_last_error(c.h) == 0
-    check_rows(host(dq), q, c, [(0, 0, n_ctx - 1)], 1, 0, sm, DECODE_STEP)
+    check_rows(host(dq), q, c, [(0, 0, n_ctx - 1)], 1, 0, sm, *DECODE_STEP)
 
 
 @pytest.mark.parametrize("exponent", [-119, -122, -124, -126, -130])
@@ -123,4 +129,119 @@ def test_decode_of_tiny_queries_on_great_keys(exponent):
     dq = dev_bf16(q)
     pa.pa_kv4_decode(c.h, np.array([(0, 199, 1, 200)], np.int32), dq, c.d_tiles, c.d_bt, 1, 0, sm, dq)
     assert pa.pa_last_error(c.h) == 0
-    check_rows(host(dq), q, c, [(0, 0, 199)], 1, 0, sm, DECODE_STEP)
+    check_rows(host(dq), q, c, [(0, 0, 199)], 1, 0, sm, *DECODE_STEP)
+
+
+# whole units (few keys; many pieces of them), split ones
+PREFILLS = [[(0, 90), (100, 33)], [(1500, 40)], [(700, 5), (40, 20)]]
+
+
+def prefill(c, pieces, q, S, W, sm, gate=None, options={}):
+    """pa_kv4_prefill of each piece (cached, new), rows end to end -> out, [(row, sequence, position)]."""
+    import torch
+
+    import windowed_prefill_attention_gb300 as pa
+    off = np.cumsum([0] + [n for _, n in pieces])
+    seqs = np.array([(off[s], a, n, a + n) for s, (a, n) in enumerate(pieces)], np.int32)
+    dq = dev_bf16(q)
+    out = torch.full_like(dq, 7.0)
+    h = pa.Handle(c.hq, c.hkv, c.n_pool, c.max_pages, **options)
+    pa.pa_kv4_prefill(h.h, seqs, dq, c.d_tiles, c.d_bt, S, W, sm, out, q_gate=gate)
+    assert pa.pa_last_error(h.h) == 0
+    return host(out), [(off[s] + i, s, a + i) for s, (a, n) in enumerate(pieces) for i in range(n)]
+
+
+@pytest.mark.parametrize("pieces", PREFILLS)
+@pytest.mark.parametrize("ratio", [12, 20, 60])
+def test_prefill_behind_which_a_far_larger_row_lies(pieces, ratio):
+    """The last token's V row 2^ratio larger than all others: the rows of the tokens before it do not see it, those beside it
+    in its block of 16 neither, and keep all their bits."""
+    lengths = [a + n for a, n in pieces]
+
+    def change(k, v, slots):
+        for pages, rows in slots:
+            v[pages[-1], rows[-1]] *= 2.0 ** ratio
+
+    c = cache_of(64, lengths, 8, 2, change)
+    q = random_rows(np.random.default_rng(13), (sum(n for _, n in pieces), 8, D))
+    got, rows = prefill(c, pieces, q, 1, 0, 1 / 128)
+    check_rows(got, q, c, rows, 1, 0, 1 / 128, *PREFILL_STEP)
+
+
+@pytest.mark.parametrize("pieces", PREFILLS)
+@pytest.mark.parametrize("ratio", [20, 40, 100])
+def test_prefill_beside_a_row_that_is_far_larger(pieces, ratio):
+    """A first and a middle V row 2^ratio larger than the others, in every row's sight but of next to no weight."""
+    lengths = [a + n for a, n in pieces]
+    sm = 1 / 128
+    base = bf16_round(np.random.default_rng(14).standard_normal(D).astype(np.float32)).astype(np.float64)
+
+    def change(k, v, slots):
+        for pages, rows in slots:
+            for at in (0, len(pages) // 2):
+                k[pages[at], rows[at]] = -base * (1.6 * ratio * np.log(2) / (base @ base) / sm)
+                v[pages[at], rows[at]] *= 2.0 ** ratio
+
+    c = cache_of(65, lengths, 4, 1, change)
+    q = np.tile(base.astype(np.float32), (sum(n for _, n in pieces), 4, 1))
+    got, rows = prefill(c, pieces, q, 1, 0, sm)
+    rows = [r for r in rows if r[2] > 0]  # a first token sees nothing else
+    check_rows(got, q, c, rows, 1, 0, sm, *PREFILL_STEP)
+
+
+@pytest.mark.parametrize("pieces", PREFILLS)
+@pytest.mark.parametrize("exponent", [-80, 60, 100, 112, 126])
+def test_prefill_of_values_at_the_ends_of_the_range(pieces, exponent):
+    """V rows of up to 2.8e38 beside ordinary ones and rows of zeros, scores that grow behind the first tile."""
+    lengths = [a + n for a, n in pieces]
+
+    def change(k, v, slots):
+        for pages, rows in slots:
+            x = np.clip(np.ldexp(v[pages, rows], exponent), -2.8e38, 2.8e38)
+            x[::5] = v[pages[::5], rows[::5]]
+            x[1::7] = 0
+            v[pages, rows] = x
+            v[pages[0], rows[0]] = np.sign(v[pages[0], rows[0]]) * (2.8e38 if exponent > 0 else 2.0 ** exponent)
+            k[pages[: len(pages) // 2], rows[: len(pages) // 2]] *= 2.0 ** -6
+
+    c = cache_of(66, lengths, 8, 2, change)
+    q = random_rows(np.random.default_rng(15), (sum(n for _, n in pieces), 8, D))
+    for sm in (1 / 16, 0.0):
+        got, rows = prefill(c, pieces, q, 1, 0, sm)
+        check_rows(got, q, c, rows, 1, 0, sm, *PREFILL_STEP)
+
+
+@pytest.mark.parametrize("q_mode,p_mode", [(1, 0), (0, 1), (1, 1)])
+def test_prefill_on_the_integer_grids_behind_which_a_far_larger_row_lies(q_mode, p_mode):
+    """The grids round relative to a row's own largest weight x scale; a later row's scale has no say in it.  Against the
+    same call without the large row, whose scores are the same: what each side's weights are off by, fp16's 2^-11 of each
+    and half a step of the largest (PREFILL_STEP), or half of the u8 grid's step, 1/255 of the largest; and bf16's 2^-8."""
+    pieces = [(0, 60), (400, 30)]
+    lengths = [a + n for a, n in pieces]
+    q = bf16_round(np.random.default_rng(16).standard_normal((90, 8, D)).astype(np.float32))
+    sm = 1 / 128
+    outs, caches = [], []
+    for ratio in (0, 30):
+        def change(k, v, slots):
+            for pages, rows in slots:
+                v[pages[-1], rows[-1]] *= 2.0 ** ratio
+        caches.append(cache_of(67, lengths, 8, 2, change))
+        outs.append(prefill(caches[-1], pieces, q, 1, 0, sm, options=dict(q_mode=q_mode, p_mode=p_mode)))
+    half_step, least = PREFILL_STEP
+    for row, s, t in outs[0][1]:
+        if t == lengths[s] - 1:
+            continue
+        c, qq = caches[0], q[row].astype(np.float64)
+        a, b = outs[0][0][row], outs[1][0][row]
+        share = largest_share(qq, c, s, t, 1, 0, sm, least)
+        for h in range(8):
+            kk, vv = c.k[s][: t + 1, h // 4], c.v[s][: t + 1, h // 4]
+            y = sm * (kk @ qq[h])
+            p = np.exp(y - y.max())
+            # the int8 grid moves a score by at most half a code, 1/254 of the query's largest, in each dim
+            p *= np.exp(2 * sm * (np.abs(kk).sum(-1) * np.abs(qq[h]).max() / 254).max()) if q_mode else 1.0
+            weighed = (p / np.exp(y - y.max()).sum()) @ np.abs(vv)
+            bound = 2 * 2.0 ** -8 * np.maximum(np.abs(a[h]), np.abs(b[h])) + 2 * 2.0 ** -133
+            steps = 2 * half_step if p_mode == 0 else 1.02 / 255
+            bound = bound + 2 * 2.0 ** -11 * weighed + steps * 2688 * (t + 1) * share[h]
+            assert np.all(np.abs(a[h] - b[h]) <= bound), (row, h)

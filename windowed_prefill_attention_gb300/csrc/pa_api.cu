@@ -460,7 +460,7 @@ int prepare(pa_handle h, int n_seq, const pa_seq* seqs, int S, int W, cudaStream
   const size_t n_rec = n_whole + split_records(P);
   // workspace
   if ((rc = reserve_rows(h, (size_t)P.n_tok_total))) return rc;
-  if ((rc = grow(h->vsmax, h->vsmax_cap, (size_t)n_seq * h->HKV))) return rc;
+  if ((rc = grow(h->vsmax, h->vsmax_cap, 2 * (size_t)n_seq * h->HKV))) return rc;
   if ((rc = grow(h->d_seqs, h->seqs_cap, P.seqs.size()))) return rc;
   if ((rc = grow(h->d_units, h->units_cap, n_rec))) return rc;
   // upload through pinned staging; never overwrite staging a copy may still read
@@ -550,7 +550,7 @@ int launch_attention_plan(pa_handle h, const Plan& P, const SeqGeom* d_seqs, con
                           const void* q, int S, int W, float sm_scale, void* out, cudaStream_t st,
                           const void* gate, bool overlap_prev = false, const unsigned int* q_ready = nullptr,
                           unsigned int q_epoch = 0, const int* d_pair_off = nullptr, int plan_pairs = 0,
-                          bool early = false, const AttnSplit* split = nullptr, const SplitUnit* split_units = nullptr) {
+                          bool kv4 = false, const AttnSplit* split = nullptr, const SplitUnit* split_units = nullptr) {
   int rc = PA_OK;
   // tensor maps
   if (h->kw != h->kv_ptr || P.n_tok_total != h->kv_rows || h->n_tok_cap != h->kv_cap) {
@@ -607,7 +607,8 @@ int launch_attention_plan(pa_handle h, const Plan& P, const SeqGeom* d_seqs, con
   a.q_ready = q_ready;
   a.q_epoch = q_epoch;
   a.debug_stall = h->opt.debug_stall;
-  a.early = early;
+  a.kv4 = kv4;
+  a.n_seq = (int)P.seqs.size();
   if (split) PA_CUDA(launch_attention_split(a, maps, *split, split_units, (int)P.split.size(), st));
   else PA_CUDA(launch_attention(a, maps, h->n_sm, st, overlap_prev));
   return PA_OK;

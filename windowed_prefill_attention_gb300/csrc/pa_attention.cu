@@ -43,8 +43,9 @@
 //                 whole rows (two rows per thread, 16-lane TMEM shapes)
 //   warps 12-15   epilogue of each unit (and Q codes on the int8 grid)
 //
-// A second form of the kernel (kSplit) runs parts of units: a call of few units would leave
-// most pairs idle, each unit's tiles in turn.  A part is a unit whose tiles are a run of the whole
+// Two more forms of the kernel serve the 4-bit pool, whose V scales may lie any power of two apart
+// (role_softmax).  The form kKv4Parts runs parts of units: a call of few units would leave most pairs
+// idle, each unit's tiles in turn.  A part is a unit whose tiles are a run of the whole
 // unit's; its epilogue writes the sums and O unnormalised, and join_units_kernel adds a
 // unit's parts up, divides, rounds and gates.  2 x 150 tokens on 900 to 2100 keys, a call: 26.1 us (38 whole).
 #include <cstdint>
@@ -52,6 +53,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <type_traits>
 
 #include "pa_early.cuh"
 #include "pa_internal.h"
@@ -117,6 +119,8 @@ constexpr float kLift = 6.f;   // a unit's first reference sits 2^kLift above it
 constexpr float kLazy = 14.f;  // the softmax reference moves when a row max grows by more than 2^kLazy;
                                // P' = p * v_scale * 2^-ev then stays below 2^14, inside the fp16 range
 
+constexpr uint32_t kAlike = 6;  // log2: how far apart the 4-bit pool's V scales may lie under one normaliser
+
 constexpr uint32_t kTmO = 0;
 constexpr uint32_t kTmS = 256;
 constexpr uint64_t kDrainNs = 200000000ull;
@@ -124,6 +128,11 @@ constexpr uint64_t kDrainNs = 200000000ull;
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
@@ -136,13 +145,20 @@ __device__ __forceinline__ int pow2_ceil_exp(float x) {
   const int eb = (int)((__float_as_uint(x) >> 23) & 0xff);
   return imax(-100, imin(100, eb - 126));
 }
+// Of the 4-bit pool's V scales of a sequence's head the largest's bits, and 0x7f800000 - those of the least over 0 (0: none).
+__device__ __forceinline__ bool scales_alike(uint32_t most, uint32_t least_inv) {
+  return most < (127u + 16u) << 23 && (least_inv == 0u || most - (0x7f800000u - least_inv) <= kAlike << 23);
+}
 // V^T chunks of a tile of nb blocks.
 __device__ __forceinline__ int n_chunks(int nb) { return (nb + 3) / 4; }
 
-// Tiles of unit u: all of its geometry's, or with kSplit its part's.
-template <bool kSplit>
+// The kernel's forms: whole units of the int8 pool, of the 4-bit pool, parts of the 4-bit pool's units.
+enum class Form { kInt8, kKv4, kKv4Parts };
+
+// Tiles of unit u: all of its geometry's, or its part's.
+template <Form kForm>
 __device__ __forceinline__ UnitPart unit_tiles(const AttnSplit& sp, int u, const UnitGeom& ug) {
-  if (kSplit) return sp.parts[u];
+  if (kForm == Form::kKv4Parts) return sp.parts[u];
   return UnitPart{0, ug.n_tiles};
 }
 
@@ -200,7 +216,7 @@ struct Ctx {
 // parity s / 4 into slot s: this CTA's N/2 keys of the tile, from key
 // rank * N/2 on, N = 16 nb (the MMA takes N/2 rows from each CTA's slot).  The
 // slot is free again once QK^T of the tile two before is done (S full).
-template <bool kSplit>
+template <Form kForm>
 __device__ __forceinline__ void role_producer_k(const AttnParams& p, const AttnSplit& sp, const AttnMaps& m, const Ctx& c,
                                                 int s) {
   const int r = s & 3, par = s >> 2;
@@ -210,7 +226,7 @@ __device__ __forceinline__ void role_producer_k(const AttnParams& p, const AttnS
     const Unit un = p.units[u];
     const SeqGeom sg = p.seqs[un.seq];
     const UnitGeom ug = unit_geom(un.t0, 2 * p.TQ, sg, p.S, p.W);
-    const UnitPart part = unit_tiles<kSplit>(sp, u, ug);
+    const UnitPart part = unit_tiles<kForm>(sp, u, ug);
     for (int j = 0; j < part.n; ++j) {
       if ((int)((tc + j) & 1) != par) continue;
       const TileGeom tg = tile_geom(ug, part.j0 + j, p.S, p.W);
@@ -236,7 +252,7 @@ __device__ __forceinline__ void role_producer_k(const AttnParams& p, const AttnS
 // parity s / 2 into slot s: this CTA's 128 of the 256 dims.  Lane (parity, 0)
 // of the even CTA expects the bytes of all the tile's chunks in both CTAs;
 // the slot is free again once PV of the tile two before is done.
-template <bool kSplit>
+template <Form kForm>
 __device__ __forceinline__ void role_producer_v(const AttnParams& p, const AttnSplit& sp, const AttnMaps& m, const Ctx& c,
                                                 int s) {
   const int ch = s & 1, par = s >> 1;
@@ -246,7 +262,7 @@ __device__ __forceinline__ void role_producer_v(const AttnParams& p, const AttnS
     const Unit un = p.units[u];
     const SeqGeom sg = p.seqs[un.seq];
     const UnitGeom ug = unit_geom(un.t0, 2 * p.TQ, sg, p.S, p.W);
-    const UnitPart part = unit_tiles<kSplit>(sp, u, ug);
+    const UnitPart part = unit_tiles<kForm>(sp, u, ug);
     for (int j = 0; j < part.n; ++j) {
       if ((int)((tc + j) & 1) != par) continue;
       const int nch = n_chunks(tile_width(ug, part.j0 + j));
@@ -289,7 +305,7 @@ __device__ __forceinline__ void prefetch_rows(const AttnParams& p, const __nv_bf
 // before they are needed) and, in the odd CTA, passes the arrival of its Q on
 // to the even CTA.  Lane 4 loads the K/V scales of each tile (two-slot ring
 // by tile parity).
-template <bool kSplit>
+template <Form kForm>
 __device__ __forceinline__ void role_producer_q(const AttnParams& p, const AttnSplit& sp, const AttnMaps& m, const Ctx& c,
                                                 int r) {
   uint32_t ts = 0;  // tiles whose scales were loaded
@@ -305,7 +321,7 @@ __device__ __forceinline__ void role_producer_q(const AttnParams& p, const AttnS
     const int t0 = un.t0 + (int)c.rank * p.TQ;  // this CTA's first token
     if (r == 4) {
       const UnitGeom ug = unit_geom(un.t0, 2 * p.TQ, sg, p.S, p.W);
-      const UnitPart part = unit_tiles<kSplit>(sp, u, ug);
+      const UnitPart part = unit_tiles<kForm>(sp, u, ug);
       for (int j = 0; j < part.n; ++j) {
         const uint32_t s = ts & 1;
         if (!(ok = c.wait(B_SCEMPTY + s, ((ts >> 1) & 1) ^ 1, 14))) break;
@@ -436,7 +452,7 @@ __device__ __forceinline__ void mma_commit_pair_if(uint32_t bar, bool pred) {
       : "memory");
 }
 
-template <bool kSplit>
+template <Form kForm>
 __device__ __forceinline__ void role_mma(const AttnParams& p, const AttnSplit& sp, const Ctx& c) {
   uint32_t tc = 0;  // global tile counter: K/V slots and S buffer by its parity
   int k_unit = 0;
@@ -453,7 +469,7 @@ __device__ __forceinline__ void role_mma(const AttnParams& p, const AttnSplit& s
     const Unit un = p.units[u];
     const SeqGeom sg = p.seqs[un.seq];
     const UnitGeom ug = unit_geom(un.t0, 2 * p.TQ, sg, p.S, p.W);
-    const UnitPart part = unit_tiles<kSplit>(sp, u, ug);
+    const UnitPart part = unit_tiles<kForm>(sp, u, ug);
     const int n = part.n;
     const int jsoon = imax(0, n - kQSoon);  // its QK^T lets the next unit's Q rows be prefetched
     const int qbar = p.debug_stall ? B_STALL : (p.q_mode == 1 ? B_QREADY2 : B_QFULL);
@@ -534,8 +550,20 @@ __device__ __forceinline__ void role_mma(const AttnParams& p, const AttnSplit& s
 // it, with no exchange between warps.  Each CTA of a pair runs its own
 // softmax over its own 128 rows; only the arrival that releases PV goes to the
 // even CTA, whose MMA issuer multiplies both.
-template <bool kSplit>
-__device__ __forceinline__ void role_softmax(const AttnParams& p, const AttnSplit& sp, const Ctx& c, uint8_t* sm) {
+//
+// References.  P' = 2^(y - m - ev) x V scale, m from the row's largest score y, 2^ev above the largest V scale of
+// the sequence's keys.  Where the 4-bit pool's scales lie further apart than 2^kAlike (or are huge), that would take
+// the bits of the rows that do not see the largest, or give it no weight: their units take kExact tiles, whose m
+// follows the row's largest z = y + d, 2^d the power of two above the key's own scale, and P' = 2^(y - m) x V scale:
+// in fp16's range whatever the scales, and held against the row's largest product.
+// There 2^(y - m) itself, which the sum takes, is at most 2^(14 - d) <= 2^113.  Its least, fp32's 2^-126, is
+// 2^-120 or less of the row's largest weight while the scales stay under 1; with greater ones m is lower by
+// 2^14, which leaves 2^-17 of the largest product at scales of 2^117 and 2^-74 at 2^60.
+//
+// Unit u, behind k_unit units of tc tiles; vsmax: its V scales' word.  The tiles, or -1 where a wait gave up.
+template <Form kForm, bool kExact>
+__device__ __forceinline__ int softmax_unit(const AttnParams& p, const AttnSplit& sp, const Ctx& c, uint8_t* sm, int u, int k_unit,
+                                            uint32_t tc, uint32_t vsmax) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lb = 32 * (warp & 3) + 16 * ((warp - 4) >> 2);  // first of this warp's 16 rows (TMEM lanes)
   const int tcol = 2 * (lane & 3);                          // this thread's first column of every 8
@@ -544,212 +572,246 @@ __device__ __forceinline__ void role_softmax(const AttnParams& p, const AttnSpli
   float* c_rows = reinterpret_cast<float*>(sm + kSmRows);
   float* l_rows = c_rows + 2 * kRows;   // [unit parity][row]
   float* sp_rows = c_rows + 4 * kRows;  // [unit parity][row]
-  const bool u8 = !kSplit && p.p_mode == 1;
-  uint32_t tc = 0;
-  int k_unit = 0;
-  bool ok = true;
-  for (int u = c.u0; u < c.u1 && ok; u += c.ustep, ++k_unit) {
-    const Unit un = p.units[u];
-    const SeqGeom sg = p.seqs[un.seq];
-    const UnitGeom ug = unit_geom(un.t0, 2 * p.TQ, sg, p.S, p.W);
-    const UnitPart part = unit_tiles<kSplit>(sp, u, ug);
-    const int n = part.n;
-    const int t0 = un.t0 + (int)c.rank * p.TQ;  // this CTA's first token
-    const int t_row[2] = {t0 + rr[0] / p.G, t0 + rr[1] / p.G};
-    const float ev = (float)pow2_ceil_exp(__uint_as_float(p.vsmax[un.seq * p.HKV + un.g]));
-    // the per-row query scale (s_q on the int8 grid, 1 for the bf16 query;
-    // sm_scale * log2(e) is in the K scales), kept positive so that -inf
-    // scores stay -inf
-    float c_row[2] = {1.f, 1.f};
-    if (p.q_mode == 1) {
-      if (!(ok = c.warp_wait(B_QREADY, k_unit & 1, 30))) break;
-      c_row[0] = c_rows[(k_unit & 1) * kRows + rr[0]];
-      c_row[1] = c_rows[(k_unit & 1) * kRows + rr[1]];
-    }
-    c_row[0] = fmaxf(c_row[0], 1e-30f);
-    c_row[1] = fmaxf(c_row[1], 1e-30f);
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f}, sp_prev[2] = {1.f, 1.f};
-    for (int j = 0; j < n; ++j) {
-      const uint32_t t = tc + j;
-      const TileGeom tg = tile_geom(ug, part.j0 + j, p.S, p.W);
-      if (!(ok = c.warp_wait(B_SFULL + (t & 1), (t >> 1) & 1, 31))) break;
-      const uint32_t sd = c.tb + lane_off + kTmS + (t & 1) * kTileKeys;
-      // this thread's K scales at +8k (two floats each); its V scales 128 floats on
-      const float* ksp = reinterpret_cast<const float*>(sm + kSmScale + (t & 1) * 1024) + tcol;
-      const float* vsp = ksp + 128;
-      tc_fence_after();
-      uint32_t sv[64];
-      tmem_ld_16x256b_x16(sd, sv);
-      // the tile's scales (normally there long since), checked while the
-      // score load is in flight
-      const bool oks = c.warp_wait(B_SCFULL + (t & 1), (t >> 1) & 1, 32);
-      tmem_wait_ld(sv);
-      if (!(ok = oks)) break;
-      // y = S * k_scale (masked: -inf), in place, and each row's maximum; the
-      // products in fp32 pairs, the maximum three operands at a time
-      // A tile every row sees in full (most of them) takes a loop without the
-      // mask: with the mask's selects inside one loop under a condition, they
-      // were executed as predicated instructions on every tile.
-      const bool full = !tg.needs_mask && tg.nb == kTileBlocks;
-      float mx[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
-      if (full) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float2 k2 = *reinterpret_cast<const float2*>(ksp + 8 * k);
-          const float2 a = mul2(make_float2(__uint_as_float(sv[4 * k]), __uint_as_float(sv[4 * k + 1])), k2);
-          const float2 b = mul2(make_float2(__uint_as_float(sv[4 * k + 2]), __uint_as_float(sv[4 * k + 3])), k2);
-          sv[4 * k] = __float_as_uint(a.x);
-          sv[4 * k + 1] = __float_as_uint(a.y);
-          sv[4 * k + 2] = __float_as_uint(b.x);
-          sv[4 * k + 3] = __float_as_uint(b.y);
-          mx[0][k & 1] = max3(mx[0][k & 1], a.x, a.y);
-          mx[1][k & 1] = max3(mx[1][k & 1], b.x, b.y);
-        }
-      } else {
-        unsigned long long vis[2][2];  // [row][key half] >> tcol
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) vis[i][hf] = visible_columns(tg, t_row[i], p.S, p.W, hf) >> tcol;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float2 k2 = *reinterpret_cast<const float2*>(ksp + 8 * k);
-          float2 a = mul2(make_float2(__uint_as_float(sv[4 * k]), __uint_as_float(sv[4 * k + 1])), k2);
-          float2 b = mul2(make_float2(__uint_as_float(sv[4 * k + 2]), __uint_as_float(sv[4 * k + 3])), k2);
-          const int hf = k >> 3, sh = 8 * (k & 7);
-          a.x = ((vis[0][hf] >> sh) & 1ull) ? a.x : -INFINITY;
-          a.y = ((vis[0][hf] >> (sh + 1)) & 1ull) ? a.y : -INFINITY;
-          b.x = ((vis[1][hf] >> sh) & 1ull) ? b.x : -INFINITY;
-          b.y = ((vis[1][hf] >> (sh + 1)) & 1ull) ? b.y : -INFINITY;
-          sv[4 * k] = __float_as_uint(a.x);
-          sv[4 * k + 1] = __float_as_uint(a.y);
-          sv[4 * k + 2] = __float_as_uint(b.x);
-          sv[4 * k + 3] = __float_as_uint(b.y);
-          mx[0][k & 1] = max3(mx[0][k & 1], a.x, a.y);
-          mx[1][k & 1] = max3(mx[1][k & 1], b.x, b.y);
-        }
-      }
-      // the reference of a row moves only when its max grew by more than 2^kLazy
-      float alpha[2] = {1.f, 1.f}, mref[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float m = fmaxf(mx[i][0], mx[i][1]);
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const float my = m * c_row[i];  // log2 units
-        if (m_run[i] == -INFINITY) {
-          m_run[i] = my == -INFINITY ? my : my + kLift;  // alpha irrelevant: nothing accumulated yet
-          alpha[i] = 0.f;
-        } else if (my > m_run[i] + kLazy) {
-          alpha[i] = ex2_approx(m_run[i] - my);
-          m_run[i] = my;
-        }
-        mref[i] = m_run[i] == -INFINITY ? 0.f : m_run[i] + ev;
-      }
-      // p = 2^(y c - mref); P' = p * v_scale (V scale folded into P)
-      float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      const float2 c2[2] = {make_float2(c_row[0], c_row[0]), make_float2(c_row[1], c_row[1])};
-      const float2 nm2[2] = {make_float2(-mref[0], -mref[0]), make_float2(-mref[1], -mref[1])};
+  const bool u8 = kForm != Form::kKv4Parts && p.p_mode == 1;
+  const Unit un = p.units[u];
+  const SeqGeom sg = p.seqs[un.seq];
+  const UnitGeom ug = unit_geom(un.t0, 2 * p.TQ, sg, p.S, p.W);
+  const UnitPart part = unit_tiles<kForm>(sp, u, ug);
+  const int n = part.n;
+  const int t0 = un.t0 + (int)c.rank * p.TQ;  // this CTA's first token
+  const int t_row[2] = {t0 + rr[0] / p.G, t0 + rr[1] / p.G};
+  const float ev = kExact ? 0.f : (float)pow2_ceil_exp(__uint_as_float(vsmax));
+  // the per-row query scale (s_q on the int8 grid, 1 for the bf16 query;
+  // sm_scale * log2(e) is in the K scales), kept positive so that -inf
+  // scores stay -inf
+  float c_row[2] = {1.f, 1.f};
+  if (p.q_mode == 1) {
+    if (!c.warp_wait(B_QREADY, k_unit & 1, 30)) return -1;
+    c_row[0] = c_rows[(k_unit & 1) * kRows + rr[0]];
+    c_row[1] = c_rows[(k_unit & 1) * kRows + rr[1]];
+  }
+  c_row[0] = fmaxf(c_row[0], 1e-30f);
+  c_row[1] = fmaxf(c_row[1], 1e-30f);
+  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f}, sp_prev[2] = {1.f, 1.f};
+  const float lift = vsmax >= 0x3f800000u ? -8.f : kLift;  // of exact tiles: scales of 1 and more
+  for (int j = 0; j < n; ++j) {
+    const uint32_t t = tc + j;
+    const TileGeom tg = tile_geom(ug, part.j0 + j, p.S, p.W);
+    if (!c.warp_wait(B_SFULL + (t & 1), (t >> 1) & 1, 31)) return -1;
+    const uint32_t sd = c.tb + lane_off + kTmS + (t & 1) * kTileKeys;
+    // this thread's K scales at +8k (two floats each); its V scales 128 floats on
+    const float* ksp = reinterpret_cast<const float*>(sm + kSmScale + (t & 1) * 1024) + tcol;
+    const float* vsp = ksp + 128;
+    tc_fence_after();
+    uint32_t sv[64];
+    tmem_ld_16x256b_x16(sd, sv);
+    // the tile's scales (normally there long since), checked while the
+    // score load is in flight
+    const bool oks = c.warp_wait(B_SCFULL + (t & 1), (t >> 1) & 1, 32);
+    tmem_wait_ld(sv);
+    if (!oks) return -1;
+    // y = S * k_scale (masked: -inf), in place, and each row's maximum; the
+    // products in fp32 pairs, the maximum three operands at a time
+    // A tile every row sees in full (most of them) takes a loop without the
+    // mask: with the mask's selects inside one loop under a condition, they
+    // were executed as predicated instructions on every tile.
+    const bool full = !tg.needs_mask && tg.nb == kTileBlocks;
+    float mx[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
+    if (full) {
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const float2 v2 = *reinterpret_cast<const float2*>(vsp + 8 * k);
-        const float2 a = fma2(make_float2(__uint_as_float(sv[4 * k]), __uint_as_float(sv[4 * k + 1])), c2[0], nm2[0]);
-        const float2 b = fma2(make_float2(__uint_as_float(sv[4 * k + 2]), __uint_as_float(sv[4 * k + 3])), c2[1], nm2[1]);
-        const float2 pa = make_float2(ex2_approx(a.x), ex2_approx(a.y));
-        const float2 pb = make_float2(ex2_approx(b.x), ex2_approx(b.y));
-        s2[0] = add2(s2[0], pa);
-        s2[1] = add2(s2[1], pb);
-        const float2 wa = mul2(pa, v2), wb = mul2(pb, v2);
-        sv[4 * k] = __float_as_uint(wa.x);
-        sv[4 * k + 1] = __float_as_uint(wa.y);
-        sv[4 * k + 2] = __float_as_uint(wb.x);
-        sv[4 * k + 3] = __float_as_uint(wb.y);
+        const float2 k2 = *reinterpret_cast<const float2*>(ksp + 8 * k);
+        const float2 a = mul2(make_float2(__uint_as_float(sv[4 * k]), __uint_as_float(sv[4 * k + 1])), k2);
+        const float2 b = mul2(make_float2(__uint_as_float(sv[4 * k + 2]), __uint_as_float(sv[4 * k + 3])), k2);
+        sv[4 * k] = __float_as_uint(a.x);
+        sv[4 * k + 1] = __float_as_uint(a.y);
+        sv[4 * k + 2] = __float_as_uint(b.x);
+        sv[4 * k + 3] = __float_as_uint(b.y);
+        mx[0][k & 1] = max3(mx[0][k & 1], a.x, a.y);
+        mx[1][k & 1] = max3(mx[1][k & 1], b.x, b.y);
       }
-      // this warp is done with the tile's scales
-      __syncwarp();
-      if (lane == 0) mbar_arrive(c.bar(B_SCEMPTY + (t & 1)));
-      float corr[2] = {alpha[0], alpha[1]};
+    } else {
+      unsigned long long vis[2][2];  // [row][key half] >> tcol
 #pragma unroll
-      for (int i = 0; i < 2; ++i) l_run[i] = l_run[i] * alpha[i] + (s2[i].x + s2[i].y);
-      if (u8) {  // P' per row on the u8 grid over the whole tile, scale max/255
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) vis[i][hf] = visible_columns(tg, t_row[i], p.S, p.W, hf) >> tcol;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float2 k2 = *reinterpret_cast<const float2*>(ksp + 8 * k);
+        float2 a = mul2(make_float2(__uint_as_float(sv[4 * k]), __uint_as_float(sv[4 * k + 1])), k2);
+        float2 b = mul2(make_float2(__uint_as_float(sv[4 * k + 2]), __uint_as_float(sv[4 * k + 3])), k2);
+        const int hf = k >> 3, sh = 8 * (k & 7);
+        a.x = ((vis[0][hf] >> sh) & 1ull) ? a.x : -INFINITY;
+        a.y = ((vis[0][hf] >> (sh + 1)) & 1ull) ? a.y : -INFINITY;
+        b.x = ((vis[1][hf] >> sh) & 1ull) ? b.x : -INFINITY;
+        b.y = ((vis[1][hf] >> (sh + 1)) & 1ull) ? b.y : -INFINITY;
+        sv[4 * k] = __float_as_uint(a.x);
+        sv[4 * k + 1] = __float_as_uint(a.y);
+        sv[4 * k + 2] = __float_as_uint(b.x);
+        sv[4 * k + 3] = __float_as_uint(b.y);
+        mx[0][k & 1] = max3(mx[0][k & 1], a.x, a.y);
+        mx[1][k & 1] = max3(mx[1][k & 1], b.x, b.y);
+      }
+    }
+    if (kExact) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) mx[i][0] = mx[i][1] = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const uint2 v2 = *reinterpret_cast<const uint2*>(vsp + 8 * k);
+        const float2 d2 = make_float2(scale_exponent(v2.x), scale_exponent(v2.y));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float pm = 0.f;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) pm = max3(pm, __uint_as_float(sv[4 * k + 2 * i]), __uint_as_float(sv[4 * k + 2 * i + 1]));
-          pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 1));
-          pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 2));
-          const float spu = pm > 0.f ? __fdiv_rn(pm, 255.f) : sp_prev[i];
-          const float inv = pm > 0.f ? __fdiv_rn(255.f, pm) : 0.f;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            sv[4 * k + 2 * i] = __float_as_uint(rintf(__uint_as_float(sv[4 * k + 2 * i]) * inv));
-            sv[4 * k + 2 * i + 1] = __float_as_uint(rintf(__uint_as_float(sv[4 * k + 2 * i + 1]) * inv));
-          }
-          corr[i] = alpha[i] * __fdiv_rn(sp_prev[i], spu);
-          sp_prev[i] = spu;
+          const float2 z = fma2(make_float2(__uint_as_float(sv[4 * k + 2 * i]), __uint_as_float(sv[4 * k + 2 * i + 1])),
+                                make_float2(c_row[i], c_row[i]), d2);
+          mx[i][k & 1] = max3(mx[i][k & 1], z.x, z.y);
         }
       }
-      // P' as fp16 pairs over S columns [0, 32) (keys 0-63) and [64, 96) (keys
-      // 64-127), where the PV issuer reads them
-      uint32_t pk0[16], pk1[16];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        pk0[2 * k] = pack_half2(__uint_as_float(sv[4 * k]), __uint_as_float(sv[4 * k + 1]));
-        pk0[2 * k + 1] = pack_half2(__uint_as_float(sv[4 * k + 2]), __uint_as_float(sv[4 * k + 3]));
-        pk1[2 * k] = pack_half2(__uint_as_float(sv[32 + 4 * k]), __uint_as_float(sv[32 + 4 * k + 1]));
-        pk1[2 * k + 1] = pack_half2(__uint_as_float(sv[32 + 4 * k + 2]), __uint_as_float(sv[32 + 4 * k + 3]));
-      }
-      tmem_st_16x128b_x8(sd, pk0);
-      tmem_st_16x128b_x8(sd + 64, pk1);
-      // O holds PV up to tile j-1 once that MMA is done; rescale this warp's
-      // rows in place.  A wait that runs out skips the rescale (the error word
-      // is set; the results of the call are void).
-      if (j > 0 && __any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f) &&
-          c.warp_wait(B_VEMPTY + ((t - 1) & 1), ((t - 1) >> 1) & 1, 33)) {
-        tc_fence_after();
-#pragma unroll 1
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t o[32];
-          const uint32_t oa = c.tb + lane_off + kTmO + 64 * cc;
-          tmem_ld_16x256b_x8(oa, o);
-          tmem_wait_ld(o);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float2 x = mul2(make_float2(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1])),
-                                  make_float2(corr[0], corr[0]));
-            const float2 y = mul2(make_float2(__uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3])),
-                                  make_float2(corr[1], corr[1]));
-            o[4 * k] = __float_as_uint(x.x);
-            o[4 * k + 1] = __float_as_uint(x.y);
-            o[4 * k + 2] = __float_as_uint(y.x);
-            o[4 * k + 3] = __float_as_uint(y.y);
-          }
-          tmem_st_16x256b_x8(oa, o);
-        }
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) c.arrive_pair_tmem(B_PFULL + (t & 1));
     }
-    if (!ok) break;
-    tc += n;
-    // each row's sum over the four threads that share it
+    // the reference of a row moves only when its max grew by more than 2^kLazy
+    float alpha[2] = {1.f, 1.f}, mref[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float l = l_run[i];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if ((lane & 3) == 0) {
-        l_rows[(k_unit & 1) * kRows + rr[i]] = l;
-        sp_rows[(k_unit & 1) * kRows + rr[i]] = kSplit ? m_run[i] : sp_prev[i];  // (the u8 grid is not split)
+      float m = fmaxf(mx[i][0], mx[i][1]);
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const float my = kExact ? m : m * c_row[i];  // log2 units
+      if (m_run[i] == -INFINITY) {
+        m_run[i] = my == -INFINITY ? my : my + (kExact ? lift : kLift);  // alpha irrelevant: nothing accumulated yet
+        alpha[i] = 0.f;
+      } else if (my > m_run[i] + kLazy) {
+        const float mn = kExact ? my + fminf(lift, 0.f) : my;
+        alpha[i] = ex2_approx(m_run[i] - mn);
+        m_run[i] = mn;
+      }
+      mref[i] = m_run[i] == -INFINITY ? 0.f : m_run[i] + ev;
+    }
+    // p = 2^(y c - mref); P' = p * v_scale (V scale folded into P)
+    float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    const float2 c2[2] = {make_float2(c_row[0], c_row[0]), make_float2(c_row[1], c_row[1])};
+    const float2 nm2[2] = {make_float2(-mref[0], -mref[0]), make_float2(-mref[1], -mref[1])};
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float2 v2 = *reinterpret_cast<const float2*>(vsp + 8 * k);
+      const float2 a = fma2(make_float2(__uint_as_float(sv[4 * k]), __uint_as_float(sv[4 * k + 1])), c2[0], nm2[0]);
+      const float2 b = fma2(make_float2(__uint_as_float(sv[4 * k + 2]), __uint_as_float(sv[4 * k + 3])), c2[1], nm2[1]);
+      const float2 pa = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+      const float2 pb = make_float2(ex2_approx(b.x), ex2_approx(b.y));
+      s2[0] = add2(s2[0], pa);
+      s2[1] = add2(s2[1], pb);
+      const float2 wa = mul2(pa, v2), wb = mul2(pb, v2);
+      sv[4 * k] = __float_as_uint(wa.x);
+      sv[4 * k + 1] = __float_as_uint(wa.y);
+      sv[4 * k + 2] = __float_as_uint(wb.x);
+      sv[4 * k + 3] = __float_as_uint(wb.y);
+    }
+    // this warp is done with the tile's scales
+    __syncwarp();
+    if (lane == 0) mbar_arrive(c.bar(B_SCEMPTY + (t & 1)));
+    float corr[2] = {alpha[0], alpha[1]};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) l_run[i] = l_run[i] * alpha[i] + (s2[i].x + s2[i].y);
+    if (u8) {  // P' per row on the u8 grid over the whole tile, scale max/255
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float pm = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) pm = max3(pm, __uint_as_float(sv[4 * k + 2 * i]), __uint_as_float(sv[4 * k + 2 * i + 1]));
+        pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 1));
+        pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 2));
+        const float spu = pm > 0.f ? __fdiv_rn(pm, 255.f) : sp_prev[i];
+        const float inv = pm > 0.f ? __fdiv_rn(255.f, pm) : 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          sv[4 * k + 2 * i] = __float_as_uint(rintf(__uint_as_float(sv[4 * k + 2 * i]) * inv));
+          sv[4 * k + 2 * i + 1] = __float_as_uint(rintf(__uint_as_float(sv[4 * k + 2 * i + 1]) * inv));
+        }
+        corr[i] = alpha[i] * __fdiv_rn(sp_prev[i], spu);
+        sp_prev[i] = spu;
       }
     }
+    // P' as fp16 pairs over S columns [0, 32) (keys 0-63) and [64, 96) (keys
+    // 64-127), where the PV issuer reads them
+    uint32_t pk0[16], pk1[16];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      pk0[2 * k] = pack_half2(__uint_as_float(sv[4 * k]), __uint_as_float(sv[4 * k + 1]));
+      pk0[2 * k + 1] = pack_half2(__uint_as_float(sv[4 * k + 2]), __uint_as_float(sv[4 * k + 3]));
+      pk1[2 * k] = pack_half2(__uint_as_float(sv[32 + 4 * k]), __uint_as_float(sv[32 + 4 * k + 1]));
+      pk1[2 * k + 1] = pack_half2(__uint_as_float(sv[32 + 4 * k + 2]), __uint_as_float(sv[32 + 4 * k + 3]));
+    }
+    tmem_st_16x128b_x8(sd, pk0);
+    tmem_st_16x128b_x8(sd + 64, pk1);
+    // O holds PV up to tile j-1 once that MMA is done; rescale this warp's
+    // rows in place.  A wait that runs out skips the rescale (the error word
+    // is set; the results of the call are void).
+    if (j > 0 && __any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f) &&
+        c.warp_wait(B_VEMPTY + ((t - 1) & 1), ((t - 1) >> 1) & 1, 33)) {
+      tc_fence_after();
+#pragma unroll 1
+      for (int cc = 0; cc < 4; ++cc) {
+        uint32_t o[32];
+        const uint32_t oa = c.tb + lane_off + kTmO + 64 * cc;
+        tmem_ld_16x256b_x8(oa, o);
+        tmem_wait_ld(o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 x = mul2(make_float2(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1])),
+                                make_float2(corr[0], corr[0]));
+          const float2 y = mul2(make_float2(__uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3])),
+                                make_float2(corr[1], corr[1]));
+          o[4 * k] = __float_as_uint(x.x);
+          o[4 * k + 1] = __float_as_uint(x.y);
+          o[4 * k + 2] = __float_as_uint(y.x);
+          o[4 * k + 3] = __float_as_uint(y.y);
+        }
+        tmem_st_16x256b_x8(oa, o);
+      }
+    }
+    tmem_wait_st();
+    tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(c.bar(B_STATS + (k_unit & 1)));
+    if (lane == 0) c.arrive_pair_tmem(B_PFULL + (t & 1));
+  }
+  // each row's sum over the four threads that share it
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float l = l_run[i];
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if ((lane & 3) == 0) {
+      l_rows[(k_unit & 1) * kRows + rr[i]] = l;
+      sp_rows[(k_unit & 1) * kRows + rr[i]] = kForm == Form::kKv4Parts ? m_run[i] + ev : sp_prev[i];  // (the u8 grid is not split)
+    }
+  }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(c.bar(B_STATS + (k_unit & 1)));
+  return n;
+}
+template <Form kForm, bool kExact>
+__device__ __forceinline__ void role_softmax(const AttnParams& p, const AttnSplit& sp, const Ctx& c, uint8_t* sm) {
+  uint32_t tc = 0;  // tiles so far
+  int k_unit = 0;
+  for (int u = c.u0; u < c.u1; u += c.ustep, ++k_unit) {
+    const int n = softmax_unit<kForm, kExact>(p, sp, c, sm, u, k_unit, tc, p.vsmax[p.units[u].seq * p.HKV + p.units[u].g]);
+    if (n < 0) break;
+    tc += n;
   }
   tmem_wait_st();
+}
+// Whether some unit of this pair has V scales too far apart.  Chosen for all of a pair's units: both kinds of tiles in one
+// loop over the units cost the common kind 4 % in registers (2 x 4096 tokens, windowed: 422 us, 413 so, 406
+// without the other kind), the exact kind alone for all 8 to 11 %.
+template <Form kForm>
+__device__ __forceinline__ bool any_unit_exact(const AttnParams& p, const Ctx& c) {
+  if (kForm == Form::kInt8) return false;
+  bool mine = false;
+  for (int u = c.u0 + (int)(threadIdx.x & 31) * c.ustep; u < c.u1; u += 32 * c.ustep) {
+    const int at = p.units[u].seq * p.HKV + p.units[u].g;
+    mine = mine || !scales_alike(p.vsmax[at], p.vsmax[p.n_seq * p.HKV + at]);
+  }
+  return __any_sync(0xffffffffu, mine);
 }
 
 // ------------------------------------------------------------------ Q codes / epilogue
@@ -918,7 +980,9 @@ __device__ __forceinline__ bool epilogue_part(const AttnSplit& sp, const Ctx& c,
   if (!c.warp_wait(B_STATS + (k_unit & 1), (k_unit >> 1) & 1, 42)) return false;
   tc_fence_after();
   const size_t row0 = (size_t)u * kUnitRows + c.rank * kRows;
-  sp.ml[row0 + r] = make_float2(m_rows[(k_unit & 1) * kRows + r], l_rows[(k_unit & 1) * kRows + r]);
+  const float m = m_rows[(k_unit & 1) * kRows + r], l = l_rows[(k_unit & 1) * kRows + r];
+  // log2 of 0 without a key; a sum past fp32's range (V rows of zeros whose weights leave the others none) stays finite
+  sp.mw[row0 + r] = make_float2(m, m + lg2_approx(l == INFINITY ? 3.4e38f : l));
   const int pc = lane & 7;
 #pragma unroll 1
   for (int cb = 0; cb < 8; ++cb) {
@@ -943,7 +1007,7 @@ __device__ __forceinline__ bool epilogue_part(const AttnSplit& sp, const Ctx& c,
   return true;
 }
 
-template <bool kSplit>
+template <Form kForm>
 __device__ __forceinline__ void role_correction(const AttnParams& p, const AttnSplit& sp, const Ctx& c, uint8_t* sm) {
   const int r = threadIdx.x - 32 * (4 + kSoftmaxWarps);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -972,7 +1036,7 @@ __device__ __forceinline__ void role_correction(const AttnParams& p, const AttnS
     }
     if (k_unit > 0) {
       const LaneRows lr = lane_rows(p, prev_t0, prev_g, prev_sg, qd, lane);
-      if (kSplit)
+      if (kForm == Form::kKv4Parts)
         ok = epilogue_part(sp, c, lr, k_unit - 1, prev_u, c.tb + lane_off + kTmO, l_rows, sp_rows, r, qd, stage, lane);
       else
         ok = epilogue(p, c, lr, k_unit - 1, c.tb + lane_off + kTmO, l_rows, sp_rows, r, stage, lane);
@@ -984,7 +1048,7 @@ __device__ __forceinline__ void role_correction(const AttnParams& p, const AttnS
   }
   if (ok && k_unit > 0) {
     const LaneRows lr = lane_rows(p, prev_t0, prev_g, prev_sg, qd, lane);
-    if (kSplit)
+    if (kForm == Form::kKv4Parts)
       (void)epilogue_part(sp, c, lr, k_unit - 1, prev_u, c.tb + lane_off + kTmO, l_rows, sp_rows, r, qd, stage, lane);
     else
       (void)epilogue(p, c, lr, k_unit - 1, c.tb + lane_off + kTmO, l_rows, sp_rows, r, stage, lane);
@@ -1003,7 +1067,7 @@ __device__ __forceinline__ void take_units(const AttnParams& p, Ctx& c) {
   }
 }
 
-template <bool kSplit>
+template <Form kForm>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnMaps m,
                      const __grid_constant__ AttnSplit sp) {
@@ -1017,7 +1081,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   c.rank = cluster_rank();
   c.pair = (int)(blockIdx.x >> 1);
   c.n_pairs = (int)(gridDim.x >> 1);
-  if (!p.early) take_units(p, c);
+  constexpr bool kEarly = kForm != Form::kInt8;  // launched early: set up while the launch before ends
+  if (!kEarly) take_units(p, c);
   c.wc = WaitCtl{p.err, p.wait_ns};
   // a launch queued behind this one that reads nothing this one writes may
   // start on each pair this one leaves
@@ -1061,7 +1126,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync_all();  // both CTAs' barriers exist before either may arrive on the other's
   tc_fence_after();
   c.tb = *tmem_slot;
-  if (p.early) {
+  if (kEarly) {
     wait_for_previous();
     take_units(p, c);  // not before: the plan may be on its way up
   }
@@ -1069,18 +1134,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   if (warp < 4) {
     if (warp == 0) {
-      if (lane < kKSlots) role_producer_k<kSplit>(p, sp, m, c, lane);
+      if (lane < kKSlots) role_producer_k<kForm>(p, sp, m, c, lane);
     } else if (warp == 1) {
-      if (lane == 0 && c.rank == 0) role_mma<kSplit>(p, sp, c);
+      if (lane == 0 && c.rank == 0) role_mma<kForm>(p, sp, c);
     } else if (warp == 2) {
-      if (lane < kVSlots) role_producer_v<kSplit>(p, sp, m, c, lane);
+      if (lane < kVSlots) role_producer_v<kForm>(p, sp, m, c, lane);
     } else {
-      if (lane < 5) role_producer_q<kSplit>(p, sp, m, c, lane);
+      if (lane < 5) role_producer_q<kForm>(p, sp, m, c, lane);
     }
   } else if (warp < 4 + kSoftmaxWarps) {
-    role_softmax<kSplit>(p, sp, c, sm);
+    if (any_unit_exact<kForm>(p, c)) role_softmax<kForm, true>(p, sp, c, sm);
+    else role_softmax<kForm, false>(p, sp, c, sm);
   } else {
-    role_correction<kSplit>(p, sp, c, sm);
+    role_correction<kForm>(p, sp, c, sm);
   }
   // the odd CTA's TMEM and shared memory are in use until the pair's last MMA is done
   if (c.rank == 1 && warp == 1 && lane == 0) (void)mbar_wait_drain(c.bar(B_DRAIN), 0, kDrainNs);
@@ -1105,35 +1171,37 @@ __global__ void __launch_bounds__(256) join_units_kernel(const __grid_constant__
   const int r = blockIdx.y * 4 + (threadIdx.x >> 6), d4 = threadIdx.x & 63;
   const RowInfo ri = row_info(p, un.t0, un.g, sg, r);
   if (!ri.valid) return;
-  float m = -INFINITY, l = 0.f;
+  float m = -INFINITY, w = -INFINITY, l = 0.f;  // acc in units of 2^m, the weights' sum l 2^w
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  // what exponents are taken from: not -inf where no key of these is in the row's sight (or NaN, which stays in the sums)
+  const auto finite_ref = [](float x) { return x == -INFINITY ? 0.f : x; };
   constexpr int kAtOnce = 4;
   for (int i = 0; i < un.n; i += kAtOnce) {
-    float2 ml[kAtOnce];
+    float2 mw[kAtOnce];
     float4 v[kAtOnce];
 #pragma unroll
     for (int e = 0; e < kAtOnce; ++e) {
       const size_t row = (size_t)(un.first + imin(i + e, un.n - 1)) * kUnitRows + r;
-      ml[e] = __ldcg(sp.ml + row);
+      mw[e] = __ldcg(sp.mw + row);
       v[e] = __ldcg(reinterpret_cast<const float4*>(sp.o + row * kHeadDim) + d4);
-      if (i + e >= un.n) ml[e].x = -INFINITY;
+      if (i + e >= un.n) mw[e] = make_float2(-INFINITY, -INFINITY);
     }
-    float mn = m;
+    float mn = m, wn = w;
 #pragma unroll
-    for (int e = 0; e < kAtOnce; ++e) mn = fmaxf(mn, ml[e].x);
-    const float ref = mn == -INFINITY ? 0.f : mn;  // no key of these in the row's sight (or NaN, which stays in the sum)
-    const float al = ex2_approx(m - ref);
-    l *= al;
+    for (int e = 0; e < kAtOnce; ++e) mn = fmaxf(mn, mw[e].x), wn = fmaxf(wn, mw[e].y);
+    const float m_ref = finite_ref(mn), w_ref = finite_ref(wn);
+    const float al = ex2_approx(m - m_ref);
+    l *= ex2_approx(w - w_ref);
     acc = make_float4(acc.x * al, acc.y * al, acc.z * al, acc.w * al);
 #pragma unroll
     for (int e = 0; e < kAtOnce; ++e) {
-      const float w = ex2_approx(ml[e].x - ref);
-      l += w * ml[e].y;
-      acc = make_float4(acc.x + w * v[e].x, acc.y + w * v[e].y, acc.z + w * v[e].z, acc.w + w * v[e].w);
+      const float f = ex2_approx(mw[e].x - m_ref);
+      l += ex2_approx(mw[e].y - w_ref);
+      acc = make_float4(acc.x + f * v[e].x, acc.y + f * v[e].y, acc.z + f * v[e].z, acc.w + f * v[e].w);
     }
-    m = mn;
+    m = mn, w = wn;
   }
-  const float fin = l == 0.f ? 0.f : 1.f / l;
+  const float fin = l == 0.f ? 0.f : ex2_approx(m - w) / l;
   const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * fin, acc.y * fin), hi = __floats2bfloat162_rn(acc.z * fin, acc.w * fin);
   uint4 out = make_uint4(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi), 0u, 0u);
   if (p.gate) {
@@ -1190,7 +1258,7 @@ cudaError_t launch_debug_qcodes(const __nv_bfloat16* q, int n, int8_t* codes, fl
 int attention_pairs(int n_sm) {
   static int max_pairs = -1;
   if (max_pairs < 0) {
-    if (cudaFuncSetAttribute(attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem) !=
+    if (cudaFuncSetAttribute(attention_kernel<Form::kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem) !=
         cudaSuccess) {
       (void)cudaGetLastError();
       return imax(1, n_sm / 2);
@@ -1200,7 +1268,7 @@ int attention_pairs(int n_sm) {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kAttnSmem;
     int mc = 0;
-    if (cudaOccupancyMaxActiveClusters(&mc, attention_kernel<false>, &cfg) != cudaSuccess || mc <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&mc, attention_kernel<Form::kInt8>, &cfg) != cudaSuccess || mc <= 0) {
       (void)cudaGetLastError();
       mc = imax(1, n_sm / 2);
     }
@@ -1210,14 +1278,15 @@ int attention_pairs(int n_sm) {
 }
 
 cudaError_t launch_attention(const AttnParams& p, const AttnMaps& m, int n_sm, cudaStream_t st, bool overlap_prev) {
-  cudaError_t e = cudaFuncSetAttribute(attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem);
+  const auto kernel = p.kv4 ? attention_kernel<Form::kKv4> : attention_kernel<Form::kInt8>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem);
   if (e != cudaSuccess) return e;
   // persistent grid: one CTA pair per co-resident cluster slot (or per unit),
   // or the pairs the host assigned the units to
   const int pairs = p.pair_off ? p.plan_pairs : imax(1, imin(p.n_units, attention_pairs(n_sm)));
-  if (p.early) return launch_early(attention_kernel<false>, dim3(2 * (unsigned)pairs), kThreads, kAttnSmem, st, p, m, AttnSplit{});
+  if (p.kv4) return launch_early(kernel, dim3(2 * (unsigned)pairs), kThreads, kAttnSmem, st, p, m, AttnSplit{});
   if (!overlap_prev) {
-    attention_kernel<false><<<2 * pairs, kThreads, kAttnSmem, st>>>(p, m, AttnSplit{});
+    attention_kernel<Form::kInt8><<<2 * pairs, kThreads, kAttnSmem, st>>>(p, m, AttnSplit{});
     return cudaGetLastError();
   }
   // programmatic dependent launch: its pairs start as the previous attention
@@ -1232,14 +1301,14 @@ cudaError_t launch_attention(const AttnParams& p, const AttnMaps& m, int n_sm, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_kernel<false>, p, m, AttnSplit{});
+  return cudaLaunchKernelEx(&cfg, attention_kernel<Form::kInt8>, p, m, AttnSplit{});
 }
 
 cudaError_t launch_attention_split(const AttnParams& p, const AttnMaps& m, const AttnSplit& sp, const SplitUnit* units,
                                    int n_units, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem);
+  cudaError_t e = cudaFuncSetAttribute(attention_kernel<Form::kKv4Parts>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem);
   if (e != cudaSuccess) return e;
-  e = launch_early(attention_kernel<true>, dim3((unsigned)(2 * p.n_units)), kThreads, kAttnSmem, st, p, m, sp);
+  e = launch_early(attention_kernel<Form::kKv4Parts>, dim3((unsigned)(2 * p.n_units)), kThreads, kAttnSmem, st, p, m, sp);
   if (e != cudaSuccess) return e;
   return launch_early(join_units_kernel, dim3((unsigned)n_units, kUnitRows / 4), 256, 0, st, p, sp, units);
 }

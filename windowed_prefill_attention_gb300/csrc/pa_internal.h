@@ -38,7 +38,9 @@ struct WidenParams {
   __half* vt;                 // [HKV][256][n_tok_cap]   integer-valued fp16 V codes, transposed
   float* ks;                  // [HKV][n_tok_cap]        per-token K scale
   float* vs;                  // [HKV][n_tok_cap]        per-token V scale
-  unsigned int* vsmax;        // [n_seq][HKV] float bits: max V scale (atomicMax)
+  // [n_seq][HKV] float bits: max V scale (atomicMax); of the 4-bit pool then [n_seq][HKV] 0x7f800000 - those of the least
+  // V scale over 0 (0 where there is none)
+  unsigned int* vsmax;
   int* err;
   float k_mult = 1.f;         // ks = k_scale * k_mult (the attention folds sm_scale * log2(e) in here)
 };
@@ -56,7 +58,8 @@ struct AttnParams {
   int plan_pairs;
   const float* ks;
   const float* vs;
-  const unsigned int* vsmax;
+  const unsigned int* vsmax;  // as WidenParams::vsmax
+  int n_seq;
   __nv_bfloat16* out;         // [total_q][HQ][256]
   const __nv_bfloat16* gate;  // [total_q][HQ][256] output gate (sigmoid), or nullptr
   int HQ, HKV, G, TQ;         // TQ = 128 / G: tokens per CTA, half a unit
@@ -69,7 +72,7 @@ struct AttnParams {
   const unsigned int* q_ready;  // nullptr, or a word that equals q_epoch once q holds the units' rows
   unsigned int q_epoch;
   int debug_stall;            // test hook: first wait targets a barrier nothing arrives at
-  int early;                  // launched early: set up while the launch before ends, which it waits for
+  bool kv4;                   // K and V are the 4-bit pool's; launched early, behind a wait for the launch before
 };
 
 // Units whose keys are split (few units, long contexts): a part of a unit's key
@@ -85,8 +88,8 @@ struct SplitUnit {
 };
 struct AttnSplit {
   const UnitPart* parts;
-  float* o;     // [slot][256 rows][256]: sum of 2^(y - m) v
-  float2* ml;   // [slot][256 rows]: m (log2; -inf: no key), sum of 2^(y - m)
+  float* o;     // [slot][256 rows][256]: sum of 2^(y - m) v, v with its scale; each part's rows have an m of their own
+  float2* mw;   // [slot][256 rows]: m (log2; -inf: no key), log2 of the sum of 2^y
 };
 
 struct AttnMaps {

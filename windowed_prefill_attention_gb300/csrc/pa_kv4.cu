@@ -255,10 +255,10 @@ __global__ void __launch_bounds__(kWidenThreads) kv4_widen_kernel(const __grid_c
   constexpr int kVWords = (2048 + 256) / 16;  // V's codes and block scales of a tile
   constexpr int kVLoads = (HKV * kVWords + kWidenThreads - 1) / kWidenThreads;
   __shared__ uint4 v_sh[HKV * kVWords];
-  __shared__ unsigned int vmax_sh[HKV];
+  __shared__ unsigned int vmax_sh[2 * HKV];  // the largest V scale's bits, 0x7f800000 - those of the least over 0
   const int blk = blockIdx.x, tid = threadIdx.x;
   dependents_may_start();
-  if (tid < HKV) vmax_sh[tid] = 0u;
+  if (tid < 2 * HKV) vmax_sh[tid] = 0u;
   wait_for_previous();
   // the block's sequence: the last one that starts at or before it
   int s = -1;
@@ -347,21 +347,24 @@ __global__ void __launch_bounds__(kWidenThreads) kv4_widen_kernel(const __grid_c
       store_pair(o, reinterpret_cast<uint4*>(row), reinterpret_cast<uint4*>(row + 2 * (size_t)p.n_tok_cap), tid & 1);
     }
   }
-  // scales (0 past the end of the context) and the largest V scale, as widen_kernel has them
+  // scales (0 past the end of the context), the largest V scale and the least
   if (tid < kPage * HKV) {
     const int r = tid & 15, g = tid >> 4;
     p.ks[(size_t)g * p.n_tok_cap + row0 + r] = ks_row * p.k_mult;
     p.vs[(size_t)g * p.n_tok_cap + row0 + r] = vs_row;
-    if (vs_row > 0.f) atomicMax(&vmax_sh[g], __float_as_uint(vs_row));
+    if (vs_row > 0.f) {
+      atomicMax(&vmax_sh[g], __float_as_uint(vs_row));
+      atomicMax(&vmax_sh[HKV + g], 0x7f800000u - __float_as_uint(vs_row));
+    }
   }
   __syncthreads();
-  if (tid < HKV) {
+  if (tid < 2 * HKV) {
     const unsigned int m = vmax_sh[tid];
-    unsigned int* gm = p.vsmax + s * HKV + tid;
+    unsigned int* gm = p.vsmax + (tid < HKV ? s * HKV + tid : (p.n_seq + s) * HKV + tid - HKV);
     if (m > *reinterpret_cast<volatile unsigned int*>(gm)) atomicMax(gm, m);
   }
 }
-// The largest V scales before the widening raises them (a kernel and not a memset: the widening
+// The largest and least V scales before the widening raises them (a kernel and not a memset: the widening
 // is then set up early too; 2 us of a call of few tokens).  The widening may start behind the wait
 // only: with the last call's attention on most SMs its CTAs would crowd on the others.
 __global__ void __launch_bounds__(256) zero_kernel(unsigned int* x, int n) {
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(256) zero_kernel(unsigned int* x, int n) {
 
 template <int HKV>
 cudaError_t launch_widen(const WidenParams& p, const uint8_t* pool, cudaStream_t st) {
-  const cudaError_t e = launch_early(zero_kernel, dim3(1), 256, 0, st, p.vsmax, p.n_seq * HKV);
+  const cudaError_t e = launch_early(zero_kernel, dim3(1), 256, 0, st, p.vsmax, 2 * p.n_seq * HKV);
   if (e != cudaSuccess) return e;
   return launch_early(kv4_widen_kernel<HKV>, dim3((unsigned)p.n_stored_blocks), kWidenThreads, 0, st, p, pool);
 }

@@ -63,9 +63,7 @@ constexpr int kSmBars = kWarps * kStages * kStepBytes;
 constexpr int kSmem = kSmBars + kWarps * kStages * 8 + 128;
 constexpr float kMargin = 8.f;  // log2: how far y and z may pass the largest ones at their references' last move
 constexpr float kLift = 7.f;    // m is that largest y, n that largest z - kLift: p <= 2^8, P' <= 2^15
-// Biased exponent that d is taken from: of row scales from 2^-100, the least that the append writes, on; for
-// less, and 0, d stays there (2^(m - n) is then at most 2^107)
-constexpr uint32_t kLeastExp = 27;
+// (2^(m - n) is at most 2^107: d is at least -99, the append's least scale being 2^-100)
 constexpr int kMergeWarps = 32;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr unsigned kAll = 0xffffffffu;
@@ -298,7 +296,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv4_decode_kernel(con
         for (int r = 0; r < 2; ++r) {
           const uint32_t bits = lds32(at + row_at + 64 + 32 * r);  // not negative
           vs[e][r] = __uint_as_float(bits);
-          d[r] = __uint_as_float(0x4b000000u | max(kLeastExp, bits >> 23)) - (8388608.f + 126.f);  // exponent - 126, exactly
+          d[r] = scale_exponent(bits);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {

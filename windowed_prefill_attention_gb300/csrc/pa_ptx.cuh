@@ -546,4 +546,10 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// d with 2^(d - 1) <= x < 2^d, of the bits of a float x >= 0; at least -99 (also for 0), and finite whatever the bits.
+__device__ __forceinline__ float scale_exponent(uint32_t bits) {
+  const uint32_t e = (bits >> 23) > 27u ? bits >> 23 : 27u;
+  return __uint_as_float(0x4b000000u | e) - (8388608.f + 126.f);  // e - 126, exactly
+}
+
 }  // namespace pa
