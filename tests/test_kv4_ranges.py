@@ -245,3 +245,56 @@ def test_prefill_on_the_integer_grids_behind_which_a_far_larger_row_lies(q_mode,
             steps = 2 * half_step if p_mode == 0 else 1.02 / 255
             bound = bound + 2 * 2.0 ** -11 * weighed + steps * 2688 * (t + 1) * share[h]
             assert np.all(np.abs(a[h] - b[h]) <= bound), (row, h)
+
+
+@pytest.mark.parametrize("drop", [60, 90, 108, 114, 117, 119, 121, 123, 125, 130])
+def test_prefill_on_the_u8_grid_of_tiles_of_next_to_no_weight(drop):
+    """Keys behind the first tile whose weights are 2^-drop of those in it: the u8 grid's step for their tile would be
+    under fp32's range, or O in units of it over that.  The outputs are the first tile's."""
+    base = bf16_round(np.random.default_rng(17).standard_normal(D).astype(np.float32)).astype(np.float64)
+    sm = 1 / 16
+
+    def change(k, v, slots):
+        for pages, rows in slots:
+            for at in range(len(pages)):
+                k[pages[at], rows[at]] = -base * (drop * np.log(2) / (base @ base) / sm) if at >= 128 else 0.0
+
+    lengths = [420, 300]
+    c = cache_of(68, lengths, 8, 2, change)
+    q = np.tile(base.astype(np.float32), (60, 8, 1))
+    got, rows = prefill(c, [(380, 40), (280, 20)], q, 1, 0, sm, options=dict(p_mode=1))
+    for row, s, t in rows:
+        for h in range(8):
+            vv = c.v[s][:128, h // 4]
+            # half a step of the grid, 1/255 of the tile's largest weight x scale, for each key; codes are at most 2688
+            scale = np.abs(vv).max()
+            bound = 2.0 ** -8 * np.abs(vv.mean(0)) + 0.51 / 255 * scale + 2.0 ** -10 * np.abs(vv).mean(0) + 2.0 ** (7 - drop) * scale
+            assert np.all(np.abs(got[row, h] - vv.mean(0)) <= bound), (row, h)
+
+
+@pytest.mark.parametrize("drop", [90, 108, 117, 123])
+def test_int8_prefill_on_the_u8_grid_of_tiles_of_next_to_no_weight(drop):
+    """The same of the int8 pool: V codes of the first 128 keys, K codes of 0 there, a large negative score behind."""
+    import torch
+
+    import windowed_prefill_attention_gb300 as pa
+    rng = np.random.default_rng(18)
+    n, new, sm = 420, 40, 1 / 16
+    pages = -(-n // PAGE)
+    codes = rng.integers(-127, 128, D)
+    kc = np.zeros((pages, PAGE, 2, D), np.int8)
+    kc.reshape(-1, 2, D)[128:] = -codes
+    vc = rng.integers(-127, 128, (pages, PAGE, 2, D)).astype(np.int8)
+    q = bf16_round(np.tile(codes.astype(np.float32) / 64, (new, 8, 1)))
+    ks = np.full((pages, PAGE, 2), drop * np.log(2) / sm / (q[0, 0].astype(np.float64) @ codes), np.float32)
+    vs = np.full((pages, PAGE, 2), 0.01, np.float32)
+    kc, vc, ks, vs = (torch.from_numpy(x).cuda() for x in (kc, vc, ks, vs))
+    dq, bt = dev_bf16(q), torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    out = torch.zeros_like(dq)
+    h = pa.Handle(8, 2, pages, pages, p_mode=1)
+    pa.pa_prefill_batch(h.h, np.array([(0, n - new, new, n)], np.int32), dq, kc, vc, ks, vs, bt, 1, 0, sm, out)
+    assert pa.pa_last_error(h.h) == 0
+    for g in range(2):
+        v = vc.cpu().numpy().astype(np.float64).reshape(-1, 2, D)[:128, g] * np.float64(np.float32(0.01))
+        bound = 2.0 ** -8 * np.abs(v.mean(0)) + 0.51 / 255 * 1.27 + 2.0 ** -10 * np.abs(v).mean(0) + 2.0 ** (7 - drop)
+        assert np.all(np.abs(host(out)[:, 4 * g: 4 * g + 4] - v.mean(0)) <= bound)

@@ -720,8 +720,11 @@ __device__ __forceinline__ int softmax_unit(const AttnParams& p, const AttnSplit
         for (int k = 0; k < 16; ++k) pm = max3(pm, __uint_as_float(sv[4 * k + 2 * i]), __uint_as_float(sv[4 * k + 2 * i + 1]));
         pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 1));
         pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 2));
-        const float spu = pm > 0.f ? __fdiv_rn(pm, 255.f) : sp_prev[i];
-        const float inv = pm > 0.f ? __fdiv_rn(255.f, pm) : 0.f;
+        // O is held in units of the step, so behind a tile of ordinary weights one of next to none may not set it: O would
+        // leave fp32's range, like the inverse of a step under 2^-126.  Its codes are 0.
+        const bool sets = pm >= 0x1p-118f && (pm >= 0x1p-80f || j == 0 || sp_prev[i] < 0x1p-88f);
+        const float spu = sets ? __fdiv_rn(pm, 255.f) : sp_prev[i];
+        const float inv = sets ? __fdiv_rn(255.f, pm) : 0.f;
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           sv[4 * k + 2 * i] = __float_as_uint(rintf(__uint_as_float(sv[4 * k + 2 * i]) * inv));
