@@ -1,0 +1,46 @@
+"""Calls on pages beside each other."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+def test_compactions_of_large_pools_from_threads():
+    """Handles whose marks take more shared memory than a kernel has without asking, each its own amount."""
+    import threading
+
+    import torch
+
+    import windowed_prefill_attention_gb300 as pa
+    steps, errors, tables, lives = 300, [], {}, {}
+
+    def run(n_pool):
+        try:
+            torch.cuda.set_device(0)
+            st = torch.cuda.Stream()
+            h = pa.Handle(4, 2, n_pool, 4)
+            bt = torch.tensor([[n_pool - 1, n_pool // 2, -1, -1]], dtype=torch.int32, device="cuda")
+            nt = torch.empty_like(bt)
+            live = torch.zeros(1, dtype=torch.int32, device="cuda")
+            part = torch.zeros(n_pool, 1, dtype=torch.int32, device="cuda")
+            seqs = np.array([(0, 0, 1, 32)], np.int32)
+            torch.cuda.synchronize()
+            gate.wait()
+            for _ in range(steps):
+                pa.pa_pages_compact(h.h, seqs, 1, 0, bt, nt, [part], live, stream=st)
+            st.synchronize()
+            assert pa.pa_last_error(h.h) == 0
+            tables[n_pool], lives[n_pool] = nt.cpu().tolist(), int(live)
+        except Exception as e:  # raised again by the test's own thread
+            errors.append(e)
+            gate.abort()
+
+    sizes = (1000000, 500000, 700000)
+    gate = threading.Barrier(len(sizes))
+    threads = [threading.Thread(target=run, args=(n,)) for n in sizes]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert lives == {n: 2 for n in sizes} and tables == {n: [[1, 0, -1, -1]] for n in sizes}

@@ -292,7 +292,8 @@ cudaError_t launch_pages_mark_plan(const CompactParams& p, const Contexts& ctx, 
   cudaError_t e = cudaSuccess;
   with_few(ctx, p.n_seq, [&](const auto& c) {
     auto* kernel = mark_plan_kernel<sizeof(c.n_ctx) / sizeof(int)>;
-    if (bytes > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    // the limit is the function's, not this call's: the same from every thread and handle
+    if (bytes > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOneCtaPages / 8);
     if (e == cudaSuccess) e = launch_early(kernel, dim3(1), kPlanThreads, (size_t)bytes, st, p, c);
   });
   return e;
