@@ -487,8 +487,8 @@ int pa_pages_fork(pa_handle h, int n_fork, const pa_fork* forks, int n_rows, int
  * gets the rows with the new pages, -1 for entries given up, and entries behind a
  * sequence's last as they were.  Afterwards the pages [L, n_pool_pages) are free; all
  * rows that use pages of the parts have to be among the sequences.
- * Entries in use outside the pool are kept and reported (PA_EBADPAGE).  new_table (but
- * in place), n_live and the parts must not overlap each other or the table
+ * Entries in use outside the pool are kept and reported (PA_EBADPAGE).  Handles of more than 2^30
+ * pages are refused (PA_EINVAL).  new_table (but in place), n_live and the parts must not overlap each other or the table
  * (PA_EINVAL).  n_seq 0 sets *n_live to 0.  Work buffers as pa_kv4_decode has them.  Asynchronous on `stream`. */
 int pa_pages_compact(pa_handle h, int n_seq, const pa_seq* seqs, int n_sink_blk, int n_win_blk,
                      const int32_t* block_table, int32_t* new_table, int n_parts, const pa_part* parts,

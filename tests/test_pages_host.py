@@ -51,3 +51,10 @@ def test_compact_refusals():
               dict(nt=TABLE + 16), dict(live=None), dict(live=LIVE + 1), dict(live=TABLE), dict(live=NEW + 4), dict(live=A + 8),
               dict(parts=((NEW + 16, 64),)), dict(parts=((A, 64), (A, 64))), dict(n_seq=-1)):
         assert _compact(**b) == pa.PA_EINVAL, b
+
+
+def test_compact_of_more_pages_than_its_kernels_count():
+    """Page numbers past 2^31 - 32, rounded up to whole words of marks, would leave int32."""
+    s = np.array([(0, 0, 1, 20)], np.int32)
+    for n_pool, want in ((1 << 30, pa.PA_OK), ((1 << 30) + 1, pa.PA_EINVAL), (2 ** 31 - 1, pa.PA_EINVAL)):
+        assert pa._lib.pa_debug_pages_compact_check(n_pool, MAX_PAGES, 1, s.ctypes.data, 1, TABLE, NEW, *_parts(), LIVE) == want

@@ -2270,6 +2270,7 @@ int fork_args(int n_pool, int max_pages, int n_fork, const pa_fork* forks, int n
 int compact_args(int n_pool, int max_pages, int n_seq, const pa_seq* seqs, int S, const int32_t* bt, int32_t* nt,
                  int n_parts, const pa_part* parts, int32_t* n_live, PageParts& out) {
   if (n_seq < 0 || (n_seq > 0 && (!seqs || !bt || !nt)) || S < 0 || !n_live || !aligned(n_live, 4)) return PA_EINVAL;
+  if (n_pool > (1 << 30)) return PA_EINVAL;  // the kernels' page numbers, rounded up to words of marks, are ints
   if (!aligned(bt, 4) || !aligned(nt, 4)) return PA_EINVAL;
   for (int s = 0; s < n_seq; ++s)
     if (seqs[s].n_ctx < 0 || seqs[s].n_ctx > (long long)max_pages * kPage || seqs[s].n_ctx > (1 << 30)) return PA_EINVAL;
