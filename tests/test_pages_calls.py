@@ -44,3 +44,20 @@ def test_compactions_of_large_pools_from_threads():
         t.join()
     assert not errors, errors
     assert lives == {n: 2 for n in sizes} and tables == {n: [[1, 0, -1, -1]] for n in sizes}
+
+
+def test_a_bad_page_is_reported_of_a_fork_without_pools():
+    import torch
+
+    import windowed_prefill_attention_gb300 as pa
+    h = pa.Handle(4, 2, 8, 3)
+    bt = torch.tensor([[1, 8, -1], [-1, -1, -1], [2, 3, -1], [-1, -1, -1]], dtype=torch.int32, device="cuda")
+    part = torch.zeros(8, 4, dtype=torch.int32, device="cuda")
+    for parts in ([part], []):
+        for src, want in ((0, pa.PA_EBADPAGE), (2, 0)):
+            t = bt.clone()
+            pa.pa_pages_fork(h.h, [(src, 1, 20, 5)], t, parts)
+            assert pa.pa_last_error(h.h) == want, (src, len(parts))
+            assert t[1].tolist() == [1 + src // 2, 5, -1]
+        pa.pa_pages_fork(h.h, [(0, 1, 32, 5)], bt.clone(), parts)  # whole pages are taken over unread
+        assert pa.pa_last_error(h.h) == 0

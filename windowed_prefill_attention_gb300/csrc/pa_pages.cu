@@ -60,6 +60,10 @@ __global__ void __launch_bounds__(kWarps * 32) fork_kernel(const __grid_constant
       const int4 k = forks.fork[f];
       const int32_t* src = p.table + (size_t)k.x * p.stride;
       int32_t* dst = p.table + (size_t)k.y * p.stride;
+      if (parts.n == 0 && k.z % kPage != 0 && lane == 0) {  // else the copies report it
+        const int from = src[k.z / kPage];
+        if (from < 0 || from >= p.n_pool) record_bad_page(p.err);
+      }
       for (int i = lane; i < (k.z + kPage - 1) / kPage; i += 32) dst[i] = i < k.z / kPage ? src[i] : k.w;
     }
     return;
