@@ -322,6 +322,7 @@ struct pa_ctx {
 namespace {
 
 int cuda_fail(cudaError_t e) {
+  (void)cudaGetLastError();  // reported once: not to be found again behind the next launch
   if (e == cudaErrorMemoryAllocation) return PA_ENOMEM;
   return PA_ECUDA;
 }
@@ -442,9 +443,14 @@ int prepare(pa_handle h, int n_seq, const pa_seq* seqs, int S, int W, cudaStream
     key.push_back(seqs[s].n_q);
     key.push_back(seqs[s].n_ctx);
   }
-  if (!h->plan_key.empty() && same_plan_key(key, h->plan_key)) return PA_OK;
+  int rc;
+  if (!h->plan_key.empty() && same_plan_key(key, h->plan_key)) {
+    // another call may have lost the workspace since, in an allocation that failed
+    if ((rc = reserve_rows(h, (size_t)h->plan.n_tok_total))) return rc;
+    return grow(h->vsmax, h->vsmax_cap, 2 * (size_t)n_seq * h->HKV);
+  }
   Plan P;
-  int rc = build_plan(h->HQ, h->HKV, n_seq, seqs, S, W, h->max_pages, P);
+  rc = build_plan(h->HQ, h->HKV, n_seq, seqs, S, W, h->max_pages, P);
   if (rc) return rc;
   // the units laid out pair by pair for the kernel's pairs, the pair offsets after them
   const int n_u = (int)P.units.size();
@@ -458,6 +464,7 @@ int prepare(pa_handle h, int n_seq, const pa_seq* seqs, int S, int W, cudaStream
   // and the split units after those
   const size_t n_whole = (size_t)n_u + pair_off_records(P.n_pairs);
   const size_t n_rec = n_whole + split_records(P);
+  h->plan_key.clear();  // from here on the tables on the device may be another plan's than h->plan, or gone
   // workspace
   if ((rc = reserve_rows(h, (size_t)P.n_tok_total))) return rc;
   if ((rc = grow(h->vsmax, h->vsmax_cap, 2 * (size_t)n_seq * h->HKV))) return rc;
