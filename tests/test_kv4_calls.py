@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from kv4_testutil import D, random_rows
-from test_kv4 import PREFILL_FLOOR, Cache, check, decode, dev_bf16, host
+from test_kv4 import DECODE_FLOOR, PREFILL_FLOOR, Cache, check, dev_bf16, host
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +75,70 @@ def test_prefill_after_one_whose_workspace_does_not_fit():
         assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
         if call is kv4:
             check(host(outs[0]), q.astype(np.float64), c, [(i, 0, 184 + i) for i in range(16)], 1, 0, 1 / 16, PREFILL_FLOOR)
+
+
+def test_recorded_times_of_whole_and_split_prefills():
+    """Each call adds one widening and one attention time, split units or not, and they are of the call's own work."""
+    import torch
+
+    import windowed_prefill_attention_gb300 as pa
+    c = Cache(62, [30000], 8, 2)
+    h = pa.Handle(8, 2, c.n_pool, c.max_pages, record_timing=True)
+    dq = dev_bf16(random_rows(np.random.default_rng(11), (3000, 8, D)))
+    out = torch.zeros_like(dq)
+
+    def times(seqs, calls):
+        for _ in range(calls):
+            pa.pa_kv4_prefill(h.h, np.array(seqs, np.int32), dq, c.d_tiles, c.d_bt, 1, 0, 1 / 16, out)
+        assert pa.pa_last_error(h.h) == 0
+        got = pa.pa_timing(h.h, reset=True)
+        assert got[2] == calls
+        return got[0] / calls, got[1] / calls
+
+    times([(0, 29970, 30, 30000)], 2)
+    split = times([(0, 29970, 30, 30000)], 3)     # 235 tiles over many pairs
+    whole = times([(0, 27000, 3000, 30000)], 3)   # as many tiles for each of 188 units
+    short = times([(0, 0, 30, 30)], 3)            # one tile
+    assert min(split + whole + short) > 0
+    assert whole[1] > 5 * split[1] > 5 * short[1]
+    assert whole[0] > 2 * short[0] and split[0] > 2 * short[0]  # 1875 blocks widened, and 2
+
+
+def test_captured_decodes_keep_their_buffers_when_a_larger_call_moves_them():
+    import torch
+
+    import windowed_prefill_attention_gb300 as pa
+    c = Cache(63, [40000, 900, 300], 8, 2)
+    short, long = [(1, 1, 900), (2, 2, 300)], [(0, 0, 40000)]
+
+    def seqs_of(rows):
+        return np.array([(r, n - 1, 1, n) for r, _, n in rows], np.int32), c.d_bt[[s for _, s, _ in rows]].contiguous()
+
+    q = random_rows(np.random.default_rng(12), (3, 8, D))
+    dq = dev_bf16(q)
+    (seqs, bt), (l_seqs, l_bt) = seqs_of(short), seqs_of(long)
+    want = torch.zeros_like(dq)
+    pa.pa_kv4_decode(c.h, seqs, dq, c.d_tiles, bt, 1, 0, 1 / 16, want)
+    outs = [torch.zeros_like(dq) for _ in range(2)]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g, o in zip(graphs, outs):
+        with torch.cuda.graph(g):
+            pa.pa_kv4_decode(c.h, seqs, dq, c.d_tiles, bt, 1, 0, 1 / 16, o)
+    with pytest.raises(pa.PAError) as e:  # the longer call's partials do not fit yet, and may not be made room for here
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            pa.pa_kv4_decode(c.h, l_seqs, dq, c.d_tiles, l_bt, 1, 0, 1 / 16, outs[0])
+    assert e.value.code == pa.PA_ENOMEM
+    torch.cuda.synchronize()
+    big = torch.zeros_like(dq)
+    pa.pa_kv4_decode(c.h, l_seqs, dq, c.d_tiles, l_bt, 1, 0, 1 / 16, big)
+    first = big.clone()
+    for i in range(3):  # replays between calls on the new buffers
+        for g, o in zip(graphs, outs):
+            o.zero_()
+            g.replay()
+            big.zero_()
+            pa.pa_kv4_decode(c.h, l_seqs, dq, c.d_tiles, l_bt, 1, 0, 1 / 16, big)
+            assert torch.equal(o, want) and torch.equal(big, first), i
+    assert pa.pa_last_error(c.h) == 0
+    check(host(want), q.astype(np.float64), c, [(1, 1, 899), (2, 2, 299)], 1, 0, 1 / 16, DECODE_FLOOR)
+    check(host(first), q.astype(np.float64), c, [(0, 0, 39999)], 1, 0, 1 / 16, DECODE_FLOOR)
