@@ -95,6 +95,21 @@ __device__ __forceinline__ uint32_t f16x2_minus_1152(uint32_t u) {
 __device__ __forceinline__ uint32_t expand_lo(uint32_t x) { return __byte_perm(x, 0x64646464u, 0x5140); }
 __device__ __forceinline__ uint32_t expand_hi(uint32_t x) { return __byte_perm(x, 0x64646464u, 0x7362); }
 
+// Position of the pairs in the launch's block list: pair (s, g) starts at
+// HKV vstart(s) + g n_vis(s).
+struct PairPos {
+  int s, g, start;
+  DecSeq d;
+};
+__device__ __forceinline__ void dec_next_pair(const DecodeParams& p, const DecodeSeqs& tab, PairPos& r) {
+  r.start += r.d.n_vis;
+  if (++r.g == p.HKV) {
+    r.g = 0;
+    ++r.s;
+    r.d = dec_seq(p, tab, r.s);
+  }
+}
+
 // The pair that holds block x (0 <= x < total): the last sequence whose first
 // block is at or before x (binary search over the table), then the kv head.
 __device__ __forceinline__ PairPos dec_locate(const DecodeParams& p, const DecodeSeqs& tab, int x) {

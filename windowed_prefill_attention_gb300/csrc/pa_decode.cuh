@@ -1,6 +1,5 @@
 // Device helpers of the decode kernels (pa_decode.cu, pa_kv4_decode.cu): the
-// warp-level products, and where a launch's blocks lie in its list of
-// (sequence, kv head) pairs.
+// warp-level products, and a sequence's visible blocks.
 #pragma once
 #include <cstdint>
 #include <cuda_fp16.h>
@@ -67,21 +66,5 @@ __device__ __forceinline__ DecSeq dec_seq(const P& p, const T& tab, int s) {
 }
 // Logical key block of the b-th visible block of a sequence.
 __device__ __forceinline__ int dec_block(const DecSeq& d, int b) { return b < d.n_sink ? b : d.lo + (b - d.n_sink); }
-
-// Position of the pairs in the launch's block list: pair (s, g) starts at
-// HKV vstart(s) + g n_vis(s).
-struct PairPos {
-  int s, g, start;
-  DecSeq d;
-};
-template <class P, class T>
-__device__ __forceinline__ void dec_next_pair(const P& p, const T& tab, PairPos& r) {
-  r.start += r.d.n_vis;
-  if (++r.g == p.HKV) {
-    r.g = 0;
-    ++r.s;
-    r.d = dec_seq(p, tab, r.s);
-  }
-}
 
 }  // namespace pa

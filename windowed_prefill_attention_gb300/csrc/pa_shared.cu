@@ -25,6 +25,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "pa_early.cuh"
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
 #include "pa_shared.h"
@@ -82,8 +83,6 @@ __device__ __forceinline__ uint4 lds_u32x4(uint32_t addr) {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // 16 TMEM lanes x 128 columns in the 16x256b shape (see pa_ptx.cuh).
 __device__ __forceinline__ void tmem_st_16x256b_x16(uint32_t taddr, const uint32_t (&r)[64]) {
 #define PA_SH_W8(i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
@@ -1390,21 +1389,6 @@ __global__ void __launch_bounds__(8 * kMergeDims / 4 * kMergeMostWays) merge_ker
   store_row(p, sq.x, g, r, dq, acc, l);
 }
 
-template <typename... Params>
-cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t st, const Params&... params) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, params...);
-}
-
 }  // namespace
 
 cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, const DecodeMaps& maps, cudaStream_t st) {
@@ -1416,16 +1400,15 @@ cudaError_t launch_decode_shared(const SharedParams& p, const SharedSeqs& t, con
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem)) != cudaSuccess) return e;
     kernel<<<p.n_cta * p.n_units, kPreThreads, kPreSmem, st>>>(p, t);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_after(own_kernel, dim3((unsigned)own_grid), kOwnWarps * 32, kOwnSmem, st, p, t, maps)) != cudaSuccess)
+    if ((e = launch_early(own_kernel, dim3((unsigned)own_grid), kOwnWarps * 32, kOwnSmem, st, p, t, maps)) != cudaSuccess)
       return e;
   } else {
     own_kernel<<<own_grid, kOwnWarps * 32, kOwnSmem, st>>>(p, t, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (p.merge_ways == 0) return cudaSuccess;
-  return launch_after(merge_kernel, dim3((unsigned)(p.n_seq * p.HKV), kHeadDim / kMergeDims),
-                      kMergeDims / 4 * p.G * p.merge_ways, 0, st,
-                      p, t);
+  return launch_early(merge_kernel, dim3((unsigned)(p.n_seq * p.HKV), kHeadDim / kMergeDims),
+                      (unsigned)(kMergeDims / 4 * p.G * p.merge_ways), 0, st, p, t);
 }
 
 }  // namespace pa
