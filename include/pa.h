@@ -438,9 +438,12 @@ int pa_kv4_decode(pa_handle h, int n_seq, const pa_seq* seqs, int n_rows, const 
  * inputs (PA_EINVAL).  With PA_P_F16 a weight times V's row scale is rounded to fp16, by 2^-11 of it or
  * 2^-12 of the row's largest such product, whatever rows the query does not see.  Few tokens on long contexts (fewer 256-row work units than the GPU
  * has pairs of SMs) have their keys split over the pairs (p_mode PA_P_F16); the sums of the
- * parts are joined in fp32, in an order that the sequences' lengths alone decide.  The plan
- * is the handle's and changes from call to call, so a call on a capturing stream is
- * PA_EINVAL. */
+ * parts are joined in fp32, in a fixed order.  Where the keys are split depends on all of the call's
+ * sequences, the mask, the head counts and the GPU, and how V's scales are held on the sequences whose
+ * units share a pair of SMs: the same call gives the same bits, a sequence in another batch may
+ * differ in rounding.  The plan and the work buffers are the handle's, as for pa_prefill: calls go one after
+ * another (on several streams, ordered by the caller), and a call on a capturing stream is PA_EINVAL.
+ * The first call of new lengths also plans and uploads (some 13 us more). */
 int pa_kv4_prefill(pa_handle h, int n_seq, const pa_seq* seqs, int n_rows, const void* q, const void* q_gate,
                    const uint8_t* pool, const int32_t* block_table, int n_sink_blk, int n_win_blk, float sm_scale,
                    void* out, void* stream);

@@ -49,8 +49,8 @@ namespace pa {
 namespace {
 
 // Two tiles a step, whose scores share one vote and whose products are independent
-// chains: 535 instructions a tile (605 one at a time) and as many registers as 8 warps an
-// SM leave.  5 contexts of 120 to 200 thousand tokens, 237 MB: 46.9 us (5.0 TB/s; the copies
+// chains: some 520 instructions a tile with all set-up (70 more one at a time) and as many registers
+// as 8 warps an SM leave.  5 contexts of 120 to 200 thousand tokens, 237 MB: 46.9 us (5.0 TB/s; the copies
 // alone take 40.6), 64 windowed contexts, 157 MB: 35.9.  With the scales under a normaliser of the
 // largest one so far, which lost what lay far below it, 45.7 and 35.7, and then: one tile a
 // step on 12 warps 48.4, on 8 warps 51.7, on 16 warps of 128 registers 52.6; three steps in the ring
