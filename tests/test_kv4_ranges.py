@@ -298,3 +298,22 @@ def test_int8_prefill_on_the_u8_grid_of_tiles_of_next_to_no_weight(drop):
         v = vc.cpu().numpy().astype(np.float64).reshape(-1, 2, D)[:128, g] * np.float64(np.float32(0.01))
         bound = 2.0 ** -8 * np.abs(v.mean(0)) + 0.51 / 255 * 1.27 + 2.0 ** -10 * np.abs(v).mean(0) + 2.0 ** (7 - drop)
         assert np.all(np.abs(host(out)[:, 4 * g: 4 * g + 4] - v.mean(0)) <= bound)
+
+
+@pytest.mark.parametrize("pieces", PREFILLS)
+@pytest.mark.parametrize("ratio", [8, 16, 30])
+def test_prefill_beside_rows_of_zeros(pieces, ratio):
+    """Every third V row of zeros, with 2^ratio times the others' weight: the outputs are small, and as right as others."""
+    lengths = [a + n for a, n in pieces]
+    sm = 1 / 128
+    base = bf16_round(np.random.default_rng(19).standard_normal(D).astype(np.float32)).astype(np.float64)
+
+    def change(k, v, slots):
+        for pages, rows in slots:
+            v[pages[::3], rows[::3]] = 0
+            k[pages[::3], rows[::3]] = base * (ratio * np.log(2) / (base @ base) / sm)
+
+    c = cache_of(69, lengths, 8, 2, change)
+    q = np.tile(base.astype(np.float32), (sum(n for _, n in pieces), 8, 1))
+    got, rows = prefill(c, pieces, q, 1, 0, sm)
+    check_rows(got, q, c, rows, 1, 0, sm, *PREFILL_STEP)

@@ -145,7 +145,8 @@ __device__ __forceinline__ int pow2_ceil_exp(float x) {
   const int eb = (int)((__float_as_uint(x) >> 23) & 0xff);
   return imax(-100, imin(100, eb - 126));
 }
-// Of the 4-bit pool's V scales of a sequence's head the largest's bits, and 0x7f800000 - those of the least over 0 (0: none).
+// Of the 4-bit pool's V scales of a sequence's head the largest's bits, and 0x7f800000 - the least's (0: it has none).  A
+// row of zeros lies apart from all others: under one normaliser its weight, not its product, would be the reference.
 __device__ __forceinline__ bool scales_alike(uint32_t most, uint32_t least_inv) {
   return most < (127u + 16u) << 23 && (least_inv == 0u || most - (0x7f800000u - least_inv) <= kAlike << 23);
 }
@@ -552,7 +553,7 @@ __device__ __forceinline__ void role_mma(const AttnParams& p, const AttnSplit& s
 // even CTA, whose MMA issuer multiplies both.
 //
 // References.  P' = 2^(y - m - ev) x V scale, m from the row's largest score y, 2^ev above the largest V scale of
-// the sequence's keys.  Where the 4-bit pool's scales lie further apart than 2^kAlike (or are huge), that would take
+// the sequence's keys.  Where the 4-bit pool's scales lie further apart than 2^kAlike (or are huge, or 0), that would take
 // the bits of the rows that do not see the largest, or give it no weight: their units take kExact tiles, whose m
 // follows the row's largest z = y + d, 2^d the power of two above the key's own scale, and P' = 2^(y - m) x V scale:
 // in fp16's range whatever the scales, and held against the row's largest product.

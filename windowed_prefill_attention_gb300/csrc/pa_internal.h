@@ -39,7 +39,6 @@ struct WidenParams {
   float* ks;                  // [HKV][n_tok_cap]        per-token K scale
   float* vs;                  // [HKV][n_tok_cap]        per-token V scale
   // [n_seq][HKV] float bits: max V scale (atomicMax); of the 4-bit pool then [n_seq][HKV] 0x7f800000 - those of the least
-  // V scale over 0 (0 where there is none)
   unsigned int* vsmax;
   int* err;
   float k_mult = 1.f;         // ks = k_scale * k_mult (the attention folds sm_scale * log2(e) in here)

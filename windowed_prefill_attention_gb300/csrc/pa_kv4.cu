@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kWidenThreads) kv4_widen_kernel(const __grid_c
   constexpr int kVWords = (2048 + 256) / 16;  // V's codes and block scales of a tile
   constexpr int kVLoads = (HKV * kVWords + kWidenThreads - 1) / kWidenThreads;
   __shared__ uint4 v_sh[HKV * kVWords];
-  __shared__ unsigned int vmax_sh[2 * HKV];  // the largest V scale's bits, 0x7f800000 - those of the least over 0
+  __shared__ unsigned int vmax_sh[2 * HKV];  // the largest V scale's bits, 0x7f800000 - the least's
   const int blk = blockIdx.x, tid = threadIdx.x;
   dependents_may_start();
   if (tid < 2 * HKV) vmax_sh[tid] = 0u;
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kWidenThreads) kv4_widen_kernel(const __grid_c
     const int r = tid & 15, g = tid >> 4;
     p.ks[(size_t)g * p.n_tok_cap + row0 + r] = ks_row * p.k_mult;
     p.vs[(size_t)g * p.n_tok_cap + row0 + r] = vs_row;
-    if (vs_row > 0.f) {
+    if (r < n_valid) {
       atomicMax(&vmax_sh[g], __float_as_uint(vs_row));
       atomicMax(&vmax_sh[HKV + g], 0x7f800000u - __float_as_uint(vs_row));
     }
