@@ -317,3 +317,24 @@ def test_prefill_beside_rows_of_zeros(pieces, ratio):
     q = np.tile(base.astype(np.float32), (sum(n for _, n in pieces), 8, 1))
     got, rows = prefill(c, pieces, q, 1, 0, sm)
     check_rows(got, q, c, rows, 1, 0, sm, *PREFILL_STEP)
+
+
+@pytest.mark.parametrize("exponent", [-30, -60, -80])
+@pytest.mark.parametrize("drop", [30, 60])
+def test_prefill_on_the_u8_grid_of_small_values(exponent, drop):
+    """Small V rows, and behind the first tile one of little weight, so that the grid's step is small too."""
+    base = bf16_round(np.random.default_rng(20).standard_normal(D).astype(np.float32)).astype(np.float64)
+    sm = 1 / 16
+
+    def change(k, v, slots):
+        for pages, rows in slots:
+            k[pages, rows] = 0
+            k[pages[128:], rows[128:]] = -base * (drop * np.log(2) / (base @ base) / sm)
+            v[pages, rows] = np.ldexp(v[pages, rows], exponent)
+            v[pages[5], rows[5]] = 0  # by products, not under one normaliser
+
+    c = cache_of(70, [180], 8, 2, change)
+    q = np.tile(base.astype(np.float32), (40, 8, 1))
+    got, rows = prefill(c, [(140, 40)], q, 1, 0, sm, options=dict(p_mode=1))
+    half_step, least = PREFILL_STEP
+    check_rows(got, q, c, rows, 1, 0, sm, half_step + 0.51 / 255, least)

@@ -53,7 +53,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
-#include <type_traits>
 
 #include "pa_early.cuh"
 #include "pa_internal.h"
@@ -920,6 +919,7 @@ __device__ __forceinline__ uint4 gate8(uint4 v, uint4 g) {
 // times sigmoid(gate) when the call has an output gate.  O may be overwritten
 // once the last round's TMEM loads are done, so the MMA issuer is released
 // before the last stores.
+template <Form kForm>
 __device__ __forceinline__ bool epilogue(const AttnParams& p, const Ctx& c, const LaneRows& lr, int k_unit,
                                          uint32_t to, const float* l_rows, const float* sp_rows, int r,
                                          uint8_t* stage, int lane) {
@@ -928,7 +928,17 @@ __device__ __forceinline__ bool epilogue(const AttnParams& p, const Ctx& c, cons
   tc_fence_after();
   const float l = l_rows[(k_unit & 1) * kRows + r];
   const float sp = sp_rows[(k_unit & 1) * kRows + r];
-  const float fin = l > 0.f ? (p.p_mode == 1 ? sp : 1.f) / l : 0.f;
+  // The u8 grid's step and the sum of weights of small V scales may be far from 1, in product under fp32's range: of the
+  // 4-bit pool O is multiplied by each in turn.
+  constexpr bool kV4 = kForm != Form::kInt8;
+  const float step = p.p_mode == 1 ? sp : 1.f;
+  const float fin = l > 0.f ? (kV4 ? 1.f : step) / l : 0.f;
+  const auto value2 = [&](uint32_t o0, uint32_t o1) {
+    float2 x = make_float2(__uint_as_float(o0), __uint_as_float(o1));
+    if (kV4) x = mul2(mul2(x, make_float2(fin, fin)), make_float2(step, step));
+    else x = make_float2(x.x * fin, x.y * fin);
+    return __floats2bfloat162_rn(x.x, x.y);
+  };
   const int pc = lane & 7;
 #pragma unroll 1
   for (int cb = 0; cb < 4; ++cb) {
@@ -945,8 +955,8 @@ __device__ __forceinline__ bool epilogue(const AttnParams& p, const Ctx& c, cons
     uint32_t w[32];
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
-      __nv_bfloat162 a = __floats2bfloat162_rn(__uint_as_float(o0[2 * q]) * fin, __uint_as_float(o0[2 * q + 1]) * fin);
-      __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o1[2 * q]) * fin, __uint_as_float(o1[2 * q + 1]) * fin);
+      __nv_bfloat162 a = value2(o0[2 * q], o0[2 * q + 1]);
+      __nv_bfloat162 b = value2(o1[2 * q], o1[2 * q + 1]);
       w[q] = *reinterpret_cast<uint32_t*>(&a);
       w[16 + q] = *reinterpret_cast<uint32_t*>(&b);
     }
@@ -957,9 +967,10 @@ __device__ __forceinline__ bool epilogue(const AttnParams& p, const Ctx& c, cons
     if (p.gate) {
       uint4 g[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        g[k] = (lr.valid >> k) & 1u ? __ldg(reinterpret_cast<const uint4*>(p.gate + (size_t)lr.row[k] * kHeadDim + cb * 64) + pc)
-                                    : make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < 8; ++k) {
+        const uint4* gate = reinterpret_cast<const uint4*>(p.gate + (size_t)lr.row[k] * kHeadDim + cb * 64) + pc;
+        g[k] = (lr.valid >> k) & 1u ? (kV4 ? __ldcg(gate) : __ldg(gate)) : make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if ((lr.valid >> k) & 1u)
@@ -1043,7 +1054,7 @@ __device__ __forceinline__ void role_correction(const AttnParams& p, const AttnS
       if (kForm == Form::kKv4Parts)
         ok = epilogue_part(sp, c, lr, k_unit - 1, prev_u, c.tb + lane_off + kTmO, l_rows, sp_rows, r, qd, stage, lane);
       else
-        ok = epilogue(p, c, lr, k_unit - 1, c.tb + lane_off + kTmO, l_rows, sp_rows, r, stage, lane);
+        ok = epilogue<kForm>(p, c, lr, k_unit - 1, c.tb + lane_off + kTmO, l_rows, sp_rows, r, stage, lane);
     }
     prev_u = u;
     prev_t0 = un.t0 + (int)c.rank * p.TQ;
@@ -1055,7 +1066,7 @@ __device__ __forceinline__ void role_correction(const AttnParams& p, const AttnS
     if (kForm == Form::kKv4Parts)
       (void)epilogue_part(sp, c, lr, k_unit - 1, prev_u, c.tb + lane_off + kTmO, l_rows, sp_rows, r, qd, stage, lane);
     else
-      (void)epilogue(p, c, lr, k_unit - 1, c.tb + lane_off + kTmO, l_rows, sp_rows, r, stage, lane);
+      (void)epilogue<kForm>(p, c, lr, k_unit - 1, c.tb + lane_off + kTmO, l_rows, sp_rows, r, stage, lane);
   }
 }
 
