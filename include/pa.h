@@ -435,10 +435,11 @@ int pa_kv4_decode(pa_handle h, int n_seq, const pa_seq* seqs, int n_rows, const 
 /* pa_prefill_batch (q_gate NULL) or pa_prefill_batch_gated on the 4-bit pool; q_mode and
  * p_mode as there.  n_rows: rows of q, q_gate and out; sequences must not share rows
  * (PA_EINVAL), rows of no sequence are left as they were.  out must not overlap the
- * inputs (PA_EINVAL).  With PA_P_F16 a weight times V's row scale is rounded to fp16, by 2^-11 of it or
- * 2^-12 of the row's largest such product, whatever rows the query does not see.  Few tokens on long contexts (fewer 256-row work units than the GPU
- * has pairs of SMs) have their keys split over the pairs (p_mode PA_P_F16); the sums of the
- * parts are joined in fp32, in a fixed order.  Where the keys are split depends on all of the call's
+ * inputs (PA_EINVAL).  With PA_P_F16 a weight times V's row scale is rounded to fp16, by 2^-11
+ * of it or 2^-12 of the row's largest such product, whatever keys the row does not see.
+ * Few tokens on long contexts (fewer 256-row work units than the GPU has pairs of SMs) have
+ * their keys split over the pairs (p_mode PA_P_F16); the sums of the parts are joined in
+ * fp32, in a fixed order.  Where the keys are split depends on all of the call's
  * sequences, the mask, the head counts and the GPU, and how V's scales are held on the sequences whose
  * units share a pair of SMs: the same call gives the same bits, a sequence in another batch may
  * differ in rounding.  The plan and the work buffers are the handle's, as for pa_prefill: calls go one after
