@@ -3,7 +3,7 @@ work buffers grow, calls that fail."""
 import numpy as np
 import pytest
 
-from kv4_testutil import D, random_rows
+from kv4_testutil import D, PAGE, quantise, random_rows, unpack, values
 from test_kv4 import DECODE_FLOOR, PREFILL_FLOOR, Cache, check, dev_bf16, host
 
 pytestmark = pytest.mark.gpu
@@ -142,3 +142,34 @@ def test_captured_decodes_keep_their_buffers_when_a_larger_call_moves_them():
     assert pa.pa_last_error(c.h) == 0
     check(host(want), q.astype(np.float64), c, [(1, 1, 899), (2, 2, 299)], 1, 0, 1 / 16, DECODE_FLOOR)
     check(host(first), q.astype(np.float64), c, [(0, 0, 39999)], 1, 0, 1 / 16, DECODE_FLOOR)
+
+
+@pytest.mark.parametrize("n_seq,hq,hkv", [(700, 4, 2), (520, 14, 7)])
+def test_every_call_of_more_sequences_than_a_launch_takes(n_seq, hq, hkv):
+    import torch
+
+    import windowed_prefill_attention_gb300 as pa
+    lengths = [1 + (37 * s) % 90 for s in range(n_seq)]
+    new = [min(n, 1 + s % 3) for s, n in enumerate(lengths)]
+    off = np.cumsum([0] + new)
+    c = Cache(n_seq, lengths, hq, hkv)
+    rng = np.random.default_rng(n_seq)
+    k, v = (random_rows(rng, (off[-1], hkv, D)) for _ in range(2))
+    q = random_rows(rng, (off[-1], hq, D))
+    seqs = np.array([(off[s], lengths[s] - new[s], new[s], lengths[s]) for s in range(n_seq)], np.int32)
+    pa.pa_kv4_append(c.h, seqs, dev_bf16(k), dev_bf16(v), c.d_bt, c.d_tiles)
+    ko, vo = (torch.zeros(off[-1], hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pa.pa_kv4_gather(c.h, seqs, c.d_bt, c.d_tiles, ko, vo)
+    assert pa.pa_last_error(c.h) == 0
+    assert np.array_equal(host(ko), values(*quantise(k))) and np.array_equal(host(vo), values(*quantise(v)))
+    c.k, c.v = ([x[c.bt[s, : -(-n // PAGE)]].reshape(-1, hkv, D)[:n] for s, n in enumerate(lengths)] for x in unpack(c.d_tiles.cpu().numpy()))
+    dq = dev_bf16(q)
+    out = torch.zeros_like(dq)
+    pa.pa_kv4_prefill(c.h, seqs, dq, c.d_tiles, c.d_bt, 1, 3, 1 / 16, out)
+    assert pa.pa_last_error(c.h) == 0
+    check(host(out), q.astype(np.float64), c, [(off[s] + i, s, lengths[s] - new[s] + i) for s in range(0, n_seq, 7) for i in range(new[s])],
+          1, 3, 1 / 16, PREFILL_FLOOR)
+    one = np.array([(s, n - 1, 1, n) for s, n in enumerate(lengths)], np.int32)
+    pa.pa_kv4_decode(c.h, one, dq, c.d_tiles, c.d_bt, 1, 3, 1 / 16, out)
+    assert pa.pa_last_error(c.h) == 0
+    check(host(out), q.astype(np.float64), c, [(s, s, n - 1) for s, n in enumerate(lengths)][::5], 1, 3, 1 / 16, DECODE_FLOOR)
